@@ -21,8 +21,10 @@
  * focus_attention_two_call_fwd (the pages' two-call strategy, a comparator),
  * focus_layer_fwd_host (the layer from host buffers), the top-k membership
  * calls (*_topk, k = 2), the Sinkhorn soft assignment (focus_assign_scores,
- * focus_sinkhorn_fwd), the backward (focus_attention_bwd) and
- * focus_build_index_static (the index without a workspace).
+ * focus_sinkhorn_fwd), the backward (focus_attention_bwd),
+ * focus_build_index_static (the index without a workspace) and, for the tokens
+ * that follow the prompt, a paged 8-bit key/value cache: focus_cache_append,
+ * focus_cache_attention_fwd and focus_cache_evict.
  *
  * Conventions shared by every call
  *   - All tensor pointers are DEVICE pointers to row-major contiguous arrays,
@@ -59,7 +61,8 @@
 extern "C" {
 #endif
 
-#define FOCUS_ABI_VERSION 3   /* 2: adds the top-k membership calls; 3: the split top-2 index layout */
+#define FOCUS_ABI_VERSION 3   /* 2: adds the top-k membership calls; 3: the split top-2 index layout.
+                                 The cache calls only add entry points: no layout changed. */
 
 #if defined(__GNUC__)
 #define FOCUS_API __attribute__((visibility("default")))
@@ -83,7 +86,8 @@ typedef enum {
   FOCUS_ERR_WORKSPACE = 3,     /* ws_bytes < focus_workspace_bytes(p)           */
   FOCUS_ERR_CUDA = 4,          /* a CUDA runtime/launch call failed             */
   FOCUS_ERR_TIMEOUT = 5,       /* device: a bounded wait ran out                */
-  FOCUS_ERR_BAD_GROUP_ID = 6   /* device: a group id outside [0, K)             */
+  FOCUS_ERR_BAD_GROUP_ID = 6,  /* device: a group id outside [0, K)             */
+  FOCUS_ERR_BAD_CACHE = 7      /* device: a cache's page, length or position out of range */
 } focus_status_t;
 
 typedef enum { FOCUS_F32 = 0, FOCUS_BF16 = 1 } focus_dtype_t;
@@ -420,8 +424,110 @@ FOCUS_API focus_status_t focus_attention_bwd(const focus_params_t* p, const void
                                              void* dK, void* dV, void* ws, size_t ws_bytes,
                                              void* stream);
 
+/* ------------------------------------------------------ key/value cache ---
+ * Decoding: keys and values of earlier tokens stay in a paged cache in 8 bits,
+ * and the attention of new tokens reads from it only the pairs that Focus
+ * keeps ("Focus: Learning Which Attention Pairs Matter" 2.2: far pairs of
+ * different groups are skipped at inference).  The pages describe no cache;
+ * its layout is this library's own.
+ *
+ * A page holds FOCUS_CACHE_PAGE slots (one token each) of one sequence for
+ * every key/value head.  table[b] lists a sequence's pages: slot s of head h is
+ * row s % 64 of page table[b][s / 64].  Entries past a sequence's last page are
+ * not read.  Heads may hold different tokens (after an eviction), so len counts
+ * slots per head; slots are in ascending token position.  K and V are e4m3
+ * codes with one scale for each page and head, a power of two 2^e with
+ * e >= FOCUS_CACHE_MIN_EXP: a row's value is code * scale. */
+#define FOCUS_CACHE_PAGE 64
+/* Smallest scale exponent of a page (values below 2^-73 are stored as 0). */
+#define FOCUS_CACHE_MIN_EXP (-64)
+/* Largest number of new tokens a sequence in one focus_cache_attention_fwd. */
+#define FOCUS_CACHE_MAX_QUERY 64
+/* Largest n_pages and max_pages. */
+#define FOCUS_CACHE_MAX_PAGES (1 << 24)
+
+/* Host struct of device pointers, all 16-byte aligned, all the caller's. */
+typedef struct {
+  uint8_t* k;          /* [n_pages][H_kv][64][d] e4m3 codes                     */
+  uint8_t* v;          /* [n_pages][H_kv][64][d] e4m3 codes                     */
+  float* k_scale;      /* [n_pages][H_kv]                                       */
+  float* v_scale;      /* [n_pages][H_kv]                                       */
+  int32_t* pos;        /* [n_pages][H_kv][64] token position of each slot       */
+  int16_t* gid;        /* [n_pages][H_kv][64] group id of each slot             */
+  float* mass;         /* [n_pages][H_kv][64] accumulated attention weight, or NULL */
+  int32_t* table;      /* [B][max_pages] page ids                               */
+  int32_t* len;        /* [B][H_kv] slots in use                                */
+  int32_t* next;       /* [B] position that the next appended token gets        */
+  int32_t n_pages, max_pages;
+} focus_cache_t;
+
+/* Bytes of device workspace the cache calls need for problem p (p->n: the most
+ * new tokens of one call) on this cache; 0 if either is invalid.  The error
+ * word comes first, as in the other workspaces; call focus_workspace_init
+ * once.  Pure host arithmetic. */
+FOCUS_API size_t focus_cache_workspace_bytes(const focus_params_t* p, const focus_cache_t* cache);
+
+/* Appends new tokens' keys and values.  Sequence b gets n_new[b] tokens
+ * (n_new == NULL: p->n of them; otherwise values in [0, p->n], rows behind them
+ * are not read), with positions next[b], next[b] + 1, ...; every head's new
+ * slots follow its len[b][h].  Per page and head the scale exponent is the
+ * least that holds the new rows' largest finite magnitude at 448, or the
+ * page's own where it already holds older slots and its exponent is larger;
+ * where it grows, the older rows are rounded again at the new one.  Infinite
+ * values are stored as +-448 * scale, NaN as NaN; a slot's mass starts at 0.
+ *   K, V [B, H_kv, n, d] dtype of p;  gid [B, A, n] int32;  n_new [B] int32 or NULL;
+ *   len_out [B, H_kv], next_out [B] int32: the new counts; may be cache->len and
+ *   cache->next (the counts are written after every block has read them).
+ * d in {64, 128}.  Pages must belong to one sequence.  A sequence for which a
+ * head's slots would not fit max_pages, or whose next would pass 2^31 - 1, is
+ * left as it was and flagged as FOCUS_ERR_BAD_CACHE in the device error word,
+ * as is a page id outside [0, n_pages) (its rows are dropped) and a gid outside
+ * [0, K) as FOCUS_ERR_BAD_GROUP_ID (clamped). */
+FOCUS_API focus_status_t focus_cache_append(const focus_params_t* p, const void* K, const void* V,
+                                            const int32_t* gid, const int32_t* n_new,
+                                            const focus_cache_t* cache, int32_t* len_out,
+                                            int32_t* next_out, void* ws, size_t ws_bytes,
+                                            void* stream);
+
+/* Focus attention of the newest tokens over the cache, usually right after
+ * their append.  Token t of sequence b sits at position
+ * i = next[b] - n_new[b] + t and keeps the slots with pos <= i and
+ * (i - pos < w or equal group id); softmax(scale * q . k) is exact over them.
+ *   Q, O [B, H, n, d] dtype of p, n <= FOCUS_CACHE_MAX_QUERY;
+ *   gid [B, A, n] int32;  n_new [B] int32 or NULL as in focus_cache_append;
+ *   lse_opt [B, H, n] fp32 or NULL.
+ * A token that keeps no slot gets O = 0 and lse = -infinity.  Rows t >= n_new[b]
+ * of O and lse_opt stay as they were.  accumulate != 0 adds to mass[slot] the
+ * softmax weights that the slot received, summed over the new tokens and the
+ * query heads of its key/value head in a fixed order.  Products are exact (q in
+ * f16 parts that hold it, codes in f16), sums in fp32; the softmax weights go
+ * into the value product as f16 (bf16 tensors) or as f16 parts that hold them
+ * to fp32 accuracy (fp32 tensors). */
+FOCUS_API focus_status_t focus_cache_attention_fwd(const focus_params_t* p, const void* Q,
+                                                   const int32_t* gid, const int32_t* n_new,
+                                                   const focus_cache_t* cache, void* O,
+                                                   float* lse_opt, int32_t accumulate, void* ws,
+                                                   size_t ws_bytes, void* stream);
+
+/* Copies what an eviction keeps from src's pages into dst's.  Per sequence and
+ * head with len > budget, the slots of the last `recent` positions
+ * (pos >= next - recent) stay, and of the others those with the most mass (ties:
+ * the lower slot; NaN counts as the most), `budget` slots in all; with
+ * len <= budget every slot stays.  Order, positions, group ids and mass are
+ * kept; a dst page's scale exponent is the least that holds its rows, to which
+ * they are rounded (exact unless a value falls below the e4m3 normals there).
+ * dst->len gets the kept counts, dst->next src's.
+ *   1 <= budget, 0 <= recent <= budget; both caches need mass; dst->max_pages
+ *   must hold budget slots.  src and dst may share pools (the same arrays and
+ *   n_pages) but no pages in use, and not the table; dst->len and dst->next may
+ *   be src's.  dst's rows past the kept slots stay as they were. */
+FOCUS_API focus_status_t focus_cache_evict(const focus_params_t* p, int32_t budget, int32_t recent,
+                                           const focus_cache_t* src, const focus_cache_t* dst,
+                                           void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, reads and clears the device error word in ws.
- * Returns FOCUS_OK, FOCUS_ERR_BAD_GROUP_ID, FOCUS_ERR_TIMEOUT or FOCUS_ERR_CUDA. */
+ * Returns FOCUS_OK, FOCUS_ERR_BAD_GROUP_ID, FOCUS_ERR_BAD_CACHE, FOCUS_ERR_TIMEOUT
+ * or FOCUS_ERR_CUDA. */
 FOCUS_API focus_status_t focus_check_errors(void* ws, void* stream);
 
 /* Static description of a status code. */

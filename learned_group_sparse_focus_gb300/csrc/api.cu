@@ -389,6 +389,7 @@ const char* focus_status_string(focus_status_t s) {
     case FOCUS_ERR_CUDA: return "CUDA error";
     case FOCUS_ERR_TIMEOUT: return "device wait timed out";
     case FOCUS_ERR_BAD_GROUP_ID: return "group id outside [0, K)";
+    case FOCUS_ERR_BAD_CACHE: return "cache page, length or position out of range";
   }
   return "unknown status";
 }
@@ -1092,6 +1093,85 @@ focus_status_t focus_attention_bwd(const focus_params_t* p, const void* Q, const
   return cuda_status(e);
 }
 
+// ------------------------------------------------------ key/value cache ---
+
+static bool cache_ok(const focus_cache_t* c) {
+  if (!c || c->n_pages < 1 || c->n_pages > FOCUS_CACHE_MAX_PAGES) return false;
+  if (c->max_pages < 1 || c->max_pages > FOCUS_CACHE_MAX_PAGES) return false;
+  const void* all[] = {c->k, c->v, c->k_scale, c->v_scale, c->pos, c->gid, c->table, c->len, c->next};
+  for (const void* x : all)
+    if (!x || !aligned16(x)) return false;
+  return aligned16(c->mass);
+}
+
+// Workspace: error word and the append's ticket, then one region that the
+// attention (a logit per slot and query row of one pass) and the eviction (the
+// kept slots per head) use in turn.
+static size_t cache_region(const focus_params_t* p, const focus_cache_t* c) {
+  if (!c->mass) return 0;
+  const size_t lists = static_cast<size_t>(p->B) * p->H_kv * (static_cast<size_t>(c->max_pages) * kPage + 1) * 4;
+  const size_t logits = static_cast<size_t>(c->n_pages) * p->H_kv * kPage * cache_logit_rows(p->H / p->H_kv, p->n) * 4;
+  return lists > logits ? lists : logits;
+}
+
+size_t focus_cache_workspace_bytes(const focus_params_t* p, const focus_cache_t* cache) {
+  if (!params_ok(p) || !cache_ok(cache)) return 0;
+  return align_up(kAlign) + align_up(cache_region(p, cache));
+}
+
+static focus_status_t cache_args(const focus_params_t* p, const focus_cache_t* c, const void* ws,
+                                 size_t ws_bytes) {
+  if (!params_ok(p) || !cache_ok(c)) return FOCUS_ERR_INVALID_ARG;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return FOCUS_ERR_INVALID_ARG;
+  if (ws_bytes < focus_cache_workspace_bytes(p, c)) return FOCUS_ERR_WORKSPACE;
+  if (!(p->d == 64 || p->d == 128) || p->H_kv > 65535) return FOCUS_ERR_UNSUPPORTED;
+  return FOCUS_OK;
+}
+
+focus_status_t focus_cache_append(const focus_params_t* p, const void* K, const void* V,
+                                  const int32_t* gid, const int32_t* n_new, const focus_cache_t* cache,
+                                  int32_t* len_out, int32_t* next_out, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  if (focus_status_t s = cache_args(p, cache, ws, ws_bytes)) return s;
+  const void* all[] = {K, V, gid, len_out, next_out};
+  for (const void* x : all)
+    if (!x || !aligned16(x)) return FOCUS_ERR_INVALID_ARG;
+  if (!aligned16(n_new)) return FOCUS_ERR_INVALID_ARG;
+  if (focus_status_t s = ensure_setup()) return s;
+  CacheAppendLaunch L{K, V, gid, n_new, *cache, len_out, next_out, p->B, p->H_kv, p->n, p->d, p->A, p->K,
+                      at<int>(ws, 64), at<int>(ws, 0)};
+  return cuda_status(launch_cache_append(L, p->dtype, static_cast<cudaStream_t>(stream)));
+}
+
+focus_status_t focus_cache_attention_fwd(const focus_params_t* p, const void* Q, const int32_t* gid,
+                                         const int32_t* n_new, const focus_cache_t* cache, void* O,
+                                         float* lse_opt, int32_t accumulate, void* ws, size_t ws_bytes,
+                                         void* stream) {
+  if (focus_status_t s = cache_args(p, cache, ws, ws_bytes)) return s;
+  const void* all[] = {Q, gid, O};
+  for (const void* x : all)
+    if (!x || !aligned16(x)) return FOCUS_ERR_INVALID_ARG;
+  if (!aligned16(n_new) || !aligned16(lse_opt) || (accumulate && !cache->mass)) return FOCUS_ERR_INVALID_ARG;
+  if (p->n > FOCUS_CACHE_MAX_QUERY) return FOCUS_ERR_UNSUPPORTED;
+  if (focus_status_t s = ensure_setup()) return s;
+  CacheAttnLaunch L{Q, gid, n_new, *cache, O, lse_opt, accumulate ? at<float>(ws, kAlign) : nullptr,
+                    p->B, p->H, p->H_kv, p->n, p->d, p->A, p->w > 1 ? p->w : 1,
+                    p->scale * 1.4426950408889634f, at<int>(ws, 0)};
+  return cuda_status(launch_cache_attn(L, p->dtype, static_cast<cudaStream_t>(stream)));
+}
+
+focus_status_t focus_cache_evict(const focus_params_t* p, int32_t budget, int32_t recent,
+                                 const focus_cache_t* src, const focus_cache_t* dst, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  if (focus_status_t s = cache_args(p, src, ws, ws_bytes)) return s;
+  if (!cache_ok(dst) || !src->mass || !dst->mass || dst->table == src->table) return FOCUS_ERR_INVALID_ARG;
+  if (budget < 1 || recent < 0 || recent > budget) return FOCUS_ERR_INVALID_ARG;
+  if (static_cast<long long>(dst->max_pages) * kPage < budget) return FOCUS_ERR_INVALID_ARG;
+  if (focus_status_t s = ensure_setup()) return s;
+  CacheEvictLaunch L{*src, *dst, p->B, p->H_kv, p->d, budget, recent, at<int32_t>(ws, kAlign), at<int>(ws, 0)};
+  return cuda_status(launch_cache_evict(L, static_cast<cudaStream_t>(stream)));
+}
+
 focus_status_t focus_check_errors(void* ws, void* stream) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return FOCUS_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1102,6 +1182,7 @@ focus_status_t focus_check_errors(void* ws, void* stream) {
   if (cudaMemset(ws, 0, sizeof(int)) != cudaSuccess) return FOCUS_ERR_CUDA;
   if (word & kErrTimeout) return FOCUS_ERR_TIMEOUT;
   if (word & kErrBadGroup) return FOCUS_ERR_BAD_GROUP_ID;
+  if (word & kErrBadCache) return FOCUS_ERR_BAD_CACHE;
   return FOCUS_ERR_CUDA;
 }
 

@@ -1,0 +1,87 @@
+// Device helpers of the paged 8-bit key/value cache: bounds-checked lookups,
+// e4m3 conversions and the page scale rule.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace focus {
+
+// Slots of head h in use, kept inside the table (a bad count raises the flag).
+__device__ __forceinline__ int cache_len(const focus_cache_t& c, int H_kv, int b, int h, int* err) {
+  const int n = c.len[b * H_kv + h];
+  const int cap = c.max_pages * kPage;
+  if (n >= 0 && n <= cap) return n;
+  atomicOr(err, kErrBadCache);
+  return n < 0 ? 0 : cap;
+}
+
+// Page j of sequence b, or -1 (and the flag) for an id outside the pool.
+__device__ __forceinline__ int cache_page(const focus_cache_t& c, int b, int j, int* err) {
+  const int g = c.table[static_cast<size_t>(b) * c.max_pages + j];
+  if (g >= 0 && g < c.n_pages) return g;
+  atomicOr(err, kErrBadCache);
+  return -1;
+}
+
+// New tokens of sequence b: n_new[b] inside [0, n] (n without the array).
+__device__ __forceinline__ int cache_new(const int32_t* n_new, int n, int b, int* err) {
+  if (!n_new) return n;
+  const int m = n_new[b];
+  if (m >= 0 && m <= n) return m;
+  atomicOr(err, kErrBadCache);
+  return m < 0 ? 0 : n;
+}
+
+// The keep rule: query position i, key position j, window w >= 1.
+__device__ __forceinline__ bool cache_keep(int i, int j, int w, bool same_group) {
+  return j <= i && (same_group || static_cast<uint32_t>(i) - static_cast<uint32_t>(j) < static_cast<uint32_t>(w));
+}
+
+__device__ __forceinline__ float exp2_int(int e) {   // 2^e, -126 <= e <= 127
+  return __int_as_float((e + 127) << 23);
+}
+
+// Exponent of a stored scale, inside the range the append writes.
+__device__ __forceinline__ int scale_exp(float s) {
+  const int e = static_cast<int>((__float_as_uint(s) >> 23) & 255u) - 127;
+  return min(max(e, kMinExp), 120);
+}
+
+// Least e >= kMinExp with a <= 448 * 2^e = 1.75 * 2^(e + 8), from the bits of a
+// finite a >= 0.  Anything below 2^-56 needs no more than kMinExp.
+__device__ __forceinline__ int need_exp(uint32_t a) {
+  const int x = static_cast<int>(a >> 23) - 127;
+  return max(x - 8 + ((a & 0x7fffffu) > 0x600000u ? 1 : 0), kMinExp);
+}
+
+// Two e4m3 codes (low byte first) <-> floats.  e4m3 fits f16 exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t c) {
+  const uint32_t r = e4m3x2_to_f16x2(c);
+  return __half22float2(*reinterpret_cast<const __half2*>(&r));
+}
+// Round to nearest even, values past 448 to +-448, NaN to NaN.
+__device__ __forceinline__ uint16_t float2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Four codes times f, rounded to e4m3 again.
+__device__ __forceinline__ uint32_t rescale4(uint32_t c, float f) {
+  const float2 a = e4m3x2_to_float2(static_cast<uint16_t>(c));
+  const float2 b = e4m3x2_to_float2(static_cast<uint16_t>(c >> 16));
+  return static_cast<uint32_t>(float2_to_e4m3x2(a.x * f, a.y * f)) |
+         (static_cast<uint32_t>(float2_to_e4m3x2(b.x * f, b.y * f)) << 16);
+}
+__device__ __forceinline__ uint4 rescale16(uint4 c, float f) {
+  return make_uint4(rescale4(c.x, f), rescale4(c.y, f), rescale4(c.z, f), rescale4(c.w, f));
+}
+
+}  // namespace focus

@@ -21,6 +21,7 @@ enum : int {
   kErrBadGroup = 1,   // a group id outside [0, K)
   kErrTimeout = 2,    // a bounded wait ran out
   kErrInternal = 4,   // an index or item failed a consistency check
+  kErrBadCache = 8,   // a cache's page id, length or position is out of range
 };
 
 // n counts the sorted items: tokens, or for top-k membership the n_tok * k
@@ -229,5 +230,46 @@ cudaError_t setup_bwd_tc_kernels();
 cudaError_t launch_bwd_permute_q(const BwdArgs& a, void* Qs, void* dOs, float* lse_s, float* delta_s,
                                  cudaStream_t st);
 cudaError_t launch_sinkhorn(const SinkhornLaunch& L, int iters, cudaStream_t st);
+
+// cache.cu, cache_attn.cu: the paged 8-bit key/value cache (layout: focus.h).
+constexpr int kPage = FOCUS_CACHE_PAGE;
+constexpr int kMinExp = FOCUS_CACHE_MIN_EXP;
+
+struct CacheAppendLaunch {
+  const void *K, *V;      // [B, H_kv, n, d]
+  const int32_t* gid;     // [B, A, n]
+  const int32_t* n_new;   // [B] or null
+  focus_cache_t c;
+  int32_t *len_out, *next_out;
+  int B, H_kv, n, d, A, K_groups;
+  int* ticket;            // blocks done in this launch (0 between launches)
+  int* err;
+};
+cudaError_t launch_cache_append(const CacheAppendLaunch& L, int dtype, cudaStream_t st);
+
+struct CacheEvictLaunch {
+  focus_cache_t src, dst;
+  int B, H_kv, d, budget, recent;
+  int32_t* keep;          // [B * H_kv][src.max_pages * 64] kept slots, ascending
+  int* err;
+};
+cudaError_t launch_cache_evict(const CacheEvictLaunch& L, cudaStream_t st);
+
+struct CacheAttnLaunch {
+  const void* Q;          // [B, H, n, d]
+  const int32_t* gid;     // [B, A, n]
+  const int32_t* n_new;   // [B] or null
+  focus_cache_t c;
+  void* O;
+  float* lse;             // or null
+  float* logits;          // accumulate: scratch, else null
+  int B, H, H_kv, n, d, A, w;
+  float scale_log2;       // scale * log2(e)
+  int* err;
+};
+// Query rows (tokens x query heads of a key/value head) whose logits one pass
+// keeps per slot when it accumulates weights.
+inline int cache_logit_rows(int group, int n) { return group * n > 8 ? 16 : 8; }
+cudaError_t launch_cache_attn(const CacheAttnLaunch& L, int dtype, cudaStream_t st);
 
 }  // namespace focus

@@ -18,9 +18,12 @@ LIB_PATH = os.path.join(_PKG, "_lib", "libfocus.so")
 F32, BF16 = 0, 1
 TILE_M = 128
 TILE_N = 128
+CACHE_PAGE = 64           # slots of a cache page
+CACHE_MAX_QUERY = 64      # new tokens a sequence in one focus_cache_attention_fwd
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace too small",
-          4: "CUDA error", 5: "device wait timed out", 6: "group id outside [0, K)"}
+          4: "CUDA error", 5: "device wait timed out", 6: "group id outside [0, K)",
+          7: "cache page, length or position out of range"}
 
 
 class FocusError(RuntimeError):
@@ -52,11 +55,17 @@ class IndexTopk(ctypes.Structure):
                 ("farlen_sub", ctypes.c_void_p)]
 
 
+class CacheStruct(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("k", "v", "k_scale", "v_scale", "pos", "gid", "mass", "table",
+                                               "len", "next")] + \
+               [("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libfocus.so not built ({LIB_PATH}); run __graft_entry__.build()")
     lib = ctypes.CDLL(LIB_PATH)
-    vp, P = ctypes.c_void_p, ctypes.POINTER(Params)
+    vp, P, C = ctypes.c_void_p, ctypes.POINTER(Params), ctypes.POINTER(CacheStruct)
     sig = {
         "focus_abi_version": ([], ctypes.c_int32),
         "focus_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -92,6 +101,11 @@ def _load():
         "focus_attention_topk_fwd_timed": ([P, vp, vp, vp, ctypes.POINTER(IndexTopk), vp, vp, vp,
                                             ctypes.c_size_t, vp, ctypes.POINTER(ctypes.c_void_p)],
                                            ctypes.c_int),
+        "focus_cache_workspace_bytes": ([P, C], ctypes.c_size_t),
+        "focus_cache_append": ([P, vp, vp, vp, vp, C, vp, vp, vp, ctypes.c_size_t, vp], ctypes.c_int),
+        "focus_cache_attention_fwd": ([P, vp, vp, vp, C, vp, vp, ctypes.c_int32, vp, ctypes.c_size_t, vp],
+                                      ctypes.c_int),
+        "focus_cache_evict": ([P, ctypes.c_int32, ctypes.c_int32, C, C, vp, ctypes.c_size_t, vp], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -109,7 +123,8 @@ EXPORTED = ("focus_abi_version", "focus_status_string", "focus_workspace_bytes",
             "focus_build_index_topk", "focus_attention_topk_fwd", "focus_attention_topk_fwd_timed",
             "focus_attention_two_call_fwd", "focus_sinkhorn_workspace_bytes", "focus_assign_scores",
             "focus_sinkhorn_fwd", "focus_backward_workspace_bytes", "focus_attention_bwd",
-            "focus_test_attention_wait_limit")
+            "focus_test_attention_wait_limit", "focus_cache_workspace_bytes", "focus_cache_append",
+            "focus_cache_attention_fwd", "focus_cache_evict")
 
 
 def lib():
@@ -355,6 +370,170 @@ def focus_sinkhorn_fwd(p: Params, iters: int, tau: float, S, G, ws, stream=None)
     """G (may be S): [B, A, n, K] fp32 soft assignment after `iters` rounds."""
     _check("focus_sinkhorn_fwd", _lib.focus_sinkhorn_fwd(ctypes.byref(p), int(iters), float(tau), _ptr(S),
                                                          _ptr(G), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+# --------------------------------------------------------- key/value cache ---
+
+def _expect(name: str, t, shape, dtype, device):
+    """A tensor argument of the cache calls: its shape, dtype, device, layout."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} "
+                         f"on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+@dataclass(frozen=True, eq=False)
+class Cache:
+    """A paged 8-bit key/value cache: the caller's device tensors, laid out as
+    focus_cache_t in include/focus.h.  Several caches may share the pool
+    tensors (k ... mass) and differ in table, len and next."""
+    k: torch.Tensor          # [n_pages, H_kv, 64, d] uint8, e4m3 codes
+    v: torch.Tensor          # [n_pages, H_kv, 64, d] uint8, e4m3 codes
+    k_scale: torch.Tensor    # [n_pages, H_kv] fp32, powers of two
+    v_scale: torch.Tensor    # [n_pages, H_kv] fp32, powers of two
+    pos: torch.Tensor        # [n_pages, H_kv, 64] int32
+    gid: torch.Tensor        # [n_pages, H_kv, 64] int16
+    mass: torch.Tensor | None  # [n_pages, H_kv, 64] fp32
+    table: torch.Tensor      # [B, max_pages] int32
+    len: torch.Tensor        # [B, H_kv] int32
+    next: torch.Tensor       # [B] int32
+
+    def __post_init__(self):
+        if self.k.dim() != 4 or self.table.dim() != 2:
+            raise ValueError("k must be [n_pages, H_kv, 64, d] and table [B, max_pages]")
+        pages, H_kv, _, d = self.k.shape
+        B, max_pages = self.table.shape
+        dev, page = self.k.device, (pages, H_kv, CACHE_PAGE)
+        c = CacheStruct(n_pages=pages, max_pages=max_pages)
+        i32, f32, u8 = torch.int32, torch.float32, torch.uint8
+        for name, shape, dtype in (("k", page + (d,), u8), ("v", page + (d,), u8), ("k_scale", page[:2], f32),
+                                   ("v_scale", page[:2], f32), ("pos", page, i32), ("gid", page, torch.int16),
+                                   ("mass", page, f32), ("table", (B, max_pages), i32), ("len", (B, H_kv), i32),
+                                   ("next", (B,), i32)):
+            t = getattr(self, name)
+            if name == "mass" and t is None:
+                continue
+            setattr(c, name, _expect(name, t, shape, dtype, dev))
+        object.__setattr__(self, "struct", c)
+        object.__setattr__(self, "device", dev)
+        object.__setattr__(self, "dims", (B, H_kv, d))
+
+
+def alloc_cache(p: Params, max_tokens: int, mass: bool = False, device="cuda") -> Cache:
+    """An empty cache with room for max_tokens slots a sequence, pages in order."""
+    if max_tokens < 1:
+        raise ValueError("max_tokens must be at least 1")
+    pages = -(-int(max_tokens) // CACHE_PAGE)
+    n, shape = p.B * pages, (p.B * pages, p.H_kv, CACHE_PAGE)
+
+    def zeros(shape, dtype):
+        return torch.zeros(shape, dtype=dtype, device=device)
+
+    return Cache(k=zeros(shape + (p.d,), torch.uint8), v=zeros(shape + (p.d,), torch.uint8),
+                 k_scale=zeros(shape[:2], torch.float32), v_scale=zeros(shape[:2], torch.float32),
+                 pos=zeros(shape, torch.int32), gid=zeros(shape, torch.int16),
+                 mass=zeros(shape, torch.float32) if mass else None,
+                 table=torch.arange(n, dtype=torch.int32, device=device).view(p.B, pages),
+                 len=zeros((p.B, p.H_kv), torch.int32), next=zeros((p.B,), torch.int32))
+
+
+def focus_cache_workspace_bytes(p: Params, cache: Cache) -> int:
+    return int(_lib.focus_cache_workspace_bytes(ctypes.byref(p), ctypes.byref(cache.struct)))
+
+
+def alloc_workspace_cache(p: Params, cache: Cache, stream=None) -> torch.Tensor:
+    """Caller-owned workspace for the cache calls on this cache (p.n: the most
+    new tokens of one call), error word cleared."""
+    nbytes = focus_cache_workspace_bytes(p, cache)
+    if nbytes == 0:
+        raise FocusError("focus_cache_workspace_bytes", 1)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+    with torch.cuda.device(cache.device):
+        focus_workspace_init(ws, stream)
+    return ws
+
+
+def _cache_call(fn: str, p: Params, cache: Cache, ws, stream, args):
+    """Runs a cache call on the cache's device (args: the C arguments between p
+    and ws)."""
+    if cache.dims != (p.B, p.H_kv, p.d):
+        raise ValueError(f"the cache holds (B, H_kv, d) = {cache.dims}, the call asks for {(p.B, p.H_kv, p.d)}")
+    dev = cache.device
+    if dev.type != "cuda":
+        raise ValueError(f"the cache must be on a CUDA device, not {dev}")
+    if ws.device != dev or (stream is not None and stream.device != dev):
+        raise ValueError(f"workspace and stream must be on the cache's device {dev}")
+    call = getattr(_lib, fn)
+    if dev.index == torch.cuda.current_device():
+        st = call(ctypes.byref(p), *args, _ptr(ws), ws.numel(), _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = call(ctypes.byref(p), *args, _ptr(ws), ws.numel(), _stream(stream))
+    _check(fn, st)
+
+
+def _float_type(p: Params):
+    return torch.bfloat16 if p.dtype == BF16 else torch.float32
+
+
+def focus_cache_append(p: Params, K, V, gid, cache: Cache, ws, n_new=None, len_out=None, next_out=None, stream=None):
+    """Appends K, V [B, H_kv, n, d] and gid [B, A, n]; n_new [B] int32: valid
+    tokens a sequence (None: all n).  The counts are updated in place, or written
+    to len_out [B, H_kv] and next_out [B]."""
+    dev, rows = cache.device, (p.B, p.H_kv, p.n, p.d)
+    ft, i32 = _float_type(p), torch.int32
+    args = (_expect("K", K, rows, ft, dev), _expect("V", V, rows, ft, dev),
+            _expect("gid", gid, (p.B, p.A, p.n), i32, dev),
+            None if n_new is None else _expect("n_new", n_new, (p.B,), i32, dev), ctypes.byref(cache.struct),
+            cache.struct.len if len_out is None else _expect("len_out", len_out, (p.B, p.H_kv), i32, dev),
+            cache.struct.next if next_out is None else _expect("next_out", next_out, (p.B,), i32, dev))
+    _cache_call("focus_cache_append", p, cache, ws, stream, args)
+
+
+def focus_cache_attention_fwd(p: Params, Q, gid, cache: Cache, O, lse, ws, n_new=None, accumulate=False,
+                              stream=None):
+    """Attention of the newest tokens Q [B, H, n, d] (the last n_new[b] appended
+    ones) over the cache into O and lse ([B, H, n] fp32 or None); accumulate adds
+    the weights each slot received to cache.mass."""
+    dev, rows, i32 = cache.device, (p.B, p.H, p.n, p.d), torch.int32
+    ft = _float_type(p)
+    args = (_expect("Q", Q, rows, ft, dev), _expect("gid", gid, (p.B, p.A, p.n), i32, dev),
+            None if n_new is None else _expect("n_new", n_new, (p.B,), i32, dev), ctypes.byref(cache.struct),
+            _expect("O", O, rows, ft, dev), None if lse is None else _expect("lse", lse, rows[:3], torch.float32, dev),
+            int(bool(accumulate)))
+    _cache_call("focus_cache_attention_fwd", p, cache, ws, stream, args)
+
+
+def focus_cache_evict(p: Params, budget: int, recent: int, src: Cache, dst: Cache, ws, stream=None):
+    """Copies the at most `budget` slots a head that stay (the last `recent`
+    positions, then the most mass) from src's pages into dst's."""
+    if dst.device != src.device or dst.dims != src.dims:
+        raise ValueError("src and dst must be on one device and agree in B, H_kv and d")
+    _cache_call("focus_cache_evict", p, src, ws, stream, (int(budget), int(recent), ctypes.byref(src.struct),
+                                                          ctypes.byref(dst.struct)))
+
+
+def run_decode_step(p: Params, h, W, C, Q, K, V, cache: Cache, ws, ws_cache, n_new=None, want_lse=False,
+                    accumulate=False, stream=None):
+    """assign -> append -> attention for p.n new tokens a sequence; returns (O,
+    gid, lse).  ws: a workspace of alloc_workspace(p); ws_cache: one of
+    alloc_workspace_cache(p, cache).  Rows behind n_new[b] of O are 0."""
+    dev = cache.device
+    with torch.cuda.device(dev), torch.cuda.stream(stream):      # the fills below run on the call's stream
+        gid = torch.empty((p.B, p.A, p.n), dtype=torch.int32, device=dev)
+        O = torch.empty_like(Q) if n_new is None else torch.zeros_like(Q)
+        lse = None
+        if want_lse:
+            lse = torch.full((p.B, p.H, p.n), float("-inf"), dtype=torch.float32, device=dev)
+        focus_assign(p, h, W, C, gid, ws, stream)
+        focus_cache_append(p, K, V, gid, cache, ws_cache, n_new=n_new, stream=stream)
+        focus_cache_attention_fwd(p, Q, gid, cache, O, lse, ws_cache, n_new=n_new, accumulate=accumulate,
+                                  stream=stream)
+    return O, gid, lse
 
 
 # ------------------------------------------------------------ index views ---
