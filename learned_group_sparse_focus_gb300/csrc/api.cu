@@ -114,6 +114,7 @@ focus_status_t ensure_setup() {
     if (setup_attn_kernels() != cudaSuccess) return FOCUS_ERR_CUDA;
     if (setup_bwd_tc_kernels() != cudaSuccess) return FOCUS_ERR_CUDA;
     if (setup_sinkhorn_kernels() != cudaSuccess) return FOCUS_ERR_CUDA;
+    if (setup_cache_kernels() != cudaSuccess) return FOCUS_ERR_CUDA;
     g_ready[dev] = true;
   }
   return FOCUS_OK;
@@ -1156,7 +1157,7 @@ focus_status_t focus_cache_attention_fwd(const focus_params_t* p, const void* Q,
   if (focus_status_t s = ensure_setup()) return s;
   CacheAttnLaunch L{Q, gid, n_new, *cache, O, lse_opt, accumulate ? at<float>(ws, kAlign) : nullptr,
                     p->B, p->H, p->H_kv, p->n, p->d, p->A, p->w > 1 ? p->w : 1,
-                    p->scale * 1.4426950408889634f, at<int>(ws, 0)};
+                    p->scale * 1.4426950408889634f, at<int>(ws, 0), sm_count()};
   return cuda_status(launch_cache_attn(L, p->dtype, static_cast<cudaStream_t>(stream)));
 }
 
