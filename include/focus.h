@@ -461,10 +461,10 @@ typedef struct {
   int32_t n_pages, max_pages;
 } focus_cache_t;
 
-/* Bytes of device workspace the cache calls need for problem p (p->n: the most
- * new tokens of one call) on this cache; 0 if either is invalid.  The error
- * word comes first, as in the other workspaces; call focus_workspace_init
- * once.  Pure host arithmetic. */
+/* Bytes of device workspace the cache calls need for problem p on this cache (an
+ * eviction: its src), whatever p->n; 0 if either is invalid.  The error word
+ * comes first, as in the other workspaces; call focus_workspace_init once.
+ * Pure host arithmetic. */
 FOCUS_API size_t focus_cache_workspace_bytes(const focus_params_t* p, const focus_cache_t* cache);
 
 /* Appends new tokens' keys and values.  Sequence b gets n_new[b] tokens
@@ -499,10 +499,11 @@ FOCUS_API focus_status_t focus_cache_append(const focus_params_t* p, const void*
  * A token that keeps no slot gets O = 0 and lse = -infinity.  Rows t >= n_new[b]
  * of O and lse_opt stay as they were.  accumulate != 0 adds to mass[slot] the
  * softmax weights that the slot received, summed over the new tokens and the
- * query heads of its key/value head in a fixed order.  Products are exact (q in
- * f16 parts that hold it, codes in f16), sums in fp32; the softmax weights go
- * into the value product as f16 (bf16 tensors) or as f16 parts that hold them
- * to fp32 accuracy (fp32 tensors). */
+ * query heads of its key/value head in a fixed order.  Sums are fp32.  q enters
+ * the products in two parts: bf16's 8 bits whole (elements below 2^-15 of the
+ * row's largest to 2^-23 of that), fp32 to 22 bits; the softmax weights enter
+ * the value product as f16 (bf16 tensors) or to 22 bits (fp32 tensors).
+ * K and V pools hold at most 2^36 bytes each (FOCUS_ERR_UNSUPPORTED). */
 FOCUS_API focus_status_t focus_cache_attention_fwd(const focus_params_t* p, const void* Q,
                                                    const int32_t* gid, const int32_t* n_new,
                                                    const focus_cache_t* cache, void* O,

@@ -1105,14 +1105,11 @@ static bool cache_ok(const focus_cache_t* c) {
   return aligned16(c->mass);
 }
 
-// Workspace: error word and the append's ticket, then one region that the
-// attention (a logit per slot and query row of one pass) and the eviction (the
-// kept slots per head) use in turn.
+// Workspace: error word and the append's ticket, then the eviction's kept slots
+// per head.
 static size_t cache_region(const focus_params_t* p, const focus_cache_t* c) {
   if (!c->mass) return 0;
-  const size_t lists = static_cast<size_t>(p->B) * p->H_kv * (static_cast<size_t>(c->max_pages) * kPage + 1) * 4;
-  const size_t logits = static_cast<size_t>(c->n_pages) * p->H_kv * kPage * cache_logit_rows(p->H / p->H_kv, p->n) * 4;
-  return lists > logits ? lists : logits;
+  return static_cast<size_t>(p->B) * p->H_kv * (static_cast<size_t>(c->max_pages) * kPage + 1) * 4;
 }
 
 size_t focus_cache_workspace_bytes(const focus_params_t* p, const focus_cache_t* cache) {
@@ -1126,6 +1123,8 @@ static focus_status_t cache_args(const focus_params_t* p, const focus_cache_t* c
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return FOCUS_ERR_INVALID_ARG;
   if (ws_bytes < focus_cache_workspace_bytes(p, c)) return FOCUS_ERR_WORKSPACE;
   if (!(p->d == 64 || p->d == 128) || p->H_kv > 65535) return FOCUS_ERR_UNSUPPORTED;
+  // the attention addresses the pools in 32-bit counts of 16 bytes
+  if (static_cast<unsigned long long>(c->n_pages) * p->H_kv * kPage * p->d > (1ull << 36)) return FOCUS_ERR_UNSUPPORTED;
   return FOCUS_OK;
 }
 
@@ -1155,7 +1154,7 @@ focus_status_t focus_cache_attention_fwd(const focus_params_t* p, const void* Q,
   if (!aligned16(n_new) || !aligned16(lse_opt) || (accumulate && !cache->mass)) return FOCUS_ERR_INVALID_ARG;
   if (p->n > FOCUS_CACHE_MAX_QUERY) return FOCUS_ERR_UNSUPPORTED;
   if (focus_status_t s = ensure_setup()) return s;
-  CacheAttnLaunch L{Q, gid, n_new, *cache, O, lse_opt, accumulate ? at<float>(ws, kAlign) : nullptr,
+  CacheAttnLaunch L{Q, gid, n_new, *cache, O, lse_opt, accumulate != 0,
                     p->B, p->H, p->H_kv, p->n, p->d, p->A, p->w > 1 ? p->w : 1,
                     p->scale * 1.4426950408889634f, at<int>(ws, 0), sm_count()};
   return cuda_status(launch_cache_attn(L, p->dtype, static_cast<cudaStream_t>(stream)));

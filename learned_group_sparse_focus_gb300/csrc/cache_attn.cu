@@ -9,10 +9,10 @@
 // its partial result: it reads its pages' group ids (and, among the last
 // w + n_new slots, positions: slots are in ascending position, so no earlier
 // slot can lie in a window), appends the kept slots to a list in shared memory,
-// and gathers their rows in tiles of 16 keys with cp.async, kStages tiles ahead.
-// Only kept rows are read.
+// and gathers their rows in tiles of 16 keys with cp.async, a tile ahead of the
+// products.  Only kept rows are read.
 //
-// Products run on mma.m16n8k16 with the keys on the 16 side and the query rows
+// Products run on mma.sync with the keys on the 16 side and the query rows
 // (tokens x query heads of the head) on the 8 side:
 //   S^T = K Q^T:    thread (g, c) = (lane / 4, lane % 4) holds row g of the key
 //                   fragment.  The sum over d may run in any order, so the thread
@@ -21,21 +21,25 @@
 //   O^T += V^T P^T: two keys' bytes of one column are zipped with one byte
 //                   permute into the pairs that the fragment wants; P^T comes
 //                   from S^T by an 8x8 register transpose.
-// Codes become f16 exactly.  Queries are scaled by a power of two per row to
-// below 2^15 and held in one f16 (bf16 tensors: 8 bits fit 11) or two (fp32
-// tensors, 22 bits).  Accumulation is fp32.
+// Codes become f16 exactly and the products run in f16 with fp32 sums (e4m3
+// operands of mma.sync are taken apart into the same f16 products on this
+// architecture, with more conversions: 14 instructions against 9 here).
+// Queries are scaled by a power of two per row to below 2^14 and held in one f16
+// (bf16 tensors: 8 bits fit 11) or two (fp32 tensors, 22 bits); weights are
+// rounded to one f16 or two likewise.
 //
 // Softmax: with v = code * 2^e per page, the running maximum is taken over
-// t_j = s_j + e_j (log2), so the f16 weights 2^(t_j - ref) multiply raw codes and
+// t_j = s_j + e_j (log2), so the weights 2^(t_j - ref) multiply raw codes and
 // stay in range for pages of any scale; the row sum adds 2^(t_j - ref) 2^-e_j in
 // fp32.  ref lies 7 below the maximum when it is set and is moved only when a
 // weight would pass 2^15, so f16's subnormals begin 2^-21 below the largest one.
 //
-// The warps' partials are joined in shared memory, the blocks' through the
-// cluster's distributed shared memory, each block writing a part of the rows.
-// With accumulate, logits of the kept slots go to scratch (4 bytes a row and
-// key, against 2 d bytes of key and value) and are turned into weights after
-// the join, by the warp that wrote them: no atomics, a fixed order.
+// The warps' partials are joined in shared memory; each block then sends every
+// other block of the cluster the part of the rows that that one writes.
+// With accumulate a second pass over the listed slots, when the rows' sums are
+// known, forms the logits again from K (d bytes a kept slot; keeping them would
+// cost 8 bytes a slot and query row) and adds each slot's weights: one addition
+// a slot, in a fixed order.
 #include <cooperative_groups.h>
 #include <type_traits>
 
@@ -50,30 +54,42 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kKeys = 16;            // keys of a tile
 constexpr int kStages = 2;           // tiles in flight per warp
-constexpr int kFar = INT_MIN;        // list position of a slot outside every window
-constexpr int kListBytes = 4096;     // a warp's list of kept slots
+constexpr int kMaxCluster = 16;      // blocks of a cluster, at most
+constexpr int kAhead = 16;           // pages whose group ids a warp holds in shared memory
+constexpr int kList = 256;           // entries of a warp's list of kept slots
+constexpr float kNoRef = -1e30f;     // reference of a row without kept slots
+static_assert(kList >= kPage + (kStages + 1) * kKeys && (kList & (kList - 1)) == 0, "list too short");
 
-template <typename T, int D, int NT, bool kMulti>
+template <typename T, int D, int NT>
 struct Cfg {
-  static constexpr int kBatch = kMulti ? 2 : 4;                           // pages scanned at a time
-  static constexpr int kList = kListBytes / (kMulti ? 16 : 8);            // list entries
-  static_assert(kList >= kBatch * kPage + (kStages + 2) * kKeys && (kList & (kList - 1)) == 0, "list too short");
   static constexpr int kParts = std::is_same<T, float>::value ? 2 : 1;   // f16 parts of q and of P
   static constexpr int kRows = 8 * NT;
-  static constexpr int kStageBytes = 2 * kKeys * D;                       // K rows, then V rows
-  static constexpr int kRing = kStages * kStageBytes > kRows * D * 4 ? kStages * kStageBytes : kRows * D * 4;
-  static constexpr int kWarpBytes = kRing + kListBytes;
-  static constexpr int kSmem = kWarps * kWarpBytes;
-  static constexpr int kSteps = D / 16;                                   // MMA steps over d
+  static constexpr int kSteps = D / 16;                                  // f16 MMA steps over d
+  static constexpr int kStageBytes = 2 * kKeys * D;                      // K rows, then V rows
+  // A warp's region: the tile ring, later its partial result (rows 16 bytes apart
+  // modulo 64, so that a fragment's stores fall on different banks), the list and
+  // the group ids.
+  static constexpr int kPitch = D * 4 + 16;
+  static constexpr int kRing = kStages * kStageBytes > kRows * kPitch ? kStages * kStageBytes : kRows * kPitch;
+  static constexpr int kWarpBytes = kRing + kList * 8 + kAhead * kPage * 2;
+  static constexpr int kItems = kRows * D / 4;                           // float4 pieces of a row block's result
+  static constexpr int kInbox = (kItems + kMaxCluster) * 16;             // pieces of every block of the cluster
+  static constexpr int kSmem = kWarps * kWarpBytes + 2 * kInbox;
 };
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
       " {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 2^x, results below the normals 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // 8x8 transpose of 16-bit elements across the warp.
@@ -106,119 +122,134 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float* f) {
   f[0] = __uint_as_float(u.x << 16); f[1] = __uint_as_float(u.x & 0xffff0000u);
   f[2] = __uint_as_float(u.y << 16); f[3] = __uint_as_float(u.y & 0xffff0000u);
 }
-__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+__device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y) {
+  *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(x, y);
 }
-
-// A warp's walk over its pages.  Table entries and scales are fetched for 32 pages at a time, one page a lane;
-// group ids and positions kBatch pages at a time, one batch ahead of their use.
-template <int kBatch>
-struct Scan {
-  int first, step, pages, n, near_from;        // the warp's pages: first, first + step, ...
-  int k;                                       // ordinal of the batch in registers
-  int lane_page, lane_exp;                     // per lane: page and exponents of 32 pages
-  int page[kBatch], exps[kBatch];
-  uint32_t ids[kBatch];
-  int2 pos[kBatch];
-
-  __device__ __forceinline__ void fetch(const CacheAttnLaunch& L, int b, int h, int lane) {
-    if ((k & 31) == 0) {
-      const int j = first + (k + lane) * step;
-      lane_page = -1;
-      lane_exp = 0;
-      if (j < pages) lane_page = cache_page(L.c, b, j, L.err);
-      if (lane_page >= 0) {
-        const size_t plane = static_cast<size_t>(lane_page) * L.H_kv + h;
-        lane_exp = (scale_exp(L.c.k_scale[plane]) & 0xffff) | (scale_exp(L.c.v_scale[plane]) << 16);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      page[i] = __shfl_sync(~0u, lane_page, (k + i) & 31);
-      exps[i] = __shfl_sync(~0u, lane_exp, (k + i) & 31);
-      ids[i] = 0;
-      pos[i] = make_int2(kFar, kFar);
-      if (page[i] >= 0) {
-        const int j = first + (k + i) * step;
-        const size_t at = (static_cast<size_t>(page[i]) * L.H_kv + h) * kPage + 2 * lane;
-        ids[i] = *reinterpret_cast<const uint32_t*>(L.c.gid + at);
-        if ((j + 1) * kPage > near_from) pos[i] = *reinterpret_cast<const int2*>(L.c.pos + at);
-      }
-    }
-  }
-
-  __device__ __forceinline__ bool done() const { return first + k * step >= pages; }
-};
 
 template <typename T, int D, int NT, bool kMulti>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(CacheAttnLaunch L) {
-  using C = Cfg<T, D, NT, kMulti>;
-  constexpr int kBatch = C::kBatch, kList = C::kList;
+  using C = Cfg<T, D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
-  __shared__ float s_M[C::kRows], s_L[C::kRows];       // the block's reference and sum per row
+  __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];   // the warps' references and sums per row
+  __shared__ float2 s_all[2][kMaxCluster][C::kRows];   // ... and the cluster's blocks'
+  __shared__ float s_factor[kMaxCluster][C::kRows];    // weight of a block's partial in the row
   __shared__ float s_lse[C::kRows];                    // log2 sum-exp of the whole row
   __shared__ int s_gid[C::kRows];                      // group id of each token of the row block
+  cg::cluster_group cluster = cg::this_cluster();
+  // Every block of the cluster has to run before another writes into it: waited
+  // for at the first join.
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int h = blockIdx.y, b = blockIdx.z;
   const int cs = gridDim.x, rank = blockIdx.x;         // the cluster spans grid x
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int gl = lane / 4, cl = lane % 4;
   const int G = L.H / L.H_kv;
-  const int n = cache_len(L.c, L.H_kv, b, h, L.err);
-  const int fresh = cache_new(L.n_new, L.n, b, L.err);
-  const int rows = G * fresh;
-  const int pos0 = L.c.next[b] - fresh;                // position of token 0
-  const int near = static_cast<int>(min(static_cast<long long>(n), static_cast<long long>(L.w) + fresh));
   uint8_t* ring = smem + warp * C::kWarpBytes;
-  // The slots that the warp's pages keep, a ring of kList entries: page * 64 + row
-  // and the scale exponents of K (low half) and V; with several tokens also the
-  // position (kFar outside every window) and the group id.
+  // Kept slots: x = first 16-byte piece of the slot's row in the pool, y = scale
+  // exponents of K and V (bytes 0 and 1) and a bit for each token that keeps it.
   int2* list = reinterpret_cast<int2*>(ring + C::kRing);
-  int2* about = list + (kMulti ? kList : 0);
+  uint32_t* ids = reinterpret_cast<uint32_t*>(ring + C::kRing + kList * 8);
+  uint8_t* inbox = smem + kWarps * C::kWarpBytes;
   const int32_t* gids = L.gid + (static_cast<size_t>(b) * L.A + (L.A == 1 ? 0 : h)) * L.n;
+  const int first = warp * cs + rank, step = kWarps * cs;          // the warp's pages
+  auto table = [&](int from) {                         // table entry of the lane's page among kAhead, unchecked
+    const int j = from + lane * step;
+    return lane < kAhead && j < L.c.max_pages ? L.c.table[static_cast<size_t>(b) * L.c.max_pages + j] : -1;
+  };
+  int n = 0, fresh = 0, pos0 = 0, pages = 0, near_from = 0;
+  int rows = G;                                        // set in the first round, which always runs
 
-  for (int r0 = 0; r0 < rows; r0 += C::kRows) {
-    const int t_lo = r0 / G, tokens = (min(r0 + C::kRows, rows) - 1) / G - t_lo + 1;
-    Scan<kBatch> scan;
-    scan.first = warp * cs + rank;
-    scan.step = kWarps * cs;
-    scan.pages = (n + kPage - 1) / kPage;
-    scan.n = n;
-    scan.near_from = n - near;
-    scan.k = 0;
-    scan.fetch(L, b, h, lane);
+  int buf = 0;
+  for (int r0 = 0; r0 < rows; r0 += C::kRows, buf ^= 1) {
+    // ---- loads that depend on nothing go first: table, group ids, query rows, counts
+    int entry = table(first);
+    const int t_lo = r0 / G;
     const int gid0 = gids[t_lo];
+    int gid_mine = 0;
+    if (kMulti && threadIdx.x < C::kRows && t_lo + threadIdx.x < L.n) gid_mine = gids[t_lo + threadIdx.x];
+    float x[NT][C::kSteps][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = r0 + nt * 8 + gl;
+      if (r < G * L.n) {
+        const T* src = static_cast<const T*>(L.Q) +
+                       ((static_cast<size_t>(b) * L.H + h * G + r % G) * L.n + r / G) * D;
+#pragma unroll
+        for (int s = 0; s < C::kSteps; ++s) load4(src + (cl + 4 * (s / 4)) * 16 + (s % 4) * 4, x[nt][s]);
+      } else {
+#pragma unroll
+        for (int s = 0; s < C::kSteps; ++s) x[nt][s][0] = x[nt][s][1] = x[nt][s][2] = x[nt][s][3] = 0.f;
+      }
+    }
+    if (r0 == 0) {
+      n = cache_len(L.c, L.H_kv, b, h, L.err);
+      fresh = cache_new(L.n_new, L.n, b, L.err);
+      pos0 = L.c.next[b] - fresh;                      // position of token 0
+      rows = G * fresh;
+      pages = (n + kPage - 1) / kPage;
+      near_from = n - static_cast<int>(min(static_cast<long long>(n), static_cast<long long>(L.w) + fresh));
+      if (rows == 0) break;                            // the same in the whole cluster
+    }
+    const int tokens = (min(r0 + C::kRows, rows) - 1) / G - t_lo + 1;
+
+    // ---- the scan: kAhead pages at a time, their group ids in shared memory
+    int j = first, i = 0;                              // next page to scan, and its place among the kAhead
+    int lane_page = -1, lane_exps = 0;
+    int2 pos{};                                        // positions of the lane's two slots of page j, if it is near
+    auto load_pos = [&]() {
+      const int page = __shfl_sync(~0u, lane_page, i);
+      if (page >= 0 && (j + 1) * kPage > near_from)
+        pos = *reinterpret_cast<const int2*>(L.c.pos + (static_cast<size_t>(page) * L.H_kv + h) * kPage + 2 * lane);
+    };
+    auto open_pages = [&]() {                          // pages j, j + step, ...
+      i = 0;
+      lane_page = -1;
+      if (lane < kAhead && j + lane * step < pages) {
+        lane_page = entry;
+        if (entry < 0 || entry >= L.c.n_pages) {
+          atomicOr(L.err, kErrBadCache);
+          lane_page = -1;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kAhead * kPage * 2 / 16 / 32; ++x) {
+        const int page = __shfl_sync(~0u, lane_page, x * 4 + lane / 8);
+        if (page >= 0)
+          cp_async_16(ids + x * 128 + lane * 4,
+                      L.c.gid + (static_cast<size_t>(page) * L.H_kv + h) * kPage + lane % 8 * 8, 16);
+      }
+      if (lane_page >= 0) {
+        const size_t plane = static_cast<size_t>(lane_page) * L.H_kv + h;
+        lane_exps = (scale_exp(L.c.k_scale[plane]) & 0xff) | (scale_exp(L.c.v_scale[plane]) & 0xff) << 8;
+      }
+      entry = table(j + kAhead * step);
+      load_pos();
+    };
+    open_pages();
     if (kMulti) {
-      if (threadIdx.x < tokens) s_gid[threadIdx.x] = gids[t_lo + threadIdx.x];
+      if (threadIdx.x < C::kRows) s_gid[threadIdx.x] = gid_mine;
       __syncthreads();
     }
 
     // ---- query fragments, row factors, and the rows this thread's logits belong to
     uint32_t q[C::kParts][NT][C::kSteps][2];
     float factor[NT][2];
-    int row_pos[NT][2], row_gid[NT][2];
+    int row_bit[NT][2];                                // bit of the row's token in a list entry, 0: no such row
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = r0 + nt * 8 + gl;
-      float x[C::kSteps][4];
       uint32_t top = 0;
-      if (r < rows) {
-        const T* src = static_cast<const T*>(L.Q) +
-                       ((static_cast<size_t>(b) * L.H + h * G + r % G) * L.n + r / G) * D;
-#pragma unroll
-        for (int s = 0; s < C::kSteps; ++s) load4(src + (cl + 4 * (s / 4)) * 16 + (s % 4) * 4, x[s]);
-      } else {
-#pragma unroll
-        for (int s = 0; s < C::kSteps; ++s) x[s][0] = x[s][1] = x[s][2] = x[s][3] = 0.f;
-      }
+      bool finite = true;
 #pragma unroll
       for (int s = 0; s < C::kSteps; ++s)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t u = __float_as_uint(x[s][e]) & 0x7fffffffu;
+          const uint32_t u = __float_as_uint(x[nt][s][e]) & 0x7fffffffu;
           if (u < 0x7f800000u) top = max(top, u);
+          else finite = false;
         }
+      // rows with an infinite or NaN element become NaN through their factor
+      finite = (__ballot_sync(~0u, finite) >> (lane & ~3) & 15) == 15;
       top = max(top, __shfl_xor_sync(~0u, top, 1));
       top = max(top, __shfl_xor_sync(~0u, top, 2));
       const int eq = min(max(static_cast<int>(top >> 23) - 127 - 13, -110), 115);   // |q| 2^-eq < 2^14
@@ -227,21 +258,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
       for (int s = 0; s < C::kSteps; ++s)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float lo = x[s][2 * e] * down, hi = x[s][2 * e + 1] * down;
+          const float lo = x[nt][s][2 * e] * down, hi = x[nt][s][2 * e + 1] * down;
           q[0][nt][s][e] = pack_half2(lo, hi);
-          if (C::kParts == 2) {
+          if constexpr (C::kParts == 2) {
             const float2 f = unpack_half2(q[0][nt][s][e]);
-            q[C::kParts - 1][nt][s][e] = pack_half2(lo - f.x, hi - f.y);
+            q[1][nt][s][e] = pack_half2(lo - f.x, hi - f.y);
           }
         }
-      const float mine = exp2_int(eq) * L.scale_log2;
+      const float mine = finite ? exp2_int(eq) * L.scale_log2 : __int_as_float(0x7fffffff);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         factor[nt][e] = __shfl_sync(~0u, mine, (2 * cl + e) * 4);
         const int rr = r0 + nt * 8 + 2 * cl + e;
-        const int t = rr < rows ? rr / G : t_lo;
-        row_pos[nt][e] = rr < rows ? pos0 + t : kFar;     // kFar: keeps nothing (see keeps)
-        row_gid[nt][e] = kMulti ? s_gid[t - t_lo] : gid0;
+        row_bit[nt][e] = rr < rows ? static_cast<int>(0x10000u << (kMulti ? rr / G - t_lo : 0)) : 0;
       }
     }
 
@@ -250,87 +279,83 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        ref[nt][e] = -INFINITY;
+        ref[nt][e] = kNoRef;
         sum[nt][e] = 0.f;
       }
 #pragma unroll
       for (int s = 0; s < C::kSteps; ++s) o[nt][s][0] = o[nt][s][1] = o[nt][s][2] = o[nt][s][3] = 0.f;
     }
 
-    // Whether a query row at position i in group g keeps a listed slot.
-    auto keeps = [&](int i, int g, const int2& slot) {
-      return slot.x == kFar ? slot.y == g : cache_keep(i, slot.x, L.w, slot.y == g);
-    };
-    // Index of a listed slot in the pool's per-slot arrays.
-    auto slot_at = [&](int row) {
-      const uint32_t r = static_cast<uint32_t>(row);
-      return (static_cast<size_t>(r / kPage) * L.H_kv + h) * kPage + r % kPage;
-    };
-
     int entries = 0;
-    // Appends the batch in registers to the list and fetches the next one.
-    auto scan_batch = [&]() {
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (scan.page[i] < 0) continue;
-        const int j = scan.first + (scan.k + i) * scan.step;
-        const int s = j * kPage + 2 * lane;
-        const int id0 = static_cast<int16_t>(scan.ids[i] & 0xffffu), id1 = static_cast<int16_t>(scan.ids[i] >> 16);
-        bool k0 = false, k1 = false;
-        const bool window = (j + 1) * kPage > scan.near_from;
-        for (int t = 0; t < (kMulti ? tokens : 1); ++t) {
-          const int g = kMulti ? s_gid[t] : gid0;
-          if (window) {
-            k0 = k0 || cache_keep(pos0 + t_lo + t, scan.pos[i].x, L.w, id0 == g);
-            k1 = k1 || cache_keep(pos0 + t_lo + t, scan.pos[i].y, L.w, id1 == g);
-          } else {
-            k0 = k0 || id0 == g;
-            k1 = k1 || id1 == g;
-          }
-        }
-        k0 = k0 && s < n;
-        k1 = k1 && s + 1 < n;
-        const uint32_t b0 = __ballot_sync(~0u, k0), b1 = __ballot_sync(~0u, k1);
-        const uint32_t before = (1u << lane) - 1;
-        const int at = entries + __popc(b0 & before) + __popc(b1 & before);
-        const int row = scan.page[i] * kPage + 2 * lane;
-        if (k0) {
-          list[at & (kList - 1)] = make_int2(row, scan.exps[i]);
-          if (kMulti) about[at & (kList - 1)] = make_int2(scan.pos[i].x, id0);
-        }
-        if (k1) {
-          list[(at + k0) & (kList - 1)] = make_int2(row + 1, scan.exps[i]);
-          if (kMulti) about[(at + k0) & (kList - 1)] = make_int2(scan.pos[i].y, id1);
-        }
-        entries += __popc(b0) + __popc(b1);
+    // Lists the kept slots of page j.
+    auto scan_page = [&]() {
+      if (i == 0) {                                    // new group ids have to have landed
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncwarp();
       }
-      scan.k += kBatch;
-      scan.fetch(L, b, h, lane);
+      const int page = __shfl_sync(~0u, lane_page, i), exps = __shfl_sync(~0u, lane_exps, i);
+      if (page >= 0) {
+        const uint32_t two = ids[i * 32 + lane];
+        const bool near = (j + 1) * kPage > near_from;
+        int m0 = 0, m1 = 0;
+        for (int t = 0; t < (kMulti ? tokens : 1); ++t) {
+          const int g = kMulti ? s_gid[t] : gid0, p = pos0 + t_lo + t;
+          bool k0 = static_cast<int16_t>(two & 0xffffu) == g, k1 = static_cast<int16_t>(two >> 16) == g;
+          if (near) {
+            k0 = cache_keep(p, pos.x, L.w, k0);
+            k1 = cache_keep(p, pos.y, L.w, k1);
+          }
+          m0 |= k0 << t;
+          m1 |= k1 << t;
+        }
+        if ((j + 1) * kPage > n) {
+          const int left = n - j * kPage - 2 * lane;
+          if (left < 1) m0 = 0;
+          if (left < 2) m1 = 0;
+        }
+        const uint32_t b0 = __ballot_sync(~0u, m0 != 0), b1 = __ballot_sync(~0u, m1 != 0);
+        if (b0 | b1) {
+          const uint32_t before = (1u << lane) - 1;
+          const int at = entries + __popc(b0 & before) + __popc(b1 & before);
+          const uint32_t row = ((static_cast<uint32_t>(page) * L.H_kv + h) * kPage + 2 * lane) * (D / 16);
+          if (m0) list[at & (kList - 1)] = make_int2(row, exps | m0 << 16);
+          if (m1) list[(at + (m0 != 0)) & (kList - 1)] = make_int2(row + D / 16, exps | m1 << 16);
+          entries += __popc(b0) + __popc(b1);
+        }
+      }
+      j += step;
+      ++i;
       __syncwarp();
+      if (i == kAhead) open_pages(); else load_pos();
     };
-    // Starts the copies of tile `tile` (rows past the list's end become zeros).
-    auto issue = [&](int tile) {
-      constexpr int kChunks = D / 16, kAtOnce = 32 / kChunks;
-      if (tile * kKeys < entries) {
+    // Starts the copies of tile `tile` (rows past the list's end become zeros).  Pieces
+    // are swizzled to spread a quarter warp's loads in compute() over all banks.
+    constexpr int kChunks = D / 16, kAtOnce = 32 / kChunks;
+    static_assert(kList % kKeys == 0, "a tile's entries are consecutive");
+    const int lr = lane / kChunks, lc = lane % kChunks;
+    const uint32_t to_k = lr * D + (D == 128 ? lc ^ (lr & 1) * 4 : lc) * 16;
+    const uint32_t to_v = kKeys * D + lr * D + (D == 128 ? lc ^ (lr >> 1) * 2 : lc ^ (lr >> 1)) * 16;
+    auto issue = [&](int tile, bool values) {
+      const int left = entries - tile * kKeys;
+      if (left > 0) {
         uint8_t* stage = ring + (tile % kStages) * C::kStageBytes;
-        const int c = lane % kChunks;
+        const int2* from = list + (tile * kKeys & (kList - 1)) + lr;
 #pragma unroll
-        for (int i = 0; i < kKeys / kAtOnce; ++i) {
-          const int r = i * kAtOnce + lane / kChunks;
-          const int idx = tile * kKeys + r;
-          const bool there = idx < entries;
-          const size_t off = slot_at(there ? list[idx & (kList - 1)].x : 0) * D + c * 16;
-          // swizzles that spread a quarter warp's loads (below) over all banks
-          const int kc = D == 128 ? c ^ ((r & 1) * 4) : c;
-          const int vc = D == 128 ? c ^ (((r >> 1) & 3) * 2) : c ^ ((r >> 1) & 3);
-          cp_async_16(stage + r * D + kc * 16, L.c.k + off, there ? 16 : 0);
-          cp_async_16(stage + kKeys * D + r * D + vc * 16, L.c.v + off, there ? 16 : 0);
+        for (int y = 0; y < kKeys / kAtOnce; ++y) {
+          const bool there = left >= kKeys || lr + y * kAtOnce < left;
+          const size_t off = static_cast<size_t>(static_cast<uint32_t>(there ? from[y * kAtOnce].x : 0) + lc) * 16;
+          cp_async_16(stage + to_k + y * kAtOnce * D, L.c.k + off, there ? 16 : 0);
+          // rows move on by kAtOnce: the value swizzle flips its upper bit with every odd y (d = 128)
+          if (values)
+            cp_async_16(stage + (to_v ^ (D == 128 ? (y & 1) * 64 : 0)) + y * kAtOnce * D, L.c.v + off, there ? 16 : 0);
         }
       }
       cp_async_commit();
     };
 
-    auto compute = [&](int tile) {
+    // Products of tile `tile`; `last`: the pass that only adds up the slots' weights.
+    auto compute = [&](int tile, bool last) {
       const uint8_t* ks = ring + (tile % kStages) * C::kStageBytes;
       const uint8_t* vs = ks + kKeys * D;
       // S^T: two chains of products
@@ -338,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) acc[nt][x][0] = acc[nt][x][1] = acc[nt][x][2] = acc[nt][x][3] = 0.f;
+        for (int y = 0; y < 2; ++y) acc[nt][y][0] = acc[nt][y][1] = acc[nt][y][2] = acc[nt][y][3] = 0.f;
 #pragma unroll
       for (int half = 0; half < D / 64; ++half) {
         const int c = cl + 4 * half, sw = D == 128 ? c ^ ((gl & 1) * 4) : c;   // gl + 8 has the same parity
@@ -355,51 +380,64 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int p = 0; p < C::kParts; ++p)
-              mma16816(acc[nt][w & 1], a0, a1, a2, a3, q[p][nt][half * 4 + w][0], q[p][nt][half * 4 + w][1]);
+              mma_f16(acc[nt][w & 1], a0, a1, a2, a3, q[p][nt][half * 4 + w][0], q[p][nt][half * 4 + w][1]);
         }
       }
-      // logits, masks and the reference
-      const int i0 = tile * kKeys + gl;
-      const int2 e0 = list[i0 & (kList - 1)], e1 = list[(i0 + 8) & (kList - 1)];
-      const int2 m0 = about[i0 & (kList - 1)], m1 = about[(i0 + 8) & (kList - 1)];
-      const bool in0 = i0 < entries, in1 = i0 + 8 < entries;
-      const float kf0 = exp2_int(static_cast<int16_t>(e0.y & 0xffff)), kf1 = exp2_int(static_cast<int16_t>(e1.y & 0xffff));
-      const int ve0 = e0.y >> 16, ve1 = e1.y >> 16;
-      bool kept[NT][4];
+      // logits; slots that a row does not keep: -inf
+      const int2* about = list + (tile * kKeys & (kList - 1)) + gl;
+      const int2 e0 = about[0], e1 = about[8];
+      const int left = entries - tile * kKeys - gl;
+      const int mask0 = left > 0 ? e0.y : 0, mask1 = left > 8 ? e1.y : 0;      // past the end: no row, scales 1
+      const float kf0 = exp2_int(static_cast<int8_t>(mask0)), kf1 = exp2_int(static_cast<int8_t>(mask1));
       float t[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          t[nt][y] = ((acc[nt][0][y] + acc[nt][1][y]) * factor[nt][y & 1]) * (y < 2 ? kf0 : kf1);
+          if (((y < 2 ? mask0 : mask1) & row_bit[nt][y & 1]) == 0) t[nt][y] = -INFINITY;
+        }
+      if (last) {
+        float w0 = 0.f, w1 = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float lse = s_lse[nt * 8 + 2 * cl + e];      // a large number for rows without kept slots
+            w0 += exp2_fast(t[nt][e] - lse);
+            w1 += exp2_fast(t[nt][2 + e] - lse);
+          }
+        w0 += __shfl_xor_sync(~0u, w0, 1);
+        w1 += __shfl_xor_sync(~0u, w1, 1);
+        w0 += __shfl_xor_sync(~0u, w0, 2);
+        w1 += __shfl_xor_sync(~0u, w1, 2);
+        // the only addition to this slot in this round: its order cannot matter
+        if (cl == 0 && left > 0) atomicAdd(L.c.mass + static_cast<uint32_t>(e0.x) / (D / 16), w0);
+        if (cl == 1 && left > 8) atomicAdd(L.c.mass + static_cast<uint32_t>(e1.x) / (D / 16), w1);
+        return;
+      }
+      // the weights' reference
+      const int ve0 = static_cast<int8_t>(mask0 >> 8), ve1 = static_cast<int8_t>(mask1 >> 8);
       bool grow = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int e = x & 1;
-          bool on = (x < 2 ? in0 : in1) && row_pos[nt][e] != kFar;
-          if (kMulti) on = on && keeps(row_pos[nt][e], row_gid[nt][e], x < 2 ? m0 : m1);
-          kept[nt][x] = on;
-          const float s = ((acc[nt][0][x] + acc[nt][1][x]) * factor[nt][e]) * (x < 2 ? kf0 : kf1);
-          acc[nt][0][x] = s;
-          t[nt][x] = s + static_cast<float>(x < 2 ? ve0 : ve1);
-          grow = grow || (on && t[nt][x] > ref[nt][e] + 15.f);
+        for (int y = 0; y < 4; ++y) {
+          t[nt][y] += static_cast<float>(y < 2 ? ve0 : ve1);
+          grow = grow || t[nt][y] > ref[nt][y & 1] + 15.f;
         }
-        if (L.logits) {
-          float2* d0 = reinterpret_cast<float2*>(L.logits + slot_at(e0.x) * C::kRows + nt * 8 + 2 * cl);
-          float2* d1 = reinterpret_cast<float2*>(L.logits + slot_at(e1.x) * C::kRows + nt * 8 + 2 * cl);
-          if (in0) *d0 = make_float2(kept[nt][0] ? acc[nt][0][0] : -INFINITY, kept[nt][1] ? acc[nt][0][1] : -INFINITY);
-          if (in1) *d1 = make_float2(kept[nt][2] ? acc[nt][0][2] : -INFINITY, kept[nt][3] ? acc[nt][0][3] : -INFINITY);
-        }
-      }
       if (__any_sync(~0u, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(kept[nt][e] ? t[nt][e] : -INFINITY, kept[nt][2 + e] ? t[nt][2 + e] : -INFINITY);
+            float top = fmaxf(t[nt][e], t[nt][2 + e]);
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
             if (top > ref[nt][e] + 15.f) {          // by the row's own weights: rows do not touch each other
-              const float fresh_ref = top - 7.f, f = exp2f(ref[nt][e] - fresh_ref);
-              ref[nt][e] = fresh_ref;
+              const float moved = top - 7.f, f = exp2_fast(ref[nt][e] - moved);
+              ref[nt][e] = moved;
               sum[nt][e] *= f;
 #pragma unroll
               for (int s = 0; s < C::kSteps; ++s) {
@@ -409,54 +447,54 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
             }
           }
       }
-      uint32_t pb[C::kParts][NT][2];
+      uint32_t pb[C::kParts][NT][2];                // [..][keys 0-7 or 8-15]
       const float vf0 = exp2_int(-ve0), vf1 = exp2_int(-ve1);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float p[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          p[x] = kept[nt][x] ? exp2f(t[nt][x] - ref[nt][x & 1]) : 0.f;
-          if (kept[nt][x]) sum[nt][x & 1] += p[x] * (x < 2 ? vf0 : vf1);
+        for (int y = 0; y < 4; ++y) {
+          p[y] = exp2_fast(t[nt][y] - ref[nt][y & 1]);
+          sum[nt][y & 1] = fmaf(p[y], y < 2 ? vf0 : vf1, sum[nt][y & 1]);
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t hp = pack_half2(p[2 * x], p[2 * x + 1]);
-          pb[0][nt][x] = transpose8x8(hp);
-          if (C::kParts == 2) {
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t hp = pack_half2(p[2 * y], p[2 * y + 1]);
+          pb[0][nt][y] = transpose8x8(hp);
+          if constexpr (C::kParts == 2) {
             const float2 f = unpack_half2(hp);
-            pb[C::kParts - 1][nt][x] = transpose8x8(pack_half2(p[2 * x] - f.x, p[2 * x + 1] - f.y));
+            pb[1][nt][y] = transpose8x8(pack_half2(p[2 * y] - f.x, p[2 * y + 1] - f.y));
           }
         }
       }
       // O^T: thread (gl, cl) holds columns gl * D / 8 ... of keys 2 cl, 2 cl + 1, 2 cl + 8, 2 cl + 9
       uint32_t v[4][D / 32];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int r = 2 * cl + (x & 1) + (x >> 1) * 8;
+      for (int y = 0; y < 4; ++y) {
+        const int r = 2 * cl + (y & 1) + (y >> 1) * 8;
         if (D == 128) {
           const uint4 u = *reinterpret_cast<const uint4*>(vs + r * D + (gl ^ (((r >> 1) & 3) * 2)) * 16);
-          v[x][0] = u.x; v[x][1] = u.y; v[x][D / 32 - 2] = u.z; v[x][D / 32 - 1] = u.w;
+          v[y][0] = u.x; v[y][1] = u.y; v[y][D / 32 - 2] = u.z; v[y][D / 32 - 1] = u.w;
         } else {
           const uint2 u = *reinterpret_cast<const uint2*>(vs + r * D + ((gl >> 1) ^ ((r >> 1) & 3)) * 16 + (gl & 1) * 8);
-          v[x][0] = u.x; v[x][1] = u.y;
+          v[y][0] = u.x; v[y][1] = u.y;
         }
       }
-      uint32_t nan_keys = 0;                 // kMulti: bit x: this thread's piece of key x holds a NaN
+      bool some_nan = false;                 // the same in the whole warp
       if (kMulti) {
         // A row that does not keep a key has weight 0 for it, and 0 * NaN would
         // reach that row: NaN codes leave the product and are put in afterwards.
         uint32_t any = 0;
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int y = 0; y < 4; ++y)
 #pragma unroll
-          for (int w = 0; w < D / 32; ++w) any |= __vcmpeq4(v[x][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-        if (__any_sync(~0u, any != 0)) {
-          nan_keys = 1;
+          for (int w = 0; w < D / 32; ++w) any |= __vcmpeq4(v[y][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+        some_nan = __any_sync(~0u, any != 0);
+        if (some_nan) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
+          for (int y = 0; y < 4; ++y)
 #pragma unroll
-            for (int w = 0; w < D / 32; ++w) v[x][w] &= ~__vcmpeq4(v[x][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            for (int w = 0; w < D / 32; ++w) v[y][w] &= ~__vcmpeq4(v[y][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
         }
       }
 #pragma unroll
@@ -473,177 +511,143 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int p = 0; p < C::kParts; ++p)
-              mma16816(o[nt][2 * w + z], a0, a1, a2, a3, pb[p][nt][0], pb[p][nt][1]);
+              mma_f16(o[nt][2 * w + z], a0, a1, a2, a3, pb[p][nt][0], pb[p][nt][1]);
         }
-      if (kMulti && nan_keys) {
-        // o[nt][s][x]: column gl * D / 8 + 2 s + x / 2 of row 2 cl + x % 2
-        for (int r = 0; r < kKeys; ++r) {
-          const int idx = tile * kKeys + r;
-          if (idx >= entries) break;
-          const int2 k = about[idx & (kList - 1)];
+      if (kMulti && some_nan) {
+        // o[nt][s][y]: column gl * D / 8 + 2 s + y / 2 of row 2 cl + y % 2
+        for (int r = 0; r < kKeys && tile * kKeys + r < entries; ++r) {
+          const int mask = list[(tile * kKeys + r) & (kList - 1)].y;
 #pragma unroll
           for (int s = 0; s < C::kSteps; ++s)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int col = gl * (D / 8) + 2 * s + x / 2;
+            for (int y = 0; y < 4; ++y) {
+              const int col = gl * (D / 8) + 2 * s + y / 2;
               const int c = D == 128 ? (col >> 4) ^ (((r >> 1) & 3) * 2) : (col >> 4) ^ ((r >> 1) & 3);
               if ((vs[r * D + c * 16 + (col & 15)] & 127) != 127) continue;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const int i = row_pos[nt][x & 1], g = row_gid[nt][x & 1];
-                if (i != kFar && keeps(i, g, k)) o[nt][s][x] = __int_as_float(0x7fffffff);
-              }
+              for (int nt = 0; nt < NT; ++nt)
+                if (mask & row_bit[nt][y & 1]) o[nt][s][y] = __int_as_float(0x7fffffff);
             }
         }
       }
     };
 
-    // ---- the warp's pages
-    auto fill = [&](int tile) {              // list every slot of tile `tile` that there is
-      while (entries < (tile + 1) * kKeys && !scan.done()) scan_batch();
-    };
-#pragma unroll
-    for (int x = 0; x < kStages - 1; ++x) {
-      fill(x);
-      issue(x);
-    }
-    for (int tile = 0;; ++tile) {
-      fill(tile + kStages - 1);
-      if (tile * kKeys >= entries) break;
-      issue(tile + kStages - 1);
-      cp_async_wait<kStages - 1>();
+    for (int pass = 0; pass < (L.accumulate ? 2 : 1); ++pass) {
+      if (pass == 1) {
+        if (entries > kList) {               // the list's start is gone: scan again
+          entries = 0;
+          j = first;
+          entry = table(first);
+          open_pages();
+        }
+      }
+      // ---- the warp's pages: copies run kStages - 1 tiles ahead of the products
+      for (int tile = 1 - kStages;; ++tile) {
+        while (entries < (tile + kStages) * kKeys && j < pages) scan_page();
+        if (tile >= 0 && tile * kKeys >= entries) break;
+        issue(tile + kStages - 1, pass == 0);
+        if (tile < 0) continue;
+        cp_async_wait<kStages - 1>();
+        __syncwarp();
+        compute(tile, pass == 1);
+        __syncwarp();                        // the stage is free for the next copies
+      }
+      cp_async_wait<0>();
       __syncwarp();
-      compute(tile);
-      __syncwarp();                          // the stage is free for the next copies
-    }
-    cp_async_wait<0>();
-    __syncwarp();
+      if (pass == 1) break;
 
-    // ---- join the block's warps
-    float* part = reinterpret_cast<float*>(ring);          // [rows][D]
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float l = sum[nt][e];
-        l += __shfl_xor_sync(~0u, l, 4);
-        l += __shfl_xor_sync(~0u, l, 8);
-        l += __shfl_xor_sync(~0u, l, 16);
-        const int r = nt * 8 + 2 * cl + e;
-        if (gl == 0) {
-          s_m[warp][r] = ref[nt][e];
-          s_l[warp][r] = l;
-        }
-#pragma unroll
-        for (int s = 0; s < C::kSteps; ++s)
-          *reinterpret_cast<float2*>(part + r * D + gl * (D / 8) + 2 * s) = make_float2(o[nt][s][e], o[nt][s][2 + e]);
-      }
-    }
-    __syncthreads();
-    // A warp without kept slots has sum 0 and is left out (its reference is -inf);
-    // a NaN sum is not 0 and carries on.
-    float4 mine[NT * D / 128 > 0 ? NT * D / 128 : 1];
-    constexpr int kItems = C::kRows * D / 4;               // float4 pieces of the row block
-#pragma unroll
-    for (int x = 0; x < (kItems + kThreads - 1) / kThreads; ++x) {
-      const int i = threadIdx.x + x * kThreads;
-      if (i >= kItems) break;
-      const int r = i / (D / 4), c = i % (D / 4) * 4;
-      float M = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (s_l[w][r] == 0.f) continue;
-        const float f = exp2f(s_m[w][r] - M);
-        const float4 u = *reinterpret_cast<const float4*>(smem + w * C::kWarpBytes + (r * D + c) * 4);
-        l += s_l[w][r] * f;
-        a.x += u.x * f; a.y += u.y * f; a.z += u.z * f; a.w += u.w * f;
-      }
-      mine[x] = a;
-      if (c == 0) {
-        s_M[r] = M;
-        s_L[r] = l;
-      }
-    }
-    __syncthreads();
-    float* whole = reinterpret_cast<float*>(smem);         // the block's partial, in warp 0's ring
-#pragma unroll
-    for (int x = 0; x < (kItems + kThreads - 1) / kThreads; ++x) {
-      const int i = threadIdx.x + x * kThreads;
-      if (i < kItems) *reinterpret_cast<float4*>(whole + 4 * i) = mine[x];
-    }
-
-    // ---- join the cluster's blocks; each writes its share of the rows
-    cg::cluster_group cluster = cg::this_cluster();
-    if (cs > 1) cluster.sync(); else __syncthreads();
-    if (threadIdx.x < C::kRows) {
-      const int r = threadIdx.x;
-      float M = -INFINITY, l = 0.f;
-      for (int x = 0; x < cs; ++x) M = fmaxf(M, cs > 1 ? *cluster.map_shared_rank(&s_M[r], x) : s_M[r]);
-      for (int x = 0; x < cs; ++x) {
-        const float m = cs > 1 ? *cluster.map_shared_rank(&s_M[r], x) : s_M[r];
-        const float y = cs > 1 ? *cluster.map_shared_rank(&s_L[r], x) : s_L[r];
-        if (y != 0.f) l += y * exp2f(m - M);
-      }
-      s_lse[r] = l != 0.f ? M + log2f(l) : -INFINITY;
-      if (rank == 0 && L.lse && r0 + r < rows) {
-        const int g = (r0 + r) % G, t = (r0 + r) / G;
-        L.lse[(static_cast<size_t>(b) * L.H + h * G + g) * L.n + t] = s_lse[r] * 0.6931471805599453f;
-      }
-    }
-    __syncthreads();
-    const int share = (kItems + cs - 1) / cs;
-    for (int i = rank * share + threadIdx.x; i < min(kItems, (rank + 1) * share); i += kThreads) {
-      const int r = i / (D / 4), c = i % (D / 4) * 4;
-      if (r0 + r >= rows) break;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x = 0; x < cs; ++x) {
-        const float m = cs > 1 ? *cluster.map_shared_rank(&s_M[r], x) : s_M[r];
-        const float y = cs > 1 ? *cluster.map_shared_rank(&s_L[r], x) : s_L[r];
-        if (y == 0.f) continue;
-        const float4 u = *reinterpret_cast<const float4*>((cs > 1 ? cluster.map_shared_rank(whole, x) : whole) + 4 * i);
-        const float f = exp2f(m - s_lse[r]);
-        a.x += u.x * f; a.y += u.y * f; a.z += u.z * f; a.w += u.w * f;
-      }
-      const int g = (r0 + r) % G, t = (r0 + r) / G;
-      store4(static_cast<T*>(L.O) + ((static_cast<size_t>(b) * L.H + h * G + g) * L.n + t) * D + c, a);
-    }
-
-    // ---- weights of the kept slots
-    if (L.logits) {
-      auto add = [&](int idx) {
-        const size_t at = slot_at(list[idx & (kList - 1)].x);
-        const float4* s = reinterpret_cast<const float4*>(L.logits + at * C::kRows);
-        float w = 0.f;
-#pragma unroll
-        for (int x = 0; x < C::kRows / 4; ++x) {
-          const float4 u = s[x];
-          const float f[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (f[e] != -INFINITY) w += exp2f(f[e] - s_lse[4 * x + e]);
-        }
-        L.c.mass[at] += w;
-      };
-      if (entries <= kList) {                // the whole list is still there
-        for (int i = lane; i < entries; i += 32) add(i);
-      } else {
-        int done = 0;
-        entries = 0;
-        scan.k = 0;
-        scan.fetch(L, b, h, lane);
-        while (done < entries || !scan.done()) {
-          if (!scan.done()) scan_batch();
-          for (int i = done + lane; i < entries; i += 32) add(i);
-          done = entries;
-          __syncwarp();
+      // ---- join the block's warps.  A piece j of a row holds columns 2 s, 2 s + 1 of the
+      // D / 8 columns of two neighbouring gl: s = j / 4, gl = 2 (j % 4) and the next.
+  #pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+  #pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float l = sum[nt][e];
+          l += __shfl_xor_sync(~0u, l, 4);
+          l += __shfl_xor_sync(~0u, l, 8);
+          l += __shfl_xor_sync(~0u, l, 16);
+          const int r = nt * 8 + 2 * cl + e;
+          if (gl == 0) {
+            s_m[warp][r] = ref[nt][e];
+            s_l[warp][r] = l;
+          }
+  #pragma unroll
+          for (int s = 0; s < C::kSteps; ++s)
+            *reinterpret_cast<float2*>(ring + r * C::kPitch + s * 64 + gl * 8) = make_float2(o[nt][s][e], o[nt][s][2 + e]);
         }
       }
+      if (r0 == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      __syncthreads();
+      // Pieces of one share go to one block's inbox, which that block joins and writes:
+      // stores into another block's memory are not waited for, loads from it would be.
+      // A warp without kept slots has sum 0 and is left out;
+      // a NaN sum is not 0 and carries on.
+      const int share = (C::kItems + cs - 1) / cs;
+  #pragma unroll
+      for (int y = 0; y < (C::kItems + kThreads - 1) / kThreads; ++y) {
+        const int i = threadIdx.x + y * kThreads;
+        if (i >= C::kItems) break;
+        const int r = i / (D / 4), j = i % (D / 4);
+        float M = -INFINITY, l = 0.f;
+  #pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  #pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 u = *reinterpret_cast<const float4*>(smem + w * C::kWarpBytes + r * C::kPitch + j * 16);
+          if (s_l[w][r] == 0.f) continue;
+          const float f = exp2f(s_m[w][r] - M);
+          l += s_l[w][r] * f;
+          a.x += u.x * f; a.y += u.y * f; a.z += u.z * f; a.w += u.w * f;
+        }
+        const int to = i / share;
+        float4* box = reinterpret_cast<float4*>(inbox + buf * C::kInbox) + rank * share + (i - to * share);
+        *cluster.map_shared_rank(box, to) = a;
+        if (j < cs) *cluster.map_shared_rank(&s_all[buf][rank][r], j) = make_float2(M, l);
+      }
+
+      // ---- join the cluster's blocks
+      cluster.sync();
+      if (threadIdx.x < kMaxCluster * C::kRows) {           // 16 lanes a row, one a block
+        const int from = threadIdx.x % kMaxCluster, r = threadIdx.x / kMaxCluster;
+        const float2 v = from < cs ? s_all[buf][from][r] : make_float2(-INFINITY, 0.f);
+        float M = v.x;
+  #pragma unroll
+        for (int y = 8; y > 0; y /= 2) M = fmaxf(M, __shfl_xor_sync(~0u, M, y));
+        const float f = v.y != 0.f ? exp2f(v.x - M) : 0.f;
+        float l = v.y != 0.f ? v.y * f : 0.f;
+  #pragma unroll
+        for (int y = 8; y > 0; y /= 2) l += __shfl_xor_sync(~0u, l, y);
+        s_factor[from][r] = v.y != 0.f ? f / l : 0.f;
+        if (from == 0) {
+          const float lse = l != 0.f ? M + log2f(l) : -INFINITY;
+          s_lse[r] = l != 0.f ? lse : -kNoRef;
+          if (rank == 0 && L.lse && r0 + r < rows)
+            L.lse[(static_cast<size_t>(b) * L.H + h * G + (r0 + r) % G) * L.n + (r0 + r) / G] = lse * 0.6931471805599453f;
+        }
+      }
+      __syncthreads();
+      for (int i = rank * share + threadIdx.x; i < min(C::kItems, (rank + 1) * share); i += kThreads) {
+        const int r = i / (D / 4), j = i % (D / 4);
+        if (r0 + r >= rows) break;
+        const float4* box = reinterpret_cast<const float4*>(inbox + buf * C::kInbox) + (i - rank * share);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  #pragma unroll 4
+        for (int from = 0; from < cs; ++from) {
+          const float4 u = box[from * share];
+          const float f = s_factor[from][r];
+          if (f == 0.f) continue;                           // nothing kept there
+          a.x += u.x * f; a.y += u.y * f; a.z += u.z * f; a.w += u.w * f;
+        }
+        T* out = static_cast<T*>(L.O) + ((static_cast<size_t>(b) * L.H + h * G + (r0 + r) % G) * L.n + (r0 + r) / G) * D +
+                 j % 4 * (D / 4) + j / 4 * 2;
+        store2(out, a.x, a.y);
+        store2(out + D / 8, a.z, a.w);
+      }
     }
-    if (cs > 1) cluster.sync(); else __syncthreads();      // shared memory is read by others until here
+    __syncthreads();                         // shared memory is free for the next row block
   }
+  if (rows == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 template <typename T, int D, int NT, bool kMulti>
@@ -651,7 +655,7 @@ cudaError_t launch(const CacheAttnLaunch& L, int cs, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(cs, L.H_kv, L.B);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg<T, D, NT, kMulti>::kSmem;
+  cfg.dynamicSmemBytes = Cfg<T, D, NT>::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -664,7 +668,7 @@ cudaError_t launch(const CacheAttnLaunch& L, int cs, cudaStream_t st) {
 
 template <typename T, int D>
 cudaError_t launch_rows(const CacheAttnLaunch& L, int cs, cudaStream_t st) {
-  const bool wide = cache_logit_rows(L.H / L.H_kv, L.n) == 16;
+  const bool wide = L.H / L.H_kv * L.n > 8;
   if (L.n == 1) return wide ? launch<T, D, 2, false>(L, cs, st) : launch<T, D, 1, false>(L, cs, st);
   return wide ? launch<T, D, 2, true>(L, cs, st) : launch<T, D, 1, true>(L, cs, st);
 }
@@ -672,7 +676,7 @@ cudaError_t launch_rows(const CacheAttnLaunch& L, int cs, cudaStream_t st) {
 template <typename T, int D, int NT, bool kMulti>
 cudaError_t prepare() {
   cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<T, D, NT, kMulti>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Cfg<T, D, NT, kMulti>::kSmem);
+                                       Cfg<T, D, NT>::kSmem);
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(cache_attn_kernel<T, D, NT, kMulti>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
@@ -695,10 +699,18 @@ cudaError_t setup_cache_kernels() {
 }
 
 cudaError_t launch_cache_attn(const CacheAttnLaunch& L, int dtype, cudaStream_t st) {
-  // Blocks per (sequence, head): enough that every SM has two, as long as each
-  // warp gets a page.
+  // Blocks per (sequence, head): one wave of the blocks that fit (two an SM with
+  // eight rows, one with sixteen), as long as each warp gets a page; a second wave
+  // where a warp still scans 16 pages, since sequences differ in what they keep
+  // (16 sequences of up to 32K tokens: 78 us with 2 blocks, 59 with 4, 72 with 8;
+  // 8 sequences of 1K tokens, 12 heads: 8.2 us with 2 blocks, 13.1 with 4).
+  const int fit = L.num_sms * (L.H / L.H_kv * L.n > 8 ? 1 : 2);
   int cs = 1;
-  while (cs < 16 && cs * L.B * L.H_kv < 2 * L.num_sms && cs * kWarps < L.c.max_pages) cs *= 2;
+  while (cs < kMaxCluster && cs * kWarps < L.c.max_pages) {
+    const int blocks = 2 * cs * L.B * L.H_kv;
+    if (blocks > fit && (blocks > 2 * fit || L.c.max_pages < 2 * cs * kWarps * 16)) break;
+    cs *= 2;
+  }
   if (dtype == FOCUS_BF16) return L.d == 128 ? launch_rows<__nv_bfloat16, 128>(L, cs, st) : launch_rows<__nv_bfloat16, 64>(L, cs, st);
   return L.d == 128 ? launch_rows<float, 128>(L, cs, st) : launch_rows<float, 64>(L, cs, st);
 }

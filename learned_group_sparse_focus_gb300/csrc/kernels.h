@@ -262,16 +262,13 @@ struct CacheAttnLaunch {
   focus_cache_t c;
   void* O;
   float* lse;             // or null
-  float* logits;          // accumulate: scratch, else null
+  int accumulate;         // add the slots' weights to c.mass
   int B, H, H_kv, n, d, A, w;
   float scale_log2;       // scale * log2(e)
   int* err;
   int num_sms;
 };
 cudaError_t setup_cache_kernels();
-// Query rows (tokens x query heads of a key/value head) whose logits one pass
-// keeps per slot when it accumulates weights.
-inline int cache_logit_rows(int group, int n) { return group * n > 8 ? 16 : 8; }
 cudaError_t launch_cache_attn(const CacheAttnLaunch& L, int dtype, cudaStream_t st);
 
 }  // namespace focus

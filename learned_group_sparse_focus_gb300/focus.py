@@ -446,8 +446,8 @@ def focus_cache_workspace_bytes(p: Params, cache: Cache) -> int:
 
 
 def alloc_workspace_cache(p: Params, cache: Cache, stream=None) -> torch.Tensor:
-    """Caller-owned workspace for the cache calls on this cache (p.n: the most
-    new tokens of one call), error word cleared."""
+    """Caller-owned workspace for the cache calls on this cache, error word
+    cleared."""
     nbytes = focus_cache_workspace_bytes(p, cache)
     if nbytes == 0:
         raise FocusError("focus_cache_workspace_bytes", 1)

@@ -169,11 +169,15 @@ def test_unsupported_and_small_workspace(fz):
     assert _calls(fz, p, _struct(fz)) == (2, 2, 2)
     p = _params(fz)
     need = fz.lib().focus_cache_workspace_bytes(ctypes.byref(p), ctypes.byref(_struct(fz)))
-    # error block + a logit per pool slot and 8 query rows (more than the kept-slot lists)
-    assert need == 256 + 4 * 2 * 64 * 8 * 4
+    # error block + per (sequence, head) a count and the kept slots of two pages
+    assert need == 256 + -(-2 * 2 * (2 * 64 + 1) * 4 // 256) * 256
     assert _calls(fz, p, _struct(fz), nbytes=need - 256) == (3, 3, 3)
     assert fz.lib().focus_cache_workspace_bytes(ctypes.byref(p), ctypes.byref(_struct(fz, mass=None))) == 256
     lib, c = fz.lib(), _struct(fz)
+    big = _struct(fz, n_pages=1 << 23)                   # 2^23 pages x 2 heads x 64 slots x 64 bytes: 2^36
+    assert _calls(fz, p, big, nbytes=0) == (3, 3, 3)
+    big.n_pages += 1
+    assert _calls(fz, p, big) == (2, 2, 2)
     q = _params(fz, n=65)
     assert lib.focus_cache_attention_fwd(ctypes.byref(q), 16, 16, None, ctypes.byref(c), 16, None, 0, 256, 1 << 40,
                                          None) == 2

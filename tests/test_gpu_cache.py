@@ -364,7 +364,7 @@ def test_nan_and_infinite_queries_stay_in_their_rows(fz):
     same = np.ones((4, 2), bool)
     same[1, 0] = same[2, 1] = False
     assert np.array_equal(outs[0][0][same], outs[1][0][same])
-    assert np.isnan(outs[1][0, 1, 0]).all()
+    assert np.isnan(outs[1][0, 1, 0]).all() and np.isnan(outs[1][0, 2, 1]).all()
 
 
 def test_nan_key_reaches_only_the_rows_that_keep_it(fz):
