@@ -114,7 +114,7 @@ focus_status_t ensure_setup() {
     if (setup_attn_kernels() != cudaSuccess) return FOCUS_ERR_CUDA;
     if (setup_bwd_tc_kernels() != cudaSuccess) return FOCUS_ERR_CUDA;
     if (setup_sinkhorn_kernels() != cudaSuccess) return FOCUS_ERR_CUDA;
-    if (setup_cache_kernels() != cudaSuccess) return FOCUS_ERR_CUDA;
+    if (setup_cache_evict() != cudaSuccess || setup_cache_attn() != cudaSuccess) return FOCUS_ERR_CUDA;
     g_ready[dev] = true;
   }
   return FOCUS_OK;
@@ -1168,7 +1168,8 @@ focus_status_t focus_cache_evict(const focus_params_t* p, int32_t budget, int32_
   if (budget < 1 || recent < 0 || recent > budget) return FOCUS_ERR_INVALID_ARG;
   if (static_cast<long long>(dst->max_pages) * kPage < budget) return FOCUS_ERR_INVALID_ARG;
   if (focus_status_t s = ensure_setup()) return s;
-  CacheEvictLaunch L{*src, *dst, p->B, p->H_kv, p->d, budget, recent, at<int32_t>(ws, kAlign), at<int>(ws, 0)};
+  CacheEvictLaunch L{*src, *dst, p->B, p->H_kv, p->d, budget, recent, at<int32_t>(ws, kAlign), at<int>(ws, 0),
+                     sm_count()};
   return cuda_status(launch_cache_evict(L, static_cast<cudaStream_t>(stream)));
 }
 

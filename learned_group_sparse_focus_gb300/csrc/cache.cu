@@ -8,7 +8,11 @@
 // The page scale is a power of two.  e4m3 keeps a relative step of 2^-3 over
 // its whole normal range, so a finer scale gains no accuracy there, and with a
 // power of two every scaling is exact: x * 2^-e is rounded once, to e4m3.
+#include <cooperative_groups.h>
+
 #include "cache.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace focus {
 namespace {
@@ -18,32 +22,51 @@ constexpr int kHalf = kThreads / 2;    // the first half moves K, the second V
 
 // ----------------------------------------------------------------- append ---
 
-// Eight consecutive elements of a row as floats.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* f) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[2 * e] = __uint_as_float(w[e] << 16);
-    f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+// Eight consecutive elements of a row as they are stored, and what the append
+// asks of them.
+template <typename T>
+struct Piece;
+template <>
+struct Piece<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ float at(int e) const {
+    const uint32_t w = (&u.x)[e / 2];
+    return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
   }
-}
-__device__ __forceinline__ void load8(const float* p, float* f) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
+  // Largest magnitude, as the bits of a float; infinities and NaN included.
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = 0x7fff7fffu;
+    const uint32_t a = __vmaxu2(__vmaxu2(u.x & m, u.y & m), __vmaxu2(u.z & m, u.w & m));
+    return max(a & 0xffff0000u, a << 16);
+  }
+};
+template <>
+struct Piece<float> {
+  uint4 u[2];
+  __device__ __forceinline__ void load(const float* p) {
+    u[0] = reinterpret_cast<const uint4*>(p)[0];
+    u[1] = reinterpret_cast<const uint4*>(p)[1];
+  }
+  __device__ __forceinline__ float at(int e) const { return __uint_as_float((&u[e / 4].x)[e % 4]); }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t a = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a = max(a, (&u[e / 4].x)[e % 4] & 0x7fffffffu);
+    return a;
+  }
+};
 
-// Whether m more tokens fit every head of sequence b (same answer in all
-// threads of the block; contains a block barrier).
+// Whether m more tokens fit every head of sequence b (same answer in all lanes
+// of a warp).
 __device__ __forceinline__ bool sequence_fits(const CacheAppendLaunch& L, int b, int m) {
-  const int cap = L.c.max_pages * kPage;
-  bool ok = L.c.next[b] >= 0 && L.c.next[b] <= 0x7fffffff - m;
-  for (int h = threadIdx.x; h < L.H_kv; h += kThreads) {
+  const int cap = L.c.max_pages * kPage, next = L.c.next[b];
+  bool ok = next >= 0 && next <= 0x7fffffff - m;
+  for (int h = threadIdx.x % 32; h < L.H_kv; h += 32) {
     const int n = L.c.len[b * L.H_kv + h];
     ok = ok && n >= 0 && n <= cap - m;
   }
-  return __syncthreads_and(ok);
+  return __all_sync(~0u, ok);
 }
 
 // One block per touched page and head: the new rows of the page stay in
@@ -51,108 +74,110 @@ __device__ __forceinline__ bool sequence_fits(const CacheAppendLaunch& L, int b,
 // they are read once.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheAppendLaunch L) {
-  constexpr int kPerRow = D / 8;                       // 8-element pieces of a row
+  constexpr int kPerRow = D / 8;                       // pieces of a row
   constexpr int kPieces = kPage * kPerRow / kHalf;     // pieces a thread holds
   __shared__ uint32_t s_max[kThreads / 32];
   __shared__ int s_last;
   const int b = blockIdx.z, h = blockIdx.y;
   const int half = threadIdx.x / kHalf, ht = threadIdx.x % kHalf;
+  const int n0 = L.c.len[b * L.H_kv + h];
   const int m = cache_new(L.n_new, L.n, b, L.err);
   const bool fits = sequence_fits(L, b, m);
-  const int n0 = L.c.len[b * L.H_kv + h];
   if (!fits && threadIdx.x == 0) atomicOr(L.err, kErrBadCache);
   const int j = n0 / kPage + blockIdx.x;
   const int lo = max(n0, j * kPage), hi = min(n0 + m, (j + 1) * kPage);
-  const int page = fits && lo < hi ? cache_page(L.c, b, j, L.err) : -1;
-  if (page >= 0) {
+  if (fits && lo < hi) {
     const int r0 = lo - j * kPage, rows = hi - lo, t0 = lo - n0;
-    const size_t plane = static_cast<size_t>(page) * L.H_kv + h;
     const T* src = static_cast<const T*>(half ? L.V : L.K) +
                    ((static_cast<size_t>(b) * L.H_kv + h) * L.n + t0) * D;
-    uint8_t* dst = (half ? L.c.v : L.c.k) + plane * kPage * D;
+    Piece<T> x[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (ht + i * kHalf < rows * kPerRow) x[i].load(src + static_cast<size_t>(ht + i * kHalf) * 8);
+    const int page = cache_page(L.c, b, j, L.err);
+    const size_t plane = static_cast<size_t>(max(page, 0)) * L.H_kv + h;
     float* scale = (half ? L.c.v_scale : L.c.k_scale) + plane;
-    float x[kPieces][8];
+    const int e_old = r0 > 0 && page >= 0 ? scale_exp(*scale) : kMinExp;
     uint32_t a = 0;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int at = ht + i * kHalf;
-      if (at >= rows * kPerRow) continue;
-      load8(src + static_cast<size_t>(at) * 8, x[i]);
-    }
+    for (int i = 0; i < kPieces; ++i)
+      if (ht + i * kHalf < rows * kPerRow) {
+        uint32_t top = x[i].top();
+        if (top >= 0x7f800000u) {                      // infinities and NaN do not count
+          top = 0;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      if (ht + i * kHalf >= rows * kPerRow) continue;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t u = __float_as_uint(x[i][e]) & 0x7fffffffu;
-        if (u < 0x7f800000u) a = max(a, u);
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t u = __float_as_uint(x[i].at(e)) & 0x7fffffffu;
+            if (u < 0x7f800000u) top = max(top, u);
+          }
+        }
+        a = max(a, top);
       }
-    }
-    const int e_old = r0 > 0 ? scale_exp(*scale) : kMinExp;
     a = __reduce_max_sync(~0u, a);
     if ((threadIdx.x & 31) == 0) s_max[threadIdx.x / 32] = a;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kHalf / 32; ++i) a = max(a, s_max[half * (kHalf / 32) + i]);
-    const int e = max(need_exp(a), e_old);
-    if (ht == 0) *scale = exp2_int(e);
-    if (e > e_old) {                                   // the page's older rows, at the new scale
-      const float f = exp2_int(max(e_old - e, -126));  // codes times 2^-126 are 0 like any smaller factor
-      uint4* old = reinterpret_cast<uint4*>(dst);
-      for (int at = ht; at < r0 * D / 16; at += kHalf) old[at] = rescale16(old[at], f);
-    }
-    const float f = exp2_int(-e);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int at = ht + i * kHalf;
-      if (at >= rows * kPerRow) continue;
-      uint32_t w[2];
-#pragma unroll
-      for (int e2 = 0; e2 < 2; ++e2) {
-        const float* y = x[i] + 4 * e2;
-        w[e2] = static_cast<uint32_t>(float2_to_e4m3x2(y[0] * f, y[1] * f)) |
-                (static_cast<uint32_t>(float2_to_e4m3x2(y[2] * f, y[3] * f)) << 16);
+    if (page >= 0) {
+      uint8_t* dst = (half ? L.c.v : L.c.k) + plane * kPage * D;
+      const int e = max(need_exp(a), e_old);
+      if (ht == 0) *scale = exp2_int(e);
+      if (e > e_old) {                                   // the page's older rows, at the new scale
+        const float f = exp2_int(max(e_old - e, -126));  // codes times 2^-126 are 0 like any smaller factor
+        uint4* old = reinterpret_cast<uint4*>(dst);
+        for (int at = ht; at < r0 * D / 16; at += kHalf) old[at] = rescale16(old[at], f);
       }
-      *reinterpret_cast<uint2*>(dst + static_cast<size_t>(r0) * D + static_cast<size_t>(at) * 8) =
-          make_uint2(w[0], w[1]);
-    }
-    if (ht < rows) {
-      const size_t at = plane * kPage + r0 + ht;
-      if (half == 0) {
-        int g = L.gid[(static_cast<size_t>(b) * L.A + (L.A == 1 ? 0 : h)) * L.n + t0 + ht];
-        if (g < 0 || g >= L.K_groups) {
-          atomicOr(L.err, kErrBadGroup);
-          g = g < 0 ? 0 : L.K_groups - 1;
+      const float f = exp2_int(-e);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int at = ht + i * kHalf;
+        if (at >= rows * kPerRow) continue;
+        uint32_t w[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          w[y] = static_cast<uint32_t>(float2_to_e4m3x2(x[i].at(4 * y) * f, x[i].at(4 * y + 1) * f)) |
+                 (static_cast<uint32_t>(float2_to_e4m3x2(x[i].at(4 * y + 2) * f, x[i].at(4 * y + 3) * f)) << 16);
+        *reinterpret_cast<uint2*>(dst + static_cast<size_t>(r0) * D + static_cast<size_t>(at) * 8) =
+            make_uint2(w[0], w[1]);
+      }
+      if (ht < rows) {
+        const size_t at = plane * kPage + r0 + ht;
+        if (half == 0) {
+          int g = L.gid[(static_cast<size_t>(b) * L.A + (L.A == 1 ? 0 : h)) * L.n + t0 + ht];
+          if (g < 0 || g >= L.K_groups) {
+            atomicOr(L.err, kErrBadGroup);
+            g = g < 0 ? 0 : L.K_groups - 1;
+          }
+          L.c.pos[at] = L.c.next[b] + t0 + ht;
+          L.c.gid[at] = static_cast<int16_t>(g);
+        } else if (L.c.mass) {
+          L.c.mass[at] = 0.f;
         }
-        L.c.pos[at] = L.c.next[b] + t0 + ht;
-        L.c.gid[at] = static_cast<int16_t>(g);
-      } else if (L.c.mass) {
-        L.c.mass[at] = 0.f;
       }
     }
   }
-  // The last block to finish writes the new counts: by then every block has
-  // read the old ones, so they may be updated in place.
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const int total = gridDim.x * gridDim.y * gridDim.z;
-    __threadfence();
-    s_last = atomicAdd(L.ticket, 1) == total - 1;
+  // Counts that go to other arrays are written at once.  Counts updated in place
+  // are written by the last block to finish: every block has used the old ones by
+  // then (a value that has come back cannot change, so the ticket needs no fence).
+  const int add = fits ? m : 0;
+  if (L.len_out != L.c.len && L.next_out != L.c.next) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      L.len_out[b * L.H_kv + h] = n0 + add;
+      if (h == 0) L.next_out[b] = L.c.next[b] + add;
+    }
+    return;
   }
+  __syncthreads();
+  if (threadIdx.x == 0)
+    s_last = atomicAdd(L.ticket, 1) == static_cast<int>(gridDim.x * gridDim.y * gridDim.z) - 1;
   __syncthreads();
   if (!s_last) return;
-  const int cap = L.c.max_pages * kPage;
   for (int s = threadIdx.x / 32; s < L.B; s += kThreads / 32) {   // a warp a sequence
     const int lane = threadIdx.x % 32;
-    const int more = cache_new(L.n_new, L.n, s, L.err), next = L.c.next[s];
-    bool ok = next >= 0 && next <= 0x7fffffff - more;
-    for (int i = lane; i < L.H_kv; i += 32) {
-      const int n = L.c.len[s * L.H_kv + i];
-      ok = ok && n >= 0 && n <= cap - more;
-    }
-    const int add = __all_sync(~0u, ok) ? more : 0;
-    for (int i = lane; i < L.H_kv; i += 32) L.len_out[s * L.H_kv + i] = L.c.len[s * L.H_kv + i] + add;
-    if (lane == 0) L.next_out[s] = next + add;
+    const int more = cache_new(L.n_new, L.n, s, L.err);
+    const int grown = sequence_fits(L, s, more) ? more : 0;
+    for (int i = lane; i < L.H_kv; i += 32) L.len_out[s * L.H_kv + i] = L.c.len[s * L.H_kv + i] + grown;
+    if (lane == 0) L.next_out[s] = L.c.next[s] + grown;
   }
   if (threadIdx.x == 0) *L.ticket = 0;
 }
@@ -170,81 +195,132 @@ __device__ __forceinline__ uint32_t keep_key(float mass, bool late) {
 }
 
 constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelCluster = 16;            // blocks of a cluster, at most
+constexpr int kSelKeys = 24576;            // keys that a block holds in shared memory
+constexpr int kSelSmem = kSelKeys * 4 + kSelWarps * 256 * 4;
 
-__device__ __forceinline__ uint32_t slot_key(const CacheEvictLaunch& L, int b, int h, int s, int first_late) {
-  const int page = cache_page(L.src, b, s / kPage, L.err);
-  if (page < 0) return 0;
-  const size_t at = (static_cast<size_t>(page) * L.H_kv + h) * kPage + s % kPage;
-  return keep_key(L.src.mass[at], L.src.pos[at] >= first_late);
-}
-
-// One block per (sequence, head): the budget-th largest key by four passes of
-// 8-bit counting, then the kept slots in order (ties: the lowest slots).
+// Which slots stay.  A cluster per (sequence, head), each block over a run of its
+// slots: the budget-th largest key by four passes of 8-bit counting, then the kept
+// slots in order (ties: the lowest slots).  Slots are in ascending position, so
+// the protected ones are among the last `recent`; only those positions are read.
+// A block's keys stay in shared memory between the passes (longer runs are formed
+// again in each), every warp counts into bins of its own, since most keys share a
+// few exponents, and the blocks exchange their counts through the cluster's
+// distributed shared memory.
 __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvictLaunch L) {
-  __shared__ int hist[256];
-  __shared__ int s_warp[2][kSelThreads / 32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_left;
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  extern __shared__ __align__(16) uint32_t s_keys[];
+  uint32_t (*s_hist)[256] = reinterpret_cast<uint32_t (*)[256]>(s_keys + kSelKeys);
+  __shared__ uint32_t s_all[2][kSelCluster][256];      // the blocks' counts of a pass
+  __shared__ uint2 s_counts[kSelCluster];              // the blocks' slots above and at the threshold
+  __shared__ uint32_t s_sum[8], s_digit, s_left;
+  __shared__ uint2 s_warp[kSelWarps];
+  cg::cluster_group cluster = cg::this_cluster();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int cs = gridDim.x, rank = blockIdx.x;
   const int n = cache_len(L.src, L.H_kv, b, h, L.err);
-  const int next = L.src.next[b];
-  int32_t* keep = L.keep + (static_cast<size_t>(b) * L.H_kv + h) * (static_cast<size_t>(L.src.max_pages) * kPage + 1);
+  const int next = L.src.next[b], first_late = next - L.recent;
   const int kept = min(n, L.budget);
-  const int first_late = next - L.recent;
+  int32_t* keep = L.keep + (static_cast<size_t>(b) * L.H_kv + h) * (static_cast<size_t>(L.src.max_pages) * kPage + 1);
+  // whole pages per block
+  const int run = ((n + kPage - 1) / kPage + cs - 1) / cs * kPage;
+  const int s0 = min(n, rank * run), s1 = min(n, s0 + run);
+  const bool held = run <= kSelKeys;
+  auto form_key = [&](int s) {
+    const int page = cache_page(L.src, b, s / kPage, L.err);
+    if (page < 0) return 0u;
+    const size_t at = (static_cast<size_t>(page) * L.H_kv + h) * kPage + s % kPage;
+    const bool late = s >= n - L.recent && L.src.pos[at] >= first_late;
+    return keep_key(L.src.mass[at], late);
+  };
+  auto key_of = [&](int s) { return held ? s_keys[s - s0] : form_key(s); };
   uint32_t thr = 0;
-  int ties = 0;                       // slots equal to the threshold that stay
+  uint32_t ties = 0;                  // slots equal to the threshold that stay
   if (n > L.budget) {
-    if (tid == 0) { s_prefix = 0; s_left = L.budget; }
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+    if (held) {
+#pragma unroll 4
+      for (int s = s0 + tid; s < s1; s += kSelThreads) s_keys[s - s0] = form_key(s);
+    }
+    uint32_t left = L.budget;
+    for (int pass = 0, shift = 24; shift >= 0; ++pass, shift -= 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s_hist[warp][lane + 32 * i] = 0;
       __syncthreads();
-      const uint32_t prefix = s_prefix;
-      for (int s = tid; s < n; s += kSelThreads) {
-        const uint32_t k = slot_key(L, b, h, s, first_late);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-          atomicAdd(&hist[(k >> shift) & 255], 1);
+      for (int s = s0 + tid; s < s1; s += kSelThreads) {
+        const uint32_t k = key_of(s);
+        if (pass == 0 || (k >> (shift + 8)) == (thr >> (shift + 8))) atomicAdd(&s_hist[warp][(k >> shift) & 255], 1u);
+      }
+      if (pass == 0) asm volatile("barrier.cluster.wait;" ::: "memory");
+      __syncthreads();
+      uint32_t mine = 0;
+      if (tid < 256) {
+#pragma unroll
+        for (int w = 0; w < kSelWarps; ++w) mine += s_hist[w][tid];
+        for (int x = 0; x < cs; ++x) *cluster.map_shared_rank(&s_all[pass & 1][rank][tid], x) = mine;
+      }
+      cluster.sync();
+      // digit d = 255 - tid: the count of slots with a larger digit decides
+      uint32_t here = 0, above = 0;
+      if (tid < 256) {
+        for (int x = 0; x < cs; ++x) here += s_all[pass & 1][x][255 - tid];
+        above = here;
+#pragma unroll
+        for (int y = 1; y < 32; y *= 2) {
+          const uint32_t v = __shfl_up_sync(~0u, above, y);
+          if (lane >= y) above += v;
+        }
+        if (lane == 31) s_sum[warp] = above;
       }
       __syncthreads();
-      if (tid == 0) {
-        int left = s_left, d = 255;
-        while (d > 0 && hist[d] < left) left -= hist[d--];
-        s_left = left;
-        s_prefix = prefix | (static_cast<uint32_t>(d) << shift);
+      if (tid < 256) {
+        for (int w = 0; w < warp; ++w) above += s_sum[w];
+        if (above >= left && above - here < left) {    // one thread: counts up to this digit reach `left`
+          s_digit = 255 - tid;
+          s_left = left - (above - here);
+        }
       }
       __syncthreads();
+      thr |= s_digit << shift;
+      left = s_left;
     }
-    thr = s_prefix;
-    ties = s_left;
+    ties = left;
+  } else {
+    asm volatile("barrier.cluster.wait;" ::: "memory");
   }
-  int base = 0, seen = 0;             // kept and tied slots before this round
-  for (int s0 = 0; s0 < n; s0 += kSelThreads) {
-    const int s = s0 + tid;
-    const uint32_t k = s < n ? (n > L.budget ? slot_key(L, b, h, s, first_late) : 1u) : 0u;
-    const bool tie = s < n && n > L.budget && k == thr;
-    const uint32_t lanes_before = (1u << (tid & 31)) - 1;
-    const uint32_t tb = __ballot_sync(~0u, tie);
-    if ((tid & 31) == 0) s_warp[0][tid / 32] = __popc(tb);
-    __syncthreads();
-    int tie_rank = seen + __popc(tb & lanes_before), tie_sum = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w < tid / 32) tie_rank += s_warp[0][w];
-      tie_sum += s_warp[0][w];
-    }
-    const bool stay = s < n && (k > thr || (tie && tie_rank < ties));
-    const uint32_t kb = __ballot_sync(~0u, stay);
-    if ((tid & 31) == 0) s_warp[1][tid / 32] = __popc(kb);
-    __syncthreads();
-    int rank = base + __popc(kb & lanes_before), sum = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w < tid / 32) rank += s_warp[1][w];
-      sum += s_warp[1][w];
-    }
-    if (stay && rank < kept) keep[1 + rank] = s;
-    base += sum;
-    seen += tie_sum;
-    __syncthreads();
+  // Ranks: slots of earlier blocks, warps and lanes.  Each warp takes a run of the
+  // block's slots, so that one exchange of counts settles every rank.
+  const int per_warp = ((s1 - s0 + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int w0 = min(s1, s0 + warp * per_warp), w1 = min(s1, w0 + per_warp);
+  uint2 c = make_uint2(0, 0);         // slots above the threshold, at it
+  for (int s = w0; s < w1; s += 32) {
+    const uint32_t k = s + lane < w1 ? (n > L.budget ? key_of(s + lane) : 1u) : 0u;
+    c.x += __popc(__ballot_sync(~0u, s + lane < w1 && k > thr));
+    c.y += __popc(__ballot_sync(~0u, s + lane < w1 && n > L.budget && k == thr));
   }
-  if (tid == 0) {
+  if (lane == 0) s_warp[warp] = c;
+  __syncthreads();
+  uint2 before = make_uint2(0, 0), total = make_uint2(0, 0);
+  for (int w = 0; w < kSelWarps; ++w) {
+    if (w < warp) { before.x += s_warp[w].x; before.y += s_warp[w].y; }
+    total.x += s_warp[w].x;
+    total.y += s_warp[w].y;
+  }
+  if (tid < cs) *cluster.map_shared_rank(&s_counts[rank], tid) = total;
+  cluster.sync();
+  for (int x = 0; x < rank; ++x) { before.x += s_counts[x].x; before.y += s_counts[x].y; }
+  for (int s = w0; s < w1; s += 32) {
+    const uint32_t k = s + lane < w1 ? (n > L.budget ? key_of(s + lane) : 1u) : 0u;
+    const bool over = s + lane < w1 && k > thr, tie = s + lane < w1 && n > L.budget && k == thr;
+    const uint32_t ob = __ballot_sync(~0u, over), tb = __ballot_sync(~0u, tie), lanes_before = (1u << lane) - 1;
+    const uint32_t tie_rank = before.y + __popc(tb & lanes_before);
+    // kept slots before this one: those above the threshold and the first `ties` at it
+    const uint32_t at = before.x + __popc(ob & lanes_before) + min(tie_rank, ties);
+    if ((over || (tie && tie_rank < ties)) && at < static_cast<uint32_t>(kept)) keep[1 + at] = s + lane;
+    before.x += __popc(ob);
+    before.y += __popc(tb);
+  }
+  if (rank == 0 && tid == 0) {
     keep[0] = kept;
     L.dst.len[b * L.H_kv + h] = kept;
     if (h == 0) L.dst.next[b] = next;
@@ -325,6 +401,11 @@ __global__ void __launch_bounds__(kThreads) cache_copy_kernel(CacheEvictLaunch L
 
 }  // namespace
 
+cudaError_t setup_cache_evict() {
+  if (cudaError_t e = cudaFuncSetAttribute(cache_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmem)) return e;
+  return cudaFuncSetAttribute(cache_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+}
+
 cudaError_t launch_cache_append(const CacheAppendLaunch& L, int dtype, cudaStream_t st) {
   // n new slots from anywhere in a page touch at most this many pages
   const dim3 grid((L.n + kPage - 2) / kPage + 1, L.H_kv, L.B);
@@ -339,8 +420,21 @@ cudaError_t launch_cache_append(const CacheAppendLaunch& L, int dtype, cudaStrea
 }
 
 cudaError_t launch_cache_evict(const CacheEvictLaunch& L, cudaStream_t st) {
-  cache_select_kernel<<<dim3(L.H_kv, L.B), kSelThreads, 0, st>>>(L);
-  if (cudaError_t e = cudaGetLastError()) return e;
+  // Blocks per (sequence, head): one wave, as long as each has a slot a thread.
+  int cs = 1;
+  while (cs < kSelCluster && 2 * cs * L.B * L.H_kv <= L.num_sms && cs * kSelThreads < L.src.max_pages * kPage) cs *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(cs, L.H_kv, L.B);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = kSelSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cs;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, cache_select_kernel, L)) return e;
   const int cap = min(L.budget, L.src.max_pages * kPage);
   const dim3 grid((cap + kPage - 1) / kPage, L.H_kv, L.B);
   if (L.d == 128) cache_copy_kernel<128><<<grid, kThreads, 0, st>>>(L);

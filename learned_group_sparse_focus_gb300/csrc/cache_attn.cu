@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
             *reinterpret_cast<float2*>(ring + r * C::kPitch + s * 64 + gl * 8) = make_float2(o[nt][s][e], o[nt][s][2 + e]);
         }
       }
-      if (r0 == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      if (r0 == 0) asm volatile("barrier.cluster.wait;" ::: "memory");
       __syncthreads();
       // Pieces of one share go to one block's inbox, which that block joins and writes:
       // stores into another block's memory are not waited for, loads from it would be.
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
     }
     __syncthreads();                         // shared memory is free for the next row block
   }
-  if (rows == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (rows == 0) asm volatile("barrier.cluster.wait;" ::: "memory");
 }
 
 template <typename T, int D, int NT, bool kMulti>
@@ -691,7 +691,7 @@ cudaError_t prepare_all() {
 
 }  // namespace
 
-cudaError_t setup_cache_kernels() {
+cudaError_t setup_cache_attn() {
   if (cudaError_t e = prepare_all<__nv_bfloat16, 64>()) return e;
   if (cudaError_t e = prepare_all<__nv_bfloat16, 128>()) return e;
   if (cudaError_t e = prepare_all<float, 64>()) return e;
@@ -701,14 +701,15 @@ cudaError_t setup_cache_kernels() {
 cudaError_t launch_cache_attn(const CacheAttnLaunch& L, int dtype, cudaStream_t st) {
   // Blocks per (sequence, head): one wave of the blocks that fit (two an SM with
   // eight rows, one with sixteen), as long as each warp gets a page; a second wave
-  // where a warp still scans 16 pages, since sequences differ in what they keep
-  // (16 sequences of up to 32K tokens: 78 us with 2 blocks, 59 with 4, 72 with 8;
-  // 8 sequences of 1K tokens, 12 heads: 8.2 us with 2 blocks, 13.1 with 4).
+  // of clusters of up to 4 where a warp still scans 16 pages, since sequences
+  // differ in what they keep (16 sequences of up to 32K tokens: 78 us with 2
+  // blocks, 59 with 4, 72 with 8; 4 drafted tokens for 4 sequences of 64K: 51 us
+  // with 4, 71 with 8; 8 sequences of 1K tokens, 12 heads: 8.2 with 2, 13.1 with 4).
   const int fit = L.num_sms * (L.H / L.H_kv * L.n > 8 ? 1 : 2);
   int cs = 1;
   while (cs < kMaxCluster && cs * kWarps < L.c.max_pages) {
     const int blocks = 2 * cs * L.B * L.H_kv;
-    if (blocks > fit && (blocks > 2 * fit || L.c.max_pages < 2 * cs * kWarps * 16)) break;
+    if (blocks > fit && (cs > 2 || blocks > 2 * fit || L.c.max_pages < 2 * cs * kWarps * 16)) break;
     cs *= 2;
   }
   if (dtype == FOCUS_BF16) return L.d == 128 ? launch_rows<__nv_bfloat16, 128>(L, cs, st) : launch_rows<__nv_bfloat16, 64>(L, cs, st);

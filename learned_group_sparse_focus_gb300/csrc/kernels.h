@@ -250,9 +250,11 @@ cudaError_t launch_cache_append(const CacheAppendLaunch& L, int dtype, cudaStrea
 struct CacheEvictLaunch {
   focus_cache_t src, dst;
   int B, H_kv, d, budget, recent;
-  int32_t* keep;          // [B * H_kv][src.max_pages * 64] kept slots, ascending
+  int32_t* keep;          // [B * H_kv][1 + src.max_pages * 64] count and kept slots, ascending
   int* err;
+  int num_sms;
 };
+cudaError_t setup_cache_evict();
 cudaError_t launch_cache_evict(const CacheEvictLaunch& L, cudaStream_t st);
 
 struct CacheAttnLaunch {
@@ -268,7 +270,7 @@ struct CacheAttnLaunch {
   int* err;
   int num_sms;
 };
-cudaError_t setup_cache_kernels();
+cudaError_t setup_cache_attn();
 cudaError_t launch_cache_attn(const CacheAttnLaunch& L, int dtype, cudaStream_t st);
 
 }  // namespace focus

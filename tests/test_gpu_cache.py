@@ -450,6 +450,30 @@ def test_eviction_matches_the_oracle(fz, H_kv, d, lens, budget, recent, ties):
         _same(_host(src), c)
 
 
+def test_eviction_of_a_long_head(fz):
+    """More slots than the blocks of a cluster hold as keys in shared memory."""
+    rng = np.random.default_rng(1)
+    n, d, budget, recent = 400_000, 64, 1500, 700
+    pages = -(-n // 64)
+    c = cr.empty(1, 1, d, pages, pages, 5)
+    c["k"] &= 0x7e                                       # no NaN codes
+    c["v"] &= 0x7e
+    c["k_scale"][:] = 2.0 ** rng.integers(-9, 3, (pages, 1))
+    c["v_scale"][:] = 0.25
+    page = c["table"][0]
+    c["pos"][page, 0] = 3 * np.arange(pages * 64, dtype=np.int32).reshape(pages, 64)
+    c["mass"][:] = rng.integers(0, 300, c["mass"].shape)     # hundreds of ties at the threshold
+    c["len"][:], c["next"][:] = n, 3 * n
+    dst = cr.empty(1, 1, d, 30, 24, 6)
+    want = cr.evict(c, dst, budget, recent)
+    p = _params(fz, 1, 1, 1, 1, d, 4, 1, 8)
+    src, to = _cache(fz, c), _cache(fz, dst)
+    ws = fz.alloc_workspace_cache(p, src)
+    fz.focus_cache_evict(p, budget, recent, src, to, ws)
+    assert fz.focus_check_errors(ws) == 0
+    _same(_host(to), want)
+
+
 def test_eviction_within_one_pool_updates_the_counts_in_place(fz):
     c = _make(31, 2, 2, 64, [600, 350], 4, 1, spare=20)
     free = [x for x in range(c["k"].shape[0]) if x not in c["table"]]
