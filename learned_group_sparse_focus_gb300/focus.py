@@ -375,15 +375,14 @@ def focus_sinkhorn_fwd(p: Params, iters: int, tau: float, S, G, ws, stream=None)
 # --------------------------------------------------------- key/value cache ---
 
 def _expect(name: str, t, shape, dtype, device):
-    """A tensor argument of the cache calls: its shape, dtype, device, layout."""
+    """Address of a tensor argument of the cache calls, its shape, dtype, device
+    and layout checked."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
-    if t.shape != shape or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} "
-                         f"on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} "
+                     f"on {t.device}, strides {t.stride()}")
 
 
 @dataclass(frozen=True, eq=False)
@@ -419,6 +418,7 @@ class Cache:
                 continue
             setattr(c, name, _expect(name, t, shape, dtype, dev))
         object.__setattr__(self, "struct", c)
+        object.__setattr__(self, "ref", ctypes.byref(c))
         object.__setattr__(self, "device", dev)
         object.__setattr__(self, "dims", (B, H_kv, d))
 
@@ -457,23 +457,31 @@ def alloc_workspace_cache(p: Params, cache: Cache, stream=None) -> torch.Tensor:
     return ws
 
 
-def _cache_call(fn: str, p: Params, cache: Cache, ws, stream, args):
+def _raw_stream(index: int) -> int:
+    """Current stream of a device (torch.cuda.current_stream builds an object, at
+    a third of the cost of a whole call)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _cache_call(fn: str, p: Params, cache: Cache, ws, stream, *args):
     """Runs a cache call on the cache's device (args: the C arguments between p
     and ws)."""
+    dev = cache.device
     if cache.dims != (p.B, p.H_kv, p.d):
         raise ValueError(f"the cache holds (B, H_kv, d) = {cache.dims}, the call asks for {(p.B, p.H_kv, p.d)}")
-    dev = cache.device
     if dev.type != "cuda":
         raise ValueError(f"the cache must be on a CUDA device, not {dev}")
     if ws.device != dev or (stream is not None and stream.device != dev):
         raise ValueError(f"workspace and stream must be on the cache's device {dev}")
     call = getattr(_lib, fn)
+    raw = _raw_stream(dev.index) if stream is None else stream.cuda_stream
     if dev.index == torch.cuda.current_device():
-        st = call(ctypes.byref(p), *args, _ptr(ws), ws.numel(), _stream(stream))
+        st = call(p, *args, _ptr(ws), ws.numel(), raw)
     else:
         with torch.cuda.device(dev):
-            st = call(ctypes.byref(p), *args, _ptr(ws), ws.numel(), _stream(stream))
-    _check(fn, st)
+            st = call(p, *args, _ptr(ws), ws.numel(), raw)
+    if st != 0:
+        raise FocusError(fn, st)
 
 
 def _float_type(p: Params):
@@ -484,14 +492,14 @@ def focus_cache_append(p: Params, K, V, gid, cache: Cache, ws, n_new=None, len_o
     """Appends K, V [B, H_kv, n, d] and gid [B, A, n]; n_new [B] int32: valid
     tokens a sequence (None: all n).  The counts are updated in place, or written
     to len_out [B, H_kv] and next_out [B]."""
-    dev, rows = cache.device, (p.B, p.H_kv, p.n, p.d)
-    ft, i32 = _float_type(p), torch.int32
-    args = (_expect("K", K, rows, ft, dev), _expect("V", V, rows, ft, dev),
-            _expect("gid", gid, (p.B, p.A, p.n), i32, dev),
-            None if n_new is None else _expect("n_new", n_new, (p.B,), i32, dev), ctypes.byref(cache.struct),
-            cache.struct.len if len_out is None else _expect("len_out", len_out, (p.B, p.H_kv), i32, dev),
-            cache.struct.next if next_out is None else _expect("next_out", next_out, (p.B,), i32, dev))
-    _cache_call("focus_cache_append", p, cache, ws, stream, args)
+    dev, B, H_kv, n, ft, i32 = cache.device, p.B, p.H_kv, p.n, _float_type(p), torch.int32
+    rows = (B, H_kv, n, p.d)
+    _cache_call("focus_cache_append", p, cache, ws, stream,
+                _expect("K", K, rows, ft, dev), _expect("V", V, rows, ft, dev),
+                _expect("gid", gid, (B, p.A, n), i32, dev),
+                None if n_new is None else _expect("n_new", n_new, (B,), i32, dev), cache.ref,
+                cache.struct.len if len_out is None else _expect("len_out", len_out, (B, H_kv), i32, dev),
+                cache.struct.next if next_out is None else _expect("next_out", next_out, (B,), i32, dev))
 
 
 def focus_cache_attention_fwd(p: Params, Q, gid, cache: Cache, O, lse, ws, n_new=None, accumulate=False,
@@ -499,13 +507,13 @@ def focus_cache_attention_fwd(p: Params, Q, gid, cache: Cache, O, lse, ws, n_new
     """Attention of the newest tokens Q [B, H, n, d] (the last n_new[b] appended
     ones) over the cache into O and lse ([B, H, n] fp32 or None); accumulate adds
     the weights each slot received to cache.mass."""
-    dev, rows, i32 = cache.device, (p.B, p.H, p.n, p.d), torch.int32
-    ft = _float_type(p)
-    args = (_expect("Q", Q, rows, ft, dev), _expect("gid", gid, (p.B, p.A, p.n), i32, dev),
-            None if n_new is None else _expect("n_new", n_new, (p.B,), i32, dev), ctypes.byref(cache.struct),
-            _expect("O", O, rows, ft, dev), None if lse is None else _expect("lse", lse, rows[:3], torch.float32, dev),
-            int(bool(accumulate)))
-    _cache_call("focus_cache_attention_fwd", p, cache, ws, stream, args)
+    dev, B, H, n, ft, i32 = cache.device, p.B, p.H, p.n, _float_type(p), torch.int32
+    rows = (B, H, n, p.d)
+    _cache_call("focus_cache_attention_fwd", p, cache, ws, stream,
+                _expect("Q", Q, rows, ft, dev), _expect("gid", gid, (B, p.A, n), i32, dev),
+                None if n_new is None else _expect("n_new", n_new, (B,), i32, dev), cache.ref,
+                _expect("O", O, rows, ft, dev),
+                None if lse is None else _expect("lse", lse, (B, H, n), torch.float32, dev), 1 if accumulate else 0)
 
 
 def focus_cache_evict(p: Params, budget: int, recent: int, src: Cache, dst: Cache, ws, stream=None):
@@ -513,8 +521,7 @@ def focus_cache_evict(p: Params, budget: int, recent: int, src: Cache, dst: Cach
     positions, then the most mass) from src's pages into dst's."""
     if dst.device != src.device or dst.dims != src.dims:
         raise ValueError("src and dst must be on one device and agree in B, H_kv and d")
-    _cache_call("focus_cache_evict", p, src, ws, stream, (int(budget), int(recent), ctypes.byref(src.struct),
-                                                          ctypes.byref(dst.struct)))
+    _cache_call("focus_cache_evict", p, src, ws, stream, int(budget), int(recent), src.ref, dst.ref)
 
 
 def run_decode_step(p: Params, h, W, C, Q, K, V, cache: Cache, ws, ws_cache, n_new=None, want_lse=False,
