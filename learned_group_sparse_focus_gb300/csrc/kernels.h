@@ -271,6 +271,11 @@ struct CacheAttnLaunch {
   int num_sms;
 };
 cudaError_t setup_cache_attn();
+// cache_attn_tc.cu: bf16, d = 128; with several tokens a table of kCacheTableGroups
+// group ids, for K up to that.
+constexpr int kCacheTableGroups = 1024;
+cudaError_t setup_cache_attn_tc();
+cudaError_t launch_cache_attn_tc(const CacheAttnLaunch& L, cudaStream_t st);
 cudaError_t launch_cache_attn(const CacheAttnLaunch& L, int dtype, cudaStream_t st);
 
 }  // namespace focus

@@ -102,14 +102,15 @@ def append(c: dict, K, V, gid, n_new=None) -> dict:
 def attention(c: dict, Q, gid, w: int, scale: float, n_new=None) -> dict:
     """Q [B, H, T, d].  Returns O, lse (NaN where t >= n_new), the weight every
     slot received (got, like mass), and for error bounds: pv = sum P |v|, dot = the
-    largest scale * sum |q| |k| of a row, kept = slots kept by a row."""
+    largest scale * sum |q| |k| of a row, kept = slots kept by a row, page = the
+    largest value that the page of the slot with the most weight * page scale holds."""
     Q = np.asarray(Q, np.float64)
     B, H, T, d = Q.shape
     H_kv, A = c["k"].shape[1], gid.shape[1]
     G = H // H_kv
     O, pv = np.full((B, H, T, d), np.nan), np.full((B, H, T, d), np.nan)
     lse, dot = np.full((B, H, T), np.nan), np.zeros((B, H, T))
-    kept = np.zeros((B, H, T), np.int64)
+    kept, big = np.zeros((B, H, T), np.int64), np.zeros((B, H, T))
     got = np.zeros(c["pos"].shape)
     for b in range(B):
         m = T if n_new is None else int(n_new[b])
@@ -127,13 +128,15 @@ def attention(c: dict, Q, gid, w: int, scale: float, n_new=None) -> dict:
                     continue
                 s = k[keep] @ Q[b, h, t] * scale
                 top = s.max()
+                vs = c["v_scale"][page[keep], kv].astype(np.float64)
+                big[b, h, t] = 448.0 * vs[np.argmax(s / np.log(2.0) + np.log2(vs))]
                 p = np.exp(s - top)
                 lse[b, h, t] = top + np.log(p.sum())
                 p /= p.sum()
                 O[b, h, t], pv[b, h, t] = p @ v[keep], p @ np.abs(v[keep])
                 dot[b, h, t] = scale * (np.abs(k[keep]) @ np.abs(Q[b, h, t])).max()
                 np.add.at(got, (page[keep], kv, row[keep]), p)
-    return dict(O=O, lse=lse, got=got, pv=pv, dot=dot, kept=kept)
+    return dict(O=O, lse=lse, got=got, pv=pv, dot=dot, kept=kept, page=big)
 
 
 def stays(mass, pos, nxt: int, budget: int, recent: int) -> np.ndarray:

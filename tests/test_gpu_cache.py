@@ -11,7 +11,12 @@ Attention bounds, per output, from the arithmetic (u = 2^-24):
             of its sum, the sum's roundings, exp2 and the join's factors);
   lse       ds + kept 2 u + 2^-22 (1 + |lse|);
   O         half a step of the output type, and (r + w) sum P|v| for the weights,
-            w = 2^-11 (one f16 rounding) for bf16 tensors and 2^-22 for fp32;
+            w = 2^-11 (one f16 rounding) for bf16 tensors and 2^-22 for fp32; and
+            kept 2^-26 M for the weights' floor: weights p = 2^(s + e) times page
+            exponents e multiply codes of at most 448 and are cut off at 2^-16 where
+            the largest is 2^10 or more; that one, in a page of exponent e0, adds at
+            least 2^10 2^-e0 to the sum, so the cut-offs move O by at most
+            kept 2^-16 448 / (2^10 2^-e0) = kept 2^-26 M, M = 448 2^e0;
   mass      r times what was added, and a step of the total.
 """
 import numpy as np
@@ -220,7 +225,8 @@ def _bounds(ref, d, dtype):
     ds = (d + 8) * 2 * U * ref["dot"]
     r = 2 * ds + ref["kept"] * 2 * U + 2.0 ** -20
     step, wt = (2.0 ** -8, 2.0 ** -11) if dtype == "bf16" else (2.0 ** -24, 2.0 ** -22)
-    return ds, r, step * np.abs(ref["O"]) + (r[..., None] + wt) * ref["pv"] * (1 + step) + 1e-38
+    return ds, r, step * np.abs(ref["O"]) + (r[..., None] + wt) * ref["pv"] * (1 + step) + \
+        (ref["kept"] * 2.0 ** -26 * ref["page"])[..., None] + 1e-38
 
 
 def _o_within(O, ref, d, dtype, there=...):
@@ -287,6 +293,15 @@ CASES = [
     (16, 1, 128, [350], 2, 3, 1, 20),
     (1, 4, 128, [300], 64, 4, 1, 30),
     (5, 1, 64, [130, 64], 13, 500, 1, 1000),
+    # more than 8, 16, 32 and 64 rows a head, tokens that straddle blocks of rows, more
+    # groups than the table holds, an empty sequence, windows of one and of everything
+    (12, 2, 128, [600, 0, 70], 1, 3, 1, 40),
+    (24, 1, 128, [500], 1, 2, 1, 1),
+    (40, 1, 128, [300, 64], 2, 3, 1, 500),
+    (3, 2, 128, [700, 65], 5, 4, 2, 30),
+    (8, 1, 128, [900, 1], 4, 6, 1, 0),
+    (6, 1, 128, [400], 13, 3, 1, 25),
+    (2, 1, 128, [333], 31, 1500, 1, 10),
 ]
 
 
@@ -302,6 +317,28 @@ def test_attention_matches_the_oracle(fz, dtype, G, H_kv, d, lens, T, K, A, w):
     n_new = rng.integers(0, T + 1, B).astype(np.int32)
     n_new[-1] = T
     _check_attention(fz, c, Q, gid, K, w, dtype, n_new=n_new, accumulate=bool(T % 2), want_lse=bool(G % 2))
+
+
+@pytest.mark.parametrize("G,d,T,K,dtype", [(2, 64, 1, 1, "bf16"), (4, 128, 1, 1, "bf16"), (1, 128, 3, 2, "f32"),
+                                           (12, 128, 1, 1, "bf16"), (8, 128, 4, 2, "bf16"), (1, 128, 64, 3, "bf16")])
+def test_attention_over_more_slots_than_the_lists_hold(fz, G, d, T, K, dtype):
+    """So many kept slots that the kernels' lists wrap around and the weights' pass scans
+    again: two sequences, one of 30,000 slots, random codes."""
+    rng = np.random.default_rng(d + T)
+    n = [30000, 9001]
+    mp = -(-n[0] // 64)
+    c = cr.empty(2, 1, d, 2 * mp, mp, 5)
+    c["k"] = (c["k"] & 0xbf).astype(np.uint8)                # below 2 in magnitude, no NaN
+    c["v"] &= 0xbf
+    c["k_scale"][:] = 2.0 ** rng.integers(-3, 1, c["k_scale"].shape)
+    c["v_scale"][:] = 2.0 ** rng.integers(-5, 6, c["v_scale"].shape)
+    for b in range(2):
+        c["pos"][c["table"][b], 0] = np.arange(mp * 64).reshape(mp, 64)
+    c["gid"][:] = rng.integers(0, K, c["gid"].shape)
+    c["mass"][:] = 0.0
+    c["len"][:, 0], c["next"][:] = n, n
+    Q = _rows(rng, (2, G, T, d), dtype, 0.2)
+    _check_attention(fz, c, Q, rng.integers(0, K, (2, 1, T)).astype(np.int32), K, 300, dtype)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -345,12 +382,13 @@ def test_attention_over_pages_of_very_different_scales(fz, dtype):
     _check_attention(fz, c, Q, gid[:, :, -2:].copy(), 3, 100, dtype)
 
 
-def test_nan_and_infinite_queries_stay_in_their_rows(fz):
+@pytest.mark.parametrize("H,d", [(4, 64), (4, 128), (8, 128)])
+def test_nan_and_infinite_queries_stay_in_their_rows(fz, H, d):
     import torch
-    c = _make(4, 1, 1, 64, [300], 2, 1)
-    Q = _rows(np.random.default_rng(1), (1, 4, 2, 64), "bf16", 0.2)
+    c = _make(4, 1, 1, d, [300], 2, 1)
+    Q = _rows(np.random.default_rng(1), (1, H, 2, d), "bf16", 0.2)
     gid = np.array([[[0, 1]]], np.int32)
-    p = fz.make_params(1, 4, 1, 2, 64, 64, 64, 2, 1, 20)
+    p = fz.make_params(1, H, 1, 2, d, 64, 64, 2, 1, 20)
     cache = _cache(fz, c)
     ws = fz.alloc_workspace_cache(p, cache)
     outs = []
@@ -358,30 +396,34 @@ def test_nan_and_infinite_queries_stay_in_their_rows(fz):
         q = Q.copy()
         if bad:
             q[0, 1, 0, 3], q[0, 2, 1, 5] = np.nan, np.inf
-        O = torch.zeros((1, 4, 2, 64), dtype=torch.bfloat16, device="cuda")
+        O = torch.zeros((1, H, 2, d), dtype=torch.bfloat16, device="cuda")
         fz.focus_cache_attention_fwd(p, _dev(q, torch.bfloat16), _dev(gid), cache, O, None, ws)
         outs.append(O.float().cpu().numpy())
-    same = np.ones((4, 2), bool)
+    same = np.ones((H, 2), bool)
     same[1, 0] = same[2, 1] = False
     assert np.array_equal(outs[0][0][same], outs[1][0][same])
     assert np.isnan(outs[1][0, 1, 0]).all() and np.isnan(outs[1][0, 2, 1]).all()
 
 
-def test_nan_key_reaches_only_the_rows_that_keep_it(fz):
+@pytest.mark.parametrize("H,d", [(2, 64), (2, 128), (6, 128), (20, 128), (32, 128)])
+def test_nan_key_reaches_only_the_rows_that_keep_it(fz, H, d):
     import torch
-    c = _make(6, 1, 1, 64, [200], 2, 1)
+    c = _make(6, 1, 1, d, [200], 2, 1)
     page, row = cr.slots(c, 0, 0)
     c["gid"][page, 0, row] = 0
     c["gid"][page[10], 0, row[10]] = 1
     c["v"][page[10], 0, row[10], 0] = 127
-    Q = _rows(np.random.default_rng(1), (1, 2, 2, 64), "bf16", 0.2)
-    p = fz.make_params(1, 2, 1, 2, 64, 64, 64, 2, 1, 20)
+    c["v"][page[150], 0, row[150], d - 1] = 255
+    c["gid"][page[150], 0, row[150]] = 1
+    Q = _rows(np.random.default_rng(1), (1, H, 2, d), "bf16", 0.2)
+    p = fz.make_params(1, H, 1, 2, d, 64, 64, 2, 1, 20)
     cache = _cache(fz, c)
     ws = fz.alloc_workspace_cache(p, cache)
-    O = torch.zeros((1, 2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    O = torch.zeros((1, H, 2, d), dtype=torch.bfloat16, device="cuda")
     fz.focus_cache_attention_fwd(p, _dev(Q, torch.bfloat16), _dev(np.array([[[0, 1]]], np.int32)), cache, O, None, ws)
     o = O.float().cpu().numpy()[0]
-    assert np.isfinite(o[:, 0]).all() and np.isnan(o[:, 1, 0]).all() and np.isfinite(o[:, 1, 1:]).all()
+    assert np.isfinite(o[:, 0]).all() and np.isfinite(o[:, 1, 1:-1]).all()
+    assert np.isnan(o[:, 1, 0]).all() and np.isnan(o[:, 1, -1]).all()
 
 
 def test_attention_with_bad_pages_and_lengths(fz):
