@@ -123,9 +123,8 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheAppendLaunc
       const int e = max(need_exp(a), e_old);
       if (ht == 0) *scale = exp2_int(e);
       if (e > e_old) {                                   // the page's older rows, at the new scale
-        const float f = exp2_int(max(e_old - e, -126));  // codes times 2^-126 are 0 like any smaller factor
         uint4* old = reinterpret_cast<uint4*>(dst);
-        for (int at = ht; at < r0 * D / 16; at += kHalf) old[at] = rescale16(old[at], f);
+        for (int at = ht; at < r0 * D / 16; at += kHalf) old[at] = rescale16(old[at], e_old - e);
       }
       const float f = exp2_int(-e);
 #pragma unroll
@@ -197,6 +196,7 @@ __device__ __forceinline__ uint32_t keep_key(float mass, bool late) {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelCluster = 16;            // blocks of a cluster, at most
+constexpr int kSelRun = 4096;              // slots that are worth a block
 constexpr int kSelKeys = 24576;            // keys that a block holds in shared memory
 constexpr int kSelSmem = kSelKeys * 4 + kSelWarps * 256 * 4;
 
@@ -205,8 +205,9 @@ constexpr int kSelSmem = kSelKeys * 4 + kSelWarps * 256 * 4;
 // slots in order (ties: the lowest slots).  Slots are in ascending position, so
 // the protected ones are among the last `recent`; only those positions are read.
 // A block's keys stay in shared memory between the passes (longer runs are formed
-// again in each), every warp counts into bins of its own, since most keys share a
-// few exponents, and the blocks exchange their counts through the cluster's
+// again in each), every warp counts into bins of its own and equal digits of a warp
+// at once (most keys share a few exponents: with an atomic a key a pass over 8,704
+// keys took 5 us), and the blocks exchange their counts through the cluster's
 // distributed shared memory.
 __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvictLaunch L) {
   extern __shared__ __align__(16) uint32_t s_keys[];
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvictLau
   uint32_t ties = 0;                  // slots equal to the threshold that stay
   if (n > L.budget) {
     if (held) {
-#pragma unroll 4
+#pragma unroll 8
       for (int s = s0 + tid; s < s1; s += kSelThreads) s_keys[s - s0] = form_key(s);
     }
     uint32_t left = L.budget;
@@ -247,9 +248,13 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvictLau
 #pragma unroll
       for (int i = 0; i < 8; ++i) s_hist[warp][lane + 32 * i] = 0;
       __syncthreads();
-      for (int s = s0 + tid; s < s1; s += kSelThreads) {
-        const uint32_t k = key_of(s);
-        if (pass == 0 || (k >> (shift + 8)) == (thr >> (shift + 8))) atomicAdd(&s_hist[warp][(k >> shift) & 255], 1u);
+      for (int s = s0 + warp * 32; s < s1; s += kSelThreads) {
+        const uint32_t k = s + lane < s1 ? key_of(s + lane) : 0u;
+        const bool in = s + lane < s1 && (pass == 0 || (k >> (shift + 8)) == (thr >> (shift + 8)));
+        const uint32_t digit = in ? (k >> shift) & 255 : 256;
+        const uint32_t peers = __match_any_sync(~0u, digit);
+        if (in && lane == __ffs(peers) - 1) s_hist[warp][digit] += __popc(peers);   // the warp's own bins
+        __syncwarp();
       }
       if (pass == 0) asm volatile("barrier.cluster.wait;" ::: "memory");
       __syncthreads();
@@ -329,7 +334,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvictLau
 
 // One block per destination page and head.
 template <int D>
-__global__ void __launch_bounds__(kThreads) cache_copy_kernel(CacheEvictLaunch L) {
+__global__ void __launch_bounds__(kThreads, 8) cache_copy_kernel(CacheEvictLaunch L) {
   constexpr int kPerRow = D / 16;
   constexpr int kPieces = kPage * kPerRow / kHalf;
   __shared__ int s_max[kThreads / 32];
@@ -341,6 +346,7 @@ __global__ void __launch_bounds__(kThreads) cache_copy_kernel(CacheEvictLaunch L
   const int to = cache_page(L.dst, b, j, L.err);
   if (to < 0) return;
   const size_t to_plane = static_cast<size_t>(to) * L.H_kv + h;
+  // All loads first: the rows' pieces and scales, and what a slot carries beside them.
   uint4 c[kPieces];
   int es[kPieces];
   int e = kMinExp;
@@ -354,21 +360,27 @@ __global__ void __launch_bounds__(kThreads) cache_copy_kernel(CacheEvictLaunch L
     const int page = cache_page(L.src, b, s / kPage, L.err);
     if (page < 0) continue;
     const size_t plane = static_cast<size_t>(page) * L.H_kv + h;
-    c[i] = *reinterpret_cast<const uint4*>((half ? L.src.v : L.src.k) + (plane * kPage + s % kPage) * D +
-                                           (at % kPerRow) * 16);
+    c[i] = __ldcs(reinterpret_cast<const uint4*>((half ? L.src.v : L.src.k) + (plane * kPage + s % kPage) * D +
+                                                 (at % kPerRow) * 16));
     es[i] = scale_exp((half ? L.src.v_scale : L.src.k_scale)[plane]);
+  }
+  int slot_page = -1, pos = 0;
+  int16_t gid = 0;
+  float mass = 0.f;
+  if (ht < rows) {
+    const int s = keep[1 + j * kPage + ht];
+    slot_page = cache_page(L.src, b, s / kPage, L.err);
+    const size_t from = (static_cast<size_t>(max(slot_page, 0)) * L.H_kv + h) * kPage + s % kPage;
+    if (slot_page >= 0 && half == 0) {
+      pos = L.src.pos[from];
+      gid = L.src.gid[from];
+    } else if (slot_page >= 0) {
+      mass = L.src.mass[from];
+    }
   }
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
-    uint32_t top = 0;                       // largest magnitude code of each byte lane, NaN left out
-    const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const uint32_t a = w[x] & 0x7f7f7f7fu;
-      top = __vmaxu4(top, a & ~__vcmpeq4(a, 0x7f7f7f7fu));
-    }
-    top = max(max(top & 255u, (top >> 8) & 255u), max((top >> 16) & 255u, top >> 24));
-    const float v = e4m3x2_to_float2(static_cast<uint16_t>(top)).x * exp2_int(es[i]);
+    const float v = e4m3x2_to_float2(static_cast<uint16_t>(top_code(c[i]))).x * exp2_int(es[i]);
     e = max(e, need_exp(__float_as_uint(v)));
   }
   e = __reduce_max_sync(~0u, e);
@@ -382,19 +394,16 @@ __global__ void __launch_bounds__(kThreads) cache_copy_kernel(CacheEvictLaunch L
   for (int i = 0; i < kPieces; ++i) {
     const int at = ht + i * kHalf;
     if (at >= rows * kPerRow) continue;
-    if (es[i] != e) c[i] = rescale16(c[i], exp2_int(min(max(es[i] - e, -126), 127)));
-    *reinterpret_cast<uint4*>(dst + static_cast<size_t>(at) * 16) = c[i];
+    if (es[i] != e) c[i] = rescale16(c[i], es[i] - e);
+    __stcs(reinterpret_cast<uint4*>(dst + static_cast<size_t>(at) * 16), c[i]);
   }
-  if (ht < rows) {
-    const int s = keep[1 + j * kPage + ht];
-    const int page = cache_page(L.src, b, s / kPage, L.err);
-    const size_t from = (static_cast<size_t>(max(page, 0)) * L.H_kv + h) * kPage + s % kPage;
+  if (slot_page >= 0) {
     const size_t at = to_plane * kPage + ht;
-    if (page >= 0 && half == 0) {
-      L.dst.pos[at] = L.src.pos[from];
-      L.dst.gid[at] = L.src.gid[from];
-    } else if (page >= 0) {
-      L.dst.mass[at] = L.src.mass[from];
+    if (half == 0) {
+      L.dst.pos[at] = pos;
+      L.dst.gid[at] = gid;
+    } else {
+      L.dst.mass[at] = mass;
     }
   }
 }
@@ -420,9 +429,9 @@ cudaError_t launch_cache_append(const CacheAppendLaunch& L, int dtype, cudaStrea
 }
 
 cudaError_t launch_cache_evict(const CacheEvictLaunch& L, cudaStream_t st) {
-  // Blocks per (sequence, head): one wave, as long as each has a slot a thread.
+  // Blocks per (sequence, head): one wave, as long as each has kSelRun slots.
   int cs = 1;
-  while (cs < kSelCluster && 2 * cs * L.B * L.H_kv <= L.num_sms && cs * kSelThreads < L.src.max_pages * kPage) cs *= 2;
+  while (cs < kSelCluster && 2 * cs * L.B * L.H_kv <= L.num_sms && 2 * cs * kSelRun <= L.src.max_pages * kPage) cs *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(cs, L.H_kv, L.B);
   cfg.blockDim = dim3(kSelThreads);

@@ -73,15 +73,54 @@ __device__ __forceinline__ uint16_t float2_to_e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Four codes times f, rounded to e4m3 again.
-__device__ __forceinline__ uint32_t rescale4(uint32_t c, float f) {
-  const float2 a = e4m3x2_to_float2(static_cast<uint16_t>(c));
-  const float2 b = e4m3x2_to_float2(static_cast<uint16_t>(c >> 16));
-  return static_cast<uint32_t>(float2_to_e4m3x2(a.x * f, a.y * f)) |
-         (static_cast<uint32_t>(float2_to_e4m3x2(b.x * f, b.y * f)) << 16);
+// Sixteen codes times 2^d, rounded to e4m3 again.  For |d| <= 14 the product is
+// exact in f16 (codes are multiples of 2^-9, f16's least is 2^-24; results that
+// overflow saturate either way), so only the rounding to e4m3 rounds.
+__device__ __forceinline__ uint4 rescale16(uint4 c, int d) {
+  uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  if (d >= -14 && d <= 14) {
+    const __half2 f = __half2half2(__ushort_as_half(static_cast<uint16_t>((d + 15) << 10)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint16_t r[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t x = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> (16 * e)));
+        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x), f);
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r[e]) : "r"(*reinterpret_cast<const uint32_t*>(&y)));
+      }
+      w[i] = r[0] | static_cast<uint32_t>(r[1]) << 16;
+    }
+  } else {
+    const float f = exp2_int(min(max(d, -126), 127));        // codes times 2^-126 are 0 like any smaller factor
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = e4m3x2_to_float2(static_cast<uint16_t>(w[i]));
+      const float2 b = e4m3x2_to_float2(static_cast<uint16_t>(w[i] >> 16));
+      w[i] = float2_to_e4m3x2(a.x * f, a.y * f) | static_cast<uint32_t>(float2_to_e4m3x2(b.x * f, b.y * f)) << 16;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ uint4 rescale16(uint4 c, float f) {
-  return make_uint4(rescale4(c.x, f), rescale4(c.y, f), rescale4(c.z, f), rescale4(c.w, f));
+
+// Largest magnitude code of sixteen, NaN left out.
+__device__ __forceinline__ uint32_t top_code(uint4 c) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t lo = 0, hi = 0;                                   // bytes 0 and 2, 1 and 3, a pair of maxima each
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lo = __vmaxu2(lo, w[i] & 0x007f007fu);
+    hi = __vmaxu2(hi, w[i] & 0x7f007f00u);
+  }
+  uint32_t top = max(max(lo & 0xffffu, lo >> 16), max(hi & 0xffffu, hi >> 16) >> 8);
+  if (top == 127) {
+    top = 0;
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t x = w[i / 4] >> (i % 4 * 8) & 127u;
+      if (x < 127) top = max(top, x);
+    }
+  }
+  return top;
 }
 
 }  // namespace focus

@@ -12,8 +12,8 @@
 //   O^T [128 dims, 4 R] += V^T P^T     V rows are an MN-major A; P is rounded to f16
 //                           and split into four e5m2 parts of three bits (an e5m2
 //                           number is the upper byte of an f16), again side by
-//                           side in N: all 11 bits, down to 2^-16 under weights of
-//                           up to 2^15
+//                           side in N: all 11 bits, down to 2^-16, which is 2^-26
+//                           of a row's largest weight or less (see below)
 // R = 16, 32 or 64 query rows (tokens x query heads of the head).  With the keys
 // on the 128 side of both products nothing is padded but R, and a thread owns a
 // key: masks, scales and the weight's sum over rows need no exchange.
