@@ -153,16 +153,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
   uint8_t* inbox = smem + kWarps * C::kWarpBytes;
   const int32_t* gids = L.gid + (static_cast<size_t>(b) * L.A + (L.A == 1 ? 0 : h)) * L.n;
   const int first = warp * cs + rank, step = kWarps * cs;          // the warp's pages
-  auto table = [&](int from) {                         // table entry of the lane's page among kAhead, unchecked
-    const int j = from + lane * step;
+  // Units of the scan: pages, and from page `split` on (where every slot of a window
+  // lies, if the windows' pages are fewer than the warps) quarters of pages, so that
+  // no warp gets four tiles while most get one.
+  int n = 0, fresh = 0, pos0 = 0, units = 0, near_from = 0, split = INT_MAX;
+  auto page_of = [&](int u) { return u < split ? u : split + (u - split) / 4; };
+  auto table = [&](int from) {                         // table entry of the lane's unit among kAhead, unchecked
+    const int j = page_of(from + lane * step);
     return lane < kAhead && j < L.c.max_pages ? L.c.table[static_cast<size_t>(b) * L.c.max_pages + j] : -1;
   };
-  int n = 0, fresh = 0, pos0 = 0, pages = 0, near_from = 0;
   int rows = G;                                        // set in the first round, which always runs
 
   int buf = 0;
   for (int r0 = 0; r0 < rows; r0 += C::kRows, buf ^= 1) {
-    // ---- loads that depend on nothing go first: table, group ids, query rows, counts
+    // ---- loads that depend on nothing go first: table (as if without quarters), group
+    // ids, query rows, counts
     int entry = table(first);
     const int t_lo = r0 / G;
     const int gid0 = gids[t_lo];
@@ -187,25 +192,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
       fresh = cache_new(L.n_new, L.n, b, L.err);
       pos0 = L.c.next[b] - fresh;                      // position of token 0
       rows = G * fresh;
-      pages = (n + kPage - 1) / kPage;
+      const int pages = (n + kPage - 1) / kPage;
       near_from = n - static_cast<int>(min(static_cast<long long>(n), static_cast<long long>(L.w) + fresh));
+      split = near_from / kPage;
+      if (pages - split > step) split = pages;
+      units = split + 4 * (pages - split);
       if (rows == 0) break;                            // the same in the whole cluster
+      if (first + lane * step > split) entry = table(first);       // another page than the guess
     }
     const int tokens = (min(r0 + C::kRows, rows) - 1) / G - t_lo + 1;
 
     // ---- the scan: kAhead pages at a time, their group ids in shared memory
-    int j = first, i = 0;                              // next page to scan, and its place among the kAhead
+    int j = first, i = 0;                              // next unit to scan, and its place among the kAhead
     int lane_page = -1, lane_exps = 0;
-    int2 pos{};                                        // positions of the lane's two slots of page j, if it is near
+    int2 pos{};                                        // positions of the lane's two slots of unit j, if it is near
     auto load_pos = [&]() {
       const int page = __shfl_sync(~0u, lane_page, i);
-      if (page >= 0 && (j + 1) * kPage > near_from)
+      if (page >= 0 && (page_of(j) + 1) * kPage > near_from)
         pos = *reinterpret_cast<const int2*>(L.c.pos + (static_cast<size_t>(page) * L.H_kv + h) * kPage + 2 * lane);
     };
-    auto open_pages = [&]() {                          // pages j, j + step, ...
+    auto open_pages = [&]() {                          // units j, j + step, ...
       i = 0;
       lane_page = -1;
-      if (lane < kAhead && j + lane * step < pages) {
+      if (lane < kAhead && j + lane * step < units) {
         lane_page = entry;
         if (entry < 0 || entry >= L.c.n_pages) {
           atomicOr(L.err, kErrBadCache);
@@ -287,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
     }
 
     int entries = 0;
-    // Lists the kept slots of page j.
+    // Lists the kept slots of unit j.
     auto scan_page = [&]() {
       if (i == 0) {                                    // new group ids have to have landed
         cp_async_commit();
@@ -297,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
       const int page = __shfl_sync(~0u, lane_page, i), exps = __shfl_sync(~0u, lane_exps, i);
       if (page >= 0) {
         const uint32_t two = ids[i * 32 + lane];
-        const bool near = (j + 1) * kPage > near_from;
+        const int from = page_of(j) * kPage;
+        const bool near = from + kPage > near_from;
         int m0 = 0, m1 = 0;
         for (int t = 0; t < (kMulti ? tokens : 1); ++t) {
           const int g = kMulti ? s_gid[t] : gid0, p = pos0 + t_lo + t;
@@ -309,11 +319,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
           m0 |= k0 << t;
           m1 |= k1 << t;
         }
-        if ((j + 1) * kPage > n) {
-          const int left = n - j * kPage - 2 * lane;
+        if (from + kPage > n) {
+          const int left = n - from - 2 * lane;
           if (left < 1) m0 = 0;
           if (left < 2) m1 = 0;
         }
+        if (j >= split && lane / 8 != ((j - split) & 3)) m0 = m1 = 0;      // another quarter's
         const uint32_t b0 = __ballot_sync(~0u, m0 != 0), b1 = __ballot_sync(~0u, m1 != 0);
         if (b0 | b1) {
           const uint32_t before = (1u << lane) - 1;
@@ -543,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
       }
       // ---- the warp's pages: copies run kStages - 1 tiles ahead of the products
       for (int tile = 1 - kStages;; ++tile) {
-        while (entries < (tile + kStages) * kKeys && j < pages) scan_page();
+        while (entries < (tile + kStages) * kKeys && j < units) scan_page();
         if (tile >= 0 && tile * kKeys >= entries) break;
         issue(tile + kStages - 1, pass == 0);
         if (tile < 0) continue;
@@ -666,10 +677,20 @@ cudaError_t launch(const CacheAttnLaunch& L, int cs, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, cache_attn_kernel<T, D, NT, kMulti>, L);
 }
 
+// More than eight rows of a single bf16 token with d = 128 go to cache_attn_tc.cu.
+template <typename T, int D>
+struct Reach {
+  static constexpr bool wide_single = !(std::is_same<T, __nv_bfloat16>::value && D == 128);
+};
+
 template <typename T, int D>
 cudaError_t launch_rows(const CacheAttnLaunch& L, int cs, cudaStream_t st) {
   const bool wide = L.H / L.H_kv * L.n > 8;
-  if (L.n == 1) return wide ? launch<T, D, 2, false>(L, cs, st) : launch<T, D, 1, false>(L, cs, st);
+  if (L.n == 1) {
+    if constexpr (Reach<T, D>::wide_single)
+      if (wide) return launch<T, D, 2, false>(L, cs, st);
+    return launch<T, D, 1, false>(L, cs, st);
+  }
   return wide ? launch<T, D, 2, true>(L, cs, st) : launch<T, D, 1, true>(L, cs, st);
 }
 
@@ -685,7 +706,8 @@ template <typename T, int D>
 cudaError_t prepare_all() {
   if (cudaError_t e = prepare<T, D, 1, false>()) return e;
   if (cudaError_t e = prepare<T, D, 1, true>()) return e;
-  if (cudaError_t e = prepare<T, D, 2, false>()) return e;
+  if constexpr (Reach<T, D>::wide_single)
+    if (cudaError_t e = prepare<T, D, 2, false>()) return e;
   return prepare<T, D, 2, true>();
 }
 
