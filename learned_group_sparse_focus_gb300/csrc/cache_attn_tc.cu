@@ -525,6 +525,8 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
             have = next && ok;
             ++it;
           }
+          // every commit has arrived before the block ends (pass 1 has no other wait for the last)
+          if (!first) mbar_wait(&pv_done[(it - 1) % kStages], ((it - 1) / kStages) & 1, abort, L.err);
           mbar_arrive(&pv_done[it % kStages]);         // the end mark's slot
           ++it;
         }
@@ -848,7 +850,7 @@ cudaError_t setup_cache_attn_tc() {
 cudaError_t launch_cache_attn_tc(const CacheAttnLaunch& L, cudaStream_t st) {
   // Blocks per (sequence, head): one wave, as long as each scans a round or so.
   int cs = 1;
-  while (cs < kMaxCluster && 2 * cs * L.B * L.H_kv <= L.num_sms && cs * 16 <= L.c.max_pages) cs *= 2;
+  while (cs < kMaxCluster && 2ll * cs * L.B * L.H_kv <= L.num_sms && cs * 16 <= L.c.max_pages) cs *= 2;
   const int rows = L.H / L.H_kv * L.n;
   if (L.n == 1) {
     if (rows <= 16) return launch<16, false>(L, cs, st);
