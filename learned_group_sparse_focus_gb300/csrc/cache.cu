@@ -452,7 +452,7 @@ cudaError_t launch_cache_append(const CacheAppendLaunch& L, int dtype, cudaStrea
 cudaError_t launch_cache_evict(const CacheEvictLaunch& L, cudaStream_t st) {
   // Blocks per (sequence, head): one wave, as long as each has kSelRun slots.
   int cs = 1;
-  while (cs < kSelCluster && 2 * cs * L.B * L.H_kv <= L.num_sms && 2 * cs * kSelRun <= L.src.max_pages * kPage) cs *= 2;
+  while (cs < kSelCluster && 2ll * cs * L.B * L.H_kv <= L.num_sms && 2 * cs * kSelRun <= L.src.max_pages * kPage) cs *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(cs, L.H_kv, L.B);
   cfg.blockDim = dim3(kSelThreads);

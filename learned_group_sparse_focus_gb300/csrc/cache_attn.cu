@@ -730,7 +730,7 @@ cudaError_t launch_cache_attn(const CacheAttnLaunch& L, int dtype, cudaStream_t 
   const int fit = L.num_sms * (L.H / L.H_kv * L.n > 8 ? 1 : 2);
   int cs = 1;
   while (cs < kMaxCluster && cs * kWarps < L.c.max_pages) {
-    const int blocks = 2 * cs * L.B * L.H_kv;
+    const long long blocks = 2ll * cs * L.B * L.H_kv;
     if (blocks > fit && (cs > 2 || blocks > 2 * fit || L.c.max_pages < 2 * cs * kWarps * 16)) break;
     cs *= 2;
   }
