@@ -477,7 +477,8 @@ FOCUS_API size_t focus_cache_workspace_bytes(const focus_params_t* p, const focu
  * values are stored as +-448 * scale, NaN as NaN; a slot's mass starts at 0.
  *   K, V [B, H_kv, n, d] dtype of p;  gid [B, A, n] int32;  n_new [B] int32 or NULL;
  *   len_out [B, H_kv], next_out [B] int32: the new counts; may be cache->len and
- *   cache->next (the counts are written after every block has read them).
+ *   cache->next (the counts are written after every block has read them), not each
+ *   other nor the other's source.
  * d in {64, 128}.  Pages must belong to one sequence.  A sequence for which a
  * head's slots would not fit max_pages, or whose next would pass 2^31 - 1, is
  * left as it was and flagged as FOCUS_ERR_BAD_CACHE in the device error word,
@@ -496,8 +497,10 @@ FOCUS_API focus_status_t focus_cache_append(const focus_params_t* p, const void*
  *   Q, O [B, H, n, d] dtype of p, n <= FOCUS_CACHE_MAX_QUERY;
  *   gid [B, A, n] int32;  n_new [B] int32 or NULL as in focus_cache_append;
  *   lse_opt [B, H, n] fp32 or NULL.
- * A token that keeps no slot gets O = 0 and lse = -infinity.  Rows t >= n_new[b]
- * of O and lse_opt stay as they were.  accumulate != 0 adds to mass[slot] the
+ * A token that keeps no slot gets O = 0 and lse = -infinity; a query row with an
+ * infinite or NaN element gets NaN; a NaN code reaches only the rows that keep it.
+ * Logits are fp32 and belong within +-1e29 (below that a slot counts as masked).
+ * Rows t >= n_new[b] of O and lse_opt stay as they were.  accumulate != 0 adds to mass[slot] the
  * softmax weights that the slot received, summed over the new tokens and the
  * query heads of its key/value head in a fixed order.  Sums are fp32.  q enters
  * the products in two parts: bf16's 8 bits whole (elements below 2^-15 of the

@@ -1138,6 +1138,7 @@ focus_status_t focus_cache_append(const focus_params_t* p, const void* K, const 
   for (const void* x : all)
     if (!x || !aligned16(x)) return FOCUS_ERR_INVALID_ARG;
   if (!aligned16(n_new)) return FOCUS_ERR_INVALID_ARG;
+  if (len_out == next_out || len_out == cache->next || next_out == cache->len) return FOCUS_ERR_INVALID_ARG;
   if (focus_status_t s = ensure_setup()) return s;
   CacheAppendLaunch L{K, V, gid, n_new, *cache, len_out, next_out, p->B, p->H_kv, p->n, p->d, p->A, p->K,
                       at<int>(ws, 64), at<int>(ws, 0)};

@@ -199,6 +199,16 @@ def test_eviction_and_accumulation_arguments(fz):
                                          None, 1, 256, 1 << 40, None) == 1
 
 
+def test_append_counts_that_overlap_are_refused(fz):
+    p, lib, c = _params(fz), fz.lib(), _struct(fz)
+
+    def append(len_out, next_out):
+        return lib.focus_cache_append(ctypes.byref(p), 1 << 27, 1 << 27, 1 << 27, None, ctypes.byref(c), len_out,
+                                      next_out, 1 << 26, 1 << 40, None)
+
+    assert append(1 << 28, 1 << 28) == append(c.next, 1 << 28) == append(1 << 28, c.len) == append(c.next, c.len) == 1
+
+
 def test_cache_struct_matches_the_header(fz):
     assert ctypes.sizeof(fz.CacheStruct) == 10 * 8 + 2 * 4
     assert fz.lib().focus_status_string(7) == b"cache page, length or position out of range"
