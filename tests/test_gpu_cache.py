@@ -462,6 +462,51 @@ def test_long_cache_positions_near_the_limit(fz):
         _check_attention(fz, c, Q, np.array([[[0, 1]]], np.int32), 2, w, "bf16")
 
 
+@pytest.mark.parametrize("H,T", [(4, 1), (8, 4)])
+def test_pages_past_four_gigabytes_of_a_pool(fz, H, T):
+    """The same calls over the last pages of a 5 GB pool and over a small pool: same bits."""
+    import torch
+    B, H_kv, d, K, w, n = 2, 2, 128, 3, 20, 700
+    p = fz.make_params(B, H, H_kv, n, d, 64, 64, K, 1, w)
+    q = fz.make_params(B, H, H_kv, T, d, 64, 64, K, 1, w)
+    rng = np.random.default_rng(H)
+    bf, mp = torch.bfloat16, -(-(n + T) // 64)
+    k, v = (_dev(_rows(rng, (B, H_kv, n, d), "bf16"), bf) for _ in range(2))
+    k1, v1 = (_dev(_rows(rng, (B, H_kv, T, d), "bf16"), bf) for _ in range(2))
+    Q = _dev(_rows(rng, (B, H, T, d), "bf16", 0.3), bf)
+    gid, gid1 = (_dev(rng.integers(0, K, (B, 1, m)).astype(np.int32)) for m in (n, T))
+    outs = []
+    for pages in (64, 5 * 2 ** 30 // (H_kv * 64 * d)):
+        def pool(shape, dtype):
+            return torch.zeros((pages, H_kv) + shape, dtype=dtype, device="cuda")
+
+        part = dict(k=pool((64, d), torch.uint8), v=pool((64, d), torch.uint8), k_scale=pool((), torch.float32),
+                    v_scale=pool((), torch.float32), pos=pool((64,), torch.int32), gid=pool((64,), torch.int16),
+                    mass=pool((64,), torch.float32))
+
+        def cache(last):
+            table = torch.arange(last - B * mp, last, dtype=torch.int32, device="cuda").flip(0).reshape(B, mp)
+            return fz.Cache(**part, table=table, len=torch.zeros((B, H_kv), dtype=torch.int32, device="cuda"),
+                            next=torch.zeros((B,), dtype=torch.int32, device="cuda"))
+
+        src, dst = cache(pages), cache(pages - 30)
+        ws = fz.alloc_workspace_cache(p, src)
+        fz.focus_cache_append(p, k, v, gid, src, ws)
+        fz.focus_cache_append(q, k1, v1, gid1, src, ws)
+        O, lse = torch.zeros_like(Q), torch.zeros(Q.shape[:3], device="cuda")
+        fz.focus_cache_attention_fwd(q, Q, gid1, src, O, lse, ws, accumulate=True)
+        fz.focus_cache_evict(q, 200, 30, src, dst, ws)
+        O2 = torch.zeros_like(Q)
+        fz.focus_cache_attention_fwd(q, Q, gid1, dst, O2, None, ws)
+        assert fz.focus_check_errors(ws) == 0
+        tail = {m: x[pages - 60:].cpu() for m, x in part.items()}
+        outs.append([O.float().cpu(), lse.cpu(), O2.float().cpu(), src.len.cpu(), dst.len.cpu(), *tail.values()])
+        if len(outs) == 2:                               # nothing was written below those pages
+            assert not any(part[m][:pages - 60].view(-1)[::7].any() for m in ("k", "v", "k_scale", "pos"))
+    assert outs[0][0].abs().max() > 0
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
 # --------------------------------------------------------------- eviction ---
 
 @pytest.mark.parametrize("H_kv,d,lens,budget,recent,ties", [
