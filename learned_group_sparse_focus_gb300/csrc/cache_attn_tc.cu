@@ -48,7 +48,7 @@ struct TcCfg {
   // scan warps and the one that issues the products.
   static constexpr int kParts = R == 64 ? 4 : 2, kSoftWarps = 4 * kParts, kScanWarps = R == 64 ? 3 : 7,
                        kMmaWarp = kSoftWarps + kScanWarps, kThreads = (kMmaWarp + 1) * 32;
-  static constexpr int kStages = R == 64 ? 2 : 3;
+  static constexpr int kStages = 3;
   // A scan round: kSlots slots a lane, so kPages pages a warp; the list holds what a
   // round can add to a tile and the tiles in flight.
   static constexpr int kSlots = 4, kPages = 2, kRound = kPages * kScanWarps;
@@ -59,9 +59,12 @@ struct TcCfg {
   static constexpr int kEntryBytes = kMulti ? 16 : 8;
   // byte offsets in dynamic shared memory
   static constexpr int kK = 0, kV = kK + kStages * kTileBytes, kQ = kV + kStages * kTileBytes, kP = kQ + 2 * R * kD,
-                       kInbox = kP + 2 * kPBytes, kListAt = kInbox + (R > kMaxCluster ? R : kMaxCluster) * kD * 4,
-                       kIds = kListAt + kList * kEntryBytes, kTable = kIds + 2 * kScanWarps * kAhead * kPage * 2,
+                       kListAt = kP + 2 * kPBytes, kIds = kListAt + kList * kEntryBytes, kTable = kIds + 2 * kScanWarps * kAhead * kPage * 2,
                        kSmem = kTable + (kMulti ? kCacheTableGroups * 8 : 0) + 1024;   // + alignment
+  // The partials' inbox lies over P: a block writes into another only when that one's
+  // tiles are done.
+  static constexpr int kInbox = kP;
+  static_assert((R > kMaxCluster ? R : kMaxCluster) * kD * 4 <= 2 * kPBytes, "inbox does not fit");
   static constexpr int kCols = 8 * R;                          // TMEM: S twice, O
 };
 
@@ -134,6 +137,14 @@ __device__ __forceinline__ void split_e5m2(uint32_t h, uint32_t& p12, uint32_t& 
   p34 = __byte_perm(r2, r3, 0x7351);
 }
 
+// mbar_wait that reads the clock only after a few tries (the read costs as much as most
+// of these waits).
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) return true;
+  return mbar_wait(bar, parity, abort, err);
+}
+
 __device__ __forceinline__ uint64_t bits_from(int k) {   // bits k ... 63
   return k >= 64 ? 0ull : ~0ull << max(k, 0);
 }
@@ -182,7 +193,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
   if (threadIdx.x == 0) {
     s_abort_word = 0;
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&k_full[i], kScanWarps * 32);
+      mbar_init(&k_full[i], kScanWarps * 32 + 1);
       mbar_init(&v_full[i], kScanWarps * 32);
       mbar_init(&qk_done[i], 1);
       mbar_init(&pv_done[i], 1);
@@ -214,7 +225,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
   auto meet = [&](uint64_t* bar, uint32_t& phase) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
-    mbar_wait(bar, phase++ & 1, abort, L.err);
+    wait(bar, phase++ & 1, abort, L.err);
   };
   uint32_t it = 0;                                     // slots (tiles and end marks) so far, the same in every role
 
@@ -326,6 +337,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           entry = entry_of(0);
           fetch(0);
         }
+        bool unmet = false;                            // rounds since the warps last met (the same in all)
         auto scan_round = [&]() {
           if (x % kAhead == 0) {                       // a new batch: it becomes current, the next one is fetched
             lane_page = next_page;
@@ -411,44 +423,54 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
               ++at;
             }
           x += kPages;
+          unmet = true;
         };
         // the round's first page lies behind the end (the same in all scan warps)
         auto scanned = [&]() { return !relist || rank + x / kPages * kRound * cs >= pages; };
+        // Copies of a tile: four rows a step and warp.  A step moves on by 4 kScanWarps rows
+        // (a multiple of 4, so only bit 2 of the row's swizzle alternates).
+        constexpr int kSteps = (kTile / 4 + kScanWarps - 1) / kScanWarps;
+        const int row0 = v * 4 + lane / 8;
+        const uint32_t piece = lane % 8 * 16, to_even = row0 * kD + (lane % 8 ^ (row0 & 7)) * 16,
+                       flip = kScanWarps & 1 ? 64 : 0;
         bool ok = true;
         for (int tile = 0;; ++tile, ++it) {
           if (tile == 0)
             while (entries < kTile && !scanned()) scan_round();
-          meet(&scan_bar, scan_phase);                 // every warp's entries are in the list
+          if (unmet) meet(&scan_bar, scan_phase);      // every warp's entries are in the list
+          unmet = false;
           const int cnt = min(kTile, entries - tile * kTile);
           // K's stage is free once its products are done, V's only after the weights' products
           const int st = it % kStages;
           const uint32_t parity = (it / kStages + 1) & 1;
-          if (v == 0 && lane == 0) s_cnt[it & 7] = max(cnt, 0);
-          size_t from[(kTile / 4 + kScanWarps - 1) / kScanWarps];
-          uint32_t to[(kTile / 4 + kScanWarps - 1) / kScanWarps];
+          uint32_t from[kSteps];
 #pragma unroll
-          for (int y = 0; y < (kTile / 4 + kScanWarps - 1) / kScanWarps; ++y) {   // four rows a step
-            const int r = (y * kScanWarps + v) * 4 + lane / 8, idx = (tile * kTile + r) & (kList - 1);
-            const bool there = r < cnt;
-            const uint32_t row = there ? static_cast<uint32_t>(kMulti ? list4[idx].x : list2[idx].x) : 0u;
-            from[y] = static_cast<size_t>(row) * kD + lane % 8 * 16;
-            to[y] = there ? r * kD + (lane % 8 ^ (r & 7)) * 16 : ~0u;
+          for (int y = 0; y < kSteps; ++y) {
+            const int idx = (tile * kTile & (kList - 1)) + row0 + y * 4 * kScanWarps;
+            from[y] = row0 + y * 4 * kScanWarps < cnt ? static_cast<uint32_t>(kMulti ? list4[idx].x : list2[idx].x) : 0u;
           }
-          if (it >= kStages) ok = ok && mbar_wait(&qk_done[st], parity, abort, L.err);
-          if (cnt > 0 && ok) {
+          auto copy = [&](uint32_t to, const uint8_t* pool) {
 #pragma unroll
-            for (int y = 0; y < (kTile / 4 + kScanWarps - 1) / kScanWarps; ++y)
-              if (to[y] != ~0u) cp_async_16(smem + C::kK + st * kTileBytes + to[y], L.c.k + from[y], 16);
+            for (int y = 0; y < kSteps; ++y)
+              if (row0 + y * 4 * kScanWarps < cnt)
+                cp_async_16(smem + (to ^ (y & 1 ? flip : 0)) + y * 4 * kScanWarps * kD,
+                            pool + static_cast<size_t>(from[y]) * kD + piece, 16);
+          };
+          if (it >= kStages) ok = ok && wait(&qk_done[st], parity, abort, L.err);
+          if (v == 0 && lane == 0) {
+            s_cnt[it & 7] = max(cnt, 0);
+            mbar_arrive(&k_full[st]);                  // its own arrival: the copies' do not order this store
+          }
+          if (cnt > 0 && ok) {
+            copy(C::kK + st * kTileBytes + to_even, L.c.k);
             cp_async_arrive(&k_full[st]);
           } else {
             mbar_arrive(&k_full[st]);
           }
           while (entries < (tile + 2) * kTile && !scanned()) scan_round();       // the next tile's slots
-          if (it >= kStages) ok = ok && mbar_wait(&pv_done[st], parity, abort, L.err);
+          if (it >= kStages) ok = ok && wait(&pv_done[st], parity, abort, L.err);
           if (cnt > 0 && ok && pass == 0) {
-#pragma unroll
-            for (int y = 0; y < (kTile / 4 + kScanWarps - 1) / kScanWarps; ++y)
-              if (to[y] != ~0u) cp_async_16(smem + C::kV + st * kTileBytes + to[y], L.c.v + from[y], 16);
+            copy(C::kV + st * kTileBytes + to_even, L.c.v);
             cp_async_arrive(&v_full[st]);
           } else {
             mbar_arrive(&v_full[st]);
@@ -541,7 +563,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
         int tile = 0;
         for (;; ++tile, ++it) {
           const int st = it % kStages, buf = it & 1;
-          const bool ok = mbar_wait(&s_ready[buf], (it >> 1) & 1, abort, L.err);
+          const bool ok = wait(&s_ready[buf], (it >> 1) & 1, abort, L.err);
           const int cnt = ok ? s_cnt[it & 7] : 0;
           if (__any_sync(~0u, cnt == 0)) {
             if (lane == 0) mbar_arrive(&p_ready[buf]);
@@ -663,7 +685,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
             meet(&part_bar[part], part_phase);
           }
           if (tile > 1)                                // P of the slot before the last one has been used
-            mbar_wait(&pv_done[(it - 2) % kStages], ((it - 2) / kStages) & 1, abort, L.err);
+            wait(&pv_done[(it - 2) % kStages], ((it - 2) / kStages) & 1, abort, L.err);
           const float vf = exp2_int(-static_cast<int8_t>(ex >> 8));
           uint32_t word[RH];
 #pragma unroll
@@ -692,7 +714,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           if (kMulti) {
             // A row that does not keep a key has weight 0 for it, and 0 * NaN would reach
             // that row: NaN codes leave the tile and mark the outputs that they reach.
-            mbar_wait(&v_full[st], (it / kStages) & 1, abort, L.err);
+            wait(&v_full[st], (it / kStages) & 1, abort, L.err);
             uint32_t any = 0;
             uint4* vrow = reinterpret_cast<uint4*>(smem + C::kV + st * kTileBytes + key * kD);
 #pragma unroll
