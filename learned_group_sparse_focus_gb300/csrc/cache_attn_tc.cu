@@ -45,15 +45,17 @@ constexpr float kNoRef = -1e30f;       // reference of a row without kept slots
 template <int R, bool kMulti>
 struct TcCfg {
   // Weight warps: four TMEM lane quadrants times kParts parts of the rows; then the
-  // scan warps and the one that issues the products.
-  static constexpr int kParts = R == 64 ? 4 : 2, kSoftWarps = 4 * kParts, kScanWarps = R == 64 ? 3 : 7,
-                       kMmaWarp = kSoftWarps + kScanWarps, kThreads = (kMmaWarp + 1) * 32;
+  // scan warps, those that gather, and the one that issues the products.
+  static constexpr int kParts = R == 64 ? 4 : 2, kSoftWarps = 4 * kParts, kScanWarps = R == 64 ? 3 : 7, kGatherWarps = 4,
+                       kGatherWarp = kSoftWarps + kScanWarps, kMmaWarp = kGatherWarp + kGatherWarps,
+                       kThreads = (kMmaWarp + 1) * 32;
   static constexpr int kStages = 3;
+  static constexpr int kListed = 4;                            // tiles listed ahead of the weights
   // A scan round: kSlots slots a lane, so kPages pages a warp; the list holds what a
-  // round can add to a tile and the tiles in flight.
+  // round can add to a tile and the tiles listed.
   static constexpr int kSlots = 4, kPages = 2, kRound = kPages * kScanWarps;
   static constexpr int kList = R == 64 ? 1024 : 2048;          // entries of the block's list of kept slots
-  static_assert(kList >= kRound * kPage + (kStages + 2) * kTile, "list too short");
+  static_assert(kList >= kRound * kPage + kListed * kTile && kStages < kListed, "list too short");
   static constexpr int kRowBytes = R >= 32 ? 128 : 4 * R;      // P's bytes of a key, per chunk of N
   static constexpr int kPBytes = kTile * 4 * R;
   static constexpr int kEntryBytes = kMulti ? 16 : 8;
@@ -156,16 +158,17 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
   constexpr int kStages = C::kStages, RH = R / C::kParts, kList = C::kList, kSlots = C::kSlots, kPages = C::kPages;
   constexpr int kRound = C::kRound, kLanes = kPage / kSlots;   // lanes a page
   constexpr int kParts = C::kParts, kSoftWarps = C::kSoftWarps, kMmaWarp = C::kMmaWarp, kThreads = C::kThreads,
-                kScanWarps = C::kScanWarps;
+                kScanWarps = C::kScanWarps, kGatherWarp = C::kGatherWarp, kGatherWarps = C::kGatherWarps, kListed = C::kListed;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t k_full[kStages], v_full[kStages], qk_done[kStages], pv_done[kStages], s_ready[2], p_ready[2];
+  __shared__ uint64_t listed[kListed], used[kListed];  // a tile's entries are in the list; the weight warps have read them
   __shared__ uint64_t part_bar[kParts], soft_bar, scan_bar; // the four warps of a part; all weight warps; the scan's
   __shared__ int s_found[2][kScanWarps];               // slots that a scan warp lists in a round
   __shared__ int s_grow[kParts][3];                    // some reference of the part moves in this tile
   __shared__ int s_cnt[8];                             // keys of a tile (by slot modulo 8); 0 ends a pass
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort_word;
-  __shared__ __align__(16) float s_factor[R], s_minus[R], s_lse[R];   // s_minus: the references, negated
+  __shared__ __align__(16) float s_factor[R], s_minus[R], s_lse[R];   // the references and log2 sums, negated
   __shared__ float s_top[4][R], s_l[4][R];             // per lane quadrant
   __shared__ float s_w[2][kParts][kTile];              // slots' weights by part (pass 1)
   float (*s_weight)[R] = reinterpret_cast<float (*)[R]>(&s_w[0][0][0]);   // weight of a block's partial in a row (join)
@@ -193,10 +196,14 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
   if (threadIdx.x == 0) {
     s_abort_word = 0;
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&k_full[i], kScanWarps * 32 + 1);
-      mbar_init(&v_full[i], kScanWarps * 32);
+      mbar_init(&k_full[i], kGatherWarps * 32);
+      mbar_init(&v_full[i], kGatherWarps * 32);
       mbar_init(&qk_done[i], 1);
       mbar_init(&pv_done[i], 1);
+    }
+    for (int i = 0; i < kListed; ++i) {
+      mbar_init(&listed[i], kScanWarps);
+      mbar_init(&used[i], kSoftWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_ready[i], 1);
@@ -293,8 +300,8 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
 
     int entries = 0, tiles = 0;                        // load warp: listed slots; softmax warps: tiles of pass 0
     for (int pass = 0; pass < (L.accumulate ? 2 : 1); ++pass) {
-      if (warp >= kSoftWarps && warp < kMmaWarp) {
-        // ------------------------------------------------ scan and gathers
+      if (warp >= kSoftWarps && warp < kGatherWarp) {
+        // ------------------------------------------------ scan
         // Pages rank, rank + cs, ... in rounds of kRound, kPages a warp: its page x is
         // number x / kPages * kRound + v * kPages + x % kPages of them.
         const int v = warp - kSoftWarps;
@@ -337,7 +344,6 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           entry = entry_of(0);
           fetch(0);
         }
-        bool unmet = false;                            // rounds since the warps last met (the same in all)
         auto scan_round = [&]() {
           if (x % kAhead == 0) {                       // a new batch: it becomes current, the next one is fetched
             lane_page = next_page;
@@ -423,59 +429,61 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
               ++at;
             }
           x += kPages;
-          unmet = true;
         };
         // the round's first page lies behind the end (the same in all scan warps)
         auto scanned = [&]() { return !relist || rank + x / kPages * kRound * cs >= pages; };
-        // Copies of a tile: four rows a step and warp.  A step moves on by 4 kScanWarps rows
-        // (a multiple of 4, so only bit 2 of the row's swizzle alternates).
-        constexpr int kSteps = (kTile / 4 + kScanWarps - 1) / kScanWarps;
-        const int row0 = v * 4 + lane / 8;
-        const uint32_t piece = lane % 8 * 16, to_even = row0 * kD + (lane % 8 ^ (row0 & 7)) * 16,
-                       flip = kScanWarps & 1 ? 64 : 0;
-        bool ok = true;
         for (int tile = 0;; ++tile, ++it) {
-          if (tile == 0)
-            while (entries < kTile && !scanned()) scan_round();
-          if (unmet) meet(&scan_bar, scan_phase);      // every warp's entries are in the list
-          unmet = false;
-          const int cnt = min(kTile, entries - tile * kTile);
-          // K's stage is free once its products are done, V's only after the weights' products
+          if (it >= kListed) wait(&used[it % kListed], (it / kListed + 1) & 1, abort, L.err);
+          while (entries < (tile + 1) * kTile && !scanned()) scan_round();
+          const int cnt = max(min(kTile, entries - tile * kTile), 0);
+          if (v == 0 && lane == 0) s_cnt[it & 7] = cnt;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&listed[it % kListed]);       // with every warp's: the tile's entries are there
+          if (cnt == 0 || *abort) {
+            ++it;
+            break;
+          }
+        }
+        cp_async_wait_all();
+      } else if (warp >= kGatherWarp && warp < kMmaWarp) {
+        // ------------------------------------------------ gathers of kept rows
+        // Four rows a step and warp (a step is a multiple of 8 rows on: one swizzle for
+        // all).  K's stage is free once its products are done, V's once the weights' are.
+        constexpr int kStep = 4 * kGatherWarps, kSteps = kTile / kStep;
+        static_assert(kStep % 8 == 0, "swizzle");
+        const int row0 = (warp - kGatherWarp) * 4 + lane / 8;
+        const uint32_t to_row = row0 * kD + (lane % 8 ^ (row0 & 7)) * 16, piece = lane % 8 * 16;
+        for (int tile = 0;; ++tile, ++it) {
           const int st = it % kStages;
           const uint32_t parity = (it / kStages + 1) & 1;
+          const bool ok = __all_sync(~0u, wait(&listed[it % kListed], (it / kListed) & 1, abort, L.err));
+          const int cnt = ok ? s_cnt[it & 7] : 0;
+          const int base = (tile * kTile & (kList - 1)) + row0;
           uint32_t from[kSteps];
 #pragma unroll
-          for (int y = 0; y < kSteps; ++y) {
-            const int idx = (tile * kTile & (kList - 1)) + row0 + y * 4 * kScanWarps;
-            from[y] = row0 + y * 4 * kScanWarps < cnt ? static_cast<uint32_t>(kMulti ? list4[idx].x : list2[idx].x) : 0u;
-          }
-          auto copy = [&](uint32_t to, const uint8_t* pool) {
+          for (int y = 0; y < kSteps; ++y)
+            from[y] = row0 + y * kStep < cnt ? static_cast<uint32_t>(kMulti ? list4[base + y * kStep].x : list2[base + y * kStep].x) : 0u;
+          auto copy = [&](uint8_t* to, const uint8_t* pool) {
 #pragma unroll
             for (int y = 0; y < kSteps; ++y)
-              if (row0 + y * 4 * kScanWarps < cnt)
-                cp_async_16(smem + (to ^ (y & 1 ? flip : 0)) + y * 4 * kScanWarps * kD,
-                            pool + static_cast<size_t>(from[y]) * kD + piece, 16);
+              if (row0 + y * kStep < cnt)
+                cp_async_16(to + to_row + y * kStep * kD, pool + static_cast<size_t>(from[y]) * kD + piece, 16);
           };
-          if (it >= kStages) ok = ok && wait(&qk_done[st], parity, abort, L.err);
-          if (v == 0 && lane == 0) {
-            s_cnt[it & 7] = max(cnt, 0);
-            mbar_arrive(&k_full[st]);                  // its own arrival: the copies' do not order this store
-          }
-          if (cnt > 0 && ok) {
-            copy(C::kK + st * kTileBytes + to_even, L.c.k);
+          if (it >= kStages) wait(&qk_done[st], parity, abort, L.err);
+          if (cnt > 0) {
+            copy(smem + C::kK + st * kTileBytes, L.c.k);
             cp_async_arrive(&k_full[st]);
           } else {
             mbar_arrive(&k_full[st]);
           }
-          while (entries < (tile + 2) * kTile && !scanned()) scan_round();       // the next tile's slots
-          if (it >= kStages) ok = ok && wait(&pv_done[st], parity, abort, L.err);
-          if (cnt > 0 && ok && pass == 0) {
-            copy(C::kV + st * kTileBytes + to_even, L.c.v);
+          if (it >= kStages) wait(&pv_done[st], parity, abort, L.err);
+          if (cnt > 0 && pass == 0) {
+            copy(smem + C::kV + st * kTileBytes, L.c.v);
             cp_async_arrive(&v_full[st]);
           } else {
             mbar_arrive(&v_full[st]);
           }
-          if (cnt <= 0 || *abort) {
+          if (cnt == 0 || *abort) {
             ++it;
             break;
           }
@@ -506,6 +514,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           };
           auto k_wait = [&](uint32_t slot) {
             ok = ok && mbar_wait_nap(&k_full[slot % kStages], (slot / kStages) & 1, abort, L.err);
+            ok = ok && mbar_wait(&listed[slot % kListed], (slot / kListed) & 1, abort, L.err);     // done: orders s_cnt
           };
           k_wait(it);
           bool have = scores(it);
@@ -519,6 +528,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
             const unsigned long long since = global_ns();
             while (ok && !asked && !mbar_test_wait(&p_ready[it & 1], (it >> 1) & 1)) {
               if (mbar_test_wait(&k_full[(it + 1) % kStages], ((it + 1) / kStages) & 1)) {
+                k_wait(it + 1);
                 next = scores(it + 1);
                 asked = true;
               } else {
@@ -527,7 +537,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
               }
             }
             ok = mbar_wait_nap(&p_ready[it & 1], (it >> 1) & 1, abort, L.err) && ok;
-            // (also in pass 1, without values: the scan warps arrive here once they have seen
+            // (also in pass 1, without values: the gathering warps arrive here once they have seen
             // pv_done of this stage's last slot, which must not complete twice before that)
             ok = ok && mbar_wait_nap(&v_full[st], (it / kStages) & 1, abort, L.err);
             if (pass == 0 && ok) {
@@ -549,7 +559,9 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           }
           // every commit has arrived before the block ends (pass 1 has no other wait for the last)
           if (!first) mbar_wait(&pv_done[(it - 1) % kStages], ((it - 1) / kStages) & 1, abort, L.err);
-          mbar_arrive(&pv_done[it % kStages]);         // the end mark's slot
+          // the end mark's slot, once the gathering warps have seen the stage's last one
+          mbar_wait_nap(&v_full[it % kStages], (it / kStages) & 1, abort, L.err);
+          mbar_arrive(&pv_done[it % kStages]);
           ++it;
         }
         it = __shfl_sync(~0u, it, 0);
@@ -557,16 +569,19 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
         // ------------------------------------------------ weights: one key a thread, a part of the rows
         const int quad = warp & 3, part = warp >> 2, key = quad * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-        float l[RH];
+        uint64_t l2[RH / 2];                           // row sums, in pairs
 #pragma unroll
-        for (int r = 0; r < RH; ++r) l[r] = 0.f;
+        for (int r = 0; r < RH / 2; ++r) l2[r] = f2_pack(0.f, 0.f);
         int tile = 0;
         for (;; ++tile, ++it) {
           const int st = it % kStages, buf = it & 1;
           const bool ok = wait(&s_ready[buf], (it >> 1) & 1, abort, L.err);
           const int cnt = ok ? s_cnt[it & 7] : 0;
           if (__any_sync(~0u, cnt == 0)) {
-            if (lane == 0) mbar_arrive(&p_ready[buf]);
+            if (lane == 0) {
+              mbar_arrive(&p_ready[buf]);
+              mbar_arrive(&used[it % kListed]);
+            }
             ++it;
             break;
           }
@@ -597,14 +612,28 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_ready[buf]);
-            float w = 0.f;
+            float w = 0.f, w1 = 0.f;
+            const uint64_t sixteenth = f2_pack(0.0625f, 0.0625f), kf2 = f2_pack(kf, kf);
 #pragma unroll
-            for (int r = 0; r < RH; ++r) {
-              const float s = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(hi[r])) * s_factor[part * RH + r];
-              if (mask >> r & 1) w += exp2_fast(fmaf(s, kf, -s_lse[part * RH + r]));
+            for (int r = 0; r < RH; r += 4) {
+              uint64_t f01, f23, m01, m23;
+              lds_f2x2(&s_factor[part * RH + r], f01, f23);
+              lds_f2x2(&s_lse[part * RH + r], m01, m23);
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                const uint64_t h2 = f2_pack(__uint_as_float(hi[r + e]), __uint_as_float(hi[r + e + 1]));
+                const uint64_t l2 = f2_pack(__uint_as_float(lo[r + e]), __uint_as_float(lo[r + e + 1]));
+                float d0, d1;
+                f2_unpack(f2_fma(f2_mul(f2_fma(l2, sixteenth, h2), e ? f23 : f01), kf2, e ? m23 : m01), d0, d1);
+                const float p0 = exp2_fast(d0), p1 = exp2_fast(d1);
+                w += mask >> (r + e) & 1 ? p0 : 0.f;
+                w1 += mask >> (r + e + 1) & 1 ? p1 : 0.f;
+              }
             }
+            w += w1;
             if (part) s_w[buf][part][key] = w;
             meet(&soft_bar, soft_phase);
+            if (lane == 0) mbar_arrive(&used[it % kListed]);
             if (!part && key < cnt) {
               for (int x = 1; x < kParts; ++x) w += s_w[buf][x][key];
               atomicAdd(L.c.mass + pool_row, w);       // the only addition to this slot in this round: its order cannot matter
@@ -660,8 +689,9 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
               const float was = -s_minus[rr];
               moved[r] = top > was + 15.f ? top - 10.f : was;
               f[r] = exp2_fast(was - moved[r]);
-              l[r] *= f[r];
             }
+#pragma unroll
+            for (int r = 0; r < RH; r += 2) l2[r / 2] = f2_mul(l2[r / 2], f2_pack(f[r], f[r + 1]));
             if (tile > 0) {
               mbar_wait(&pv_done[(it - 1) % kStages], ((it - 1) / kStages) & 1, abort, L.err);
               tc_fence_after();
@@ -687,6 +717,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           if (tile > 1)                                // P of the slot before the last one has been used
             wait(&pv_done[(it - 2) % kStages], ((it - 2) / kStages) & 1, abort, L.err);
           const float vf = exp2_int(-static_cast<int8_t>(ex >> 8));
+          const uint64_t vf2 = f2_pack(vf, vf);
           uint32_t word[RH];
 #pragma unroll
           for (int r = 0; r < RH; r += 4) {
@@ -697,8 +728,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
               float d0, d1;
               f2_unpack(f2_add(f2_pack(t[r + e], t[r + e + 1]), e ? m23 : m01), d0, d1);
               const float p0 = exp2_fast(d0), p1 = exp2_fast(d1);
-              l[r + e] = fmaf(p0, vf, l[r + e]);
-              l[r + e + 1] = fmaf(p1, vf, l[r + e + 1]);
+              l2[(r + e) / 2] = f2_fma(f2_pack(p0, p1), vf2, l2[(r + e) / 2]);
               const __half2 hp = __floats2half2_rn(p0, p1);
               split_e5m2(*reinterpret_cast<const uint32_t*>(&hp), word[r + e], word[r + e + 1]);
             }
@@ -720,10 +750,11 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 8 / kParts; ++c) {
               const uint4 u = vrow[(part * (8 / kParts) + c) ^ (key & 7)];
-              any |= __vcmpeq4(u.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(u.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
-                     __vcmpeq4(u.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(u.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              const uint32_t m = 0x7f7f7f7fu, one = 0x01010101u;       // a magnitude of 127 carries into the sign's bit
+              any |= ((u.x & m) + one) | ((u.y & m) + one);
+              any |= ((u.z & m) + one) | ((u.w & m) + one);
             }
-            if (any) {
+            if (any & 0x80808080u) {
               uint8_t* bytes = reinterpret_cast<uint8_t*>(vrow);
               const int4 e = list4[(tile * kTile + key) & (kList - 1)];
               const uint64_t keepers = key < cnt ? static_cast<uint32_t>(e.z) | static_cast<uint64_t>(static_cast<uint32_t>(e.w)) << 32 : 0ull;
@@ -739,14 +770,19 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_ready[buf]);
+          if (lane == 0) {
+            mbar_arrive(&p_ready[buf]);
+            mbar_arrive(&used[it % kListed]);
+          }
         }
         if (pass == 0) {
           // ---- the block's partial: every row's sum, and its part of O to the block that writes it
           tiles = tile;
 #pragma unroll
           for (int r = 0; r < RH; ++r) {
-            float x = l[r];
+            float l0, l1;
+            f2_unpack(l2[r / 2], l0, l1);
+            float x = r & 1 ? l1 : l0;
 #pragma unroll
             for (int y = 16; y > 0; y /= 2) x += __shfl_xor_sync(~0u, x, y);
             if (lane == 0) s_l[quad][part * RH + r] = x;
@@ -800,7 +836,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
         for (int x = 0; x < cs; ++x)
           if (s_all[x][r].y != 0.f) l += s_all[x][r].y * exp2f(s_all[x][r].x - M);
         const float lse = l != 0.f ? M + log2f(l) : -INFINITY;
-        s_lse[r] = l != 0.f ? lse : -kNoRef;
+        s_lse[r] = l != 0.f ? -lse : kNoRef;
         for (int x = 0; x < cs; ++x)
           s_weight[x][r] = s_all[x][r].y != 0.f ? exp2f(s_all[x][r].x - M) / l : 0.f;
         if (rank == 0 && L.lse && r < live)
