@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort_word;
   __shared__ __align__(16) float s_factor[R], s_minus[R], s_lse[R];   // the references and log2 sums, negated
-  __shared__ float s_top[4][R], s_l[4][R];             // per lane quadrant
+  __shared__ int s_top[4][R];                          // per lane quadrant, in integer order
+  __shared__ float s_l[4][R];
   __shared__ float s_w[2][kParts][kTile];              // slots' weights by part (pass 1)
   float (*s_weight)[R] = reinterpret_cast<float (*)[R]>(&s_w[0][0][0]);   // weight of a block's partial in a row (join)
   static_assert(sizeof(s_w) >= kMaxCluster * R * sizeof(float), "shared");
@@ -241,6 +242,47 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
     const int live = min(R, rows - r0);
     const int tokens = (r0 + live - 1) / G - t_lo + 1;
     const int gid0 = gids[t_lo];
+    // ---- the scan's state, and its first loads.  Pages rank, rank + cs, ... in rounds of
+    // kRound, kPages a warp: its page x is number x / kPages * kRound + v * kPages +
+    // x % kPages of them.
+    const int v = warp - kSoftWarps;
+    auto page_of = [&](int x) { return rank + (x / kPages * kRound + v * kPages + x % kPages) * cs; };
+    auto entry_of = [&](int x) {                   // table entry of the warp's page x + lane, unchecked
+      const int j = page_of(x + lane);
+      return lane < kAhead && j < L.c.max_pages ? L.c.table[static_cast<size_t>(b) * L.c.max_pages + j] : -1;
+    };
+    uint8_t* ids = smem + C::kIds + v * 2 * kAhead * kPage * 2;      // two batches of kAhead pages
+    int next_page = -1, next_exps = 0, lane_page = -1, lane_exps = 0, entry = 0;
+    auto fetch = [&](int x) {                      // starts on pages x ... x + kAhead - 1, and on the table behind them
+      next_page = -1;
+      next_exps = 0;
+      if (lane < kAhead && page_of(x + lane) < pages) {
+        next_page = entry;
+        if (entry < 0 || entry >= L.c.n_pages) {
+          atomicOr(L.err, kErrBadCache);
+          next_page = -1;
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int y = 0; y < kAhead * kPage * 2 / 16 / 32; ++y) {
+        const int page = __shfl_sync(~0u, next_page, y * 4 + lane / 8);
+        if (page >= 0)
+          cp_async_16(ids + (x / kAhead & 1) * kAhead * kPage * 2 + y * 512 + lane * 16,
+                      L.c.gid + (static_cast<size_t>(page) * L.H_kv + h) * kPage + lane % 8 * 8, 16);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (next_page >= 0) {
+        const size_t plane = static_cast<size_t>(next_page) * L.H_kv + h;
+        next_exps = (scale_exp(L.c.k_scale[plane]) & 0xff) | (scale_exp(L.c.v_scale[plane]) & 0xff) << 8;
+      }
+      entry = entry_of(x + kAhead);
+    };
+    const bool scans = warp >= kSoftWarps && warp < kGatherWarp;
+    if (scans) {
+      entry = entry_of(0);
+      fetch(0);
+    }
     // ---- queries: two e4m3 parts, a warp a row; references, masks
     if (warp < kSoftWarps) {
       uint2 u[R / kSoftWarps];
@@ -300,49 +342,16 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
 
     int entries = 0, tiles = 0;                        // load warp: listed slots; softmax warps: tiles of pass 0
     for (int pass = 0; pass < (L.accumulate ? 2 : 1); ++pass) {
-      if (warp >= kSoftWarps && warp < kGatherWarp) {
+      if (scans) {
         // ------------------------------------------------ scan
-        // Pages rank, rank + cs, ... in rounds of kRound, kPages a warp: its page x is
-        // number x / kPages * kRound + v * kPages + x % kPages of them.
-        const int v = warp - kSoftWarps;
-        auto page_of = [&](int x) { return rank + (x / kPages * kRound + v * kPages + x % kPages) * cs; };
-        auto entry_of = [&](int x) {                   // table entry of the warp's page x + lane, unchecked
-          const int j = page_of(x + lane);
-          return lane < kAhead && j < L.c.max_pages ? L.c.table[static_cast<size_t>(b) * L.c.max_pages + j] : -1;
-        };
-        uint8_t* ids = smem + C::kIds + v * 2 * kAhead * kPage * 2;      // two batches of kAhead pages
-        int next_page = -1, next_exps = 0, lane_page = -1, lane_exps = 0, entry = 0;
-        auto fetch = [&](int x) {                      // starts on pages x ... x + kAhead - 1, and on the table behind them
-          next_page = -1;
-          next_exps = 0;
-          if (lane < kAhead && page_of(x + lane) < pages) {
-            next_page = entry;
-            if (entry < 0 || entry >= L.c.n_pages) {
-              atomicOr(L.err, kErrBadCache);
-              next_page = -1;
-            }
-          }
-          __syncwarp();
-#pragma unroll
-          for (int y = 0; y < kAhead * kPage * 2 / 16 / 32; ++y) {
-            const int page = __shfl_sync(~0u, next_page, y * 4 + lane / 8);
-            if (page >= 0)
-              cp_async_16(ids + (x / kAhead & 1) * kAhead * kPage * 2 + y * 512 + lane * 16,
-                          L.c.gid + (static_cast<size_t>(page) * L.H_kv + h) * kPage + lane % 8 * 8, 16);
-          }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          if (next_page >= 0) {
-            const size_t plane = static_cast<size_t>(next_page) * L.H_kv + h;
-            next_exps = (scale_exp(L.c.k_scale[plane]) & 0xff) | (scale_exp(L.c.v_scale[plane]) & 0xff) << 8;
-          }
-          entry = entry_of(x + kAhead);
-        };
         const bool relist = pass == 0 || entries > kList;  // else the whole list is still there
         int x = 0;                                     // the warp's next page
         if (relist) {
           entries = 0;
-          entry = entry_of(0);
-          fetch(0);
+          if (pass > 0) {
+            entry = entry_of(0);
+            fetch(0);
+          }
         }
         auto scan_round = [&]() {
           if (x % kAhead == 0) {                       // a new batch: it becomes current, the next one is fetched
@@ -669,49 +678,45 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           meet(&part_bar[part], part_phase);
           if (s_grow[part][it % 3]) {
             // some row's reference moves, by the row's own weights: rows do not touch each
-            // other.  A warp none of whose keys passes the limit has no say in the maximum.
+            // other.  Lane r takes row r (the same result in the part's four warps).
+            int top = INT_MIN;
 #pragma unroll
             for (int r = 0; r < RH; ++r) {
-              float top = -INFINITY;
-              if (__any_sync(~0u, t[r] + s_minus[part * RH + r] > 15.f)) {
-                const int u = __float_as_int(t[r]), order = u ^ (u >> 31 & 0x7fffffff);   // floats' order as integers
-                const int m = __reduce_max_sync(~0u, t[r] == t[r] ? order : INT_MIN);
-                top = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
-              }
-              if (lane == 0) s_top[quad][part * RH + r] = top;
+              const int u = __float_as_int(t[r]), order = u ^ (u >> 31 & 0x7fffffff);   // floats' order as integers
+              const int m = __reduce_max_sync(~0u, t[r] == t[r] ? order : INT_MIN);
+              if (lane == r) top = m;
             }
+            if (lane < RH) s_top[quad][part * RH + lane] = top;
             meet(&part_bar[part], part_phase);
-            float f[RH], moved[RH];
-#pragma unroll
-            for (int r = 0; r < RH; ++r) {
-              const int rr = part * RH + r;
-              const float top = fmaxf(fmaxf(s_top[0][rr], s_top[1][rr]), fmaxf(s_top[2][rr], s_top[3][rr]));
-              const float was = -s_minus[rr];
-              moved[r] = top > was + 15.f ? top - 10.f : was;
-              f[r] = exp2_fast(was - moved[r]);
+            float moved = 0.f, f = 1.f;
+            if (lane < RH) {
+              const int rr = part * RH + lane;
+              const int m = max(max(s_top[0][rr], s_top[1][rr]), max(s_top[2][rr], s_top[3][rr]));
+              const float was = -s_minus[rr], highest = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
+              moved = highest > was + 15.f ? highest - 10.f : was;
+              f = exp2_fast(was - moved);
             }
 #pragma unroll
-            for (int r = 0; r < RH; r += 2) l2[r / 2] = f2_mul(l2[r / 2], f2_pack(f[r], f[r + 1]));
+            for (int r = 0; r < RH; r += 2)
+              l2[r / 2] = f2_mul(l2[r / 2], f2_pack(__shfl_sync(~0u, f, r), __shfl_sync(~0u, f, r + 1)));
             if (tile > 0) {
               mbar_wait(&pv_done[(it - 1) % kStages], ((it - 1) / kStages) & 1, abort, L.err);
               tc_fence_after();
 #pragma unroll
               for (int y = 0; y < RH / 2; ++y) {       // two rows, eight columns
-                if (f[2 * y] == 1.f && f[2 * y + 1] == 1.f) continue;
+                const float f0 = __shfl_sync(~0u, f, 2 * y), f1 = __shfl_sync(~0u, f, 2 * y + 1);
+                if (f0 == 1.f && f1 == 1.f) continue;
                 uint32_t v[8];
                 tmem_ld<8>(tmem_o + lanes + part * 4 * RH + y * 8, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int x = 0; x < 8; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f[2 * y + (x >> 1 & 1)]);
+                for (int x = 0; x < 8; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * (x >> 1 & 1 ? f1 : f0));
                 tmem_st8(tmem_o + lanes + part * 4 * RH + y * 8, v);
               }
               tmem_wait_st();
             }
             meet(&part_bar[part], part_phase);         // every warp has read the old references
-            if (quad == 0 && lane == 0) {
-#pragma unroll
-              for (int r = 0; r < RH; ++r) s_minus[part * RH + r] = -moved[r];
-            }
+            if (quad == 0 && lane < RH) s_minus[part * RH + lane] = -moved;
             meet(&part_bar[part], part_phase);
           }
           if (tile > 1)                                // P of the slot before the last one has been used
