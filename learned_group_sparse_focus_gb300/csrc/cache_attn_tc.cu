@@ -46,14 +46,14 @@ template <int R, bool kMulti>
 struct TcCfg {
   // Weight warps: four TMEM lane quadrants times kParts parts of the rows; then the
   // scan warps, those that gather, and the one that issues the products.
-  static constexpr int kParts = R == 64 ? 4 : 2, kSoftWarps = 4 * kParts, kScanWarps = R == 64 ? 3 : 7, kGatherWarps = 4,
+  static constexpr int kParts = R == 64 ? 4 : 2, kSoftWarps = 4 * kParts, kScanWarps = R == 64 ? 3 : 5, kGatherWarps = 4,
                        kGatherWarp = kSoftWarps + kScanWarps, kMmaWarp = kGatherWarp + kGatherWarps,
                        kThreads = (kMmaWarp + 1) * 32;
   static constexpr int kStages = 3;
   static constexpr int kListed = 4;                            // tiles listed ahead of the weights
   // A scan round: kSlots slots a lane, so kPages pages a warp; the list holds what a
   // round can add to a tile and the tiles listed.
-  static constexpr int kSlots = 4, kPages = 2, kRound = kPages * kScanWarps;
+  static constexpr int kSlots = R == 64 ? 4 : 8, kPages = kSlots / 2, kRound = kPages * kScanWarps;
   static constexpr int kList = R == 64 ? 1024 : 2048;          // entries of the block's list of kept slots
   static_assert(kList >= kRound * kPage + kListed * kTile && kStages < kListed, "list too short");
   static constexpr int kRowBytes = R >= 32 ? 128 : 4 * R;      // P's bytes of a key, per chunk of N
@@ -346,13 +346,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
         // ------------------------------------------------ scan
         const bool relist = pass == 0 || entries > kList;  // else the whole list is still there
         int x = 0;                                     // the warp's next page
-        if (relist) {
-          entries = 0;
-          if (pass > 0) {
-            entry = entry_of(0);
-            fetch(0);
-          }
-        }
+        if (relist) entries = 0;
         auto scan_round = [&]() {
           if (x % kAhead == 0) {                       // a new batch: it becomes current, the next one is fetched
             lane_page = next_page;
@@ -454,6 +448,10 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           }
         }
         cp_async_wait_all();
+        if (pass == 0 && L.accumulate && entries > kList) {        // the second pass starts over
+          entry = entry_of(0);
+          fetch(0);
+        }
       } else if (warp >= kGatherWarp && warp < kMmaWarp) {
         // ------------------------------------------------ gathers of kept rows
         // Four rows a step and warp (a step is a multiple of 8 rows on: one swizzle for
