@@ -114,7 +114,8 @@ focus_status_t ensure_setup() {
     if (setup_attn_kernels() != cudaSuccess) return FOCUS_ERR_CUDA;
     if (setup_bwd_tc_kernels() != cudaSuccess) return FOCUS_ERR_CUDA;
     if (setup_sinkhorn_kernels() != cudaSuccess) return FOCUS_ERR_CUDA;
-    if (setup_cache_evict() != cudaSuccess || setup_cache_attn() != cudaSuccess || setup_cache_attn_tc() != cudaSuccess)
+    if (setup_cache_evict(dev) != cudaSuccess || setup_cache_attn(dev) != cudaSuccess ||
+        setup_cache_attn_tc(dev) != cudaSuccess)
       return FOCUS_ERR_CUDA;
     g_ready[dev] = true;
   }
@@ -141,6 +142,12 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, u
 focus_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? FOCUS_OK : FOCUS_ERR_CUDA; }
 
 // SMs of the current device (valid after ensure_setup).
+int current_device() {                 // after ensure_setup: in range
+  int dev = 0;
+  cudaGetDevice(&dev);
+  return dev;
+}
+
 int sm_count() {
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1158,7 +1165,7 @@ focus_status_t focus_cache_attention_fwd(const focus_params_t* p, const void* Q,
   if (focus_status_t s = ensure_setup()) return s;
   CacheAttnLaunch L{Q, gid, n_new, *cache, O, lse_opt, accumulate != 0,
                     p->B, p->H, p->H_kv, p->n, p->d, p->A, p->w > 1 ? p->w : 1,
-                    p->scale * 1.4426950408889634f, at<int>(ws, 0), sm_count()};
+                    p->scale * 1.4426950408889634f, at<int>(ws, 0), current_device()};
   // More than eight query rows a key/value head go to the tcgen05 kernel (four drafted
   // tokens for 4 sequences of 64K, 32 rows: 42 us against 51; 64 tokens over 8K, 64
   // rows: 142 against 242); for eight or fewer its setup and single scan cost more
@@ -1177,7 +1184,7 @@ focus_status_t focus_cache_evict(const focus_params_t* p, int32_t budget, int32_
   if (static_cast<long long>(dst->max_pages) * kPage < budget) return FOCUS_ERR_INVALID_ARG;
   if (focus_status_t s = ensure_setup()) return s;
   CacheEvictLaunch L{*src, *dst, p->B, p->H_kv, p->d, budget, recent, at<int32_t>(ws, kAlign), at<int>(ws, 0),
-                     sm_count()};
+                     current_device()};
   return cuda_status(launch_cache_evict(L, static_cast<cudaStream_t>(stream)));
 }
 

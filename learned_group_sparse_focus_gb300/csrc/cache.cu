@@ -195,7 +195,7 @@ __device__ __forceinline__ uint32_t keep_key(float mass, bool late) {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelCluster = 16;            // blocks of a cluster, at most
+constexpr int kSelCluster = kMaxClusterBlocks;
 constexpr int kSelRun = 4096;              // slots that are worth a block
 constexpr int kSelKeys = 24576;            // keys that a block holds in shared memory
 constexpr int kSelSmem = kSelKeys * 4 + kSelWarps * 256 * 4;
@@ -353,6 +353,8 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvictLau
   }
 }
 
+ClusterFit g_select_fit[kMaxDevices];
+
 // One block per destination page and head.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 8) cache_copy_kernel(CacheEvictLaunch L) {
@@ -431,9 +433,8 @@ __global__ void __launch_bounds__(kThreads, 8) cache_copy_kernel(CacheEvictLaunc
 
 }  // namespace
 
-cudaError_t setup_cache_evict() {
-  if (cudaError_t e = cudaFuncSetAttribute(cache_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmem)) return e;
-  return cudaFuncSetAttribute(cache_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+cudaError_t setup_cache_evict(int device) {
+  return cluster_fit(reinterpret_cast<const void*>(cache_select_kernel), kSelThreads, kSelSmem, &g_select_fit[device]);
 }
 
 cudaError_t launch_cache_append(const CacheAppendLaunch& L, int dtype, cudaStream_t st) {
@@ -451,8 +452,13 @@ cudaError_t launch_cache_append(const CacheAppendLaunch& L, int dtype, cudaStrea
 
 cudaError_t launch_cache_evict(const CacheEvictLaunch& L, cudaStream_t st) {
   // Blocks per (sequence, head): one wave, as long as each has kSelRun slots.
-  int cs = 1;
-  while (cs < kSelCluster && 2ll * cs * L.B * L.H_kv <= L.num_sms && 2 * cs * kSelRun <= L.src.max_pages * kPage) cs *= 2;
+  const ClusterFit& fit = g_select_fit[L.device];
+  int cs = 1, i = 0;
+  while (cs < kSelCluster && static_cast<long long>(L.B) * L.H_kv <= fit.n[i + 1] &&
+         2 * cs * kSelRun <= L.src.max_pages * kPage) {
+    cs *= 2;
+    ++i;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(cs, L.H_kv, L.B);
   cfg.blockDim = dim3(kSelThreads);

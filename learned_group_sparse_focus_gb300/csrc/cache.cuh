@@ -123,4 +123,33 @@ __device__ __forceinline__ uint32_t top_code(uint4 c) {
   return top;
 }
 
+// Clusters of 1, 2, 4, 8 and 16 blocks of a kernel that a device runs at once.  A
+// cluster lies within one part of the GPU and the parts differ in SMs, so these are
+// fewer than the SMs hold blocks: with one block an SM, 16 blocks a cluster leave so
+// many SMs over that eight clusters take two waves.
+struct ClusterFit {
+  int n[5];
+};
+constexpr int kMaxClusterBlocks = 16;
+constexpr int kMaxDevices = 64;
+
+inline cudaError_t cluster_fit(const void* kernel, int threads, size_t smem, ClusterFit* fit) {
+  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) return e;
+  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) return e;
+  for (int i = 0; i < 5; ++i) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(1 << i);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1 << i;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaError_t e = cudaOccupancyMaxActiveClusters(&fit->n[i], kernel, &cfg)) return e;
+  }
+  return cudaSuccess;
+}
+
 }  // namespace focus

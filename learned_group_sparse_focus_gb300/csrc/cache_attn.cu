@@ -54,7 +54,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kKeys = 16;            // keys of a tile
 constexpr int kStages = 2;           // tiles in flight per warp
-constexpr int kMaxCluster = 16;      // blocks of a cluster, at most
+constexpr int kMaxCluster = kMaxClusterBlocks;
 constexpr int kAhead = 16;           // pages whose group ids a warp holds in shared memory
 constexpr int kList = 256;           // entries of a warp's list of kept slots
 constexpr float kNoRef = -1e30f;     // reference of a row without kept slots
@@ -662,7 +662,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
 }
 
 template <typename T, int D, int NT, bool kMulti>
-cudaError_t launch(const CacheAttnLaunch& L, int cs, cudaStream_t st) {
+ClusterFit g_fit[kMaxDevices];
+
+template <typename T, int D, int NT, bool kMulti>
+cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
+  // Blocks per (sequence, head): one wave of the clusters that fit, as long as each warp
+  // gets a page; a second wave of clusters of up to 4 where a warp still scans 16 pages,
+  // since sequences differ in what they keep (16 sequences of up to 32K tokens: 78 us
+  // with 2 blocks, 59 with 4, 72 with 8; 8 sequences of 1K tokens, 12 heads: 8.2 with 2,
+  // 13.1 with 4).
+  const ClusterFit& fit = g_fit<T, D, NT, kMulti>[L.device];
+  const long long heads = static_cast<long long>(L.B) * L.H_kv;
+  int cs = 1, i = 0;
+  while (cs < kMaxCluster && cs * kWarps < L.c.max_pages) {
+    const int runs = fit.n[i + 1];
+    if (heads > runs && (cs > 2 || heads > 2 * runs || L.c.max_pages < 2 * cs * kWarps * 16)) break;
+    cs *= 2;
+    ++i;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(cs, L.H_kv, L.B);
   cfg.blockDim = dim3(kThreads);
@@ -684,58 +701,43 @@ struct Reach {
 };
 
 template <typename T, int D>
-cudaError_t launch_rows(const CacheAttnLaunch& L, int cs, cudaStream_t st) {
+cudaError_t launch_rows(const CacheAttnLaunch& L, cudaStream_t st) {
   const bool wide = L.H / L.H_kv * L.n > 8;
   if (L.n == 1) {
     if constexpr (Reach<T, D>::wide_single)
-      if (wide) return launch<T, D, 2, false>(L, cs, st);
-    return launch<T, D, 1, false>(L, cs, st);
+      if (wide) return launch<T, D, 2, false>(L, st);
+    return launch<T, D, 1, false>(L, st);
   }
-  return wide ? launch<T, D, 2, true>(L, cs, st) : launch<T, D, 1, true>(L, cs, st);
+  return wide ? launch<T, D, 2, true>(L, st) : launch<T, D, 1, true>(L, st);
 }
 
 template <typename T, int D, int NT, bool kMulti>
-cudaError_t prepare() {
-  cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<T, D, NT, kMulti>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Cfg<T, D, NT>::kSmem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(cache_attn_kernel<T, D, NT, kMulti>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+cudaError_t prepare(int device) {
+  return cluster_fit(reinterpret_cast<const void*>(cache_attn_kernel<T, D, NT, kMulti>), kThreads, Cfg<T, D, NT>::kSmem,
+                     &g_fit<T, D, NT, kMulti>[device]);
 }
 
 template <typename T, int D>
-cudaError_t prepare_all() {
-  if (cudaError_t e = prepare<T, D, 1, false>()) return e;
-  if (cudaError_t e = prepare<T, D, 1, true>()) return e;
+cudaError_t prepare_all(int device) {
+  if (cudaError_t e = prepare<T, D, 1, false>(device)) return e;
+  if (cudaError_t e = prepare<T, D, 1, true>(device)) return e;
   if constexpr (Reach<T, D>::wide_single)
-    if (cudaError_t e = prepare<T, D, 2, false>()) return e;
-  return prepare<T, D, 2, true>();
+    if (cudaError_t e = prepare<T, D, 2, false>(device)) return e;
+  return prepare<T, D, 2, true>(device);
 }
 
 }  // namespace
 
-cudaError_t setup_cache_attn() {
-  if (cudaError_t e = prepare_all<__nv_bfloat16, 64>()) return e;
-  if (cudaError_t e = prepare_all<__nv_bfloat16, 128>()) return e;
-  if (cudaError_t e = prepare_all<float, 64>()) return e;
-  return prepare_all<float, 128>();
+cudaError_t setup_cache_attn(int device) {
+  if (cudaError_t e = prepare_all<__nv_bfloat16, 64>(device)) return e;
+  if (cudaError_t e = prepare_all<__nv_bfloat16, 128>(device)) return e;
+  if (cudaError_t e = prepare_all<float, 64>(device)) return e;
+  return prepare_all<float, 128>(device);
 }
 
 cudaError_t launch_cache_attn(const CacheAttnLaunch& L, int dtype, cudaStream_t st) {
-  // Blocks per (sequence, head): one wave of the blocks that fit (two an SM with
-  // eight rows, one with sixteen), as long as each warp gets a page; a second wave
-  // of clusters of up to 4 where a warp still scans 16 pages, since sequences
-  // differ in what they keep (16 sequences of up to 32K tokens: 78 us with 2
-  // blocks, 59 with 4, 72 with 8; 4 drafted tokens for 4 sequences of 64K: 51 us
-  // with 4, 71 with 8; 8 sequences of 1K tokens, 12 heads: 8.2 with 2, 13.1 with 4).
-  const int fit = L.num_sms * (L.H / L.H_kv * L.n > 8 ? 1 : 2);
-  int cs = 1;
-  while (cs < kMaxCluster && cs * kWarps < L.c.max_pages) {
-    const long long blocks = 2ll * cs * L.B * L.H_kv;
-    if (blocks > fit && (cs > 2 || blocks > 2 * fit || L.c.max_pages < 2 * cs * kWarps * 16)) break;
-    cs *= 2;
-  }
-  if (dtype == FOCUS_BF16) return L.d == 128 ? launch_rows<__nv_bfloat16, 128>(L, cs, st) : launch_rows<__nv_bfloat16, 64>(L, cs, st);
-  return L.d == 128 ? launch_rows<float, 128>(L, cs, st) : launch_rows<float, 64>(L, cs, st);
+  if (dtype == FOCUS_BF16) return L.d == 128 ? launch_rows<__nv_bfloat16, 128>(L, st) : launch_rows<__nv_bfloat16, 64>(L, st);
+  return L.d == 128 ? launch_rows<float, 128>(L, st) : launch_rows<float, 64>(L, st);
 }
 
 }  // namespace focus

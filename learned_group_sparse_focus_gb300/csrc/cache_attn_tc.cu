@@ -38,7 +38,7 @@ namespace {
 constexpr int kTile = 128;             // keys of a tile
 constexpr int kD = 128;
 constexpr int kTileBytes = kTile * kD;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = kMaxClusterBlocks;
 constexpr int kAhead = 8;              // pages a scan warp fetches group ids of at a time
 constexpr float kNoRef = -1e30f;       // reference of a row without kept slots
 
@@ -874,7 +874,17 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
 }
 
 template <int R, bool kMulti>
-cudaError_t launch(const CacheAttnLaunch& L, int cs, cudaStream_t st) {
+ClusterFit g_fit[kMaxDevices];
+
+template <int R, bool kMulti>
+cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
+  // Blocks per (sequence, head): one wave, as long as each scans a round or so.
+  int cs = 1, i = 0;
+  while (cs < kMaxCluster && static_cast<long long>(L.B) * L.H_kv <= g_fit<R, kMulti>[L.device].n[i + 1] &&
+         cs * 16 <= L.c.max_pages) {
+    cs *= 2;
+    ++i;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(cs, L.H_kv, L.B);
   cfg.blockDim = dim3(TcCfg<R, kMulti>::kThreads);
@@ -890,35 +900,30 @@ cudaError_t launch(const CacheAttnLaunch& L, int cs, cudaStream_t st) {
 }
 
 template <int R, bool kMulti>
-cudaError_t prepare() {
-  cudaError_t e = cudaFuncSetAttribute(cache_attn_tc_kernel<R, kMulti>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       TcCfg<R, kMulti>::kSmem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(cache_attn_tc_kernel<R, kMulti>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+cudaError_t prepare(int device) {
+  return cluster_fit(reinterpret_cast<const void*>(cache_attn_tc_kernel<R, kMulti>), TcCfg<R, kMulti>::kThreads,
+                     TcCfg<R, kMulti>::kSmem, &g_fit<R, kMulti>[device]);
 }
 
 }  // namespace
 
-cudaError_t setup_cache_attn_tc() {
-  if (cudaError_t e = prepare<16, false>()) return e;
-  if (cudaError_t e = prepare<16, true>()) return e;
-  if (cudaError_t e = prepare<32, true>()) return e;
-  if (cudaError_t e = prepare<32, false>()) return e;
-  if (cudaError_t e = prepare<64, false>()) return e;
-  return prepare<64, true>();
+cudaError_t setup_cache_attn_tc(int device) {
+  if (cudaError_t e = prepare<16, false>(device)) return e;
+  if (cudaError_t e = prepare<16, true>(device)) return e;
+  if (cudaError_t e = prepare<32, true>(device)) return e;
+  if (cudaError_t e = prepare<32, false>(device)) return e;
+  if (cudaError_t e = prepare<64, false>(device)) return e;
+  return prepare<64, true>(device);
 }
 
 cudaError_t launch_cache_attn_tc(const CacheAttnLaunch& L, cudaStream_t st) {
-  // Blocks per (sequence, head): one wave, as long as each scans a round or so.
-  int cs = 1;
-  while (cs < kMaxCluster && 2ll * cs * L.B * L.H_kv <= L.num_sms && cs * 16 <= L.c.max_pages) cs *= 2;
   const int rows = L.H / L.H_kv * L.n;
   if (L.n == 1) {
-    if (rows <= 16) return launch<16, false>(L, cs, st);
-    return rows <= 32 ? launch<32, false>(L, cs, st) : launch<64, false>(L, cs, st);
+    if (rows <= 16) return launch<16, false>(L, st);
+    return rows <= 32 ? launch<32, false>(L, st) : launch<64, false>(L, st);
   }
-  if (rows <= 16) return launch<16, true>(L, cs, st);
-  return rows <= 32 ? launch<32, true>(L, cs, st) : launch<64, true>(L, cs, st);
+  if (rows <= 16) return launch<16, true>(L, st);
+  return rows <= 32 ? launch<32, true>(L, st) : launch<64, true>(L, st);
 }
 
 }  // namespace focus

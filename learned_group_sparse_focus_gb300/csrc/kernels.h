@@ -252,9 +252,9 @@ struct CacheEvictLaunch {
   int B, H_kv, d, budget, recent;
   int32_t* keep;          // [B * H_kv][1 + src.max_pages * 64] count and kept slots, ascending
   int* err;
-  int num_sms;
+  int device;
 };
-cudaError_t setup_cache_evict();
+cudaError_t setup_cache_evict(int device);
 cudaError_t launch_cache_evict(const CacheEvictLaunch& L, cudaStream_t st);
 
 struct CacheAttnLaunch {
@@ -268,13 +268,13 @@ struct CacheAttnLaunch {
   int B, H, H_kv, n, d, A, w;
   float scale_log2;       // scale * log2(e)
   int* err;
-  int num_sms;
+  int device;
 };
-cudaError_t setup_cache_attn();
+cudaError_t setup_cache_attn(int device);
 // cache_attn_tc.cu: bf16, d = 128; with several tokens a table of kCacheTableGroups
 // group ids, for K up to that.
 constexpr int kCacheTableGroups = 1024;
-cudaError_t setup_cache_attn_tc();
+cudaError_t setup_cache_attn_tc(int device);
 cudaError_t launch_cache_attn_tc(const CacheAttnLaunch& L, cudaStream_t st);
 cudaError_t launch_cache_attn(const CacheAttnLaunch& L, int dtype, cudaStream_t st);
 
