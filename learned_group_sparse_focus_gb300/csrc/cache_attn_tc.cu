@@ -878,10 +878,19 @@ ClusterFit g_fit[kMaxDevices];
 
 template <int R, bool kMulti>
 cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
-  // Blocks per (sequence, head): one wave, as long as each scans a round or so.
+  // Blocks per (sequence, head): one wave of the clusters that run at once, as long as
+  // each block scans a round or so.  For single tokens a second wave where a block still
+  // has 128 pages, since sequences of a batch differ in length (16 query heads a head,
+  // sequences of up to 32K: 16 of them 143 us with 1 block, 95 with 2, 101 with 4; 8 of
+  // them 95 with 2, 58 with 4).  Several tokens keep more of each page and gain less
+  // from it (four tokens, 64K: 8 sequences 59 us with 2, 69 with 4; 64 tokens, 8K:
+  // 4 sequences 201 with 1, 222 with 2).
+  const ClusterFit& fit = g_fit<R, kMulti>[L.device];
+  const long long heads = static_cast<long long>(L.B) * L.H_kv;
   int cs = 1, i = 0;
-  while (cs < kMaxCluster && static_cast<long long>(L.B) * L.H_kv <= g_fit<R, kMulti>[L.device].n[i + 1] &&
-         cs * 16 <= L.c.max_pages) {
+  while (cs < kMaxCluster && cs * 16 <= L.c.max_pages) {
+    const int runs = fit.n[i + 1];
+    if (heads > runs && (kMulti || heads > 2 * runs || L.c.max_pages < 2 * cs * 128)) break;
     cs *= 2;
     ++i;
   }
