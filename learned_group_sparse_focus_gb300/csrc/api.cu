@@ -1167,9 +1167,10 @@ focus_status_t focus_cache_attention_fwd(const focus_params_t* p, const void* Q,
                     p->B, p->H, p->H_kv, p->n, p->d, p->A, p->w > 1 ? p->w : 1,
                     p->scale * 1.4426950408889634f, at<int>(ws, 0), current_device()};
   // More than eight query rows a key/value head go to the tcgen05 kernel (four drafted
-  // tokens for 4 sequences of 64K, 32 rows: 42 us against 51; 64 tokens over 8K, 64
-  // rows: 142 against 242); for eight or fewer its setup and single scan cost more
-  // than they save (one step at 32K: 16 us against 12; 16 such: 84 against 59).
+  // tokens for 4 sequences of 64K, 32 rows: 37 us against 53; 64 tokens over 8K, 64
+  // rows: 117 against 255); for eight or fewer its setup and single scan cost more
+  // than they save (one step at 32K, 4 rows: 15 us against 11; 16 sequences of up to
+  // 32K with the weights accumulated: 140 with a block a head, against 55).
   if (p->dtype == FOCUS_BF16 && p->d == 128 && p->H / p->H_kv * p->n > 8 && (p->n == 1 || p->K <= kCacheTableGroups))
     return cuda_status(launch_cache_attn_tc(L, static_cast<cudaStream_t>(stream)));
   return cuda_status(launch_cache_attn(L, p->dtype, static_cast<cudaStream_t>(stream)));

@@ -19,13 +19,27 @@
 // key: masks, scales and the weight's sum over rows need no exchange.
 //
 // Work split, softmax reference and join are cache_attn.cu's: a cluster of blocks
-// per (sequence, head), pages round-robin over the blocks.  In a block three or seven
+// per (sequence, head), pages round-robin over the blocks.  In a block three or five
 // warps scan group ids (and the last slots' positions) into a list of kept slots, in
-// rounds, and gather the tiles; one warp issues the products; eight
-// or sixteen (two or four a TMEM lane quadrant, each for a part of the rows) form
-// the weights.  The reference of a row is common to the block: it is set 10 below
-// the largest t and moves only when a weight would pass 2^15, so the accumulator in
-// TMEM is rescaled hardly ever.
+// rounds, up to four tiles ahead; four gather the tiles; one issues the products;
+// eight or sixteen (two or four a TMEM lane quadrant, each for a part of the rows)
+// form the weights.  The reference of a row is common to the block: it is set 10
+// below the largest t and moves only when a weight would pass 2^15, so the
+// accumulator in TMEM is rescaled hardly ever.
+//
+// A warp issues one cp.async of 512 gathered bytes in about 70 clocks, so the copies
+// of a tile (64 of them) want several warps; in the scanning warps they made the scan
+// the bottleneck (64 tokens over 8K: 132 us against 117), in the weight warps the
+// weights (161 us), and a single gathering warp takes 4,600 clocks a tile (190 us).
+//
+// What bounds it now: 64 query rows, the weight warps' instructions (some 330 a
+// thread and tile over 16 rows each; 4,100 clocks a tile with the tensor pipe at 10%),
+// then the second pass's (2,400 clocks a tile); 16 or 32 rows over long caches, the scan
+// (2,600 clocks for 20 pages) and the fixed 14,000 clocks from the launch to the
+// first weights and 6,000 of the join.  64 tokens for 2 sequences of 8K slots, 32
+// heads, with the weights accumulated: 117 us (146 MB of HBM traffic: 1.3 TB/s); four
+// tokens for 4 sequences of 64K slots, 64 / 8 heads: 37 us; a step of 16, 32, 64 query
+// heads a head at 32K: 15, 17, 22 us.
 #include <cooperative_groups.h>
 
 #include "cache.cuh"
