@@ -49,6 +49,17 @@ __device__ __forceinline__ int scale_exp(float s) {
   return min(max(e, kMinExp), 120);
 }
 
+// Scales of K and V of a page as they are stored, and their exponents in two bytes.
+// Kept apart: the bytes are formed when they are needed, not when the loads start.
+struct PageScales {
+  float k, v;
+  __device__ __forceinline__ void load(const focus_cache_t& c, size_t plane) {
+    k = c.k_scale[plane];
+    v = c.v_scale[plane];
+  }
+  __device__ __forceinline__ int bytes() const { return (scale_exp(k) & 0xff) | (scale_exp(v) & 0xff) << 8; }
+};
+
 // Least e >= kMinExp with a <= 448 * 2^e = 1.75 * 2^(e + 8), from the bits of a
 // finite a >= 0.  Anything below 2^-56 needs no more than kMinExp.
 __device__ __forceinline__ int need_exp(uint32_t a) {

@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
     // ---- the scan: kAhead pages at a time, their group ids in shared memory
     int j = first, i = 0;                              // next unit to scan, and its place among the kAhead
     int lane_page = -1, lane_exps = 0;
+    PageScales scales{1.f, 1.f};
     int2 pos{};                                        // positions of the lane's two slots of unit j, if it is near
     auto load_pos = [&]() {
       const int page = __shfl_sync(~0u, lane_page, i);
@@ -237,10 +238,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
           cp_async_16(ids + x * 128 + lane * 4,
                       L.c.gid + (static_cast<size_t>(page) * L.H_kv + h) * kPage + lane % 8 * 8, 16);
       }
-      if (lane_page >= 0) {
-        const size_t plane = static_cast<size_t>(lane_page) * L.H_kv + h;
-        lane_exps = (scale_exp(L.c.k_scale[plane]) & 0xff) | (scale_exp(L.c.v_scale[plane]) & 0xff) << 8;
-      }
+      if (lane_page >= 0) scales.load(L.c, static_cast<size_t>(lane_page) * L.H_kv + h);
       entry = table(j + kAhead * step);
       load_pos();
     };
@@ -311,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
         cp_async_commit();
         cp_async_wait<0>();
         __syncwarp();
+        lane_exps = scales.bytes();
       }
       const int page = __shfl_sync(~0u, lane_page, i), exps = __shfl_sync(~0u, lane_exps, i);
       if (page >= 0) {

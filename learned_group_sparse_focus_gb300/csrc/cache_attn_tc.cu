@@ -266,10 +266,10 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
       return lane < kAhead && j < L.c.max_pages ? L.c.table[static_cast<size_t>(b) * L.c.max_pages + j] : -1;
     };
     uint8_t* ids = smem + C::kIds + v * 2 * kAhead * kPage * 2;      // two batches of kAhead pages
-    int next_page = -1, next_exps = 0, lane_page = -1, lane_exps = 0, entry = 0;
+    int next_page = -1, lane_page = -1, lane_exps = 0, entry = 0;
+    PageScales next_scales{1.f, 1.f};
     auto fetch = [&](int x) {                      // starts on pages x ... x + kAhead - 1, and on the table behind them
       next_page = -1;
-      next_exps = 0;
       if (lane < kAhead && page_of(x + lane) < pages) {
         next_page = entry;
         if (entry < 0 || entry >= L.c.n_pages) {
@@ -286,10 +286,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
                       L.c.gid + (static_cast<size_t>(page) * L.H_kv + h) * kPage + lane % 8 * 8, 16);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
-      if (next_page >= 0) {
-        const size_t plane = static_cast<size_t>(next_page) * L.H_kv + h;
-        next_exps = (scale_exp(L.c.k_scale[plane]) & 0xff) | (scale_exp(L.c.v_scale[plane]) & 0xff) << 8;
-      }
+      if (next_page >= 0) next_scales.load(L.c, static_cast<size_t>(next_page) * L.H_kv + h);
       entry = entry_of(x + kAhead);
     };
     const bool scans = warp >= kSoftWarps && warp < kGatherWarp;
@@ -364,7 +361,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
         auto scan_round = [&]() {
           if (x % kAhead == 0) {                       // a new batch: it becomes current, the next one is fetched
             lane_page = next_page;
-            lane_exps = next_exps;
+            lane_exps = next_scales.bytes();
             fetch(x + kAhead);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncwarp();
