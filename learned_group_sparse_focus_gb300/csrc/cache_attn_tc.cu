@@ -53,7 +53,6 @@ constexpr int kTile = 128;             // keys of a tile
 constexpr int kD = 128;
 constexpr int kTileBytes = kTile * kD;
 constexpr int kMaxCluster = kMaxClusterBlocks;
-constexpr int kAhead = 8;              // pages a scan warp fetches group ids of at a time
 constexpr float kNoRef = -1e30f;       // reference of a row without kept slots
 
 template <int R, bool kMulti>
@@ -64,6 +63,7 @@ struct TcCfg {
                        kGatherWarp = kSoftWarps + kScanWarps, kMmaWarp = kGatherWarp + kGatherWarps,
                        kThreads = (kMmaWarp + 1) * 32;
   static constexpr int kStages = 3;
+  static constexpr int kAhead = R == 64 ? 8 : 16;              // pages a scan warp fetches group ids of at a time
   static constexpr int kListed = 4;                            // tiles listed ahead of the weights
   // A scan round: kSlots slots a lane, so kPages pages a warp; the list holds what a
   // round can add to a tile and the tiles listed.
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
   constexpr int kStages = C::kStages, RH = R / C::kParts, kList = C::kList, kSlots = C::kSlots, kPages = C::kPages;
   constexpr int kRound = C::kRound, kLanes = kPage / kSlots;   // lanes a page
   constexpr int kParts = C::kParts, kSoftWarps = C::kSoftWarps, kMmaWarp = C::kMmaWarp, kThreads = C::kThreads,
-                kScanWarps = C::kScanWarps, kGatherWarp = C::kGatherWarp, kGatherWarps = C::kGatherWarps, kListed = C::kListed;
+                kScanWarps = C::kScanWarps, kGatherWarp = C::kGatherWarp, kGatherWarps = C::kGatherWarps, kListed = C::kListed, kAhead = C::kAhead;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t k_full[kStages], v_full[kStages], qk_done[kStages], pv_done[kStages], s_ready[2], p_ready[2];
   __shared__ uint64_t listed[kListed], used[kListed];  // a tile's entries are in the list; the weight warps have read them
