@@ -1167,7 +1167,7 @@ focus_status_t focus_cache_attention_fwd(const focus_params_t* p, const void* Q,
                     p->B, p->H, p->H_kv, p->n, p->d, p->A, p->w > 1 ? p->w : 1,
                     p->scale * 1.4426950408889634f, at<int>(ws, 0), current_device()};
   // More than eight query rows a key/value head go to the tcgen05 kernel (four drafted
-  // tokens for 4 sequences of 64K, 32 rows: 37 us against 53; 64 tokens over 8K, 64
+  // tokens for 4 sequences of 64K, 32 rows: 35 us against 53; 64 tokens over 8K, 64
   // rows: 117 against 255); for eight or fewer its setup and single scan cost more
   // than they save (one step at 32K, 4 rows: 15 us against 11; 16 sequences of up to
   // 32K with the weights accumulated: 140 with a block a head, against 55).

@@ -41,8 +41,8 @@
 // cost 8 bytes a slot and query row) and adds each slot's weights: one addition
 // a slot, in a fixed order.
 //
-// Measured: one step of 32 / 8 heads over 32K slots 10.9 us; 16 sequences of up to 32K
-// 55 us with the weights accumulated (86 MB: 1.6 TB/s); a step of 8 sequences of up to
+// Measured: one step of 32 / 8 heads over 32K slots 10.7 us; 16 sequences of up to 32K
+// 54 us with the weights accumulated (86 MB: 1.6 TB/s); a step of 8 sequences of up to
 // 1K slots, 12 heads, d = 64, 8.3 us.
 // The two small ones are a chain of latencies: launch, counts and table, group ids,
 // rows, products, two joins (18,400 clocks at 32K: first tile there at 10,000,

@@ -35,11 +35,11 @@
 // What bounds it now: 64 query rows, the weight warps' instructions (some 330 a
 // thread and tile over 16 rows each; 4,100 clocks a tile with the tensor pipe at 10%),
 // then the second pass's (2,400 clocks a tile); 16 or 32 rows over long caches, the scan
-// (2,600 clocks for 20 pages) and the fixed 14,000 clocks from the launch to the
+// (2,800 clocks for 20 pages) and the fixed 14,000 clocks from the launch to the
 // first weights and 6,000 of the join.  64 tokens for 2 sequences of 8K slots, 32
 // heads, with the weights accumulated: 117 us (146 MB of HBM traffic: 1.3 TB/s); four
-// tokens for 4 sequences of 64K slots, 64 / 8 heads: 37 us; a step of 16, 32, 64 query
-// heads a head at 32K: 15, 17, 22 us.
+// tokens for 4 sequences of 64K slots, 64 / 8 heads: 35 us; a step of 16, 32, 64 query
+// heads a head at 32K: 14, 16, 22 us.
 #include <cooperative_groups.h>
 
 #include "cache.cuh"
