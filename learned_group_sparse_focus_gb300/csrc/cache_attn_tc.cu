@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
     wait(bar, phase++ & 1, abort, L.err);
   };
   uint32_t it = 0;                                     // slots (tiles and end marks) so far, the same in every role
+  uint32_t skip = 0;                                   // of them in second passes, which use no values: V's slot is it - skip
 
   for (int r0 = 0; r0 < rows; r0 += R) {
     const int t_lo = r0 / G, off = r0 - t_lo * G;      // the block's rows start `off` rows into token t_lo
@@ -353,6 +354,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
 
     int entries = 0, tiles = 0;                        // load warp: listed slots; softmax warps: tiles of pass 0
     for (int pass = 0; pass < (L.accumulate ? 2 : 1); ++pass) {
+      const uint32_t it0 = it;
       if (scans) {
         // ------------------------------------------------ scan
         const bool relist = pass == 0 || entries > kList;  // else the whole list is still there
@@ -494,12 +496,15 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           } else {
             mbar_arrive(&k_full[st]);
           }
-          if (it >= kStages) wait(&pv_done[st], parity, abort, L.err);
-          if (cnt > 0 && pass == 0) {
-            copy(smem + C::kV + st * kTileBytes, L.c.v);
-            cp_async_arrive(&v_full[st]);
-          } else {
-            mbar_arrive(&v_full[st]);
+          if (pass == 0) {
+            const uint32_t vi = it - skip;
+            if (vi >= kStages) wait(&pv_done[vi % kStages], (vi / kStages + 1) & 1, abort, L.err);
+            if (cnt > 0) {
+              copy(smem + C::kV + vi % kStages * kTileBytes, L.c.v);
+              cp_async_arrive(&v_full[vi % kStages]);
+            } else {
+              mbar_arrive(&v_full[vi % kStages]);
+            }
           }
           if (cnt == 0 || *abort) {
             ++it;
@@ -538,7 +543,8 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           bool have = scores(it);
           bool first = true;
           while (have) {
-            const int st = it % kStages;
+            const uint32_t vi = it - skip;
+            const int st = vi % kStages;
             const int cnt = s_cnt[it & 7];
             // The next tile's S if its K comes before this tile's P (its S buffer was read
             // before P of slot it - 1 was ready); else after this tile's product.
@@ -555,9 +561,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
               }
             }
             ok = mbar_wait_nap(&p_ready[it & 1], (it >> 1) & 1, abort, L.err) && ok;
-            // (also in pass 1, without values: the gathering warps arrive here once they have seen
-            // pv_done of this stage's last slot, which must not complete twice before that)
-            ok = ok && mbar_wait_nap(&v_full[st], (it / kStages) & 1, abort, L.err);
+            if (pass == 0) ok = ok && mbar_wait_nap(&v_full[st], (vi / kStages) & 1, abort, L.err);
             if (pass == 0 && ok) {
               fence_proxy_async_smem();
               tc_fence_after();
@@ -566,7 +570,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
                        desc_rows(pb + (it & 1) * C::kPBytes + x * 32 * C::kRowBytes, C::kRowBytes, kTile * 128),
                        idesc_f8(4 * R, true, true, true), !(first && x == 0));
             }
-            mma_commit(&pv_done[st]);
+            if (pass == 0) mma_commit(&pv_done[st]);
             first = false;
             if (!asked) {
               k_wait(it + 1);
@@ -575,11 +579,15 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
             have = next && ok;
             ++it;
           }
-          // every commit has arrived before the block ends (pass 1 has no other wait for the last)
-          if (!first) mbar_wait(&pv_done[(it - 1) % kStages], ((it - 1) / kStages) & 1, abort, L.err);
-          // the end mark's slot, once the gathering warps have seen the stage's last one
-          mbar_wait_nap(&v_full[it % kStages], (it / kStages) & 1, abort, L.err);
-          mbar_arrive(&pv_done[it % kStages]);
+          // Every commit has arrived before the block ends.  The end mark's V slot is passed on
+          // once the gathering warps have seen the stage's last one.
+          if (!first) mbar_wait(&qk_done[(it - 1) % kStages], ((it - 1) / kStages) & 1, abort, L.err);
+          if (pass == 0) {
+            const uint32_t vi = it - skip;
+            if (!first) mbar_wait(&pv_done[(vi - 1) % kStages], ((vi - 1) / kStages) & 1, abort, L.err);
+            mbar_wait_nap(&v_full[vi % kStages], (vi / kStages) & 1, abort, L.err);
+            mbar_arrive(&pv_done[vi % kStages]);
+          }
           ++it;
         }
         it = __shfl_sync(~0u, it, 0);
@@ -592,7 +600,8 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
         for (int r = 0; r < RH / 2; ++r) l2[r] = f2_pack(0.f, 0.f);
         int tile = 0;
         for (;; ++tile, ++it) {
-          const int st = it % kStages, buf = it & 1;
+          const uint32_t vi = it - skip;
+          const int st = vi % kStages, buf = it & 1;
           const bool ok = wait(&s_ready[buf], (it >> 1) & 1, abort, L.err);
           const int cnt = ok ? s_cnt[it & 7] : 0;
           if (__any_sync(~0u, cnt == 0)) {
@@ -709,7 +718,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
             for (int r = 0; r < RH; r += 2)
               l2[r / 2] = f2_mul(l2[r / 2], f2_pack(__shfl_sync(~0u, f, r), __shfl_sync(~0u, f, r + 1)));
             if (tile > 0) {
-              mbar_wait(&pv_done[(it - 1) % kStages], ((it - 1) / kStages) & 1, abort, L.err);
+              mbar_wait(&pv_done[(vi - 1) % kStages], ((vi - 1) / kStages) & 1, abort, L.err);
               tc_fence_after();
 #pragma unroll
               for (int y = 0; y < RH / 2; ++y) {       // two rows, eight columns
@@ -729,7 +738,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
             meet(&part_bar[part], part_phase);
           }
           if (tile > 1)                                // P of the slot before the last one has been used
-            wait(&pv_done[(it - 2) % kStages], ((it - 2) / kStages) & 1, abort, L.err);
+            wait(&pv_done[(vi - 2) % kStages], ((vi - 2) / kStages) & 1, abort, L.err);
           const float vf = exp2_int(-static_cast<int8_t>(ex >> 8));
           const uint64_t vf2 = f2_pack(vf, vf);
           uint32_t word[RH];
@@ -758,7 +767,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           if (kMulti) {
             // A row that does not keep a key has weight 0 for it, and 0 * NaN would reach
             // that row: NaN codes leave the tile and mark the outputs that they reach.
-            wait(&v_full[st], (it / kStages) & 1, abort, L.err);
+            wait(&v_full[st], (vi / kStages) & 1, abort, L.err);
             uint32_t any = 0;
             uint4* vrow = reinterpret_cast<uint4*>(smem + C::kV + st * kTileBytes + key * kD);
 #pragma unroll
@@ -802,14 +811,17 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
             if (lane == 0) s_l[quad][part * RH + r] = x;
           }
           if (tiles > 0) {
-            const uint32_t last = it - 2;              // the last tile's slot: `it` is past the end mark
+            const uint32_t last = it - skip - 2;       // the last tile's slot: `it` is past the end mark
             mbar_wait(&pv_done[last % kStages], (last / kStages) & 1, abort, L.err);
             tc_fence_after();
           }
         }
       }
       __syncwarp();
-      if (pass == 1) break;
+      if (pass == 1) {
+        skip += it - it0;
+        break;
+      }
 
       // ---- join: the same exchange as in cache_attn.cu
       cluster.sync();                                  // every block runs and is past its last round
