@@ -731,6 +731,90 @@ def test_attention_is_the_same_bits_again_and_on_another_stream(fz):
                    for a, b in zip(o, outs[0]))
 
 
+def _cycle(fz, seed):
+    """Append, attention and eviction over buffers of their own, and what they leave."""
+    import torch
+    B, H, H_kv, L, T, d, K = 2, 16, 2, 3000, 4, 128, 8
+    rng = np.random.default_rng(seed)
+    p = fz.make_params(B, H, H_kv, L, d, 64, 64, K, 1, 64)
+    q = fz.make_params(B, H, H_kv, T, d, 64, 64, K, 1, 64)
+    bf = torch.bfloat16
+    k, v = (_dev(_rows(rng, (B, H_kv, L, d), "bf16"), bf) for _ in range(2))
+    Q = _dev(_rows(rng, (B, H, T, d), "bf16", 0.3), bf)
+    gid = _dev(rng.integers(0, K, (B, 1, L)).astype(np.int32))
+    gid1 = gid[:, :, -T:].contiguous()
+    src, dst = fz.alloc_cache(p, L, mass=True), fz.alloc_cache(p, 640, mass=True)
+    ws, O = fz.alloc_workspace_cache(p, src), torch.zeros_like(Q)
+
+    def run():
+        src.len.zero_()
+        src.next.zero_()
+        fz.focus_cache_append(p, k, v, gid, src, ws)
+        fz.focus_cache_attention_fwd(q, Q, gid1, src, O, None, ws, accumulate=True)
+        fz.focus_cache_evict(p, 600, 64, src, dst, ws)
+
+    return run, ws, lambda: [x.cpu().clone() for x in (O.float(), src.mass, dst.k, dst.pos, dst.mass, dst.len)]
+
+
+def test_two_threads_on_two_streams(fz):
+    import threading
+
+    import torch
+    jobs = [_cycle(fz, seed) for seed in (2, 3)]
+    want = []
+    for run, ws, out in jobs:
+        run()
+        want.append(out())
+
+    def work(run):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(50):
+                run()
+        stream.synchronize()
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(run,)) for run, _, _ in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for (_, ws, out), w in zip(jobs, want):
+        assert fz.focus_check_errors(ws) == 0
+        assert all(torch.equal(a, b) for a, b in zip(out(), w))
+
+
+FIRST_CALL = """
+import sys
+import torch
+sys.path[:0] = [{root!r}, {tests!r}]
+from learned_group_sparse_focus_gb300 import focus as fz
+import test_gpu_cache as t
+run, ws, out = t._cycle(fz, 1)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run()
+g.replay()
+torch.cuda.synchronize()
+a = out()
+run()
+assert fz.focus_check_errors(ws) == 0 and a[0].abs().max() > 0
+assert all(torch.equal(x, y) for x, y in zip(a, out()))
+"""
+
+
+def test_a_process_may_capture_its_first_call():
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALL.format(root=os.path.dirname(tests), tests=tests)
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
 def test_writes_stay_inside_their_buffers(fz):
     """Every buffer that a call writes sits between guard bytes."""
     import torch
