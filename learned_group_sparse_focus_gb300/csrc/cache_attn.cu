@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
         w1 += __shfl_xor_sync(~0u, w1, 1);
         w0 += __shfl_xor_sync(~0u, w0, 2);
         w1 += __shfl_xor_sync(~0u, w1, 2);
-        // the only addition to this slot in this round: its order cannot matter
+        // the only addition to this slot for these rows: its order cannot matter
         if (cl == 0 && left > 0) atomicAdd(L.c.mass + static_cast<uint32_t>(e0.x) / (D / 16), w0);
         if (cl == 1 && left > 8) atomicAdd(L.c.mass + static_cast<uint32_t>(e1.x) / (D / 16), w1);
         return;

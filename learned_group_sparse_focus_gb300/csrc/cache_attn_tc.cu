@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
             if (lane == 0) mbar_arrive(&used[it % kListed]);
             if (!part && key < cnt) {
               for (int x = 1; x < kParts; ++x) w += s_w[buf][x][key];
-              atomicAdd(L.c.mass + pool_row, w);       // the only addition to this slot in this round: its order cannot matter
+              atomicAdd(L.c.mass + pool_row, w);       // the only addition to this slot for these rows: its order cannot matter
             }
             continue;
           }
