@@ -505,7 +505,8 @@ FOCUS_API focus_status_t focus_cache_append(const focus_params_t* p, const void*
  * query heads of its key/value head in a fixed order.  Sums are fp32.  q enters
  * the products in two parts: bf16's 8 bits whole (elements below 2^-15 of the
  * row's largest to 2^-23 of that), fp32 to 22 bits; the softmax weights enter
- * the value product as f16 (bf16 tensors) or to 22 bits (fp32 tensors).
+ * the value product with an error of at most 2^-16 of each (bf16 tensors, and
+ * 2^-26 of the row's largest) or 2^-22 (fp32 tensors).
  * K and V pools hold at most 2^36 bytes each (FOCUS_ERR_UNSUPPORTED). */
 FOCUS_API focus_status_t focus_cache_attention_fwd(const focus_params_t* p, const void* Q,
                                                    const int32_t* gid, const int32_t* n_new,

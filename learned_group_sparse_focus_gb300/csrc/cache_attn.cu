@@ -25,8 +25,8 @@
 // operands of mma.sync are taken apart into the same f16 products on this
 // architecture, with more conversions: 14 instructions against 9 here).
 // Queries are scaled by a power of two per row to below 2^14 and held in one f16
-// (bf16 tensors: 8 bits fit 11) or two (fp32 tensors, 22 bits); weights are
-// rounded to one f16 or two likewise.
+// (bf16 tensors: 8 bits fit 11) or two (fp32 tensors, 22 bits); weights are held in
+// two, since one alone would be off by up to 2^-11, an eighth of bf16's half step.
 //
 // Softmax: with v = code * 2^e per page, the running maximum is taken over
 // t_j = s_j + e_j (log2), so the weights 2^(t_j - ref) multiply raw codes and
@@ -42,7 +42,7 @@
 // a slot, in a fixed order.
 //
 // Measured: one step of 32 / 8 heads over 32K slots 10.7 us; 16 sequences of up to 32K
-// 54 us with the weights accumulated (86 MB: 1.6 TB/s); a step of 8 sequences of up to
+// 57 us with the weights accumulated (86 MB: 1.5 TB/s; 54 with weights of one f16); a step of 8 sequences of up to
 // 1K slots, 12 heads, d = 64, 8.3 us.
 // The two small ones are a chain of latencies: launch, counts and table, group ids,
 // rows, products, two joins (18,400 clocks at 32K: first tile there at 10,000,
@@ -71,7 +71,7 @@ static_assert(kList >= kPage + (kStages + 1) * kKeys && (kList & (kList - 1)) ==
 
 template <typename T, int D, int NT>
 struct Cfg {
-  static constexpr int kParts = std::is_same<T, float>::value ? 2 : 1;   // f16 parts of q and of P
+  static constexpr int kParts = std::is_same<T, float>::value ? 2 : 1;   // f16 parts of q; of P there are two
   static constexpr int kRows = 8 * NT;
   static constexpr int kSteps = D / 16;                                  // f16 MMA steps over d
   static constexpr int kStageBytes = 2 * kKeys * D;                      // K rows, then V rows
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
             }
           }
       }
-      uint32_t pb[C::kParts][NT][2];                // [..][keys 0-7 or 8-15]
+      uint32_t pb[2][NT][2];                        // [part][..][keys 0-7 or 8-15]
       const float vf0 = exp2_int(-ve0), vf1 = exp2_int(-ve1);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -480,10 +480,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
         for (int y = 0; y < 2; ++y) {
           const uint32_t hp = pack_half2(p[2 * y], p[2 * y + 1]);
           pb[0][nt][y] = transpose8x8(hp);
-          if constexpr (C::kParts == 2) {
-            const float2 f = unpack_half2(hp);
-            pb[1][nt][y] = transpose8x8(pack_half2(p[2 * y] - f.x, p[2 * y + 1] - f.y));
-          }
+          const float2 f = unpack_half2(hp);
+          pb[1][nt][y] = transpose8x8(pack_half2(p[2 * y] - f.x, p[2 * y + 1] - f.y));
         }
       }
       // O^T: thread (gl, cl) holds columns gl * D / 8 ... of keys 2 cl, 2 cl + 1, 2 cl + 8, 2 cl + 9
@@ -529,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int p = 0; p < C::kParts; ++p)
+            for (int p = 0; p < 2; ++p)
               mma_f16(o[nt][2 * w + z], a0, a1, a2, a3, pb[p][nt][0], pb[p][nt][1]);
         }
       if (kMulti && some_nan) {

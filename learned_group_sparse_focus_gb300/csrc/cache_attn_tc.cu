@@ -9,11 +9,11 @@
 //                           e4m3, both parts side by side in N: 4 + 4 bits hold
 //                           bf16's 8, elements below 2^-15 of a row's largest are
 //                           held to 2^-23 of it
-//   O^T [128 dims, 4 R] += V^T P^T     V rows are an MN-major A; P is rounded to f16
-//                           and split into four e5m2 parts of three bits (an e5m2
-//                           number is the upper byte of an f16), again side by
-//                           side in N: all 11 bits, down to 2^-16, which is 2^-26
-//                           of a row's largest weight or less (see below)
+//   O^T [128 dims, 4 R] += V^T P^T     V rows are an MN-major A; P as p1 + p2 / 16 +
+//                           p3 / 256 + p4 / 4096 in e4m3, again side by side in N
+//                           with sums of their own: 2^-16 of a weight, and 2^-22
+//                           where that is more, which is 2^-26 of a row's largest
+//                           weight or less (see below)
 // R = 16, 32 or 64 query rows (tokens x query heads of the head).  With the keys
 // on the 128 side of both products nothing is padded but R, and a thread owns a
 // key: masks, scales and the weight's sum over rows need no exchange.
@@ -23,8 +23,8 @@
 // warps scan group ids (and the last slots' positions) into a list of kept slots, in
 // rounds, up to four tiles ahead; four gather the tiles; one issues the products;
 // eight or sixteen (two or four a TMEM lane quadrant, each for a part of the rows)
-// form the weights.  The reference of a row is common to the block: it is set 10
-// below the largest t and moves only when a weight would pass 2^15, so the
+// form the weights.  The reference of a row is common to the block: it is set kBelow
+// below the largest t and moves only when a weight would pass 2^kTop, so the
 // accumulator in TMEM is rescaled hardly ever.
 //
 // A warp issues one cp.async of 512 gathered bytes in about 70 clocks, so the copies
@@ -37,7 +37,8 @@
 // then the second pass's (2,400 clocks a tile); 16 or 32 rows over long caches, the scan
 // (2,800 clocks for 20 pages) and the fixed 14,000 clocks from the launch to the
 // first weights and 6,000 of the join.  64 tokens for 2 sequences of 8K slots, 32
-// heads, with the weights accumulated: 117 us (146 MB of HBM traffic: 1.3 TB/s); four
+// heads, with the weights accumulated: 126 us (146 MB of HBM traffic: 1.2 TB/s; 116 with
+// weights of one f16 in four e5m2 parts, which differed from fp32 weights by 9e-4); four
 // tokens for 4 sequences of 64K slots, 64 / 8 heads: 35 us; a step of 16, 32, 64 query
 // heads a head at 32K: 14, 16, 22 us.
 #include <cooperative_groups.h>
@@ -54,6 +55,7 @@ constexpr int kD = 128;
 constexpr int kTileBytes = kTile * kD;
 constexpr int kMaxCluster = kMaxClusterBlocks;
 constexpr float kNoRef = -1e30f;       // reference of a row without kept slots
+constexpr float kBelow = 4.f, kTop = 8.f;   // e4m3 ends at 448: weights start at 2^4 and stay below 2^8
 
 template <int R, bool kMulti>
 struct TcCfg {
@@ -109,9 +111,9 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) 
                : "memory");
 }
 
-// kind::f8f6f4, A e4m3, fp32 accumulate; M = 128.
-constexpr uint32_t idesc_f8(int N, bool b_e5m2, bool a_mn_major, bool b_mn_major) {
-  return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+// kind::f8f6f4, A and B e4m3, fp32 accumulate; M = 128.
+constexpr uint32_t idesc_f8(int N, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
 // D[tmem] (+)= A[smem] * B[smem], 32 steps of the inner dimension
@@ -140,17 +142,32 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// The e5m2 parts of two f16 numbers, each part the upper byte of what is left: parts
-// 1, 2 of the first number, then of the second; and parts 3, 4.
-__device__ __forceinline__ void split_e5m2(uint32_t h, uint32_t& p12, uint32_t& p34) {
-  auto rest = [](uint32_t x) {
-    const uint32_t top = x & 0xff00ff00u;
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&top));
-    return *reinterpret_cast<const uint32_t*>(&r);
+// The e4m3 parts of two weights of at most 2^8: the first parts of both, then the second
+// ones; and the third and fourth ones.  A part leaves at most 2^-4 of what it stands for
+// (half a step of four bits), so sixteen times that fits the next one.  The rest behind
+// the first part is held in f16, at most 2^-16 of the weight off; what follows is exact.
+__device__ __forceinline__ void split_e4m3(float p0, float p1, uint32_t& c12, uint32_t& c34) {
+  const uint32_t c1 = float2_to_e4m3x2(p0, p1);
+  const float2 h = e4m3x2_to_float2(static_cast<uint16_t>(c1));
+  float d0, d1;
+  f2_unpack(f2_fma(f2_pack(h.x, h.y), f2_pack(-1.f, -1.f), f2_pack(p0, p1)), d0, d1);
+  const __half2 sixteen = __floats2half2_rn(16.f, 16.f);
+  __half2 r = __hmul2(__floats2half2_rn(d0, d1), sixteen);
+  auto part = [&]() {
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(*reinterpret_cast<const uint32_t*>(&r)));
+    return static_cast<uint32_t>(c);
   };
-  const uint32_t r1 = rest(h), r2 = rest(r1), r3 = rest(r2);
-  p12 = __byte_perm(h, r1, 0x7351);
-  p34 = __byte_perm(r2, r3, 0x7351);
+  auto rest = [&](uint32_t c) {
+    const uint32_t x = e4m3x2_to_f16x2(static_cast<uint16_t>(c));
+    r = __hmul2(__hsub2(r, *reinterpret_cast<const __half2*>(&x)), sixteen);
+  };
+  const uint32_t c2 = part();
+  rest(c2);
+  const uint32_t c3 = part();
+  rest(c3);
+  c12 = c1 | c2 << 16;
+  c34 = c3 | part() << 16;
 }
 
 // mbar_wait that reads the clock only after a few tries (the read costs as much as most
@@ -530,7 +547,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
 #pragma unroll
             for (int x = 0; x < kD / 32; ++x)
               mma_f8(tmem + (slot & 1) * 2 * R, desc_rows(kb + st * kTileBytes + x * 32, 128, 16),
-                     desc_rows(qb + x * 32, 128, 16), idesc_f8(2 * R, false, false, false), x > 0);
+                     desc_rows(qb + x * 32, 128, 16), idesc_f8(2 * R, false, false), x > 0);
             mma_commit(&qk_done[st]);
             mma_commit(&s_ready[slot & 1]);
             return true;
@@ -568,7 +585,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
               for (int x = 0; x < (cnt + 31) / 32; ++x)
                 mma_f8(tmem_o, desc_rows(vb + st * kTileBytes + x * 32 * kD, 128, 16),
                        desc_rows(pb + (it & 1) * C::kPBytes + x * 32 * C::kRowBytes, C::kRowBytes, kTile * 128),
-                       idesc_f8(4 * R, true, true, true), !(first && x == 0));
+                       idesc_f8(4 * R, true, true), !(first && x == 0));
             }
             if (pass == 0) mma_commit(&pv_done[st]);
             first = false;
@@ -692,7 +709,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           }
           // (three flags in turn: the one cleared here was last read before the previous meeting)
           if (quad == 0 && lane == 0) s_grow[part][(it + 1) % 3] = 0;
-          if (__any_sync(~0u, over > 15.f) && lane == 0) s_grow[part][it % 3] = 1;
+          if (__any_sync(~0u, over > kTop) && lane == 0) s_grow[part][it % 3] = 1;
           meet(&part_bar[part], part_phase);
           if (s_grow[part][it % 3]) {
             // some row's reference moves, by the row's own weights: rows do not touch each
@@ -711,7 +728,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
               const int rr = part * RH + lane;
               const int m = max(max(s_top[0][rr], s_top[1][rr]), max(s_top[2][rr], s_top[3][rr]));
               const float was = -s_minus[rr], highest = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
-              moved = highest > was + 15.f ? highest - 10.f : was;
+              moved = highest > was + kTop ? highest - kBelow : was;
               f = exp2_fast(was - moved);
             }
 #pragma unroll
@@ -728,7 +745,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
                 tmem_ld<8>(tmem_o + lanes + part * 4 * RH + y * 8, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int x = 0; x < 8; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * (x >> 1 & 1 ? f1 : f0));
+                for (int x = 0; x < 8; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * (x & 1 ? f1 : f0));
                 tmem_st8(tmem_o + lanes + part * 4 * RH + y * 8, v);
               }
               tmem_wait_st();
@@ -752,8 +769,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
               f2_unpack(f2_add(f2_pack(t[r + e], t[r + e + 1]), e ? m23 : m01), d0, d1);
               const float p0 = exp2_fast(d0), p1 = exp2_fast(d1);
               l2[(r + e) / 2] = f2_fma(f2_pack(p0, p1), vf2, l2[(r + e) / 2]);
-              const __half2 hp = __floats2half2_rn(p0, p1);
-              split_e5m2(*reinterpret_cast<const uint32_t*>(&hp), word[r + e], word[r + e + 1]);
+              split_e4m3(p0, p1, word[r + e], word[r + e + 1]);
             }
           }
           // this thread's 4 RH bytes of the key's row of P (R = 64: two chunks of 128 bytes)
@@ -831,15 +847,15 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         if (tiles > 0) {
 #pragma unroll
-          for (int y = 0; y < RH / 2; ++y) {           // two rows: parts 1, 2 of each, then parts 3, 4
+          for (int y = 0; y < RH / 2; ++y) {           // two rows: part 1 of both, then parts 2, 3, 4
             uint32_t v[8];
             tmem_ld<8>(tmem_o + lanes + part * 4 * RH + y * 8, v);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int r = part * RH + 2 * y + e;
-              float x = (__uint_as_float(v[2 * e]) + __uint_as_float(v[2 * e + 1])) +
-                        (__uint_as_float(v[4 + 2 * e]) + __uint_as_float(v[5 + 2 * e]));
+              float x = fmaf(fmaf(fmaf(__uint_as_float(v[6 + e]), 0.0625f, __uint_as_float(v[4 + e])), 0.0625f,
+                                  __uint_as_float(v[2 + e])), 0.0625f, __uint_as_float(v[e]));
               if (kMulti && (s_nan[kMulti ? r : 0][quad] >> lane & 1)) x = __int_as_float(0x7fffffff);
               const int to = r / share;
               *cluster.map_shared_rank(inbox + (rank * share + r - to * share) * kD + d, to) = x;
