@@ -423,8 +423,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float lse = s_lse[nt * 8 + 2 * cl + e];      // a large number for rows without kept slots
-            w0 += exp2_fast(t[nt][e] - lse);
-            w1 += exp2_fast(t[nt][2 + e] - lse);
+            // rows that do not keep the slot add nothing, also where their sum is NaN
+            w0 += mask0 & row_bit[nt][e] ? exp2_fast(t[nt][e] - lse) : 0.f;
+            w1 += mask1 & row_bit[nt][e] ? exp2_fast(t[nt][2 + e] - lse) : 0.f;
           }
         w0 += __shfl_xor_sync(~0u, w0, 1);
         w1 += __shfl_xor_sync(~0u, w1, 1);

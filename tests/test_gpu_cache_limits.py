@@ -1,6 +1,7 @@
 """Attention over the paged cache at the ends of its contract, against the fp64
-oracle: the bits that the softmax weights keep.  Bounds are those of
-test_gpu_cache.py; where one is tighter, the test derives it.
+oracle: the bits that the softmax weights keep, and NaN rows beside sound ones with
+the weights accumulated.  Bounds are those of test_gpu_cache.py; where one is
+tighter, the test derives it.
 """
 import numpy as np
 import pytest
@@ -74,3 +75,82 @@ def test_weights_keep_sixteen_bits(fz, G, d, T):
 def _power(x):
     """Twice the power of two at or below |x|: a bf16 rounding is off by at most 2^-9 of it."""
     return 2.0 * 2.0 ** np.floor(np.log2(np.maximum(np.abs(x), 1e-38)))
+
+
+# -------------------------------------------------------------------- NaN ---
+
+def _nan_case(fz, c, Q, gid, K, w, bad_rows, what):
+    """Attention with accumulate over a cache or queries with NaN: rows outside bad_rows
+    [H, T] have the outputs and lse of the sound call bit for bit, the others are NaN;
+    returns the mass."""
+    import torch
+    _, H, T, d = Q.shape
+    p = fz.make_params(1, H, 1, T, d, 64, 64, K, 1, w)
+    outs = []
+    for bad in (False, True):
+        cache = base._cache(fz, c[bad])
+        ws = fz.alloc_workspace_cache(p, cache)
+        O = torch.zeros((1, H, T, d), dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros((1, H, T), device="cuda")
+        q = what[bad]
+        fz.focus_cache_attention_fwd(p, base._dev(q, torch.bfloat16), base._dev(gid), cache, O, lse, ws, accumulate=True)
+        assert fz.focus_check_errors(ws) == 0
+        outs.append((O.float().cpu().numpy()[0], lse.cpu().numpy()[0], cache.mass.cpu().numpy()))
+    (o0, l0, _), (o1, l1, mass) = outs
+    assert np.array_equal(o0[~bad_rows], o1[~bad_rows]) and np.array_equal(l0[~bad_rows], l1[~bad_rows])
+    assert np.isnan(o1[bad_rows]).all() and np.isnan(l1[bad_rows]).all()
+    return mass
+
+
+def _mass_of_others(c, Q, gid, w, mass):
+    """NaN where token 0 (group 0: the even slots) keeps the slot, the oracle's elsewhere."""
+    T, d, n = Q.shape[2], Q.shape[3], len(mass)
+    ref = cr.attention(c, Q, gid, w, 1 / d ** 0.5)
+    got, slot, pos0 = ref["got"][cr.slots(c, 0, 0)[0], 0, cr.slots(c, 0, 0)[1]], np.arange(n), n - T
+    kept_by_0 = (slot <= pos0) & ((slot % 2 == 0) | (pos0 - slot < w))
+    assert np.isnan(mass[kept_by_0]).all()
+    off = np.abs(mass - got) - base._bounds(ref, d, "bf16")[1].max() * got - 2.0 ** -23 * np.abs(mass)
+    assert (off[~kept_by_0] <= 0).all() and (got[~kept_by_0] > 0).any()
+
+
+NAN_FORMS = [(2, 64, 2), (4, 128, 2), (8, 64, 2), (6, 128, 2), (16, 128, 2), (32, 128, 2), (1, 128, 16)]
+
+
+@pytest.mark.parametrize("H,d,T", NAN_FORMS)
+def test_nan_queries_leave_the_mass_of_other_tokens_slots(fz, H, d, T):
+    """Token 0 has group 0, the others group 1, and one query row of token 0 is NaN: slots
+    that only the other tokens keep have the mass of a call without it."""
+    n, w = 300, 4
+    c = base._make(4, 1, 1, d, [n], 2, 1)
+    c["mass"][:] = 0
+    page, row = cr.slots(c, 0, 0)
+    c["gid"][page, 0, row] = np.arange(n) % 2
+    gid = np.array([[[0] + [1] * (T - 1)]], np.int32)
+    Q = base._rows(np.random.default_rng(1), (1, H, T, d), "bf16", 0.2)
+    for v in (np.nan, np.inf):
+        q = Q.copy()
+        q[0, H // 2, 0, 3] = v
+        bad = np.zeros((H, T), bool)
+        bad[H // 2, 0] = True
+        mass = _nan_case(fz, (c, c), Q, gid, 2, w, bad, (Q, q))[page, 0, row]
+        _mass_of_others(c, Q, gid, w, mass)
+
+
+@pytest.mark.parametrize("H,d,T", NAN_FORMS)
+def test_nan_key_codes_leave_the_mass_of_other_tokens_slots(fz, H, d, T):
+    """A NaN in a key that only token 0 keeps: that token's rows and slots are NaN, every
+    other row, lse and mass is as without it."""
+    n, w = 300, 4
+    c = base._make(5, 1, 1, d, [n], 2, 1)
+    c["mass"][:] = 0
+    page, row = cr.slots(c, 0, 0)
+    c["gid"][page, 0, row] = np.arange(n) % 2
+    gid = np.array([[[0] + [1] * (T - 1)]], np.int32)
+    Q = base._rows(np.random.default_rng(1), (1, H, T, d), "bf16", 0.2)
+    broken = cr.copy(c)
+    broken["k"][page[10], 0, row[10], 5] = 127
+    broken["k"][page[200], 0, row[200], d - 1] = 255
+    bad = np.zeros((H, T), bool)
+    bad[:, 0] = True
+    mass = _nan_case(fz, (c, broken), Q, gid, 2, w, bad, (Q, Q))[page, 0, row]
+    _mass_of_others(c, Q, gid, w, mass)
