@@ -43,10 +43,12 @@ __device__ __forceinline__ float exp2_int(int e) {   // 2^e, -126 <= e <= 127
   return __int_as_float((e + 127) << 23);
 }
 
+constexpr int kMaxExp = 120;           // largest exponent that the append writes: fp32 ends below 448 * 2^120
+
 // Exponent of a stored scale, inside the range the append writes.
 __device__ __forceinline__ int scale_exp(float s) {
   const int e = static_cast<int>((__float_as_uint(s) >> 23) & 255u) - 127;
-  return min(max(e, kMinExp), 120);
+  return min(max(e, kMinExp), kMaxExp);
 }
 
 // Scales of K and V of a page as they are stored, and their exponents in two bytes.
@@ -65,6 +67,22 @@ struct PageScales {
 __device__ __forceinline__ int need_exp(uint32_t a) {
   const int x = static_cast<int>(a >> 23) - 127;
   return max(x - 8 + ((a & 0x7fffffu) > 0x600000u ? 1 : 0), kMinExp);
+}
+
+// The attention's running sums.  With t_j = s_j + e_j (log2; e_j the exponent of the
+// slot's value page) weights are 2^(t_j - ref) and the sum adds 2^(s_j - ref), which is
+// the weight times 2^-e_j: exact, unless the weight itself has fallen below the normals.
+// ref lies at most s_max + e_top, so for pages whose exponents are no further than this
+// apart that happens only below 2^-34 of the row's largest term.  Where the pages of a
+// head that have been scanned differ by more, the sum's terms are exponentials of their
+// own (kLift at the kernels keeps them in range for any exponents).
+constexpr int kScaleSpan = 96;
+constexpr float kNoRef = -1e30f;       // reference of a row without kept slots
+
+__device__ __forceinline__ float exp2_fast(float x) {   // 2^x, results below the normals are 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Two e4m3 codes (low byte first) <-> floats.  e4m3 fits f16 exactly.

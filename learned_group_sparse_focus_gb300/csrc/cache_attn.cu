@@ -31,8 +31,9 @@
 // Softmax: with v = code * 2^e per page, the running maximum is taken over
 // t_j = s_j + e_j (log2), so the weights 2^(t_j - ref) multiply raw codes and
 // stay in range for pages of any scale; the row sum adds 2^(t_j - ref) 2^-e_j in
-// fp32.  ref lies 7 below the maximum when it is set and is moved only when a
-// weight would pass 2^15, so f16's subnormals begin 2^-21 below the largest one.
+// fp32, or 2^(s_j - ref) where the scales lie far apart (kScaleSpan).  ref lies 7
+// below the maximum when it is set and is moved only when a weight would pass 2^15,
+// so f16's subnormals begin 2^-21 below the largest one.
 //
 // The warps' partials are joined in shared memory; each block then sends every
 // other block of the cluster the part of the rows that that one writes.
@@ -66,7 +67,10 @@ constexpr int kStages = 2;           // tiles in flight per warp
 constexpr int kMaxCluster = kMaxClusterBlocks;
 constexpr int kAhead = 16;           // pages whose group ids a warp holds in shared memory
 constexpr int kList = 256;           // entries of a warp's list of kept slots
-constexpr float kNoRef = -1e30f;     // reference of a row without kept slots
+// Sums are held times 2^kLift.  s_max - ref lies within [7 - 120, 15 + 64], so a row's
+// largest term within 2^-96 and 2^96: 2^30 slots of it do not overflow, and a term is
+// lost only below 2^-30 of it.
+constexpr int kLift = 17;
 static_assert(kList >= kPage + (kStages + 1) * kKeys && (kList & (kList - 1)) == 0, "list too short");
 
 template <typename T, int D, int NT>
@@ -94,13 +98,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// 2^x, results below the normals 0.
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // 8x8 transpose of 16-bit elements across the warp.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
@@ -303,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
     }
 
     int entries = 0;
+    int e_top = kMinExp, e_bot = kMaxExp;              // value exponents of the pages opened so far
     // Lists the kept slots of unit j.
     auto scan_page = [&]() {
       if (i == 0) {                                    // new group ids have to have landed
@@ -310,6 +308,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
         cp_async_wait<0>();
         __syncwarp();
         lane_exps = scales.bytes();
+        const int ve = static_cast<int8_t>(lane_exps >> 8);
+        e_top = max(e_top, __reduce_max_sync(~0u, lane_page >= 0 ? ve : kMinExp));
+        e_bot = min(e_bot, __reduce_min_sync(~0u, lane_page >= 0 ? ve : kMaxExp));
       }
       const int page = __shfl_sync(~0u, lane_page, i), exps = __shfl_sync(~0u, lane_exps, i);
       if (page >= 0) {
@@ -456,9 +457,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
             if (top > ref[nt][e] + 15.f) {          // by the row's own weights: rows do not touch each other
-              const float moved = top - 7.f, f = exp2_fast(ref[nt][e] - moved);
+              // in two steps: the factor may lie below the normals where the sum does not
+              const float moved = top - 7.f, fh = exp2_fast(0.5f * (ref[nt][e] - moved)), f = fh * fh;
               ref[nt][e] = moved;
-              sum[nt][e] *= f;
+              sum[nt][e] = sum[nt][e] * fh * fh;
 #pragma unroll
               for (int s = 0; s < C::kSteps; ++s) {
                 o[nt][s][e] *= f;
@@ -468,7 +470,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
           }
       }
       uint32_t pb[2][NT][2];                        // [part][..][keys 0-7 or 8-15]
-      const float vf0 = exp2_int(-ve0), vf1 = exp2_int(-ve1);
+      float vf0 = exp2_int(kLift - ve0), vf1 = exp2_int(kLift - ve1);
+      if (e_top - e_bot > kScaleSpan) {              // the same in the whole warp
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            sum[nt][y & 1] += exp2_fast(t[nt][y] - ref[nt][y & 1] + static_cast<float>(kLift - (y < 2 ? ve0 : ve1)));
+        vf0 = vf1 = 0.f;
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float p[4];
@@ -614,8 +624,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
         for (int w = 0; w < kWarps; ++w) {
           const float4 u = *reinterpret_cast<const float4*>(smem + w * C::kWarpBytes + r * C::kPitch + j * 16);
           if (s_l[w][r] == 0.f) continue;
-          const float f = exp2f(s_m[w][r] - M);
-          l += s_l[w][r] * f;
+          const float fh = exp2f(0.5f * (s_m[w][r] - M)), f = fh * fh;   // two steps for the sum, as above
+          l += s_l[w][r] * fh * fh;
           a.x += u.x * f; a.y += u.y * f; a.z += u.z * f; a.w += u.w * f;
         }
         const int to = i / share;
@@ -632,13 +642,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
         float M = v.x;
   #pragma unroll
         for (int y = 8; y > 0; y /= 2) M = fmaxf(M, __shfl_xor_sync(~0u, M, y));
-        const float f = v.y != 0.f ? exp2f(v.x - M) : 0.f;
-        float l = v.y != 0.f ? v.y * f : 0.f;
+        const float fh = v.y != 0.f ? exp2f(0.5f * (v.x - M)) : 0.f, f = fh * fh;
+        float l = v.y != 0.f ? v.y * fh * fh : 0.f;
   #pragma unroll
         for (int y = 8; y > 0; y /= 2) l += __shfl_xor_sync(~0u, l, y);
-        s_factor[from][r] = v.y != 0.f ? f / l : 0.f;
+        s_factor[from][r] = v.y != 0.f ? f / l * exp2_int(kLift) : 0.f;
         if (from == 0) {
-          const float lse = l != 0.f ? M + log2f(l) : -INFINITY;
+          const float lse = l != 0.f ? M + (log2f(l) - kLift) : -INFINITY;
           s_lse[r] = l != 0.f ? lse : -kNoRef;
           if (rank == 0 && L.lse && r0 + r < rows)
             L.lse[(static_cast<size_t>(b) * L.H + h * G + (r0 + r) % G) * L.n + (r0 + r) / G] = lse * 0.6931471805599453f;

@@ -37,9 +37,9 @@
 // then the second pass's (2,400 clocks a tile); 16 or 32 rows over long caches, the scan
 // (2,800 clocks for 20 pages) and the fixed 14,000 clocks from the launch to the
 // first weights and 6,000 of the join.  64 tokens for 2 sequences of 8K slots, 32
-// heads, with the weights accumulated: 126 us (146 MB of HBM traffic: 1.2 TB/s; 116 with
+// heads, with the weights accumulated: 128 us (146 MB of HBM traffic: 1.1 TB/s; 116 with
 // weights of one f16 in four e5m2 parts, which differed from fp32 weights by 9e-4); four
-// tokens for 4 sequences of 64K slots, 64 / 8 heads: 35 us; a step of 16, 32, 64 query
+// tokens for 4 sequences of 64K slots, 64 / 8 heads: 36 us; a step of 16, 32, 64 query
 // heads a head at 32K: 14, 16, 22 us.
 #include <cooperative_groups.h>
 
@@ -54,8 +54,10 @@ constexpr int kTile = 128;             // keys of a tile
 constexpr int kD = 128;
 constexpr int kTileBytes = kTile * kD;
 constexpr int kMaxCluster = kMaxClusterBlocks;
-constexpr float kNoRef = -1e30f;       // reference of a row without kept slots
 constexpr float kBelow = 4.f, kTop = 8.f;   // e4m3 ends at 448: weights start at 2^4 and stay below 2^8
+// Sums are held times 2^kLift: s_max - ref lies within [4 - 120, 8 + 64], so a row's
+// largest term within 2^-92 and 2^96, and a term is lost only below 2^-34 of it.
+constexpr int kLift = 24;
 
 template <int R, bool kMulti>
 struct TcCfg {
@@ -131,12 +133,6 @@ __device__ __forceinline__ uint64_t desc_rows(uint32_t saddr, int row_bytes, uin
          static_cast<uint64_t>((8 * row_bytes) >> 4) << 32 | static_cast<uint64_t>(1) << 46 | swizzle << 61;
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {   // results below the normals are 0
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Arrives on `bar` (counted in its arrivals) when this thread's cp.async so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -194,9 +190,12 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
   __shared__ uint64_t k_full[kStages], v_full[kStages], qk_done[kStages], pv_done[kStages], s_ready[2], p_ready[2];
   __shared__ uint64_t listed[kListed], used[kListed];  // a tile's entries are in the list; the weight warps have read them
   __shared__ uint64_t part_bar[kParts], soft_bar, scan_bar; // the four warps of a part; all weight warps; the scan's
-  __shared__ int s_found[2][kScanWarps];               // slots that a scan warp lists in a round
+  __shared__ uint2 s_found[2][kScanWarps];             // slots that a scan warp lists in a round, and its scales' range
   __shared__ int s_grow[kParts][3];                    // some reference of the part moves in this tile
-  __shared__ int s_cnt[8];                             // keys of a tile (by slot modulo 8); 0 ends a pass
+  // Keys of a tile (by slot modulo 8), and kWide where the scales scanned by then lie more
+  // than kScaleSpan apart; 0 ends a pass.
+  __shared__ int s_cnt[8];
+  constexpr int kWide = 256;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort_word;
   __shared__ __align__(16) float s_factor[R], s_minus[R], s_lse[R];   // the references and log2 sums, negated
@@ -285,6 +284,10 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
     };
     uint8_t* ids = smem + C::kIds + v * 2 * kAhead * kPage * 2;      // two batches of kAhead pages
     int next_page = -1, lane_page = -1, lane_exps = 0, entry = 0;
+    // Value exponents of the pages begun: the largest + 64 and 120 - the smallest in two
+    // 16-bit halves, of this warp and of all scan warps.
+    uint32_t my_range = 0, range = 0;
+    auto wide = [&]() { return static_cast<int>((range & 0xffffu) + (range >> 16)) - (kMaxExp - kMinExp) > kScaleSpan; };
     PageScales next_scales{1.f, 1.f};
     auto fetch = [&](int x) {                      // starts on pages x ... x + kAhead - 1, and on the table behind them
       next_page = -1;
@@ -381,6 +384,10 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           if (x % kAhead == 0) {                       // a new batch: it becomes current, the next one is fetched
             lane_page = next_page;
             lane_exps = next_scales.bytes();
+            const int ve = static_cast<int8_t>(lane_exps >> 8);
+            const uint32_t high = __reduce_max_sync(~0u, lane_page >= 0 ? static_cast<uint32_t>(ve - kMinExp) : 0u);
+            const uint32_t low = __reduce_max_sync(~0u, lane_page >= 0 ? static_cast<uint32_t>(kMaxExp - ve) : 0u);
+            my_range = __vmaxu2(my_range, high | low << 16);
             fetch(x + kAhead);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncwarp();
@@ -442,12 +449,14 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
             if (lane >= y) sum += u;
           }
           const int turn = x / kPages & 1;
-          if (lane == 31) s_found[turn][v] = sum;
+          if (lane == 31) s_found[turn][v] = make_uint2(sum, my_range);
           meet(&scan_bar, scan_phase);
           int at = entries + sum - mine;
 #pragma unroll
           for (int w = 0; w < kScanWarps; ++w) {
-            const int found = s_found[turn][w];
+            const uint2 word = s_found[turn][w];
+            const int found = word.x;
+            range = __vmaxu2(range, word.y);
             if (w < v) at += found;
             entries += found;
           }
@@ -469,7 +478,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           if (it >= kListed) wait(&used[it % kListed], (it / kListed + 1) & 1, abort, L.err);
           while (entries < (tile + 1) * kTile && !scanned()) scan_round();
           const int cnt = max(min(kTile, entries - tile * kTile), 0);
-          if (v == 0 && lane == 0) s_cnt[it & 7] = cnt;
+          if (v == 0 && lane == 0) s_cnt[it & 7] = cnt > 0 && wide() ? cnt | kWide : cnt;
           __syncwarp();
           if (lane == 0) mbar_arrive(&listed[it % kListed]);       // with every warp's: the tile's entries are there
           if (cnt == 0 || *abort) {
@@ -494,7 +503,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           const int st = it % kStages;
           const uint32_t parity = (it / kStages + 1) & 1;
           const bool ok = __all_sync(~0u, wait(&listed[it % kListed], (it / kListed) & 1, abort, L.err));
-          const int cnt = ok ? s_cnt[it & 7] : 0;
+          const int cnt = ok ? s_cnt[it & 7] & (kWide - 1) : 0;
           const int base = (tile * kTile & (kList - 1)) + row0;
           uint32_t from[kSteps];
 #pragma unroll
@@ -562,7 +571,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           while (have) {
             const uint32_t vi = it - skip;
             const int st = vi % kStages;
-            const int cnt = s_cnt[it & 7];
+            const int cnt = s_cnt[it & 7] & (kWide - 1);
             // The next tile's S if its K comes before this tile's P (its S buffer was read
             // before P of slot it - 1 was ready); else after this tile's product.
             bool next = false, asked = false;
@@ -620,7 +629,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           const uint32_t vi = it - skip;
           const int st = vi % kStages, buf = it & 1;
           const bool ok = wait(&s_ready[buf], (it >> 1) & 1, abort, L.err);
-          const int cnt = ok ? s_cnt[it & 7] : 0;
+          const int tile_word = ok ? s_cnt[it & 7] : 0, cnt = tile_word & (kWide - 1);
           if (__any_sync(~0u, cnt == 0)) {
             if (lane == 0) {
               mbar_arrive(&p_ready[buf]);
@@ -723,24 +732,28 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
             }
             if (lane < RH) s_top[quad][part * RH + lane] = top;
             meet(&part_bar[part], part_phase);
-            float moved = 0.f, f = 1.f;
+            float moved = 0.f, fh = 1.f;               // the factor's root: it may lie below the normals where sums do not
             if (lane < RH) {
               const int rr = part * RH + lane;
               const int m = max(max(s_top[0][rr], s_top[1][rr]), max(s_top[2][rr], s_top[3][rr]));
               const float was = -s_minus[rr], highest = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
               moved = highest > was + kTop ? highest - kBelow : was;
-              f = exp2_fast(was - moved);
+              fh = exp2_fast(0.5f * (was - moved));
             }
 #pragma unroll
-            for (int r = 0; r < RH; r += 2)
-              l2[r / 2] = f2_mul(l2[r / 2], f2_pack(__shfl_sync(~0u, f, r), __shfl_sync(~0u, f, r + 1)));
+            for (int r = 0; r < RH; r += 2) {
+              const uint64_t fh2 = f2_pack(__shfl_sync(~0u, fh, r), __shfl_sync(~0u, fh, r + 1));
+              l2[r / 2] = f2_mul(f2_mul(l2[r / 2], fh2), fh2);
+            }
             if (tile > 0) {
               mbar_wait(&pv_done[(vi - 1) % kStages], ((vi - 1) / kStages) & 1, abort, L.err);
               tc_fence_after();
 #pragma unroll
               for (int y = 0; y < RH / 2; ++y) {       // two rows, eight columns
-                const float f0 = __shfl_sync(~0u, f, 2 * y), f1 = __shfl_sync(~0u, f, 2 * y + 1);
+                float f0 = __shfl_sync(~0u, fh, 2 * y), f1 = __shfl_sync(~0u, fh, 2 * y + 1);
                 if (f0 == 1.f && f1 == 1.f) continue;
+                f0 *= f0;
+                f1 *= f1;
                 uint32_t v[8];
                 tmem_ld<8>(tmem_o + lanes + part * 4 * RH + y * 8, v);
                 tmem_wait_ld();
@@ -756,7 +769,16 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           }
           if (tile > 1)                                // P of the slot before the last one has been used
             wait(&pv_done[(vi - 2) % kStages], ((vi - 2) / kStages) & 1, abort, L.err);
-          const float vf = exp2_int(-static_cast<int8_t>(ex >> 8));
+          float vf = exp2_int(kLift - static_cast<int8_t>(ex >> 8));
+          if (tile_word & kWide) {                     // the sum's terms on their own (the same in all warps)
+            const float up = static_cast<float>(kLift) - ve;
+#pragma unroll
+            for (int r = 0; r < RH; r += 2) {
+              const float t0 = t[r] + s_minus[part * RH + r] + up, t1 = t[r + 1] + s_minus[part * RH + r + 1] + up;
+              l2[r / 2] = f2_add(l2[r / 2], f2_pack(exp2_fast(t0), exp2_fast(t1)));
+            }
+            vf = 0.f;
+          }
           const uint64_t vf2 = f2_pack(vf, vf);
           uint32_t word[RH];
 #pragma unroll
@@ -876,11 +898,14 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
         float M = kNoRef, l = 0.f;
         for (int x = 0; x < cs; ++x) M = fmaxf(M, s_all[x][r].x);
         for (int x = 0; x < cs; ++x)
-          if (s_all[x][r].y != 0.f) l += s_all[x][r].y * exp2f(s_all[x][r].x - M);
-        const float lse = l != 0.f ? M + log2f(l) : -INFINITY;
+          if (s_all[x][r].y != 0.f) {
+            const float fh = exp2f(0.5f * (s_all[x][r].x - M));
+            l += s_all[x][r].y * fh * fh;
+          }
+        const float lse = l != 0.f ? M + (log2f(l) - kLift) : -INFINITY;
         s_lse[r] = l != 0.f ? -lse : kNoRef;
         for (int x = 0; x < cs; ++x)
-          s_weight[x][r] = s_all[x][r].y != 0.f ? exp2f(s_all[x][r].x - M) / l : 0.f;
+          s_weight[x][r] = s_all[x][r].y != 0.f ? exp2f(s_all[x][r].x - M) / l * exp2_int(kLift) : 0.f;
         if (rank == 0 && L.lse && r < live)
           L.lse[(static_cast<size_t>(b) * L.H + h * G + (r0 + r) % G) * L.n + (r0 + r) / G] = lse * 0.6931471805599453f;
       }

@@ -1,7 +1,8 @@
 """Attention over the paged cache at the ends of its contract, against the fp64
-oracle: the bits that the softmax weights keep, and NaN rows beside sound ones with
-the weights accumulated.  Bounds are those of test_gpu_cache.py; where one is
-tighter, the test derives it.
+oracle: the bits that the softmax weights keep, pages whose scales lie as far
+apart as the format allows, and NaN rows beside sound ones with the weights
+accumulated.  Bounds are those of test_gpu_cache.py; where one is tighter, the
+test derives it.
 """
 import numpy as np
 import pytest
@@ -75,6 +76,33 @@ def test_weights_keep_sixteen_bits(fz, G, d, T):
 def _power(x):
     """Twice the power of two at or below |x|: a bf16 rounding is off by at most 2^-9 of it."""
     return 2.0 * 2.0 ** np.floor(np.log2(np.maximum(np.abs(x), 1e-38)))
+
+
+# ----------------------------------------------------------------- scales ---
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,d,T", FORMS)
+@pytest.mark.parametrize("pages", [4, 300])
+def test_value_scales_as_far_apart_as_the_format_allows(fz, dtype, G, d, T, pages):
+    """Exponents -64 to 120 side by side, in rising, falling and random order: every slot
+    counts in the sum, the lse and the mass, however small its page's values are.  With
+    300 pages a warp or a block meets several scales itself."""
+    rng = np.random.default_rng(pages + G)
+    K = 1 if pages == 4 else 3
+    for order in ("up", "down", "any"):
+        c = _random_cache(G, 1, 1, d, pages, K)
+        e = np.array([-64, 0, 75, 118])[np.arange(pages) * 4 // pages]
+        if order != "up":
+            e = e[::-1] if order == "down" else rng.permutation(np.tile(np.array([-64, -63, 3, 60, 70, 118]), pages)[:pages])
+        c["v_scale"][c["table"][0], 0] = 2.0 ** e.astype(np.float64)
+        c["v"] = np.where(c["v"] & 127 > 0x70, 0x38, c["v"]).astype(np.uint8)      # at most 128: |v| <= 2^125
+        c["k_scale"][:] = 2.0 ** -8
+        if order == "any":
+            c["v"][c["table"][0][e == -64]] = 0
+        Q = base._rows(rng, (1, G, T, d), dtype, 0.2)
+        Q[:, 0] = 0.0                                                              # a row of equal logits
+        gid = rng.integers(0, K, (1, 1, T)).astype(np.int32)
+        base._check_attention(fz, c, Q, gid, K, 100, dtype)
 
 
 # -------------------------------------------------------------------- NaN ---
