@@ -62,12 +62,18 @@ struct PageScales {
   __device__ __forceinline__ int bytes() const { return (scale_exp(k) & 0xff) | (scale_exp(v) & 0xff) << 8; }
 };
 
-// Least e >= kMinExp with a <= 448 * 2^e = 1.75 * 2^(e + 8), from the bits of a
-// finite a >= 0.  Anything below 2^-56 needs no more than kMinExp.
-__device__ __forceinline__ int need_exp(uint32_t a) {
+// Least e >= least with a <= 448 * 2^e = 1.75 * 2^(e + 8), from the bits of a finite
+// a >= 0.  For a page anything below 2^-56 needs no more than kMinExp.
+__device__ __forceinline__ int need_exp(uint32_t a, int least = kMinExp) {
   const int x = static_cast<int>(a >> 23) - 127;
-  return max(x - 8 + ((a & 0x7fffffu) > 0x600000u ? 1 : 0), kMinExp);
+  return max(x - 8 + ((a & 0x7fffffu) > 0x600000u ? 1 : 0), least);
 }
+
+// Least exponent that a query row is scaled by.  There bf16 numbers, multiples of 2^-133,
+// are multiples of 2^-10 and whole in either kernel's parts, fp32 rows of normal numbers
+// (2^-3 or more) keep 22 bits in two f16 parts, and the row's factor 2^e * scale * log2(e)
+// is still a normal number for the usual scale.
+constexpr int kMinQueryExp = -123;
 
 // The attention's running sums.  With t_j = s_j + e_j (log2; e_j the exponent of the
 // slot's value page) weights are 2^(t_j - ref) and the sum adds 2^(s_j - ref), which is

@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
       finite = (__ballot_sync(~0u, finite) >> (lane & ~3) & 15) == 15;
       top = max(top, __shfl_xor_sync(~0u, top, 1));
       top = max(top, __shfl_xor_sync(~0u, top, 2));
-      const int eq = min(max(static_cast<int>(top >> 23) - 127 - 13, -110), 115);   // |q| 2^-eq < 2^14
+      const int eq = min(max(static_cast<int>(top >> 23) - 127 - 13, kMinQueryExp), 115);   // |q| 2^-eq < 2^14
       const float down = exp2_int(-eq);
 #pragma unroll
       for (int s = 0; s < C::kSteps; ++s)

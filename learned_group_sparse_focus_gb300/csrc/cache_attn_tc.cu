@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
         }
         top = __reduce_max_sync(~0u, top);
         finite = __all_sync(~0u, finite);
-        const int eq = need_exp(top);
+        const int eq = need_exp(top, kMinQueryExp);
         const float down = exp2_int(-eq);
         uint32_t part[2];
         const uint16_t a = float2_to_e4m3x2(f[0] * down, f[1] * down), c = float2_to_e4m3x2(f[2] * down, f[3] * down);

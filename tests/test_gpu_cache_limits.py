@@ -1,8 +1,8 @@
 """Attention over the paged cache at the ends of its contract, against the fp64
 oracle: the bits that the softmax weights keep, pages whose scales lie as far
-apart as the format allows, and NaN rows beside sound ones with the weights
-accumulated.  Bounds are those of test_gpu_cache.py; where one is tighter, the
-test derives it.
+apart as the format allows, the smallest and largest queries, and NaN rows beside
+sound ones with the weights accumulated.  Bounds are those of test_gpu_cache.py;
+where one is tighter, the test derives it.
 """
 import numpy as np
 import pytest
@@ -103,6 +103,25 @@ def test_value_scales_as_far_apart_as_the_format_allows(fz, dtype, G, d, T, page
         Q[:, 0] = 0.0                                                              # a row of equal logits
         gid = rng.integers(0, K, (1, 1, T)).astype(np.int32)
         base._check_attention(fz, c, Q, gid, K, 100, dtype)
+
+
+# ---------------------------------------------------------------- queries ---
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,d,T", FORMS)
+def test_smallest_and_largest_queries(fz, dtype, G, d, T):
+    """Rows down to the least normal numbers against keys near the largest, and the other
+    way round: logits of order one."""
+    rng = np.random.default_rng(G * T + d)
+    for e in (120, 114, 100, 70, 0, -64):
+        c = _random_cache(G + e + 64, 1, 1, d, 5, 2)
+        c["k"] = np.where(c["k"] & 127 > 0x70, 0x38, c["k"]).astype(np.uint8)
+        c["k_scale"][:] = 2.0 ** e
+        c["v_scale"][:] = 2.0 ** -3
+        Q = base._rows(rng, (1, G, T, d), dtype, 0.0)
+        Q = (Q.astype(np.float64) * 2.0 ** max(-e - 4, -122)).astype(np.float32)
+        gid = rng.integers(0, 2, (1, 1, T)).astype(np.int32)
+        base._check_attention(fz, c, Q, gid, 2, 60, dtype)
 
 
 # -------------------------------------------------------------------- NaN ---
