@@ -114,9 +114,6 @@ focus_status_t ensure_setup() {
     if (setup_attn_kernels() != cudaSuccess) return FOCUS_ERR_CUDA;
     if (setup_bwd_tc_kernels() != cudaSuccess) return FOCUS_ERR_CUDA;
     if (setup_sinkhorn_kernels() != cudaSuccess) return FOCUS_ERR_CUDA;
-    if (setup_cache_evict(dev) != cudaSuccess || setup_cache_attn(dev) != cudaSuccess ||
-        setup_cache_attn_tc(dev) != cudaSuccess)
-      return FOCUS_ERR_CUDA;
     g_ready[dev] = true;
   }
   return FOCUS_OK;
@@ -141,13 +138,15 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, u
 
 focus_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? FOCUS_OK : FOCUS_ERR_CUDA; }
 
-// SMs of the current device (valid after ensure_setup).
-int current_device() {                 // after ensure_setup: in range
+// Index of the current device, or -1: none, or one past those that the library keeps
+// figures for.  The cache calls need no more set-up than this: their kernels ask for
+// their own at their first launch on a device.
+int device_index() {
   int dev = 0;
-  cudaGetDevice(&dev);
-  return dev;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices ? dev : -1;
 }
 
+// SMs of the current device (valid after ensure_setup).
 int sm_count() {
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1146,7 +1145,6 @@ focus_status_t focus_cache_append(const focus_params_t* p, const void* K, const 
     if (!x || !aligned16(x)) return FOCUS_ERR_INVALID_ARG;
   if (!aligned16(n_new)) return FOCUS_ERR_INVALID_ARG;
   if (len_out == next_out || len_out == cache->next || next_out == cache->len) return FOCUS_ERR_INVALID_ARG;
-  if (focus_status_t s = ensure_setup()) return s;
   CacheAppendLaunch L{K, V, gid, n_new, *cache, len_out, next_out, p->B, p->H_kv, p->n, p->d, p->A, p->K,
                       at<int>(ws, 64), at<int>(ws, 0)};
   return cuda_status(launch_cache_append(L, p->dtype, static_cast<cudaStream_t>(stream)));
@@ -1162,10 +1160,11 @@ focus_status_t focus_cache_attention_fwd(const focus_params_t* p, const void* Q,
     if (!x || !aligned16(x)) return FOCUS_ERR_INVALID_ARG;
   if (!aligned16(n_new) || !aligned16(lse_opt) || (accumulate && !cache->mass)) return FOCUS_ERR_INVALID_ARG;
   if (p->n > FOCUS_CACHE_MAX_QUERY) return FOCUS_ERR_UNSUPPORTED;
-  if (focus_status_t s = ensure_setup()) return s;
+  const int dev = device_index();
+  if (dev < 0) return FOCUS_ERR_CUDA;
   CacheAttnLaunch L{Q, gid, n_new, *cache, O, lse_opt, accumulate != 0,
                     p->B, p->H, p->H_kv, p->n, p->d, p->A, p->w > 1 ? p->w : 1,
-                    p->scale * 1.4426950408889634f, at<int>(ws, 0), current_device()};
+                    p->scale * 1.4426950408889634f, at<int>(ws, 0), dev};
   // More than eight query rows a key/value head go to the tcgen05 kernel (four drafted
   // tokens for 4 sequences of 64K, 32 rows: 35 us against 53; 64 tokens over 8K, 64
   // rows: 117 against 255); for eight or fewer its setup and single scan cost more
@@ -1183,9 +1182,10 @@ focus_status_t focus_cache_evict(const focus_params_t* p, int32_t budget, int32_
   if (!cache_ok(dst) || !src->mass || !dst->mass || dst->table == src->table) return FOCUS_ERR_INVALID_ARG;
   if (budget < 1 || recent < 0 || recent > budget) return FOCUS_ERR_INVALID_ARG;
   if (static_cast<long long>(dst->max_pages) * kPage < budget) return FOCUS_ERR_INVALID_ARG;
-  if (focus_status_t s = ensure_setup()) return s;
+  const int dev = device_index();
+  if (dev < 0) return FOCUS_ERR_CUDA;
   CacheEvictLaunch L{*src, *dst, p->B, p->H_kv, p->d, budget, recent, at<int32_t>(ws, kAlign), at<int>(ws, 0),
-                     current_device()};
+                     dev};
   return cuda_status(launch_cache_evict(L, static_cast<cudaStream_t>(stream)));
 }
 

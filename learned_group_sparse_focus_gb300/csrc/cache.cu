@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(CacheEvictLau
   }
 }
 
-ClusterFit g_select_fit[kMaxDevices];
+ClusterFits g_select_fits;
 
 // One block per destination page and head.
 template <int D>
@@ -438,10 +438,6 @@ __global__ void __launch_bounds__(kThreads, 8) cache_copy_kernel(CacheEvictLaunc
 
 }  // namespace
 
-cudaError_t setup_cache_evict(int device) {
-  return cluster_fit(reinterpret_cast<const void*>(cache_select_kernel), kSelThreads, kSelSmem, &g_select_fit[device]);
-}
-
 cudaError_t launch_cache_append(const CacheAppendLaunch& L, int dtype, cudaStream_t st) {
   // n new slots from anywhere in a page touch at most this many pages
   const dim3 grid((L.n + kPage - 2) / kPage + 1, L.H_kv, L.B);
@@ -457,9 +453,11 @@ cudaError_t launch_cache_append(const CacheAppendLaunch& L, int dtype, cudaStrea
 
 cudaError_t launch_cache_evict(const CacheEvictLaunch& L, cudaStream_t st) {
   // Blocks per (sequence, head): one wave, as long as each has kSelRun slots.
-  const ClusterFit& fit = g_select_fit[L.device];
+  const ClusterFit* fit;
+  if (cudaError_t e = g_select_fits.get(L.device, reinterpret_cast<const void*>(cache_select_kernel), kSelThreads, kSelSmem, &fit))
+    return e;
   int cs = 1, i = 0;
-  while (cs < kSelCluster && static_cast<long long>(L.B) * L.H_kv <= fit.n[i + 1] &&
+  while (cs < kSelCluster && static_cast<long long>(L.B) * L.H_kv <= fit->n[i + 1] &&
          2 * cs * kSelRun <= L.src.max_pages * kPage) {
     cs *= 2;
     ++i;

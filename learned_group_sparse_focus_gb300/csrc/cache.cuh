@@ -4,6 +4,9 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
+#include <mutex>
+
 #include "common.cuh"
 
 namespace focus {
@@ -166,7 +169,6 @@ struct ClusterFit {
   int n[5];
 };
 constexpr int kMaxClusterBlocks = 16;
-constexpr int kMaxDevices = 64;
 
 inline cudaError_t cluster_fit(const void* kernel, int threads, size_t smem, ClusterFit* fit) {
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) return e;
@@ -186,5 +188,27 @@ inline cudaError_t cluster_fit(const void* kernel, int threads, size_t smem, Clu
   }
   return cudaSuccess;
 }
+
+// A kernel's attributes and cluster figures per device, asked for at its first launch
+// there: a program that makes no such call loads no such kernel.
+class ClusterFits {
+ public:
+  cudaError_t get(int device, const void* kernel, int threads, size_t smem, const ClusterFit** fit) {
+    if (!ready_[device].load(std::memory_order_acquire)) {
+      std::lock_guard<std::mutex> lock(mu_);
+      if (!ready_[device].load(std::memory_order_relaxed)) {
+        if (cudaError_t e = cluster_fit(kernel, threads, smem, &fit_[device])) return e;
+        ready_[device].store(true, std::memory_order_release);
+      }
+    }
+    *fit = &fit_[device];
+    return cudaSuccess;
+  }
+
+ private:
+  std::mutex mu_;
+  std::atomic<bool> ready_[kMaxDevices] = {};
+  ClusterFit fit_[kMaxDevices];
+};
 
 }  // namespace focus

@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
 }
 
 template <typename T, int D, int NT, bool kMulti>
-ClusterFit g_fit[kMaxDevices];
+ClusterFits g_fits;
 
 template <typename T, int D, int NT, bool kMulti>
 cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
@@ -688,11 +688,14 @@ cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
   // since sequences differ in what they keep (16 sequences of up to 32K tokens: 78 us
   // with 2 blocks, 55 with 4, 72 with 8; 8 sequences of 1K tokens, 12 heads: 8.2 with 2,
   // 13.1 with 4).
-  const ClusterFit& fit = g_fit<T, D, NT, kMulti>[L.device];
+  const ClusterFit* fit;
+  if (cudaError_t e = g_fits<T, D, NT, kMulti>.get(L.device, reinterpret_cast<const void*>(cache_attn_kernel<T, D, NT, kMulti>),
+                                                   kThreads, Cfg<T, D, NT>::kSmem, &fit))
+    return e;
   const long long heads = static_cast<long long>(L.B) * L.H_kv;
   int cs = 1, i = 0;
   while (cs < kMaxCluster && cs * kWarps < L.c.max_pages) {
-    const int runs = fit.n[i + 1];
+    const int runs = fit->n[i + 1];
     if (heads > runs && (cs > 2 || heads > 2 * runs || L.c.max_pages < 2 * cs * kWarps * 16)) break;
     cs *= 2;
     ++i;
@@ -728,29 +731,7 @@ cudaError_t launch_rows(const CacheAttnLaunch& L, cudaStream_t st) {
   return wide ? launch<T, D, 2, true>(L, st) : launch<T, D, 1, true>(L, st);
 }
 
-template <typename T, int D, int NT, bool kMulti>
-cudaError_t prepare(int device) {
-  return cluster_fit(reinterpret_cast<const void*>(cache_attn_kernel<T, D, NT, kMulti>), kThreads, Cfg<T, D, NT>::kSmem,
-                     &g_fit<T, D, NT, kMulti>[device]);
-}
-
-template <typename T, int D>
-cudaError_t prepare_all(int device) {
-  if (cudaError_t e = prepare<T, D, 1, false>(device)) return e;
-  if (cudaError_t e = prepare<T, D, 1, true>(device)) return e;
-  if constexpr (Reach<T, D>::wide_single)
-    if (cudaError_t e = prepare<T, D, 2, false>(device)) return e;
-  return prepare<T, D, 2, true>(device);
-}
-
 }  // namespace
-
-cudaError_t setup_cache_attn(int device) {
-  if (cudaError_t e = prepare_all<__nv_bfloat16, 64>(device)) return e;
-  if (cudaError_t e = prepare_all<__nv_bfloat16, 128>(device)) return e;
-  if (cudaError_t e = prepare_all<float, 64>(device)) return e;
-  return prepare_all<float, 128>(device);
-}
 
 cudaError_t launch_cache_attn(const CacheAttnLaunch& L, int dtype, cudaStream_t st) {
   if (dtype == FOCUS_BF16) return L.d == 128 ? launch_rows<__nv_bfloat16, 128>(L, st) : launch_rows<__nv_bfloat16, 64>(L, st);

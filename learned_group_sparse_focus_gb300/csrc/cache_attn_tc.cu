@@ -938,7 +938,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
 }
 
 template <int R, bool kMulti>
-ClusterFit g_fit[kMaxDevices];
+ClusterFits g_fits;
 
 template <int R, bool kMulti>
 cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
@@ -949,11 +949,14 @@ cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
   // them 95 with 2, 58 with 4).  Several tokens keep more of each page and gain less
   // from it (four tokens, 64K: 8 sequences 59 us with 2, 69 with 4; 64 tokens, 8K:
   // 4 sequences 201 with 1, 222 with 2).
-  const ClusterFit& fit = g_fit<R, kMulti>[L.device];
+  const ClusterFit* fit;
+  if (cudaError_t e = g_fits<R, kMulti>.get(L.device, reinterpret_cast<const void*>(cache_attn_tc_kernel<R, kMulti>),
+                                            TcCfg<R, kMulti>::kThreads, TcCfg<R, kMulti>::kSmem, &fit))
+    return e;
   const long long heads = static_cast<long long>(L.B) * L.H_kv;
   int cs = 1, i = 0;
   while (cs < kMaxCluster && cs * 16 <= L.c.max_pages) {
-    const int runs = fit.n[i + 1];
+    const int runs = fit->n[i + 1];
     if (heads > runs && (kMulti || heads > 2 * runs || L.c.max_pages < 2 * cs * 128)) break;
     cs *= 2;
     ++i;
@@ -972,22 +975,7 @@ cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, cache_attn_tc_kernel<R, kMulti>, L);
 }
 
-template <int R, bool kMulti>
-cudaError_t prepare(int device) {
-  return cluster_fit(reinterpret_cast<const void*>(cache_attn_tc_kernel<R, kMulti>), TcCfg<R, kMulti>::kThreads,
-                     TcCfg<R, kMulti>::kSmem, &g_fit<R, kMulti>[device]);
-}
-
 }  // namespace
-
-cudaError_t setup_cache_attn_tc(int device) {
-  if (cudaError_t e = prepare<16, false>(device)) return e;
-  if (cudaError_t e = prepare<16, true>(device)) return e;
-  if (cudaError_t e = prepare<32, true>(device)) return e;
-  if (cudaError_t e = prepare<32, false>(device)) return e;
-  if (cudaError_t e = prepare<64, false>(device)) return e;
-  return prepare<64, true>(device);
-}
 
 cudaError_t launch_cache_attn_tc(const CacheAttnLaunch& L, cudaStream_t st) {
   const int rows = L.H / L.H_kv * L.n;

@@ -232,6 +232,7 @@ cudaError_t launch_bwd_permute_q(const BwdArgs& a, void* Qs, void* dOs, float* l
 cudaError_t launch_sinkhorn(const SinkhornLaunch& L, int iters, cudaStream_t st);
 
 // cache.cu, cache_attn.cu: the paged 8-bit key/value cache (layout: focus.h).
+constexpr int kMaxDevices = 64;   // devices that launch figures are kept for
 constexpr int kPage = FOCUS_CACHE_PAGE;
 constexpr int kMinExp = FOCUS_CACHE_MIN_EXP;
 
@@ -254,7 +255,6 @@ struct CacheEvictLaunch {
   int* err;
   int device;
 };
-cudaError_t setup_cache_evict(int device);
 cudaError_t launch_cache_evict(const CacheEvictLaunch& L, cudaStream_t st);
 
 struct CacheAttnLaunch {
@@ -270,11 +270,9 @@ struct CacheAttnLaunch {
   int* err;
   int device;
 };
-cudaError_t setup_cache_attn(int device);
 // cache_attn_tc.cu: bf16, d = 128; with several tokens a table of kCacheTableGroups
 // group ids, for K up to that.
 constexpr int kCacheTableGroups = 1024;
-cudaError_t setup_cache_attn_tc(int device);
 cudaError_t launch_cache_attn_tc(const CacheAttnLaunch& L, cudaStream_t st);
 cudaError_t launch_cache_attn(const CacheAttnLaunch& L, int dtype, cudaStream_t st);
 

@@ -201,3 +201,45 @@ def test_nan_key_codes_leave_the_mass_of_other_tokens_slots(fz, H, d, T):
     bad[:, 0] = True
     mass = _nan_case(fz, (c, broken), Q, gid, 2, w, bad, (Q, Q))[page, 0, row]
     _mass_of_others(c, Q, gid, w, mass)
+
+
+# ----------------------------------------------------------------- set-up ---
+
+PREFILL_FIRST = """
+import sys
+import time
+import torch
+sys.path.insert(0, {root!r})
+from learned_group_sparse_focus_gb300 import focus as fz
+bf = torch.bfloat16
+p = fz.make_params(1, 4, 2, 256, 64, 64, 32, 4, 1, 16)
+h, W, C = (torch.zeros(s, dtype=bf, device="cuda") for s in ((1, 256, 64), (1, 32, 64), (1, 4, 32)))
+gid = torch.zeros((1, 1, 256), dtype=torch.int32, device="cuda")
+ws = fz.alloc_workspace(p)
+fz.focus_assign(p, h, W, C, gid, ws)
+q = fz.make_params(1, 4, 2, 4, 64, 64, 32, 4, 1, 16)
+cache = fz.alloc_cache(q, 512)
+wc = fz.alloc_workspace_cache(q, cache)
+Q = torch.zeros((1, 4, 4, 64), dtype=bf, device="cuda")
+O, ids = torch.zeros_like(Q), gid[:, :, :4].contiguous()
+took = []
+for _ in range(20):
+    torch.cuda.synchronize()
+    start = time.perf_counter()
+    fz.focus_cache_attention_fwd(q, Q, ids, cache, O, None, wc)
+    took.append(time.perf_counter() - start)
+print(took[0] / sorted(took)[10])
+"""
+
+
+def test_the_prefill_does_not_set_up_the_cache_kernels():
+    """The cache's kernels are loaded and asked for their cluster figures by the first call
+    that launches them: it takes many times a later call's time on the host, also where
+    the process has already run the prefill."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", PREFILL_FIRST.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
+    assert float(done.stdout) > 6, done.stdout
