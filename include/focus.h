@@ -525,7 +525,8 @@ FOCUS_API focus_status_t focus_cache_attention_fwd(const focus_params_t* p, cons
  *   1 <= budget, 0 <= recent <= budget; both caches need mass; dst->max_pages
  *   must hold budget slots.  src and dst may share pools (the same arrays and
  *   n_pages) but no pages in use, and not the table; dst->len and dst->next may
- *   be src's.  dst's rows past the kept slots stay as they were. */
+ *   be src's own, not each other nor the other's source.  dst's rows past the
+ *   kept slots stay as they were. */
 FOCUS_API focus_status_t focus_cache_evict(const focus_params_t* p, int32_t budget, int32_t recent,
                                            const focus_cache_t* src, const focus_cache_t* dst,
                                            void* ws, size_t ws_bytes, void* stream);

@@ -1180,6 +1180,7 @@ focus_status_t focus_cache_evict(const focus_params_t* p, int32_t budget, int32_
                                  size_t ws_bytes, void* stream) {
   if (focus_status_t s = cache_args(p, src, ws, ws_bytes)) return s;
   if (!cache_ok(dst) || !src->mass || !dst->mass || dst->table == src->table) return FOCUS_ERR_INVALID_ARG;
+  if (dst->len == dst->next || dst->len == src->next || dst->next == src->len) return FOCUS_ERR_INVALID_ARG;
   if (budget < 1 || recent < 0 || recent > budget) return FOCUS_ERR_INVALID_ARG;
   if (static_cast<long long>(dst->max_pages) * kPage < budget) return FOCUS_ERR_INVALID_ARG;
   const int dev = device_index();

@@ -209,6 +209,18 @@ def test_append_counts_that_overlap_are_refused(fz):
     assert append(1 << 28, 1 << 28) == append(c.next, 1 << 28) == append(1 << 28, c.len) == append(c.next, c.len) == 1
 
 
+def test_eviction_counts_that_overlap_are_refused(fz):
+    """dst's counts may be src's own, not each other nor the other one's source: blocks
+    still read a sequence's next while others write their counts."""
+    p, lib, src = _params(fz), fz.lib(), _struct(fz)
+
+    def evict(length, nxt):
+        d = _struct(fz, table=1 << 25, len=length, next=nxt)
+        return lib.focus_cache_evict(ctypes.byref(p), 64, 8, ctypes.byref(src), ctypes.byref(d), 1 << 26, 1 << 40, None)
+
+    assert evict(1 << 28, 1 << 28) == evict(src.next, 1 << 28) == evict(1 << 28, src.len) == evict(src.next, src.len) == 1
+
+
 def test_cache_struct_matches_the_header(fz):
     assert ctypes.sizeof(fz.CacheStruct) == 10 * 8 + 2 * 4
     assert fz.lib().focus_status_string(7) == b"cache page, length or position out of range"
