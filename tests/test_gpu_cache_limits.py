@@ -1,7 +1,8 @@
 """Attention over the paged cache at the ends of its contract, against the fp64
 oracle: the bits that the softmax weights keep, pages whose scales lie as far
-apart as the format allows, the smallest and largest queries, and NaN rows beside
-sound ones with the weights accumulated.  Bounds are those of test_gpu_cache.py;
+apart as the format allows, the smallest and largest queries, NaN rows beside
+sound ones with the weights accumulated, and bad pages, guard zones and group ids
+per head in every form of the kernels.  Bounds are those of test_gpu_cache.py;
 where one is tighter, the test derives it.
 """
 import numpy as np
@@ -201,6 +202,97 @@ def test_nan_key_codes_leave_the_mass_of_other_tokens_slots(fz, H, d, T):
     bad[:, 0] = True
     mass = _nan_case(fz, (c, broken), Q, gid, 2, w, bad, (Q, Q))[page, 0, row]
     _mass_of_others(c, Q, gid, w, mass)
+
+
+# ----------------------------------------------- heads, pages and buffers ---
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,H_kv,d,T", [(1, 3, 64, 1), (4, 2, 128, 1), (12, 2, 128, 1), (40, 2, 128, 1), (2, 2, 128, 3),
+                                        (8, 2, 128, 3), (2, 2, 128, 64), (70, 2, 128, 2)])
+def test_a_group_id_for_each_key_value_head(fz, dtype, G, H_kv, d, T):
+    """A = H_kv: every head keeps by its own ids; two sequences, ragged new tokens, up to
+    three blocks of 64 rows."""
+    rng = np.random.default_rng(G + T)
+    c = base._make(G, 2, H_kv, d, [260, 131], 4, H_kv, dtype)
+    Q = base._rows(rng, (2, G * H_kv, T, d), dtype, 0.3)
+    gid = np.stack([rng.permutation(4)[:H_kv] for _ in range(2 * T)]).reshape(2, T, H_kv).transpose(0, 2, 1)
+    gid = np.ascontiguousarray(gid, np.int32)                 # heads of a token never share an id
+    base._check_attention(fz, c, Q, gid, 4, 9, dtype)
+    base._check_attention(fz, c, Q, gid, 4, 9, dtype, n_new=np.array([T, T // 2], np.int32))
+
+
+def test_lists_that_wrap_in_several_blocks_of_rows(fz):
+    """256 rows over more kept slots than the list holds: every block of rows scans again
+    for its second pass."""
+    rng = np.random.default_rng(9)
+    c = _random_cache(8, 1, 1, 128, 60, 2)
+    c["k_scale"][:] = 2.0 ** -8
+    Q = base._rows(rng, (1, 4, 64, 128), "bf16", 0.2)
+    base._check_attention(fz, c, Q, rng.integers(0, 2, (1, 1, 64)).astype(np.int32), 2, 30, "bf16")
+
+
+ALL_FORMS = FORMS + [(4, 128, 64)]
+
+
+@pytest.mark.parametrize("G,d,T", ALL_FORMS)
+def test_bad_pages_and_lengths_in_every_form(fz, G, d, T):
+    """A bad page's slots are skipped, a bad count is clamped, both are flagged; the other
+    sequence's outputs, lse and mass are the oracle's."""
+    import torch
+    n, w, H_kv = 333, 20, 2
+    c = base._make(7, 2, H_kv, d, [n, n], 2, 1)
+    c["mass"][:] = 0
+    rng = np.random.default_rng(1)
+    Q = base._rows(rng, (2, G * H_kv, T, d), "bf16", 0.2)
+    gid = rng.integers(0, 2, (2, 1, T)).astype(np.int32)
+    p = fz.make_params(2, G * H_kv, H_kv, T, d, 64, 64, 2, 1, w)
+    without = cr.copy(c)
+    without["gid"][c["table"][0, 1]] = 2                      # nobody keeps that page's slots
+    for page, ln in ((-5, None), (1 << 30, None), (None, 1 << 20), (None, -3)):
+        broken = cr.copy(c)
+        if page is not None:
+            broken["table"][0, 1] = page
+        if ln is not None:
+            broken["len"][0, 1] = ln
+        cache = base._cache(fz, broken)
+        ws = fz.alloc_workspace_cache(p, cache)
+        O = torch.zeros((2, G * H_kv, T, d), dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros((2, G * H_kv, T), device="cuda")
+        fz.focus_cache_attention_fwd(p, base._dev(Q, torch.bfloat16), base._dev(gid), cache, O, lse, ws, accumulate=True)
+        assert fz.focus_check_errors(ws) == 7
+        ref = cr.attention(without if page is not None else c, Q, gid, w, p.scale)
+        ds, r, _ = base._bounds(ref, d, "bf16")
+        sound = (0, 1) if page is not None else (1,)
+        mass, off = cache.mass.cpu().numpy(), lse.cpu().numpy() - ref["lse"]
+        for b in sound:
+            base._o_within(O, ref, d, "bf16", there=b)
+            assert (np.abs(off[b]) <= ds[b] + ref["kept"][b] * 2 * U + 2.0 ** -22 * (1 + np.abs(ref["lse"][b]))).all()
+            for h in range(H_kv):
+                at = c["table"][b, :-(-n // 64)], h
+                assert (np.abs(mass[at] - ref["got"][at]) <= r.max() * ref["got"][at] + 2.0 ** -23 * mass[at]).all()
+
+
+@pytest.mark.parametrize("G,d,T", ALL_FORMS)
+def test_attention_writes_stay_inside_their_buffers_in_every_form(fz, G, d, T):
+    """O, lse, mass and the workspace sit between guard bytes, the last tile is partial."""
+    import torch
+    from test_gpu_canary import Guarded
+    B, H_kv, w = 2, 2, 10
+    c = base._make(51, B, H_kv, d, [333, 63], 3, 1, spare=0)
+    c["mass"][:] = 0
+    mass = Guarded(c["mass"].shape, torch.float32, base._dev(c["mass"]))
+    cache = fz.Cache(**{k: mass.t if k == "mass" else base._dev(c[k]) for k in base.NAMES})
+    p = fz.make_params(B, G * H_kv, H_kv, T, d, 64, 64, 3, 1, w)
+    ws = Guarded((fz.focus_cache_workspace_bytes(p, cache),), torch.uint8)
+    fz.focus_workspace_init(ws.t)
+    rng = np.random.default_rng(2)
+    q = base._dev(base._rows(rng, (B, G * H_kv, T, d), "bf16"), torch.bfloat16)
+    gid = base._dev(rng.integers(0, 3, (B, 1, T)).astype(np.int32))
+    O, lse = Guarded(q.shape, torch.bfloat16), Guarded(q.shape[:3], torch.float32)
+    fz.focus_cache_attention_fwd(p, q, gid, cache, O.t, lse.t, ws.t, accumulate=True)
+    assert fz.focus_check_errors(ws.t) == 0
+    for x in (mass, ws, O, lse):
+        assert x.intact()
 
 
 # ----------------------------------------------------------------- set-up ---
