@@ -1165,12 +1165,14 @@ focus_status_t focus_cache_attention_fwd(const focus_params_t* p, const void* Q,
   CacheAttnLaunch L{Q, gid, n_new, *cache, O, lse_opt, accumulate != 0,
                     p->B, p->H, p->H_kv, p->n, p->d, p->A, p->w > 1 ? p->w : 1,
                     p->scale * 1.4426950408889634f, at<int>(ws, 0), dev};
-  // More than eight query rows a key/value head go to the tcgen05 kernel (four drafted
-  // tokens for 4 sequences of 64K, 32 rows: 35 us against 53; 64 tokens over 8K, 64
-  // rows: 117 against 255); for eight or fewer its setup and single scan cost more
-  // than they save (one step at 32K, 4 rows: 15 us against 11; 16 sequences of up to
-  // 32K with the weights accumulated: 140 with a block a head, against 55).
-  if (p->dtype == FOCUS_BF16 && p->d == 128 && p->H / p->H_kv * p->n > 8 && (p->n == 1 || p->K <= kCacheTableGroups))
+  // The mma.sync kernel takes up to 16 query rows of a key/value head in one pass, and
+  // there it is the faster one: 1 to 32 sequences of 8 heads with up to 16, 128 and 512
+  // pages, 4, 8, 12 and 16 rows of one token and of several, with and without the weights
+  // accumulated, 66 cases (16 rows of one token: 12 us against 15 for one sequence, 45
+  // against 47 for 16 and 110 against 130 for 32 of up to 32K tokens; four tokens of 4
+  // rows for 16 of them 101 against 126).  More rows are two passes or more there: 24 and
+  // 32 rows 21 against 18 us, 83 against 52 and 212 against 144; 64 rows 165 against 83.
+  if (p->dtype == FOCUS_BF16 && p->d == 128 && p->H / p->H_kv * p->n > kCacheRows && (p->n == 1 || p->K <= kCacheTableGroups))
     return cuda_status(launch_cache_attn_tc(L, static_cast<cudaStream_t>(stream)));
   return cuda_status(launch_cache_attn(L, p->dtype, static_cast<cudaStream_t>(stream)));
 }

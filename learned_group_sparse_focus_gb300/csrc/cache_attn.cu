@@ -714,20 +714,10 @@ cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, cache_attn_kernel<T, D, NT, kMulti>, L);
 }
 
-// More than eight rows of a single bf16 token with d = 128 go to cache_attn_tc.cu.
-template <typename T, int D>
-struct Reach {
-  static constexpr bool wide_single = !(std::is_same<T, __nv_bfloat16>::value && D == 128);
-};
-
 template <typename T, int D>
 cudaError_t launch_rows(const CacheAttnLaunch& L, cudaStream_t st) {
   const bool wide = L.H / L.H_kv * L.n > 8;
-  if (L.n == 1) {
-    if constexpr (Reach<T, D>::wide_single)
-      if (wide) return launch<T, D, 2, false>(L, st);
-    return launch<T, D, 1, false>(L, st);
-  }
+  if (L.n == 1) return wide ? launch<T, D, 2, false>(L, st) : launch<T, D, 1, false>(L, st);
   return wide ? launch<T, D, 2, true>(L, st) : launch<T, D, 1, true>(L, st);
 }
 

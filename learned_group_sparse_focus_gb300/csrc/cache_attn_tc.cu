@@ -1,6 +1,6 @@
 // Focus attention of new tokens over the paged 8-bit cache on the tcgen05 tensor
-// cores: bf16 tensors, d = 128 (contract: focus.h; cache_attn.cu has the form for
-// every other case).
+// cores: bf16 tensors, d = 128, more than 16 query rows a head (contract: focus.h;
+// cache_attn.cu has the form for every other case).
 //
 // The codes go into the products as they are, kind::f8f6f4, gathered into tiles of
 // 128 kept slots with cp.async (TMA's row gather took 80 clocks for four rows, 6 B a
@@ -14,7 +14,8 @@
 //                           with sums of their own: 2^-16 of a weight, and 2^-22
 //                           where that is more, which is 2^-26 of a row's largest
 //                           weight or less (see below)
-// R = 16, 32 or 64 query rows (tokens x query heads of the head).  With the keys
+// R = 32 or 64 query rows (tokens x query heads of the head; 16 or fewer are faster on
+// mma.sync).  With the keys
 // on the 128 side of both products nothing is padded but R, and a thread owns a
 // key: masks, scales and the weight's sum over rows need no exchange.
 //
@@ -34,13 +35,13 @@
 //
 // What bounds it now: 64 query rows, the weight warps' instructions (some 330 a
 // thread and tile over 16 rows each; 4,100 clocks a tile with the tensor pipe at 10%),
-// then the second pass's (2,400 clocks a tile); 16 or 32 rows over long caches, the scan
+// then the second pass's (2,400 clocks a tile); 32 rows over long caches, the scan
 // (2,800 clocks for 20 pages) and the fixed 14,000 clocks from the launch to the
 // first weights and 6,000 of the join.  64 tokens for 2 sequences of 8K slots, 32
 // heads, with the weights accumulated: 128 us (146 MB of HBM traffic: 1.1 TB/s; 116 with
 // weights of one f16 in four e5m2 parts, which differed from fp32 weights by 9e-4); four
-// tokens for 4 sequences of 64K slots, 64 / 8 heads: 36 us; a step of 16, 32, 64 query
-// heads a head at 32K: 14, 16, 22 us.
+// tokens for 4 sequences of 64K slots, 64 / 8 heads: 36 us; a step of 32 and 64 query
+// heads a head at 32K: 18 and 23 us.
 #include <cooperative_groups.h>
 
 #include "cache.cuh"
@@ -74,7 +75,7 @@ struct TcCfg {
   static constexpr int kSlots = R == 64 ? 4 : 8, kPages = kSlots / 2, kRound = kPages * kScanWarps;
   static constexpr int kList = R == 64 ? 1024 : 2048;          // entries of the block's list of kept slots
   static_assert(kList >= kRound * kPage + kListed * kTile && kStages < kListed, "list too short");
-  static constexpr int kRowBytes = R >= 32 ? 128 : 4 * R;      // P's bytes of a key, per chunk of N
+  static constexpr int kRowBytes = 128;                        // P's bytes of a key, per chunk of 32 rows
   static constexpr int kPBytes = kTile * 4 * R;
   static constexpr int kEntryBytes = kMulti ? 16 : 8;
   // byte offsets in dynamic shared memory
@@ -88,24 +89,16 @@ struct TcCfg {
   static constexpr int kCols = 8 * R;                          // TMEM: S twice, O
 };
 
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
-  static_assert(N == 4 || N == 8 || N == 16 || N == 32, "columns");
-  if constexpr (N == 32) {
-    tmem_ld32(addr, r);
-  } else if constexpr (N == 16) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(addr));
-  } else if constexpr (N == 8) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(addr));
-  } else {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
-  }
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
 }
 __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
@@ -125,12 +118,10 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, 
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
       ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
-// Shared-memory descriptor of an operand with rows of 128, 64 or 32 bytes and the
-// swizzle of that width; see sw128_desc.
-__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr, int row_bytes, uint32_t lbo) {
-  const uint64_t swizzle = row_bytes == 128 ? 2 : row_bytes == 64 ? 4 : 6;
+// Shared-memory descriptor of an operand with rows of 128 bytes; see sw128_desc.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr, uint32_t lbo) {
   return static_cast<uint64_t>((saddr >> 4) & 0x3fffu) | static_cast<uint64_t>((lbo >> 4) & 0x3fffu) << 16 |
-         static_cast<uint64_t>((8 * row_bytes) >> 4) << 32 | static_cast<uint64_t>(1) << 46 | swizzle << 61;
+         static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
 }
 
 // Arrives on `bar` (counted in its arrivals) when this thread's cp.async so far have landed.
@@ -555,8 +546,8 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
             tc_fence_after();
 #pragma unroll
             for (int x = 0; x < kD / 32; ++x)
-              mma_f8(tmem + (slot & 1) * 2 * R, desc_rows(kb + st * kTileBytes + x * 32, 128, 16),
-                     desc_rows(qb + x * 32, 128, 16), idesc_f8(2 * R, false, false), x > 0);
+              mma_f8(tmem + (slot & 1) * 2 * R, desc_rows(kb + st * kTileBytes + x * 32, 16),
+                     desc_rows(qb + x * 32, 16), idesc_f8(2 * R, false, false), x > 0);
             mma_commit(&qk_done[st]);
             mma_commit(&s_ready[slot & 1]);
             return true;
@@ -592,8 +583,8 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
               fence_proxy_async_smem();
               tc_fence_after();
               for (int x = 0; x < (cnt + 31) / 32; ++x)
-                mma_f8(tmem_o, desc_rows(vb + st * kTileBytes + x * 32 * kD, 128, 16),
-                       desc_rows(pb + (it & 1) * C::kPBytes + x * 32 * C::kRowBytes, C::kRowBytes, kTile * 128),
+                mma_f8(tmem_o, desc_rows(vb + st * kTileBytes + x * 32 * kD, 16),
+                       desc_rows(pb + (it & 1) * C::kPBytes + x * 32 * C::kRowBytes, kTile * C::kRowBytes),
                        idesc_f8(4 * R, true, true), !(first && x == 0));
             }
             if (pass == 0) mma_commit(&pv_done[st]);
@@ -658,8 +649,8 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           }
           const float kf = exp2_int(static_cast<int8_t>(ex)), ve = static_cast<float>(static_cast<int8_t>(ex >> 8));
           uint32_t hi[RH], lo[RH];
-          tmem_ld<RH>(tmem + lanes + buf * 2 * R + part * RH, hi);
-          tmem_ld<RH>(tmem + lanes + buf * 2 * R + R + part * RH, lo);
+          tmem_ld(tmem + lanes + buf * 2 * R + part * RH, hi);
+          tmem_ld(tmem + lanes + buf * 2 * R + R + part * RH, lo);
           tmem_wait_ld();
           if (pass == 1) {
             tc_fence_before();
@@ -755,7 +746,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
                 f0 *= f0;
                 f1 *= f1;
                 uint32_t v[8];
-                tmem_ld<8>(tmem_o + lanes + part * 4 * RH + y * 8, v);
+                tmem_ld(tmem_o + lanes + part * 4 * RH + y * 8, v);
                 tmem_wait_ld();
 #pragma unroll
                 for (int x = 0; x < 8; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * (x & 1 ? f1 : f0));
@@ -797,10 +788,9 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
           // this thread's 4 RH bytes of the key's row of P (R = 64: two chunks of 128 bytes)
           constexpr int kPieces = RH / 4, kInRow = C::kRowBytes / 16;
           uint8_t* prow = smem + C::kP + buf * C::kPBytes + part * kPieces / kInRow * kTile * C::kRowBytes + key * C::kRowBytes;
-          const int sw = C::kRowBytes == 128 ? key & 7 : C::kRowBytes == 64 ? key >> 1 & 3 : key >> 2 & 1;
 #pragma unroll
           for (int c = 0; c < kPieces; ++c)
-            *reinterpret_cast<uint4*>(prow + ((part * kPieces % kInRow + c) ^ sw) * 16) =
+            *reinterpret_cast<uint4*>(prow + ((part * kPieces % kInRow + c) ^ (key & 7)) * 16) =
                 make_uint4(word[4 * c], word[4 * c + 1], word[4 * c + 2], word[4 * c + 3]);
           if (kMulti) {
             // A row that does not keep a key has weight 0 for it, and 0 * NaN would reach
@@ -871,7 +861,7 @@ __global__ void __launch_bounds__(TcCfg<R, kMulti>::kThreads, 1)
 #pragma unroll
           for (int y = 0; y < RH / 2; ++y) {           // two rows: part 1 of both, then parts 2, 3, 4
             uint32_t v[8];
-            tmem_ld<8>(tmem_o + lanes + part * 4 * RH + y * 8, v);
+            tmem_ld(tmem_o + lanes + part * 4 * RH + y * 8, v);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -979,11 +969,7 @@ cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
 
 cudaError_t launch_cache_attn_tc(const CacheAttnLaunch& L, cudaStream_t st) {
   const int rows = L.H / L.H_kv * L.n;
-  if (L.n == 1) {
-    if (rows <= 16) return launch<16, false>(L, st);
-    return rows <= 32 ? launch<32, false>(L, st) : launch<64, false>(L, st);
-  }
-  if (rows <= 16) return launch<16, true>(L, st);
+  if (L.n == 1) return rows <= 32 ? launch<32, false>(L, st) : launch<64, false>(L, st);
   return rows <= 32 ? launch<32, true>(L, st) : launch<64, true>(L, st);
 }
 

@@ -270,8 +270,9 @@ struct CacheAttnLaunch {
   int* err;
   int device;
 };
-// cache_attn_tc.cu: bf16, d = 128; with several tokens a table of kCacheTableGroups
-// group ids, for K up to that.
+constexpr int kCacheRows = 16;   // query rows of a head that cache_attn.cu takes in one pass
+// cache_attn_tc.cu: bf16, d = 128, more rows than that; with several tokens a table of
+// kCacheTableGroups group ids, for K up to that.
 constexpr int kCacheTableGroups = 1024;
 cudaError_t launch_cache_attn_tc(const CacheAttnLaunch& L, cudaStream_t st);
 cudaError_t launch_cache_attn(const CacheAttnLaunch& L, int dtype, cudaStream_t st);
