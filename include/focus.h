@@ -494,7 +494,8 @@ FOCUS_API focus_status_t focus_cache_append(const focus_params_t* p, const void*
  * their append.  Token t of sequence b sits at position
  * i = next[b] - n_new[b] + t and keeps the slots with pos <= i and
  * (i - pos < w or equal group id); softmax(scale * q . k) is exact over them.
- *   Q, O [B, H, n, d] dtype of p, n <= FOCUS_CACHE_MAX_QUERY;
+ *   Q, O [B, H, n, d] dtype of p, n <= FOCUS_CACHE_MAX_QUERY (a longer chunk behind
+ *   a cached prefix goes in by turns: append up to that many, attend them, go on);
  *   gid [B, A, n] int32;  n_new [B] int32 or NULL as in focus_cache_append;
  *   lse_opt [B, H, n] fp32 or NULL.
  * A token that keeps no slot gets O = 0 and lse = -infinity; a query row with an

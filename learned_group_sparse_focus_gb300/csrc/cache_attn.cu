@@ -21,9 +21,8 @@
 //   O^T += V^T P^T: two keys' bytes of one column are zipped with one byte
 //                   permute into the pairs that the fragment wants; P^T comes
 //                   from S^T by an 8x8 register transpose.
-// Codes become f16 exactly and the products run in f16 with fp32 sums (e4m3
-// operands of mma.sync are taken apart into the same f16 products on this
-// architecture, with more conversions: 14 instructions against 9 here).
+// Codes become f16 exactly and the products run in f16 with fp32 sums (an e4m3
+// m16n8k32 of mma.sync is two f16 products here as well, by the counters of a probe).
 // Queries are scaled by a power of two per row to below 2^14 and held in one f16
 // (bf16 tensors: 8 bits fit 11) or two (fp32 tensors, 22 bits); weights are held in
 // two, since one alone would be off by up to 2^-11, an eighth of bf16's half step.
@@ -42,14 +41,15 @@
 // cost 8 bytes a slot and query row) and adds each slot's weights: one addition
 // a slot, in a fixed order.
 //
-// Measured: one step of 32 / 8 heads over 32K slots 10.7 us; 16 sequences of up to 32K
+// Measured: one step of 32 / 8 heads over 32K slots 11.0 us; 16 sequences of up to 32K
 // 57 us with the weights accumulated (86 MB: 1.5 TB/s; 54 with weights of one f16); a step of 8 sequences of up to
-// 1K slots, 12 heads, d = 64, 8.3 us.
+// 1K slots, 12 heads, d = 64, 8.4 us.
 // The two small ones are a chain of latencies: launch, counts and table, group ids,
-// rows, products, two joins (18,400 clocks at 32K: first tile there at 10,000,
-// products done at 11,300, cluster joined at 16,300).  The batch runs at 37% of the
-// issue rate with 12% of the DRAM rate: two blocks an SM do not hide the latencies
-// of a block, and the sequences are uneven.
+// rows, products, two joins (18,400 clocks at 32K: first tile there at 10,200,
+// products done at 13,100, cluster joined at 16,200).  The batch runs at 47% of the
+// issue rate with 13% of the DRAM rate: two blocks an SM do not hide the latencies
+// of a block, the sequences are uneven, and the second pass takes a third of a block's
+// time (47,700 clocks to the join, 22,600 after it).
 #include <cooperative_groups.h>
 #include <type_traits>
 

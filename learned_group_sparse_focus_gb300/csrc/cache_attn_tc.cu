@@ -33,14 +33,14 @@
 // the bottleneck (64 tokens over 8K: 132 us against 117), in the weight warps the
 // weights (161 us), and a single gathering warp takes 4,600 clocks a tile (190 us).
 //
-// What bounds it now: 64 query rows, the weight warps' instructions (some 330 a
-// thread and tile over 16 rows each; 4,100 clocks a tile with the tensor pipe at 10%),
-// then the second pass's (2,400 clocks a tile); 32 rows over long caches, the scan
+// What bounds it now: 64 query rows, the weight warps (4,800 clocks a tile, of which
+// their own work is about 4,100 and the wait for the scores the rest; the tensor pipe is
+// at 9%), then the second pass (2,200 clocks a tile); 32 rows over long caches, the scan
 // (2,800 clocks for 20 pages) and the fixed 14,000 clocks from the launch to the
 // first weights and 6,000 of the join.  64 tokens for 2 sequences of 8K slots, 32
 // heads, with the weights accumulated: 128 us (146 MB of HBM traffic: 1.1 TB/s; 116 with
 // weights of one f16 in four e5m2 parts, which differed from fp32 weights by 9e-4); four
-// tokens for 4 sequences of 64K slots, 64 / 8 heads: 36 us; a step of 32 and 64 query
+// tokens for 4 sequences of 64K slots, 64 / 8 heads: 37 us; a step of 32 and 64 query
 // heads a head at 32K: 18 and 23 us.
 #include <cooperative_groups.h>
 

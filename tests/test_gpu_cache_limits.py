@@ -295,6 +295,32 @@ def test_attention_writes_stay_inside_their_buffers_in_every_form(fz, G, d, T):
         assert x.intact()
 
 
+@pytest.mark.parametrize("G,d,dtype", [(2, 64, "bf16"), (4, 128, "bf16"), (1, 128, "f32")])
+def test_a_long_chunk_goes_in_by_turns(fz, G, d, dtype):
+    """150 tokens behind prefixes of 70 and 0: appends and attentions of 64, 64 and 22 give
+    every token the oracle's output over the whole."""
+    import torch
+    rng = np.random.default_rng(d + G)
+    B, H_kv, n, K, w = 2, 2, 150, 3, 25
+    c = base._make(3, B, H_kv, d, [70, 0], K, 1, dtype, room=n)
+    k, v = (base._rows(rng, (B, H_kv, n, d), dtype, 0.3) for _ in range(2))
+    Q, gid = base._rows(rng, (B, G * H_kv, n, d), dtype, 0.3), rng.integers(0, K, (B, 1, n)).astype(np.int32)
+    cache, dt = base._cache(fz, c), base._type(fz, dtype)
+    for t in range(0, n, 64):
+        m = min(64, n - t)
+        p = fz.make_params(B, G * H_kv, H_kv, m, d, 64, 64, K, 1, w, dtype=dtype)
+        part = [np.ascontiguousarray(x[:, :, t:t + m]) for x in (k, v, Q, gid)]
+        ws = fz.alloc_workspace_cache(p, cache)
+        O = torch.zeros((B, G * H_kv, m, d), dtype=dt, device="cuda")
+        ids = base._dev(part[3])
+        fz.focus_cache_append(p, base._dev(part[0], dt), base._dev(part[1], dt), ids, cache, ws)
+        fz.focus_cache_attention_fwd(p, base._dev(part[2], dt), ids, cache, O, None, ws)
+        assert fz.focus_check_errors(ws) == 0
+        c = cr.append(c, part[0], part[1], part[3])
+        base._o_within(O, cr.attention(c, part[2], part[3], w, p.scale), d, dtype)
+    assert (cache.len.cpu().numpy() == c["len"]).all() and c["len"].min() == n
+
+
 # ----------------------------------------------------------------- set-up ---
 
 PREFILL_FIRST = """
