@@ -1168,7 +1168,7 @@ focus_status_t focus_cache_attention_fwd(const focus_params_t* p, const void* Q,
   // The mma.sync kernel takes up to 16 query rows of a key/value head in one pass, and
   // there it is the faster one: 1 to 32 sequences of 8 heads with up to 16, 128 and 512
   // pages, 4, 8, 12 and 16 rows of one token and of several, with and without the weights
-  // accumulated, 66 cases (16 rows of one token: 12 us against 15 for one sequence, 45
+  // accumulated, 114 cases (16 rows of one token: 12 us against 15 for one sequence, 45
   // against 47 for 16 and 110 against 130 for 32 of up to 32K tokens; four tokens of 4
   // rows for 16 of them 101 against 126).  More rows are two passes or more there: 24 and
   // 32 rows 21 against 18 us, 83 against 52 and 212 against 144; 64 rows 165 against 83.
