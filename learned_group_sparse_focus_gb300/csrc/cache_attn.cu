@@ -684,16 +684,18 @@ ClusterFits g_fits;
 template <typename T, int D, int NT, bool kMulti>
 cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
   // Blocks per (sequence, head): one wave of the clusters that fit, as long as each warp
-  // gets a page.  More of them, up to 4 a head, where a warp still has 8 pages for each
-  // wave, or 4 if they are read twice (accumulate): sequences differ in what they keep,
-  // and a block's latencies hide behind others'.  Up to n pages for each of B sequences of 8
-  // heads, us with 1, 2, 4 blocks, in brackets with the weights accumulated; * is taken:
+  // gets a page.  In several waves 2 a head, and in up to two waves 4, where a warp still
+  // has 8 pages for each wave, or 4 if they are read twice (accumulate): sequences differ
+  // in what they keep, and a block's latencies hide behind others'.  Up to n pages for each
+  // of B sequences of 8 heads, 4 rows, us with 1, 2, 4 blocks, in brackets with the weights
+  // accumulated; * is taken:
   //   B = 16, n = 128:  25, 20*, 25 (42, 27*, 29)     256: 46, 28*, 26 (81, 47, 32*)
   //           n = 512:  61, 36, 32* (110, 62, 40*)    1024: 111, 62, 49* (203, 110, 77*)
   //   B = 32, n = 64:   21*, 28, 40 (29*, 36, 48)     128: 31*, 36, 46 (52, 45*, 56)
-  //           n = 256:  44, 45*, 53 (74, 58*, 66)     1024: 167, 149, 125* (306, 204, 182*)
+  //           n = 256:  44, 45*, 53 (74, 58*, 66)     1024: 167, 149*, 125 (306, 204*, 182)
   //   B = 64, n = 128:  58*, 58, 82 (87*, 76, 100)    512: 134, 109*, 128 (221, 170*, 167)
-  // Eight blocks in several waves gain up to an eighth for 1,024 pages and lose more below.
+  // The table's size is what the launch knows: sequences much shorter than that lose by
+  // more blocks what the figures for small n show, so four stay within two waves.
   const ClusterFit* fit;
   if (cudaError_t e = g_fits<T, D, NT, kMulti>.get(L.device, reinterpret_cast<const void*>(cache_attn_kernel<T, D, NT, kMulti>),
                                                    kThreads, Cfg<T, D, NT>::kSmem, &fit))
@@ -703,7 +705,8 @@ cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
   while (cs < kMaxCluster && cs * kWarps < L.c.max_pages) {
     const int runs = fit->n[i + 1];
     const long long worth = static_cast<long long>(2 * cs * kWarps) * (L.accumulate ? 4 : 8);   // pages, for one wave
-    if (heads > runs && (cs > 2 || heads * worth > static_cast<long long>(L.c.max_pages) * runs)) break;
+    const bool pays = heads * worth <= static_cast<long long>(L.c.max_pages) * runs;
+    if (heads > runs && (!pays || cs > 2 || (cs == 2 && heads > 2 * runs))) break;
     cs *= 2;
     ++i;
   }

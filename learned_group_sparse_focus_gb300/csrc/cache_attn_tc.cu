@@ -934,16 +934,17 @@ template <int R, bool kMulti>
 cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
   // Blocks per (sequence, head): one wave of the clusters that run at once, as long as
   // each block scans a round or so.  Two in several waves where a block still has 64 pages
-  // for each wave, 32 if there are several tokens, which keep more of a page; and then
-  // four where it has 64.  Up to n pages for each of B sequences of 8 heads, us with 1, 2,
+  // for each wave, 32 if there are several tokens, which keep more of a page.  (Four would
+  // gain a fifth for several tokens in full tables of 512 pages, but sequences that fill
+  // an eighth of theirs would lose half.)  Up to n pages for each of B sequences of 8 heads, us with 1, 2,
   // 4 blocks; * is taken:
   //   24 rows of one token   B = 8, n = 512: 62, 37*, 42     B = 16, n = 128: 41*, 43, 63
   //     B = 16, n = 256: 67, 42*, 67    B = 20, n = 256: 66*, 64, 86   n = 512: 136, 102*, 114
   //     B = 32, n = 256: 84*, 88, 130   n = 512: 145, 122*, 150        n = 1024: 277, 220*, 225
-  //   32 rows of four tokens B = 8, n = 256: 79, 50*, 60     n = 512: 170, 93, 77*
+  //   32 rows of four tokens B = 8, n = 256: 79, 50*, 60     n = 512: 170, 93*, 77
   //     B = 16, n = 64: 44*, 47, 77     n = 128: 56, 58*, 82   n = 256: 100, 70*, 97
-  //     B = 16, n = 1024: 334, 223, 212*   B = 32, n = 128: 99*, 99, 152   n = 512: 267, 210*, 257
-  //   64 rows of 64 tokens   B = 8, n = 128: 175, 103*, 104  n = 512: 560, 298, 258*
+  //     B = 16, n = 1024: 334, 223*, 212   B = 32, n = 128: 99*, 99, 152   n = 512: 267, 210*, 257
+  //   64 rows of 64 tokens   B = 8, n = 128: 175, 103*, 104  n = 512: 560, 298*, 258
   //     B = 16, n = 64: 103*, 104, 146  n = 256: 317, 255*, 291        n = 512: 613, 514*, 468
   //     B = 20, n = 128: 204*, 183, 229 B = 32, n = 128: 332*, 304, 376   n = 256: 516, 455*, 535
   const ClusterFit* fit;
@@ -954,8 +955,8 @@ cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
   int cs = 1, i = 0;
   while (cs < kMaxCluster && cs * 16 <= L.c.max_pages) {
     const int runs = fit->n[i + 1];
-    const long long worth = 2 * cs * (kMulti ? 32 * cs : 64);      // pages, for one wave
-    if (heads > runs && (cs > (kMulti ? 2 : 1) || heads * worth > static_cast<long long>(L.c.max_pages) * runs)) break;
+    const long long worth = kMulti ? 64 : 128;         // pages of two blocks, for one wave
+    if (heads > runs && (cs > 1 || heads * worth > static_cast<long long>(L.c.max_pages) * runs)) break;
     cs *= 2;
     ++i;
   }
