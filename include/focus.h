@@ -24,7 +24,9 @@
  * focus_sinkhorn_fwd), the backward (focus_attention_bwd),
  * focus_build_index_static (the index without a workspace) and, for the tokens
  * that follow the prompt, a paged 8-bit key/value cache: focus_cache_append,
- * focus_cache_attention_fwd and focus_cache_evict.
+ * focus_cache_attention_fwd and focus_cache_evict; beside it the rotation of
+ * queries and keys to their positions (focus_rotary, focus_cache_append_rotary)
+ * and trees of drafted tokens (focus_cache_attention_tree_fwd, focus_tree_accept).
  *
  * Conventions shared by every call
  *   - All tensor pointers are DEVICE pointers to row-major contiguous arrays,
@@ -62,7 +64,8 @@ extern "C" {
 #endif
 
 #define FOCUS_ABI_VERSION 3   /* 2: adds the top-k membership calls; 3: the split top-2 index layout.
-                                 The cache calls only add entry points: no layout changed. */
+                                 The cache, rotary and tree calls only add entry points: no
+                                 layout changed. */
 
 #if defined(__GNUC__)
 #define FOCUS_API __attribute__((visibility("default")))
@@ -87,7 +90,8 @@ typedef enum {
   FOCUS_ERR_CUDA = 4,          /* a CUDA runtime/launch call failed             */
   FOCUS_ERR_TIMEOUT = 5,       /* device: a bounded wait ran out                */
   FOCUS_ERR_BAD_GROUP_ID = 6,  /* device: a group id outside [0, K)             */
-  FOCUS_ERR_BAD_CACHE = 7      /* device: a cache's page, length or position out of range */
+  FOCUS_ERR_BAD_CACHE = 7,     /* device: a cache's page, length or position out of range */
+  FOCUS_ERR_BAD_TREE = 8       /* device: a drafted tree's parent or row out of range     */
 } focus_status_t;
 
 typedef enum { FOCUS_F32 = 0, FOCUS_BF16 = 1 } focus_dtype_t;
@@ -532,9 +536,99 @@ FOCUS_API focus_status_t focus_cache_evict(const focus_params_t* p, int32_t budg
                                            const focus_cache_t* src, const focus_cache_t* dst,
                                            void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------ rotary positions ---
+ * Models whose queries and keys are turned by their positions.  The pages leave
+ * positions to the model that is retrofitted; this is the usual rotation: of a
+ * row's first `dim` elements, pair i is turned by the angle x * inv_freq[i], x
+ * the row's position, and multiplied by `scale`:
+ *   (a, b) -> scale (a cos - b sin, a sin + b cos).
+ * Elements from `dim` on stay as they are.  Angles are formed modulo a turn in
+ * 64-bit fixed point, so they are as good at position 2^31 as at 0; the rotation
+ * runs in fp32 and is rounded once.  A NaN or infinite element reaches its pair
+ * and nothing else. */
+typedef struct {
+  const float* inv_freq;   /* device [dim / 2], finite (below 2^60), 16-byte aligned */
+  int32_t dim;             /* elements that turn: a multiple of 16, 16 <= dim <= d */
+  int32_t interleaved;     /* pairs: 0 (i, i + dim / 2), 1 (2 i, 2 i + 1)          */
+  float scale;             /* finite; 1 in the usual setting                       */
+} focus_rotary_t;
+
+/* Rotation of queries and keys.  Token t of sequence b sits at base[b] + t, or,
+ * with parent, at base[b] + the depth of node t in the tree (see below; then
+ * n <= FOCUS_CACHE_MAX_QUERY).
+ *   Q, Q_out [B, H, n, d], K, K_out [B, H_kv, n, d] dtype of p, d in {64, 128}; Q with
+ *   Q_out or K with K_out may be NULL; Q_out may be Q and K_out K (in place), no
+ *   other overlap;
+ *   base [B] int32 or NULL (0); parent [B, n] int32 or NULL; n_new [B] int32 or NULL:
+ *   tokens of a sequence, rows behind them are neither read nor written.
+ *   transpose != 0: the transposed rotation, scale included: Q = dL/dQ_out gives
+ *   Q_out = dL/dQ.
+ * ws: any workspace of this library (its error word is used).  A n_new outside [0, n] is
+ * flagged as FOCUS_ERR_BAD_CACHE (clamped), a parent as FOCUS_ERR_BAD_TREE. */
+FOCUS_API focus_status_t focus_rotary(const focus_params_t* p, const focus_rotary_t* rot,
+                                      int32_t transpose, const int32_t* base, const int32_t* parent,
+                                      const int32_t* n_new, const void* Q, const void* K, void* Q_out,
+                                      void* K_out, void* ws, size_t ws_bytes, void* stream);
+
+/* focus_cache_append with the rotation on the way: token t's key is turned to
+ * its position next[b] + t and rounded once, to e4m3: the codes and scales are
+ * those of exact arithmetic.  In the same launch the queries of these tokens are
+ * turned (Q to Q_out), and the turned keys are written to K_out in p's dtype, for
+ * a prompt's own attention.
+ *   rot may be NULL (nothing turns; Q and Q_out NULL); Q with Q_out, and K_out, may be
+ *   NULL; Q_out may be Q and K_out K, no other overlap;
+ *   rows [B, n] int32 or NULL: token t is row rows[b][t] of K, V and gid (a tree's
+ *   accepted path; each row at most once; needs Q and K_out NULL); rows behind
+ *   n_new[b] are not read, a row outside [0, n) is flagged as FOCUS_ERR_BAD_TREE (clamped).
+ * The rest as focus_cache_append; Q_out and K_out rows of a sequence that does not fit,
+ * and those behind n_new[b], stay as they were.  ws: of focus_cache_workspace_bytes. */
+FOCUS_API focus_status_t focus_cache_append_rotary(const focus_params_t* p, const focus_rotary_t* rot,
+                                                   const void* Q, const void* K, const void* V,
+                                                   const int32_t* gid, const int32_t* rows,
+                                                   const int32_t* n_new, const focus_cache_t* cache,
+                                                   void* Q_out, void* K_out, int32_t* len_out,
+                                                   int32_t* next_out, void* ws, size_t ws_bytes,
+                                                   void* stream);
+
+/* -------------------------------------------------- trees of drafted tokens ---
+ * Several continuations of a sequence in one step.  The n <= FOCUS_CACHE_MAX_QUERY
+ * drafted tokens of a sequence are the nodes of a tree: node t hangs below node
+ * parent[t], -1 <= parent[t] < t, or with -1 below the last cached token, and its
+ * position is next[b] + its depth (0 below the last cached token).  Its line is
+ * itself and its ancestors.  Several nodes may have parent -1.  A parent outside
+ * [-1, t) is flagged as FOCUS_ERR_BAD_TREE and counts as -1; parents behind n_new[b]
+ * are not read.
+ * The step of one layer: focus_assign, focus_rotary (base = cache->next, parent),
+ * focus_cache_attention_tree_fwd; after the model's choices focus_tree_accept once,
+ * then for each layer focus_cache_append_rotary with its rows and counts.  Drafted keys
+ * and values stay out of the cache until they are accepted: a rejected one would leave
+ * its page's scale raised and the page's older rows rounded again. */
+
+/* Bytes of device workspace for the calls on trees of problem p (0 if p is
+ * invalid).  Pure host arithmetic. */
+FOCUS_API size_t focus_tree_workspace_bytes(const focus_params_t* p);
+
+/* The accepted path of a verified tree.  target[b][t] is the token that the model
+ * chose after node t, prev[b] the one it had chosen after the last cached token.
+ * Node t is accepted when its token is the choice after its parent and its parent
+ * is accepted (-1 always is).  The deepest accepted node (ties: the lowest index)
+ * ends the path.
+ *   token, target, parent [B, n] int32; prev [B] int32; n_new [B] int32 or NULL as above;
+ *   rows [B, n] int32: the path's nodes from the root on, entries behind it stay as they
+ *   were; count [B] int32: its length, 0 ... n_new[b];
+ *   last [B] int32: the choice after the path's end (prev[b] if it is empty), the next
+ *   step's prev; may be prev.  No other overlap.
+ * rows and count go to focus_cache_append_rotary as rows and n_new.  ws: any workspace of
+ * this library (its error word is used). */
+FOCUS_API focus_status_t focus_tree_accept(const focus_params_t* p, const int32_t* token,
+                                           const int32_t* target, const int32_t* prev,
+                                           const int32_t* parent, const int32_t* n_new, int32_t* rows,
+                                           int32_t* count, int32_t* last, void* ws, size_t ws_bytes,
+                                           void* stream);
+
 /* Synchronises `stream`, reads and clears the device error word in ws.
- * Returns FOCUS_OK, FOCUS_ERR_BAD_GROUP_ID, FOCUS_ERR_BAD_CACHE, FOCUS_ERR_TIMEOUT
- * or FOCUS_ERR_CUDA. */
+ * Returns FOCUS_OK, FOCUS_ERR_BAD_GROUP_ID, FOCUS_ERR_BAD_CACHE, FOCUS_ERR_BAD_TREE,
+ * FOCUS_ERR_TIMEOUT or FOCUS_ERR_CUDA. */
 FOCUS_API focus_status_t focus_check_errors(void* ws, void* stream);
 
 /* Static description of a status code. */

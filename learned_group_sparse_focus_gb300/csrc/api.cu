@@ -398,6 +398,7 @@ const char* focus_status_string(focus_status_t s) {
     case FOCUS_ERR_TIMEOUT: return "device wait timed out";
     case FOCUS_ERR_BAD_GROUP_ID: return "group id outside [0, K)";
     case FOCUS_ERR_BAD_CACHE: return "cache page, length or position out of range";
+    case FOCUS_ERR_BAD_TREE: return "parent or row of a drafted tree out of range";
   }
   return "unknown status";
 }
@@ -1192,6 +1193,92 @@ focus_status_t focus_cache_evict(const focus_params_t* p, int32_t budget, int32_
   return cuda_status(launch_cache_evict(L, static_cast<cudaStream_t>(stream)));
 }
 
+// ---------------------------------------- rotary positions, drafted trees ---
+
+static bool rotary_ok(const focus_rotary_t* r, const focus_params_t* p) {
+  if (!r || !r->inv_freq || !aligned16(r->inv_freq)) return false;
+  if (r->dim < 16 || r->dim % 16 != 0 || r->dim > p->d) return false;
+  return (r->interleaved == 0 || r->interleaved == 1) && std::isfinite(r->scale);
+}
+
+// Workspace of the calls on trees: the error word, then what the attention keeps of the
+// tree's own part.
+size_t focus_tree_workspace_bytes(const focus_params_t* p) {
+  if (!params_ok(p)) return 0;
+  return align_up(kAlign);
+}
+
+static focus_status_t tree_args(const focus_params_t* p, const void* ws, size_t ws_bytes) {
+  if (!params_ok(p)) return FOCUS_ERR_INVALID_ARG;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return FOCUS_ERR_INVALID_ARG;
+  if (ws_bytes < kAlign) return FOCUS_ERR_WORKSPACE;
+  return FOCUS_OK;
+}
+
+focus_status_t focus_rotary(const focus_params_t* p, const focus_rotary_t* rot, int32_t transpose,
+                            const int32_t* base, const int32_t* parent, const int32_t* n_new, const void* Q,
+                            const void* K, void* Q_out, void* K_out, void* ws, size_t ws_bytes, void* stream) {
+  if (focus_status_t s = tree_args(p, ws, ws_bytes)) return s;
+  if (!rotary_ok(rot, p) || !Q != !Q_out || !K != !K_out || (!Q && !K)) return FOCUS_ERR_INVALID_ARG;
+  const void* all[] = {base, parent, n_new, Q, K, Q_out, K_out};
+  for (const void* x : all)
+    if (!aligned16(x)) return FOCUS_ERR_INVALID_ARG;
+  if (Q && K && (Q_out == K || K_out == Q || Q_out == K_out)) return FOCUS_ERR_INVALID_ARG;
+  if (!(p->d == 64 || p->d == 128) || (parent && p->n > FOCUS_CACHE_MAX_QUERY)) return FOCUS_ERR_UNSUPPORTED;
+  RotaryLaunch L{rot->inv_freq, rot->dim, rot->interleaved, transpose != 0, rot->scale, base, parent, n_new, Q, K,
+                 Q_out, K_out, p->B, Q ? p->H : 0, K ? p->H_kv : 0, p->n, at<int>(ws, 0), 0, 0};
+  return cuda_status(launch_rotary(L, p->d, p->dtype, static_cast<cudaStream_t>(stream)));
+}
+
+focus_status_t focus_cache_append_rotary(const focus_params_t* p, const focus_rotary_t* rot, const void* Q,
+                                         const void* K, const void* V, const int32_t* gid, const int32_t* rows,
+                                         const int32_t* n_new, const focus_cache_t* cache, void* Q_out, void* K_out,
+                                         int32_t* len_out, int32_t* next_out, void* ws, size_t ws_bytes,
+                                         void* stream) {
+  if (focus_status_t s = cache_args(p, cache, ws, ws_bytes)) return s;
+  const void* all[] = {K, V, gid, len_out, next_out};
+  for (const void* x : all)
+    if (!x || !aligned16(x)) return FOCUS_ERR_INVALID_ARG;
+  const void* may[] = {Q, rows, n_new, Q_out, K_out};
+  for (const void* x : may)
+    if (!aligned16(x)) return FOCUS_ERR_INVALID_ARG;
+  if ((rot && !rotary_ok(rot, p)) || !Q != !Q_out || (Q && !rot)) return FOCUS_ERR_INVALID_ARG;
+  if (rows && (Q || K_out)) return FOCUS_ERR_INVALID_ARG;
+  if (K_out && (K_out == V || K_out == Q || K_out == Q_out)) return FOCUS_ERR_INVALID_ARG;
+  if (Q && (Q_out == K || Q_out == V)) return FOCUS_ERR_INVALID_ARG;
+  if (len_out == next_out || len_out == cache->next || next_out == cache->len) return FOCUS_ERR_INVALID_ARG;
+  int* err = at<int>(ws, 0);
+  CacheAppendRotaryLaunch L{};
+  L.a = CacheAppendLaunch{K, V, gid, n_new, *cache, len_out, next_out, p->B, p->H_kv, p->n, p->d, p->A, p->K,
+                          at<int>(ws, 64), err};
+  L.rot = RotaryLaunch{nullptr, 0, 0, 0, 1.f, nullptr, nullptr, n_new, Q, K, Q_out, K_out, p->B, Q ? p->H : 0, 0, p->n, err, 0, 0};
+  if (rot) {
+    L.rot.inv_freq = rot->inv_freq;
+    L.rot.dim = rot->dim;
+    L.rot.interleaved = rot->interleaved;
+    L.rot.scale = rot->scale;
+  }
+  L.rows = rows;
+  return cuda_status(launch_cache_append_rotary(L, p->dtype, static_cast<cudaStream_t>(stream)));
+}
+
+focus_status_t focus_tree_accept(const focus_params_t* p, const int32_t* token, const int32_t* target,
+                                 const int32_t* prev, const int32_t* parent, const int32_t* n_new, int32_t* rows,
+                                 int32_t* count, int32_t* last, void* ws, size_t ws_bytes, void* stream) {
+  if (focus_status_t s = tree_args(p, ws, ws_bytes)) return s;
+  const void* all[] = {token, target, prev, parent, rows, count, last};
+  for (const void* x : all)
+    if (!x || !aligned16(x)) return FOCUS_ERR_INVALID_ARG;
+  if (!aligned16(n_new)) return FOCUS_ERR_INVALID_ARG;
+  const void* in[] = {token, target, prev, parent, n_new};
+  for (const void* x : in)
+    if (rows == x || count == x || (last == x && x != prev)) return FOCUS_ERR_INVALID_ARG;
+  if (rows == count || rows == last || count == last) return FOCUS_ERR_INVALID_ARG;
+  if (p->n > FOCUS_CACHE_MAX_QUERY) return FOCUS_ERR_UNSUPPORTED;
+  TreeAcceptLaunch L{token, target, prev, parent, n_new, rows, count, last, p->B, p->n, at<int>(ws, 0)};
+  return cuda_status(launch_tree_accept(L, static_cast<cudaStream_t>(stream)));
+}
+
 focus_status_t focus_check_errors(void* ws, void* stream) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return FOCUS_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1203,6 +1290,7 @@ focus_status_t focus_check_errors(void* ws, void* stream) {
   if (word & kErrTimeout) return FOCUS_ERR_TIMEOUT;
   if (word & kErrBadGroup) return FOCUS_ERR_BAD_GROUP_ID;
   if (word & kErrBadCache) return FOCUS_ERR_BAD_CACHE;
+  if (word & kErrBadTree) return FOCUS_ERR_BAD_TREE;
   return FOCUS_ERR_CUDA;
 }
 

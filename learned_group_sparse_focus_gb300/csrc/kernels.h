@@ -22,6 +22,7 @@ enum : int {
   kErrTimeout = 2,    // a bounded wait ran out
   kErrInternal = 4,   // an index or item failed a consistency check
   kErrBadCache = 8,   // a cache's page id, length or position is out of range
+  kErrBadTree = 16,   // a drafted tree's parent or row is out of range
 };
 
 // n counts the sorted items: tokens, or for top-k membership the n_tok * k
@@ -276,5 +277,39 @@ constexpr int kCacheRows = 16;   // query rows of a head that cache_attn.cu take
 constexpr int kCacheTableGroups = 1024;
 cudaError_t launch_cache_attn_tc(const CacheAttnLaunch& L, cudaStream_t st);
 cudaError_t launch_cache_attn(const CacheAttnLaunch& L, int dtype, cudaStream_t st);
+
+// rotary.cu: rows turned to their positions.
+struct RotaryLaunch {
+  const float* inv_freq;   // [dim / 2]
+  int dim, interleaved, transpose;
+  float scale;
+  const int32_t* base;     // [B] or null (0): position of token 0
+  const int32_t* parent;   // [B, n] or null: a token's position is base + its depth, or + its number
+  const int32_t* n_new;    // [B] or null
+  const void *Q, *K;       // [B, Hq, n, d], [B, Hk, n, d]
+  void *Q_out, *K_out;
+  int B, Hq, Hk, n;        // Hq, Hk: 0 without them
+  int* err;
+  int tokens, heads;       // a block's (set by the launch)
+};
+constexpr int kFillBlocks = 8 * 152;   // blocks that are enough for every SM
+cudaError_t launch_rotary(RotaryLaunch L, int d, int dtype, cudaStream_t st);
+
+struct CacheAppendRotaryLaunch {
+  CacheAppendLaunch a;
+  RotaryLaunch rot;        // dim 0: nothing turns; Hk 0 (the keys go by pages)
+  const int32_t* rows;     // [B, n] source row of each token, or null
+  int touched;             // pages a head may touch (set by the launch)
+};
+cudaError_t launch_cache_append_rotary(CacheAppendRotaryLaunch L, int dtype, cudaStream_t st);
+
+// tree.cu: the accepted path of a drafted tree.
+struct TreeAcceptLaunch {
+  const int32_t *token, *target, *prev, *parent, *n_new;
+  int32_t *rows, *count, *last;
+  int B, n;
+  int* err;
+};
+cudaError_t launch_tree_accept(const TreeAcceptLaunch& L, cudaStream_t st);
 
 }  // namespace focus

@@ -23,7 +23,7 @@ CACHE_MAX_QUERY = 64      # new tokens a sequence in one focus_cache_attention_f
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace too small",
           4: "CUDA error", 5: "device wait timed out", 6: "group id outside [0, K)",
-          7: "cache page, length or position out of range"}
+          7: "cache page, length or position out of range", 8: "parent or row of a drafted tree out of range"}
 
 
 class FocusError(RuntimeError):
@@ -61,11 +61,17 @@ class CacheStruct(ctypes.Structure):
                [("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
 
+class RotaryStruct(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libfocus.so not built ({LIB_PATH}); run __graft_entry__.build()")
     lib = ctypes.CDLL(LIB_PATH)
     vp, P, C = ctypes.c_void_p, ctypes.POINTER(Params), ctypes.POINTER(CacheStruct)
+    R = ctypes.POINTER(RotaryStruct)
     sig = {
         "focus_abi_version": ([], ctypes.c_int32),
         "focus_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -106,6 +112,10 @@ def _load():
         "focus_cache_attention_fwd": ([P, vp, vp, vp, C, vp, vp, ctypes.c_int32, vp, ctypes.c_size_t, vp],
                                       ctypes.c_int),
         "focus_cache_evict": ([P, ctypes.c_int32, ctypes.c_int32, C, C, vp, ctypes.c_size_t, vp], ctypes.c_int),
+        "focus_rotary": ([P, R, ctypes.c_int32] + [vp] * 8 + [ctypes.c_size_t, vp], ctypes.c_int),
+        "focus_cache_append_rotary": ([P, R] + [vp] * 6 + [C] + [vp] * 5 + [ctypes.c_size_t, vp], ctypes.c_int),
+        "focus_tree_workspace_bytes": ([P], ctypes.c_size_t),
+        "focus_tree_accept": ([P] + [vp] * 9 + [ctypes.c_size_t, vp], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -124,7 +134,8 @@ EXPORTED = ("focus_abi_version", "focus_status_string", "focus_workspace_bytes",
             "focus_attention_two_call_fwd", "focus_sinkhorn_workspace_bytes", "focus_assign_scores",
             "focus_sinkhorn_fwd", "focus_backward_workspace_bytes", "focus_attention_bwd",
             "focus_test_attention_wait_limit", "focus_cache_workspace_bytes", "focus_cache_append",
-            "focus_cache_attention_fwd", "focus_cache_evict")
+            "focus_cache_attention_fwd", "focus_cache_evict", "focus_rotary", "focus_cache_append_rotary",
+            "focus_tree_workspace_bytes", "focus_tree_accept")
 
 
 def lib():
@@ -466,13 +477,18 @@ def _raw_stream(index: int) -> int:
 def _cache_call(fn: str, p: Params, cache: Cache, ws, stream, *args):
     """Runs a cache call on the cache's device (args: the C arguments between p
     and ws)."""
-    dev = cache.device
     if cache.dims != (p.B, p.H_kv, p.d):
         raise ValueError(f"the cache holds (B, H_kv, d) = {cache.dims}, the call asks for {(p.B, p.H_kv, p.d)}")
+    _device_call(fn, p, cache.device, "the cache", ws, stream, *args)
+
+
+def _device_call(fn: str, p: Params, dev, owner: str, ws, stream, *args):
+    """Runs a call on device dev, that of `owner` (args: the C arguments between p
+    and ws)."""
     if dev.type != "cuda":
-        raise ValueError(f"the cache must be on a CUDA device, not {dev}")
+        raise ValueError(f"{owner} must be on a CUDA device, not {dev}")
     if ws.device != dev or (stream is not None and stream.device != dev):
-        raise ValueError(f"workspace and stream must be on the cache's device {dev}")
+        raise ValueError(f"workspace and stream must be on {owner}'s device {dev}")
     call = getattr(_lib, fn)
     raw = _raw_stream(dev.index) if stream is None else stream.cuda_stream
     if dev.index == torch.cuda.current_device():
@@ -541,6 +557,96 @@ def run_decode_step(p: Params, h, W, C, Q, K, V, cache: Cache, ws, ws_cache, n_n
         focus_cache_attention_fwd(p, Q, gid, cache, O, lse, ws_cache, n_new=n_new, accumulate=accumulate,
                                   stream=stream)
     return O, gid, lse
+
+
+# ---------------------------------------- rotary positions, drafted trees ---
+
+@dataclass(frozen=True, eq=False)
+class Rotary:
+    """The rotation of queries and keys to their positions (focus_rotary_t in
+    include/focus.h): pair i of a row's first 2 len(inv_freq) elements turns by
+    position * inv_freq[i] and is multiplied by scale."""
+    inv_freq: torch.Tensor   # [dim / 2] fp32
+    interleaved: bool = False
+    scale: float = 1.0
+
+    def __post_init__(self):
+        t = self.inv_freq
+        if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.numel() < 8 or t.numel() % 8:
+            raise ValueError("inv_freq must be a tensor of a positive multiple of 8 frequencies")
+        c = RotaryStruct(_expect("inv_freq", t, t.shape, torch.float32, t.device), 2 * t.numel(),
+                         1 if self.interleaved else 0, float(self.scale))
+        object.__setattr__(self, "struct", c)
+        object.__setattr__(self, "ref", ctypes.byref(c))
+
+
+def _maybe(name: str, t, shape, dtype, device):
+    return None if t is None else _expect(name, t, shape, dtype, device)
+
+
+def _same_device(rot: Rotary, dev):
+    if rot.inv_freq.device != dev:
+        raise ValueError(f"the rotation's frequencies must be on {dev}, not {rot.inv_freq.device}")
+
+
+def focus_rotary(p: Params, rot: Rotary, ws, Q=None, K=None, Q_out=None, K_out=None, base=None, parent=None,
+                 n_new=None, transpose=False, stream=None):
+    """Turns Q [B, H, n, d] into Q_out and K [B, H_kv, n, d] into K_out (in place: the
+    same tensor) to positions base[b] + t, or + the depth of node t of the tree
+    `parent` [B, n].  transpose: the transposed rotation (its gradient).  ws: any
+    workspace."""
+    dev, B, n, ft, i32 = rot.inv_freq.device, p.B, p.n, _float_type(p), torch.int32
+    q, k = (B, p.H, n, p.d), (B, p.H_kv, n, p.d)
+    _device_call("focus_rotary", p, dev, "the rotation", ws, stream, rot.ref, 1 if transpose else 0,
+                 _maybe("base", base, (B,), i32, dev), _maybe("parent", parent, (B, n), i32, dev),
+                 _maybe("n_new", n_new, (B,), i32, dev), _maybe("Q", Q, q, ft, dev), _maybe("K", K, k, ft, dev),
+                 _maybe("Q_out", Q_out, q, ft, dev), _maybe("K_out", K_out, k, ft, dev))
+
+
+def focus_cache_append_rotary(p: Params, rot: Rotary | None, K, V, gid, cache: Cache, ws, Q=None, Q_out=None,
+                              K_out=None, rows=None, n_new=None, len_out=None, next_out=None, stream=None):
+    """focus_cache_append with K turned to the tokens' positions on the way (rot None:
+    as it is).  Q [B, H, n, d] is turned into Q_out in the same launch; K_out gets the
+    turned keys.  rows [B, n]: token t is row rows[b, t] of K, V and gid (the path
+    of focus_tree_accept, with its count as n_new)."""
+    dev, B, H_kv, n, ft, i32 = cache.device, p.B, p.H_kv, p.n, _float_type(p), torch.int32
+    q, k = (B, p.H, n, p.d), (B, H_kv, n, p.d)
+    if rot is not None:
+        _same_device(rot, dev)
+    _cache_call("focus_cache_append_rotary", p, cache, ws, stream, None if rot is None else rot.ref,
+                _maybe("Q", Q, q, ft, dev), _expect("K", K, k, ft, dev), _expect("V", V, k, ft, dev),
+                _expect("gid", gid, (B, p.A, n), i32, dev), _maybe("rows", rows, (B, n), i32, dev),
+                _maybe("n_new", n_new, (B,), i32, dev), cache.ref, _maybe("Q_out", Q_out, q, ft, dev),
+                _maybe("K_out", K_out, k, ft, dev),
+                cache.struct.len if len_out is None else _expect("len_out", len_out, (B, H_kv), i32, dev),
+                cache.struct.next if next_out is None else _expect("next_out", next_out, (B,), i32, dev))
+
+
+def focus_tree_workspace_bytes(p: Params) -> int:
+    return int(_lib.focus_tree_workspace_bytes(ctypes.byref(p)))
+
+
+def alloc_workspace_tree(p: Params, device="cuda", stream=None) -> torch.Tensor:
+    """Caller-owned workspace for the calls on drafted trees, error word cleared."""
+    nbytes = focus_tree_workspace_bytes(p)
+    if nbytes == 0:
+        raise FocusError("focus_tree_workspace_bytes", 1)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.device(ws.device):
+        focus_workspace_init(ws, stream)
+    return ws
+
+
+def focus_tree_accept(p: Params, token, target, prev, parent, rows, count, last, ws, n_new=None, stream=None):
+    """The accepted path of drafted trees: token, target, parent [B, n], prev [B] int32
+    -> rows [B, n] (entries behind the path stay), count [B], last [B] (may be prev)."""
+    dev, B, n, i32 = ws.device, p.B, p.n, torch.int32
+    one, all_ = (B,), (B, n)
+    _device_call("focus_tree_accept", p, dev, "the workspace", ws, stream, _expect("token", token, all_, i32, dev),
+                 _expect("target", target, all_, i32, dev), _expect("prev", prev, one, i32, dev),
+                 _expect("parent", parent, all_, i32, dev), _maybe("n_new", n_new, one, i32, dev),
+                 _expect("rows", rows, all_, i32, dev), _expect("count", count, one, i32, dev),
+                 _expect("last", last, one, i32, dev))
 
 
 # ------------------------------------------------------------ index views ---
