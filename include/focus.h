@@ -608,6 +608,27 @@ FOCUS_API focus_status_t focus_cache_append_rotary(const focus_params_t* p, cons
  * invalid).  Pure host arithmetic. */
 FOCUS_API size_t focus_tree_workspace_bytes(const focus_params_t* p);
 
+/* Focus attention of the nodes of drafted trees.  Node t of sequence b at position
+ * i = next[b] + its depth keeps the cached slots with pos <= i and (i - pos < w or
+ * equal group id), and of its line itself and the ancestors with i - their position < w
+ * or its group id; softmax(scale * q . k) is exact over both.  The cache is read only.
+ *   Q, O [B, H, n, d], K, V [B, H_kv, n, d] dtype of p (the drafted tokens' own keys and
+ *   values, as they are), n <= FOCUS_CACHE_MAX_QUERY, d in {64, 128};
+ *   gid [B, A, n], parent [B, n] int32; n_new [B] int32 or NULL: nodes of a sequence; rows
+ *   behind them of O and lse_opt stay as they were;
+ *   lse_opt [B, H, n] fp32 or NULL.
+ * O overlaps no input.  Precision, logits and NaN codes as focus_cache_attention_fwd; a
+ * drafted key or value row with an infinite or NaN element gives NaN to the nodes that keep
+ * it and to no others; drafted values below 2^-73 count as 0.  To gather mass for an
+ * eviction, attend the accepted tokens with focus_cache_attention_fwd once they are
+ * appended.  ws: of focus_tree_workspace_bytes. */
+FOCUS_API focus_status_t focus_cache_attention_tree_fwd(const focus_params_t* p, const void* Q,
+                                                        const void* K, const void* V, const int32_t* gid,
+                                                        const int32_t* parent, const int32_t* n_new,
+                                                        const focus_cache_t* cache, void* O,
+                                                        float* lse_opt, void* ws, size_t ws_bytes,
+                                                        void* stream);
+
 /* The accepted path of a verified tree.  target[b][t] is the token that the model
  * chose after node t, prev[b] the one it had chosen after the last cached token.
  * Node t is accepted when its token is the choice after its parent and its parent

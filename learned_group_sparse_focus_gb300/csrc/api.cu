@@ -1126,10 +1126,10 @@ size_t focus_cache_workspace_bytes(const focus_params_t* p, const focus_cache_t*
 }
 
 static focus_status_t cache_args(const focus_params_t* p, const focus_cache_t* c, const void* ws,
-                                 size_t ws_bytes) {
+                                 size_t ws_bytes, bool tree = false) {
   if (!params_ok(p) || !cache_ok(c)) return FOCUS_ERR_INVALID_ARG;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return FOCUS_ERR_INVALID_ARG;
-  if (ws_bytes < focus_cache_workspace_bytes(p, c)) return FOCUS_ERR_WORKSPACE;
+  if (ws_bytes < (tree ? focus_tree_workspace_bytes(p) : focus_cache_workspace_bytes(p, c))) return FOCUS_ERR_WORKSPACE;
   if (!(p->d == 64 || p->d == 128) || p->H_kv > 65535) return FOCUS_ERR_UNSUPPORTED;
   // the attention addresses the pools in 32-bit counts of 16 bytes
   if (static_cast<unsigned long long>(c->n_pages) * p->H_kv * kPage * p->d > (1ull << 36)) return FOCUS_ERR_UNSUPPORTED;
@@ -1165,7 +1165,7 @@ focus_status_t focus_cache_attention_fwd(const focus_params_t* p, const void* Q,
   if (dev < 0) return FOCUS_ERR_CUDA;
   CacheAttnLaunch L{Q, gid, n_new, *cache, O, lse_opt, accumulate != 0,
                     p->B, p->H, p->H_kv, p->n, p->d, p->A, p->w > 1 ? p->w : 1,
-                    p->scale * 1.4426950408889634f, at<int>(ws, 0), dev};
+                    p->scale * 1.4426950408889634f, at<int>(ws, 0), dev, nullptr, nullptr, nullptr};
   // The mma.sync kernel takes up to 16 query rows of a key/value head in one pass, and
   // there it is the faster one: 1 to 32 sequences of 8 heads with up to 16, 128 and 512
   // pages, 4, 8, 12 and 16 rows of one token and of several, with and without the weights
@@ -1260,6 +1260,24 @@ focus_status_t focus_cache_append_rotary(const focus_params_t* p, const focus_ro
   }
   L.rows = rows;
   return cuda_status(launch_cache_append_rotary(L, p->dtype, static_cast<cudaStream_t>(stream)));
+}
+
+focus_status_t focus_cache_attention_tree_fwd(const focus_params_t* p, const void* Q, const void* K, const void* V,
+                                              const int32_t* gid, const int32_t* parent, const int32_t* n_new,
+                                              const focus_cache_t* cache, void* O, float* lse_opt, void* ws,
+                                              size_t ws_bytes, void* stream) {
+  if (focus_status_t s = cache_args(p, cache, ws, ws_bytes, true)) return s;
+  const void* all[] = {Q, K, V, gid, parent, O};
+  for (const void* x : all)
+    if (!x || !aligned16(x)) return FOCUS_ERR_INVALID_ARG;
+  if (!aligned16(n_new) || !aligned16(lse_opt) || O == Q || O == K || O == V) return FOCUS_ERR_INVALID_ARG;
+  if (p->n > FOCUS_CACHE_MAX_QUERY) return FOCUS_ERR_UNSUPPORTED;
+  const int dev = device_index();
+  if (dev < 0) return FOCUS_ERR_CUDA;
+  CacheAttnLaunch L{Q, gid, n_new, *cache, O, lse_opt, 0,
+                    p->B, p->H, p->H_kv, p->n, p->d, p->A, p->w > 1 ? p->w : 1,
+                    p->scale * 1.4426950408889634f, at<int>(ws, 0), dev, K, V, parent};
+  return cuda_status(launch_cache_tree(L, p->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 focus_status_t focus_tree_accept(const focus_params_t* p, const int32_t* token, const int32_t* target,

@@ -1,0 +1,21 @@
+// Attention of a tree of drafted tokens over the paged 8-bit cache and over the tree itself
+// (contract: focus.h), on cache_attn.cu's kernel.
+#include "cache_attn.cuh"
+
+namespace focus {
+namespace {
+
+template <typename T, int D>
+cudaError_t launch_rows(const CacheAttnLaunch& L, cudaStream_t st) {
+  if (L.H / L.H_kv * L.n > 8) return launch<T, D, 2, true, true>(L, st);
+  return launch<T, D, 1, true, true>(L, st);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_tree(const CacheAttnLaunch& L, int dtype, cudaStream_t st) {
+  if (dtype == FOCUS_BF16) return L.d == 128 ? launch_rows<__nv_bfloat16, 128>(L, st) : launch_rows<__nv_bfloat16, 64>(L, st);
+  return L.d == 128 ? launch_rows<float, 128>(L, st) : launch_rows<float, 64>(L, st);
+}
+
+}  // namespace focus

@@ -270,6 +270,9 @@ struct CacheAttnLaunch {
   float scale_log2;       // scale * log2(e)
   int* err;
   int device;
+  // a tree of drafted tokens: their keys and values [B, H_kv, n, d] and parents [B, n]
+  const void *K, *V;
+  const int32_t* parent;
 };
 constexpr int kCacheRows = 16;   // query rows of a head that cache_attn.cu takes in one pass
 // cache_attn_tc.cu: bf16, d = 128, more rows than that; with several tokens a table of
@@ -277,6 +280,8 @@ constexpr int kCacheRows = 16;   // query rows of a head that cache_attn.cu take
 constexpr int kCacheTableGroups = 1024;
 cudaError_t launch_cache_attn_tc(const CacheAttnLaunch& L, cudaStream_t st);
 cudaError_t launch_cache_attn(const CacheAttnLaunch& L, int dtype, cudaStream_t st);
+// cache_tree.cu: the tokens are the nodes of a tree, not in the cache.
+cudaError_t launch_cache_tree(const CacheAttnLaunch& L, int dtype, cudaStream_t st);
 
 // rotary.cu: rows turned to their positions.
 struct RotaryLaunch {

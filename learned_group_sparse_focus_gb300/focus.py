@@ -115,6 +115,7 @@ def _load():
         "focus_rotary": ([P, R, ctypes.c_int32] + [vp] * 8 + [ctypes.c_size_t, vp], ctypes.c_int),
         "focus_cache_append_rotary": ([P, R] + [vp] * 6 + [C] + [vp] * 5 + [ctypes.c_size_t, vp], ctypes.c_int),
         "focus_tree_workspace_bytes": ([P], ctypes.c_size_t),
+        "focus_cache_attention_tree_fwd": ([P] + [vp] * 6 + [C] + [vp] * 3 + [ctypes.c_size_t, vp], ctypes.c_int),
         "focus_tree_accept": ([P] + [vp] * 9 + [ctypes.c_size_t, vp], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
@@ -135,7 +136,7 @@ EXPORTED = ("focus_abi_version", "focus_status_string", "focus_workspace_bytes",
             "focus_sinkhorn_fwd", "focus_backward_workspace_bytes", "focus_attention_bwd",
             "focus_test_attention_wait_limit", "focus_cache_workspace_bytes", "focus_cache_append",
             "focus_cache_attention_fwd", "focus_cache_evict", "focus_rotary", "focus_cache_append_rotary",
-            "focus_tree_workspace_bytes", "focus_tree_accept")
+            "focus_tree_workspace_bytes", "focus_cache_attention_tree_fwd", "focus_tree_accept")
 
 
 def lib():
@@ -541,10 +542,11 @@ def focus_cache_evict(p: Params, budget: int, recent: int, src: Cache, dst: Cach
 
 
 def run_decode_step(p: Params, h, W, C, Q, K, V, cache: Cache, ws, ws_cache, n_new=None, want_lse=False,
-                    accumulate=False, stream=None):
+                    accumulate=False, stream=None, rot: Rotary | None = None):
     """assign -> append -> attention for p.n new tokens a sequence; returns (O,
     gid, lse).  ws: a workspace of alloc_workspace(p); ws_cache: one of
-    alloc_workspace_cache(p, cache).  Rows behind n_new[b] of O are 0."""
+    alloc_workspace_cache(p, cache).  Rows behind n_new[b] of O are 0.  rot: queries
+    and keys are turned to their positions in the append."""
     dev = cache.device
     with torch.cuda.device(dev), torch.cuda.stream(stream):      # the fills below run on the call's stream
         gid = torch.empty((p.B, p.A, p.n), dtype=torch.int32, device=dev)
@@ -553,7 +555,12 @@ def run_decode_step(p: Params, h, W, C, Q, K, V, cache: Cache, ws, ws_cache, n_n
         if want_lse:
             lse = torch.full((p.B, p.H, p.n), float("-inf"), dtype=torch.float32, device=dev)
         focus_assign(p, h, W, C, gid, ws, stream)
-        focus_cache_append(p, K, V, gid, cache, ws_cache, n_new=n_new, stream=stream)
+        if rot is None:
+            focus_cache_append(p, K, V, gid, cache, ws_cache, n_new=n_new, stream=stream)
+        else:
+            turned = torch.empty_like(Q)
+            focus_cache_append_rotary(p, rot, K, V, gid, cache, ws_cache, Q=Q, Q_out=turned, n_new=n_new, stream=stream)
+            Q = turned
         focus_cache_attention_fwd(p, Q, gid, cache, O, lse, ws_cache, n_new=n_new, accumulate=accumulate,
                                   stream=stream)
     return O, gid, lse
@@ -637,6 +644,20 @@ def alloc_workspace_tree(p: Params, device="cuda", stream=None) -> torch.Tensor:
     return ws
 
 
+def focus_cache_attention_tree_fwd(p: Params, Q, K, V, gid, parent, cache: Cache, O, lse, ws, n_new=None, stream=None):
+    """Attention of the nodes of drafted trees, Q [B, H, n, d], K, V [B, H_kv, n, d],
+    gid [B, A, n], parent [B, n], over the cache and over each node's line into O and
+    lse ([B, H, n] fp32 or None); n_new [B]: nodes a sequence (None: all n).  ws: of
+    alloc_workspace_tree(p)."""
+    dev, B, H, n, ft, i32 = cache.device, p.B, p.H, p.n, _float_type(p), torch.int32
+    q, k = (B, H, n, p.d), (B, p.H_kv, n, p.d)
+    _cache_call("focus_cache_attention_tree_fwd", p, cache, ws, stream,
+                _expect("Q", Q, q, ft, dev), _expect("K", K, k, ft, dev), _expect("V", V, k, ft, dev),
+                _expect("gid", gid, (B, p.A, n), i32, dev), _expect("parent", parent, (B, n), i32, dev),
+                _maybe("n_new", n_new, (B,), i32, dev), cache.ref, _expect("O", O, q, ft, dev),
+                _maybe("lse", lse, (B, H, n), torch.float32, dev))
+
+
 def focus_tree_accept(p: Params, token, target, prev, parent, rows, count, last, ws, n_new=None, stream=None):
     """The accepted path of drafted trees: token, target, parent [B, n], prev [B] int32
     -> rows [B, n] (entries behind the path stay), count [B], last [B] (may be prev)."""
@@ -647,6 +668,29 @@ def focus_tree_accept(p: Params, token, target, prev, parent, rows, count, last,
                  _expect("parent", parent, all_, i32, dev), _maybe("n_new", n_new, one, i32, dev),
                  _expect("rows", rows, all_, i32, dev), _expect("count", count, one, i32, dev),
                  _expect("last", last, one, i32, dev))
+
+
+def run_tree_step(p: Params, h, W, C, Q, K, V, parent, cache: Cache, ws, ws_tree, rot: Rotary | None = None, n_new=None,
+                  want_lse=False, stream=None):
+    """assign -> rotation -> attention for trees of p.n drafted tokens a sequence; returns
+    (O, gid, K, lse), K turned to its positions: what focus_cache_append_rotary takes (with rot None)
+    once focus_tree_accept has picked the path.  ws: a workspace of alloc_workspace(p); ws_tree:
+    one of alloc_workspace_tree(p).  Rows behind n_new[b] of O are 0."""
+    dev = cache.device
+    with torch.cuda.device(dev), torch.cuda.stream(stream):      # the fills below run on the call's stream
+        gid = torch.empty((p.B, p.A, p.n), dtype=torch.int32, device=dev)
+        O = torch.empty_like(Q) if n_new is None else torch.zeros_like(Q)
+        lse = None
+        if want_lse:
+            lse = torch.full((p.B, p.H, p.n), float("-inf"), dtype=torch.float32, device=dev)
+        focus_assign(p, h, W, C, gid, ws, stream)
+        if rot is not None:
+            q, k = torch.empty_like(Q), torch.empty_like(K)
+            focus_rotary(p, rot, ws_tree, Q=Q, K=K, Q_out=q, K_out=k, base=cache.next, parent=parent, n_new=n_new,
+                         stream=stream)
+            Q, K = q, k
+        focus_cache_attention_tree_fwd(p, Q, K, V, gid, parent, cache, O, lse, ws_tree, n_new=n_new, stream=stream)
+    return O, gid, K, lse
 
 
 # ------------------------------------------------------------ index views ---

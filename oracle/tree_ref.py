@@ -90,7 +90,7 @@ def attention(c: dict, Q, K, V, gid, parent, w: int, scale: float, n_new=None) -
                 own = [j for x, j in enumerate(line[t]) if len(line[t]) - 1 - x < max(w, 1) or mine[j] == mine[t]]
                 ks, vs = np.concatenate([k[keep], K[b, kv, own]]), np.concatenate([v[keep], V[b, kv, own]])
                 step = np.concatenate([c["v_scale"][page[keep], kv].astype(np.float64),
-                                       np.maximum(np.abs(V[b, kv, own]).max(-1), 2.0 ** -64) / 448])
+                                       [2.0 ** cr.need_exp(V[b, kv, j]) for j in own]])
                 with np.errstate(invalid="ignore", over="ignore"):
                     s = ks @ Q[b, h, t] * scale
                     top = s.max()

@@ -224,3 +224,44 @@ def test_python_binding_checks_tensors(fz):
         x[i] = x[i].long()
         with pytest.raises(ValueError, match="must be"):
             fz.focus_tree_accept(p, *x, ws)
+
+
+def test_tree_attention_refusals(fz):
+    lib = fz.lib()
+
+    def call(p=None, Q=X[0], K=X[1], V=X[2], gid=X[3], parent=X[4], n_new=None, cache=None, O=X[5], lse=None, ws=1 << 26,
+             nbytes=1 << 40):
+        p, cache = p or _params(fz), cache or _struct(fz)
+        return lib.focus_cache_attention_tree_fwd(ctypes.byref(p), Q, K, V, gid, parent, n_new, ctypes.byref(cache), O, lse, ws,
+                                                  nbytes, None)
+
+    for name in ("Q", "K", "V", "gid", "parent", "O"):
+        assert call(**{name: None}) == 1 and call(**{name: X[9] + 8}) == 1, name
+    for kw in (dict(n_new=4), dict(lse=8), dict(O=X[0]), dict(O=X[1]), dict(O=X[2]), dict(ws=None), dict(ws=(1 << 26) + 128),
+               dict(cache=_struct(fz, k=0)), dict(cache=_struct(fz, table=8)), dict(cache=_struct(fz, max_pages=0))):
+        assert call(**kw) == 1, kw
+    p = _params(fz)
+    p.w = -1
+    assert call(p=p) == 1 and lib.focus_tree_workspace_bytes(ctypes.byref(p)) == 0
+    assert call(nbytes=lib.focus_tree_workspace_bytes(ctypes.byref(_params(fz))) - 1) == 3
+    assert call(p=_params(fz, d=96)) == 2 and call(p=_params(fz, n=65)) == 2
+    assert call(cache=_struct(fz, n_pages=(1 << 23) + 1)) == 2              # pools past 2^36 bytes
+
+
+def test_python_binding_checks_tree_tensors(fz):
+    import torch
+    p = _params(fz)
+    c = fz.alloc_cache(p, 100, device="cpu")
+    q, k = (torch.zeros((2, h, 3, 64), dtype=torch.bfloat16) for h in (4, 2))
+    gid, parent = torch.zeros((2, 1, 3), dtype=torch.int32), torch.zeros((2, 3), dtype=torch.int32)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    good = [q, k, k, gid, parent, c, q, None, ws]
+    with pytest.raises(ValueError, match="CUDA"):
+        fz.focus_cache_attention_tree_fwd(p, *good)
+    for i, bad in ((0, k), (1, q), (2, k.float()), (3, gid.long()), (4, gid), (6, k), (7, parent)):
+        args = list(good)
+        args[i] = bad
+        with pytest.raises(ValueError, match="must be"):
+            fz.focus_cache_attention_tree_fwd(p, *args)
+    with pytest.raises(ValueError, match="must be"):
+        fz.focus_cache_attention_tree_fwd(p, *good, n_new=parent)
