@@ -1277,6 +1277,8 @@ focus_status_t focus_cache_attention_tree_fwd(const focus_params_t* p, const voi
   CacheAttnLaunch L{Q, gid, n_new, *cache, O, lse_opt, 0,
                     p->B, p->H, p->H_kv, p->n, p->d, p->A, p->w > 1 ? p->w : 1,
                     p->scale * 1.4426950408889634f, at<int>(ws, 0), dev, K, V, parent};
+  if (p->dtype == FOCUS_BF16 && p->H / p->H_kv * p->n > kCacheRows && p->K <= kCacheTableGroups)
+    return cuda_status(launch_cache_tree_tc(L, static_cast<cudaStream_t>(stream)));
   return cuda_status(launch_cache_tree(L, p->dtype, static_cast<cudaStream_t>(stream)));
 }
 

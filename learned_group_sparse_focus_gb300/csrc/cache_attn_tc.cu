@@ -44,7 +44,7 @@
 // heads a head at 32K: 18 and 23 us.
 #include <cooperative_groups.h>
 
-#include "cache.cuh"
+#include "cache_tc.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -89,23 +89,6 @@ struct TcCfg {
   static constexpr int kCols = 8 * R;                          // TMEM: S twice, O
 };
 
-__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-               : "r"(addr));
-}
-__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(addr));
-}
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-               ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 // kind::f8f6f4, A and B e4m3, fp32 accumulate; M = 128.
 constexpr uint32_t idesc_f8(int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
@@ -118,12 +101,6 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, 
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
       ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
-// Shared-memory descriptor of an operand with rows of 128 bytes; see sw128_desc.
-__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr, uint32_t lbo) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3fffu) | static_cast<uint64_t>((lbo >> 4) & 0x3fffu) << 16 |
-         static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
-}
-
 // Arrives on `bar` (counted in its arrivals) when this thread's cp.async so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -155,14 +132,6 @@ __device__ __forceinline__ void split_e4m3(float p0, float p1, uint32_t& c12, ui
   rest(c3);
   c12 = c1 | c2 << 16;
   c34 = c3 | part() << 16;
-}
-
-// mbar_wait that reads the clock only after a few tries (the read costs as much as most
-// of these waits).
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
-  for (int i = 0; i < 16; ++i)
-    if (mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) return true;
-  return mbar_wait(bar, parity, abort, err);
 }
 
 __device__ __forceinline__ uint64_t bits_from(int k) {   // bits k ... 63

@@ -1,0 +1,877 @@
+// Attention of a tree of drafted tokens over the paged 8-bit cache and over the tree itself
+// on the tcgen05 tensor cores: bf16 tensors, more than 16 query rows a head (contract:
+// focus.h; cache_tree.cu launches the mma.sync kernel for every other case).
+//
+// A tree's nodes fall into many groups, so most slots are kept by some node, and few by any
+// one: products over gathered tiles of 128 keys and 32 or 64 query rows, masked.  A kept
+// slot is read once a block of rows (2 d bytes), and costs 6 d flops a row as computed
+// (4 d for S and P V, 2 d more for the weights' second half).
+//
+//   S^T [128 keys, R rows]      = K Q^T        kind::f16: a code is an f16 number, a bf16
+//                                 query row times a power of two is one too
+//   O^T [128 dims, 2 R]        += V^T [P1 P2]  weights in two f16 parts, 22 bits, side by side
+//                                 in N with accumulators of their own
+// The gathering warps read codes (and the drafted rows, scaled to f16 by a power of two of
+// their own) into registers, convert and store them as the tensor core reads them: f16 costs
+// twice the shared memory of codes, but half the tensor time of four e4m3 parts and a
+// third of the instructions a weight (cache_attn_tc.cu's form, which keeps codes).
+//
+// A thread of the weight warps owns a key and 16 rows.  Masks are a bit per row, held in an
+// order in which one shift brings four rows' bits to the tops of four bytes and a byte
+// permute spreads each to a word: a weight is masked by one AND, which also drops a NaN or an
+// infinity that the row does not keep.
+//
+// The reference of a row is common to the block and moves only when a weight would pass
+// 2^kTop: weights are formed with the old one first, and a barrier with a vote tells a part's
+// four warps whether they start over.
+//
+// Work split: a cluster of blocks for each sequence, head and block of rows; pages go round
+// over the cluster's blocks, the tree's own keys are the first tile of its last block.
+#include <cooperative_groups.h>
+
+#include "cache_tc.cuh"
+#include "tree.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace focus {
+namespace {
+
+constexpr int kTile = 128;             // keys of a tile
+constexpr int kMaxCluster = kMaxClusterBlocks;
+constexpr float kBelow = 7.f, kTop = 15.f;   // f16 ends at 2^16: weights start at 2^7 and stay below 2^15
+// Sums are held times 2^kLift: s_max - ref lies within [7 - 120, 15 + 64], so a row's largest
+// term within 2^-96 and 2^96, and a term is lost only below 2^-30 of it.
+constexpr int kLift = 17;
+
+template <int D, int R>
+struct Cfg {
+  // Weight warps: four TMEM lane quadrants times kParts parts of the rows; then the scan
+  // warps, those that gather, and the one that issues the products.
+  static constexpr int kParts = R / 16, kSoftWarps = 4 * kParts, kScanWarps = R == 64 ? 3 : 5, kGatherWarps = 8,
+                       kGatherWarp = kSoftWarps + kScanWarps, kMmaWarp = kGatherWarp + kGatherWarps,
+                       kThreads = (kMmaWarp + 1) * 32;
+  static constexpr int kStages = 2, kListed = 4;               // tiles gathered, and listed, ahead of the products
+  static constexpr int kAhead = R == 64 ? 8 : 16;              // pages a scan warp fetches group ids of at a time
+  static constexpr int kSlots = R == 64 ? 4 : 8, kPages = kSlots / 2, kRound = kPages * kScanWarps;   // slots a lane, pages a warp, a round
+  static constexpr int kList = R == 64 ? 1024 : 2048;          // entries of the block's list of kept slots
+  static_assert(kList >= kRound * kPage + kListed * kTile && kStages < kListed, "list too short");
+  static constexpr int kChunk = kTile * 128;                   // 64 f16 columns of a tile's rows
+  static constexpr int kTileBytes = D / 64 * kChunk, kPBytes = R / 32 * kChunk;
+  // byte offsets in dynamic shared memory
+  static constexpr int kK = 0, kV = kK + kStages * kTileBytes, kP = kV + kStages * kTileBytes, kQ = kP + kPBytes,
+                       kListAt = kQ + R * D * 2, kIds = kListAt + kList * 16, kTable = kIds + 2 * kScanWarps * kAhead * kPage * 2,
+                       kSmem = kTable + kCacheTableGroups * 8 + 1024;   // + alignment
+  static constexpr int kInbox = kP;                            // the partials', once the block's tiles are done
+  static_assert(R * D * 4 <= kPBytes && R % kMaxCluster == 0, "inbox does not fit");
+  static constexpr int kCols = 4 * R;                          // TMEM: S twice, O in two parts
+};
+
+// kind::f16, A and B f16, fp32 accumulate; M = 128.
+constexpr uint32_t idesc_f16(int N, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+// Row masks: row 4 q + i of 32 is bit 8 i + 7 - q of its word.
+__device__ __forceinline__ uint64_t row_bit(int r) {
+  return 1ull << ((r & 32) | (r & 3) * 8 | (7 - ((r & 31) >> 2)));
+}
+__device__ __forceinline__ int row_of_bit(int b) { return (b & 32) | (7 - (b & 7)) * 4 | ((b & 31) >> 3); }
+
+// 32 times bit 8 i + 7 of x.
+template <int i>
+__device__ __forceinline__ uint32_t spread(uint32_t x) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(x), "n"(0x8888 | 0x1111 * i));
+  return r;
+}
+
+// Barrier of `count` threads that returns whether any of them says so.
+__device__ __forceinline__ bool named_barrier_or(int id, int count, bool v) {
+  int r;
+  asm volatile(
+      "{\n .reg .pred pi, po;\n setp.ne.s32 pi, %1, 0;\n bar.red.or.pred po, %2, %3, pi;\n"
+      " selp.s32 %0, 1, 0, po;\n}"
+      : "=r"(r) : "r"(v ? 1 : 0), "r"(id), "r"(count) : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(CacheAttnLaunch L) {
+  using C = Cfg<D, R>;
+  constexpr int kStages = C::kStages, RH = 16, kList = C::kList, kSlots = C::kSlots, kPages = C::kPages;
+  constexpr int kRound = C::kRound, kLanes = kPage / kSlots, kAhead = C::kAhead, kListed = C::kListed;
+  constexpr int kSoftWarps = C::kSoftWarps, kScanWarps = C::kScanWarps, kGatherWarp = C::kGatherWarp,
+                kGatherWarps = C::kGatherWarps, kMmaWarp = C::kMmaWarp, kThreads = C::kThreads;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t k_full[kStages], v_full[kStages], qk_done[kStages], pv_done[kStages], s_ready[2], p_ready;
+  __shared__ uint64_t listed[kListed], used[kListed];  // a tile's entries are in the list; the weight warps have read them
+  __shared__ uint64_t scan_bar;
+  __shared__ uint2 s_found[2][kScanWarps];             // slots that a scan warp lists in a round, and its scales' range
+  // Keys of a tile (by tile modulo 8), kWide where the scales scanned by then lie more than
+  // kScaleSpan apart, kOwn for the tree's own; 0 ends the tiles.
+  __shared__ int s_cnt[8];
+  constexpr int kWide = 256, kOwn = 512;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort_word;
+  __shared__ __align__(16) float s_factor[R], s_minus[R];   // the rows' factors; the references, negated
+  __shared__ int s_top[4][R];                          // per lane quadrant, in integer order
+  __shared__ float s_l[4][R];
+  __shared__ float s_weight[kMaxCluster][R];           // weight of a block's partial in a row (join)
+  __shared__ float2 s_all[kMaxCluster][R];             // the cluster's references and sums
+  __shared__ uint32_t s_nan[R][D / 32];                // outputs that a kept NaN value reaches
+  __shared__ unsigned long long s_line[kMaxNodes], s_keepers[kMaxNodes], s_below[kMaxNodes + 1];   // rows that keep a node; rows of a depth below
+  __shared__ int s_node[kMaxNodes], s_depth[R];        // group id of a node, depth of a row
+  __shared__ uint32_t s_range[2];                      // of the drafted values: the largest exponent + 64, 120 - the smallest
+  volatile int* abort = &s_abort_word;
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  int4* list = reinterpret_cast<int4*>(smem + C::kListAt);
+  float* inbox = reinterpret_cast<float*>(smem + C::kInbox);
+  unsigned long long* table = reinterpret_cast<unsigned long long*>(smem + C::kTable);   // rows per group id
+  cg::cluster_group cluster = cg::this_cluster();
+  const int blocks = (L.H / L.H_kv * L.n + R - 1) / R; // blocks of rows a head may have
+  const int cs = gridDim.x / blocks, rank = blockIdx.x % cs, r0 = blockIdx.x / cs * R, h = blockIdx.y, b = blockIdx.z;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int G = L.H / L.H_kv;
+  const int fresh = cache_new(L.n_new, L.n, b, L.err);
+  const int rows = G * fresh;
+  if (r0 >= rows) return;                              // the same in the whole cluster
+  const int live = min(R, rows - r0);
+  const int n = cache_len(L.c, L.H_kv, b, h, L.err);
+  const int next = L.c.next[b];                        // position of a node at depth 0
+  const int pages = (n + kPage - 1) / kPage;
+  const int near_from = n - min(n, L.w);               // slots are in ascending position, before `next`
+  const int32_t* gids = L.gid + (static_cast<size_t>(b) * L.A + (L.A == 1 ? 0 : h)) * L.n;
+
+  // ---- the scan's state, and its first loads.  Pages rank, rank + cs, ... in rounds of
+  // kRound, kPages a warp: its page x is number x / kPages * kRound + v * kPages +
+  // x % kPages of them.
+  const int v = warp - kSoftWarps;
+  auto page_of = [&](int x) { return rank + (x / kPages * kRound + v * kPages + x % kPages) * cs; };
+  auto entry_of = [&](int x) {                         // table entry of the warp's page x + lane, unchecked
+    const int j = page_of(x + lane);
+    return lane < kAhead && j < L.c.max_pages ? L.c.table[static_cast<size_t>(b) * L.c.max_pages + j] : -1;
+  };
+  uint8_t* ids = smem + C::kIds + v * 2 * kAhead * kPage * 2;          // two batches of kAhead pages
+  int next_page = -1, entry = 0;
+  PageScales next_scales{1.f, 1.f};
+  auto fetch = [&](int x) {                            // starts on pages x ... x + kAhead - 1, and on the table behind them
+    next_page = -1;
+    if (lane < kAhead && page_of(x + lane) < pages) {
+      next_page = entry;
+      if (entry < 0 || entry >= L.c.n_pages) {
+        atomicOr(L.err, kErrBadCache);
+        next_page = -1;
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int y = 0; y < kAhead * kPage * 2 / 16 / 32; ++y) {
+      const int page = __shfl_sync(~0u, next_page, y * 4 + lane / 8);
+      if (page >= 0)
+        cp_async_16(ids + (x / kAhead & 1) * kAhead * kPage * 2 + y * 512 + lane * 16,
+                    L.c.gid + (static_cast<size_t>(page) * L.H_kv + h) * kPage + lane % 8 * 8, 16);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (next_page >= 0) next_scales.load(L.c, static_cast<size_t>(next_page) * L.H_kv + h);
+    entry = entry_of(x + kAhead);
+  };
+  const bool scans = warp >= kSoftWarps && warp < kGatherWarp;
+  if (scans) {
+    entry = entry_of(0);
+    fetch(0);
+  }
+
+  // ---- barriers, tree, masks
+  if (threadIdx.x == 0) {
+    s_abort_word = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&k_full[i], kGatherWarps);
+      mbar_init(&v_full[i], kGatherWarps);
+      mbar_init(&qk_done[i], 1);
+      mbar_init(&pv_done[i], 1);
+    }
+    for (int i = 0; i < kListed; ++i) {
+      mbar_init(&listed[i], kScanWarps);
+      mbar_init(&used[i], kSoftWarps);
+    }
+    mbar_init(&s_ready[0], 1);
+    mbar_init(&s_ready[1], 1);
+    mbar_init(&p_ready, kSoftWarps);
+    mbar_init(&scan_bar, kScanWarps);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(&s_tmem, C::kCols);
+  if (warp == kGatherWarp) tree_lines(L.parent + static_cast<size_t>(b) * L.n, fresh, s_line, s_node, L.err);
+  for (int i = threadIdx.x; i < kCacheTableGroups; i += kThreads) table[i] = 0;
+  for (int i = threadIdx.x; i < R * (D / 32); i += kThreads) s_nan[0][i] = 0;
+  if (threadIdx.x < kMaxNodes) s_keepers[threadIdx.x] = 0;
+  if (threadIdx.x < 2) s_range[threadIdx.x] = 0;
+  // queries: f16 by a power of two a row, a warp a row
+  if (warp < kSoftWarps) {
+    constexpr int kEach = D / 32;                      // elements a lane
+    uint32_t u[R / kSoftWarps][kEach / 2];
+#pragma unroll
+    for (int i = 0; i < R / kSoftWarps; ++i) {
+      const int r = warp + i * kSoftWarps, g = (r0 + r) % G, t = (r0 + r) / G;
+#pragma unroll
+      for (int e = 0; e < kEach / 2; ++e) u[i][e] = 0;
+      if (r < live) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(L.Q) +
+                                                                ((static_cast<size_t>(b) * L.H + h * G + g) * L.n + t) * D);
+#pragma unroll
+        for (int e = 0; e < kEach / 2; ++e) u[i][e] = src[lane * (kEach / 2) + e];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < R / kSoftWarps; ++i) {
+      const int r = warp + i * kSoftWarps;
+      uint32_t top = 0;
+      bool finite = true;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const uint32_t a = (e & 1 ? u[i][e / 2] & 0x7fff0000u : u[i][e / 2] << 16 & 0x7fff0000u);
+        if (a < 0x7f800000u) top = max(top, a);
+        else finite = false;
+      }
+      top = __reduce_max_sync(~0u, top);
+      finite = __all_sync(~0u, finite);
+      const int eq = min(max(static_cast<int>(top >> 23) - 127 - 13, kMinQueryExp), 115);   // |q| 2^-eq < 2^14
+      const float down = exp2_int(-eq);
+      const int d = lane * kEach;                      // a row's 16-byte piece d / 8 of its chunk
+      uint8_t* to = smem + C::kQ + d / 64 * R * 128 + r * 128 + ((d % 64 / 8) ^ (r & 7)) * 16 + d % 8 * 2;
+#pragma unroll
+      for (int e = 0; e < kEach / 2; ++e)
+        reinterpret_cast<uint32_t*>(to)[e] = half2_bits(__uint_as_float(u[i][e] << 16) * down, __uint_as_float(u[i][e] & 0xffff0000u) * down);
+      if (lane == 0) {
+        // rows with an infinite or NaN element become NaN through their factor
+        s_factor[r] = finite ? exp2_int(eq) * L.scale_log2 : __int_as_float(0x7fffffff);
+        s_minus[r] = -kNoRef;
+      }
+    }
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  if (threadIdx.x < kMaxNodes) s_node[threadIdx.x] = threadIdx.x < fresh ? gids[threadIdx.x] : 0;
+  __syncthreads();
+  const bool has_own = rank == cs - 1;                 // the block that takes the tree's own keys
+  if (has_own && warp >= kGatherWarp && warp < kMmaWarp) {
+    for (int j = warp - kGatherWarp; j < fresh; j += kGatherWarps) {
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(L.V) +
+                                                              ((static_cast<size_t>(b) * L.H_kv + h) * L.n + j) * D);
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const uint32_t two = src[i * 32 + lane], lo = two << 16 & 0x7fff0000u, hi = two & 0x7fff0000u;
+        if (lo < 0x7f800000u) top = max(top, lo);
+        if (hi < 0x7f800000u) top = max(top, hi);
+      }
+      const int e = min(need_exp(__reduce_max_sync(~0u, top)), kMaxExp);
+      if (lane == 0) {
+        atomicMax(&s_range[0], static_cast<uint32_t>(e - kMinExp));
+        atomicMax(&s_range[1], static_cast<uint32_t>(kMaxExp - e));
+      }
+    }
+  }
+  if (threadIdx.x < R) {                               // a thread a row
+    const int r = threadIdx.x;
+    int depth = INT_MAX;
+    if (r < live) {
+      const int t = (r0 + r) / G, g = s_node[t];
+      const unsigned long long line = s_line[t], bit = row_bit(r);
+      depth = __popcll(line) - 1;
+      int up = 0;                                      // from the root down: j is `depth - up` steps above
+      for (unsigned long long left = line; left; left &= left - 1, ++up) {
+        const int j = __ffsll(left) - 1;
+        if (depth - up < L.w || s_node[j] == g) atomicOr(&s_keepers[j], bit);
+      }
+      if (g >= 0 && g < kCacheTableGroups) atomicOr(&table[g], bit);
+    }
+    s_depth[r] = depth;
+  }
+  __syncthreads();
+  if (threadIdx.x <= kMaxNodes) {
+    unsigned long long below = 0;
+    for (int r = 0; r < live; ++r) below |= s_depth[r] < static_cast<int>(threadIdx.x) ? row_bit(r) : 0ull;
+    s_below[threadIdx.x] = below;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem, tmem_o = tmem + 2 * R;
+
+  int tiles = 0;                                       // weight warps: tiles of the block
+  if (scans) {
+    // -------------------------------------------------- scan
+    int entries = 0, x = 0;                            // listed slots; the warp's next page
+    int lane_page = -1, lane_exps = 0;
+    uint32_t scan_phase = 0;
+    // Value exponents of the pages begun: the largest + 64 and 120 - the smallest in two
+    // 16-bit halves, of this warp and of all scan warps.
+    uint32_t my_range = has_own ? s_range[0] | s_range[1] << 16 : 0, range = my_range;
+    auto wide = [&]() { return static_cast<int>((range & 0xffffu) + (range >> 16)) - (kMaxExp - kMinExp) > kScaleSpan; };
+    if (has_own) {
+      entries = kTile;                                 // the first tile is the tree's own
+      if (v == 0)
+        for (int j = lane; j < fresh; j += 32) {
+          const unsigned long long rows_of = s_keepers[j];
+          list[j] = make_int4(j, 0, static_cast<int>(rows_of), static_cast<int>(rows_of >> 32));   // exponents: by the gathering warp
+        }
+    }
+    auto scan_round = [&]() {
+      if (x % kAhead == 0) {                           // a new batch: it becomes current, the next one is fetched
+        lane_page = next_page;
+        lane_exps = next_scales.bytes();
+        const int ve = static_cast<int8_t>(lane_exps >> 8);
+        const uint32_t high = __reduce_max_sync(~0u, lane_page >= 0 ? static_cast<uint32_t>(ve - kMinExp) : 0u);
+        const uint32_t low = __reduce_max_sync(~0u, lane_page >= 0 ? static_cast<uint32_t>(kMaxExp - ve) : 0u);
+        my_range = __vmaxu2(my_range, high | low << 16);
+        fetch(x + kAhead);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+      }
+      const int sub = lane / kLanes, at_page = x % kAhead + sub, slot0 = lane % kLanes * kSlots;
+      const int page = __shfl_sync(~0u, lane_page, at_page), exps = __shfl_sync(~0u, lane_exps, at_page);
+      const int j = page_of(x + sub), s = j * kPage + slot0;
+      uint32_t idw[kSlots / 2];
+      const uint2* src = reinterpret_cast<const uint2*>(ids + (x / kAhead & 1) * kAhead * kPage * 2 + (at_page * kPage + slot0) * 2);
+#pragma unroll
+      for (int e = 0; e < kSlots / 4; ++e) {
+        idw[2 * e] = src[e].x;
+        idw[2 * e + 1] = src[e].y;
+      }
+      const size_t plane = static_cast<size_t>(max(page, 0)) * L.H_kv + h;
+      const int left = page >= 0 ? n - s : 0;          // slots of this lane that are in use
+      uint64_t mk[kSlots];                             // rows that keep the slot
+      uint32_t kept = 0;
+#pragma unroll
+      for (int e = 0; e < kSlots; ++e) {
+        const int id = static_cast<int16_t>(idw[e / 2] >> (e % 2 * 16));
+        mk[e] = id >= 0 && id < kCacheTableGroups ? table[id] : 0ull;
+      }
+      const bool near = page >= 0 && (j + 1) * kPage > near_from;
+      if (__any_sync(~0u, near)) {
+        int at[kSlots];
+#pragma unroll
+        for (int e = 0; e < kSlots; e += 4) {
+          int4 p = make_int4(0, 0, 0, 0);
+          if (near) p = *reinterpret_cast<const int4*>(L.c.pos + plane * kPage + slot0 + e);
+          at[e] = p.x; at[e + 1] = p.y; at[e + 2] = p.z; at[e + 3] = p.w;
+        }
+#pragma unroll
+        for (int e = 0; e < kSlots; ++e) {
+          if (!near) continue;
+          // rows of a depth below `from` lie before the slot, those below `to` have it in their window
+          const long long ahead = static_cast<long long>(at[e]) - next;
+          const uint64_t before = s_below[min(max(ahead, 0ll), static_cast<long long>(kMaxNodes))];
+          mk[e] = (mk[e] | s_below[min(max(ahead + L.w, 0ll), static_cast<long long>(kMaxNodes))]) & ~before;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kSlots; ++e)
+        if (e < left && mk[e]) kept |= 1u << e;
+      // ranks: lanes of the warp, then the warps of the round
+      int sum = __popc(kept);
+      const int mine = sum;
+#pragma unroll
+      for (int y = 1; y < 32; y *= 2) {
+        const int u = __shfl_up_sync(~0u, sum, y);
+        if (lane >= y) sum += u;
+      }
+      const int turn = x / kPages & 1;
+      if (lane == 31) s_found[turn][v] = make_uint2(sum, my_range);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&scan_bar);
+      wait(&scan_bar, scan_phase++ & 1, abort, L.err);
+      int at = entries + sum - mine;
+#pragma unroll
+      for (int w = 0; w < kScanWarps; ++w) {
+        const uint2 word = s_found[turn][w];
+        const int found = word.x;
+        range = __vmaxu2(range, word.y);
+        if (w < v) at += found;
+        entries += found;
+      }
+      const uint32_t row = static_cast<uint32_t>(plane) * kPage + slot0;
+#pragma unroll
+      for (int e = 0; e < kSlots; ++e)
+        if (kept >> e & 1) {
+          list[at & (kList - 1)] = make_int4(row + e, exps, static_cast<int>(mk[e]), static_cast<int>(mk[e] >> 32));
+          ++at;
+        }
+      x += kPages;
+    };
+    // the round's first page lies behind the end (the same in all scan warps)
+    auto scanned = [&]() { return rank + x / kPages * kRound * cs >= pages; };
+    for (int tile = 0;; ++tile) {
+      if (tile >= kListed) wait(&used[tile % kListed], (tile / kListed + 1) & 1, abort, L.err);
+      const bool own = has_own && tile == 0;
+      if (!own)
+        while (entries < (tile + 1) * kTile && !scanned()) scan_round();
+      const int cnt = own ? fresh : max(min(kTile, entries - tile * kTile), 0);
+      if (v == 0 && lane == 0) s_cnt[tile & 7] = (own ? cnt | kOwn : cnt) | (cnt > 0 && wide() ? kWide : 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&listed[tile % kListed]);         // with every warp's: the tile's entries are there
+      if (__any_sync(~0u, cnt == 0 || *abort)) break;
+    }
+    cp_async_wait_all();
+  } else if (warp >= kGatherWarp && warp < kMmaWarp) {
+    // -------------------------------------------------- gathers of kept rows, as f16
+    // A lane has 16 codes of a row (kRowLanes lanes a row).
+    constexpr int kRowLanes = D / 16, kRowsAtOnce = 32 / kRowLanes, kLoads = kTile / kGatherWarps / kRowsAtOnce;
+    const int gw = warp - kGatherWarp, sub = lane / kRowLanes, piece = lane % kRowLanes;
+    auto row_at = [&](int y) { return gw * (kTile / kGatherWarps) + y * kRowsAtOnce + sub; };
+    // 16 f16 numbers, columns piece * 16 ..., of row r of a tile
+    auto put = [&](uint8_t* tile_at, int r, const uint32_t (&w)[8]) {
+      uint8_t* to = tile_at + piece / 4 * C::kChunk + r * 128;
+      const int c = piece % 4 * 2;
+      *reinterpret_cast<uint4*>(to + (c ^ (r & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(to + ((c + 1) ^ (r & 7)) * 16) = make_uint4(w[4], w[5], w[6], w[7]);
+    };
+    auto widen = [&](uint4 c, uint32_t (&w)[8]) {
+      const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[2 * i] = e4m3x2_to_f16x2(static_cast<uint16_t>(in[i]));
+        w[2 * i + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(in[i] >> 16));
+      }
+    };
+    auto arrive = [&](uint64_t* bar) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    for (int tile = 0;; ++tile) {
+      const int st = tile % kStages;
+      const uint32_t parity = (tile / kStages + 1) & 1;
+      const bool ok = __all_sync(~0u, wait(&listed[tile % kListed], (tile / kListed) & 1, abort, L.err));
+      const int word = ok ? s_cnt[tile & 7] : 0, cnt = word & (kWide - 1);
+      if (__any_sync(~0u, cnt == 0 || *abort)) {
+        // not before the stage's last phase has been seen: a wait on it would miss two in a row
+        if (tile >= kStages) wait(&qk_done[st], parity, abort, L.err);
+        arrive(&k_full[st]);
+        break;
+      }
+      uint8_t* const k_at = smem + C::kK + st * C::kTileBytes;
+      uint8_t* const v_at = smem + C::kV + st * C::kTileBytes;
+      int4* const about = list + (tile * kTile & (kList - 1));
+      if (word & kOwn) {                               // the tree's rows, each times a power of two
+        if (tile >= kStages) wait(&qk_done[st], parity, abort, L.err);
+        if (tile >= kStages) wait(&pv_done[st], parity, abort, L.err);
+        for (int y = 0; y < kLoads; ++y) {
+          const int r = row_at(y);
+          int exps = 0;
+          bool bad = false;
+          for (int x = 0; x < 2; ++x) {
+            uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            if (r < cnt) {
+              const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x ? L.V : L.K) +
+                                                                ((static_cast<size_t>(b) * L.H_kv + h) * L.n + r) * D + piece * 16);
+              u[0] = src[0];
+              u[1] = src[1];
+            }
+            float f[16], top = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const uint32_t two = (&u[e / 8].x)[e % 8 / 2];
+              f[e] = __uint_as_float(e & 1 ? two & 0xffff0000u : two << 16);
+              if (!(fabsf(f[e]) < INFINITY)) {
+                bad = true;
+                f[e] = 0.f;
+              }
+              top = fmaxf(top, fabsf(f[e]));
+            }
+#pragma unroll
+            for (int z = 1; z < kRowLanes; z *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, z));
+            const int e_row = min(need_exp(__float_as_uint(top)), kMaxExp);
+            const float down = exp2_int(-e_row);
+            exps |= (e_row & 0xff) << (8 * x);
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = half2_bits(f[2 * e] * down, f[2 * e + 1] * down);
+            put(x ? v_at : k_at, r, w);
+          }
+          const uint32_t bad_lanes = __ballot_sync(~0u, bad) >> (sub * kRowLanes) & ((1u << kRowLanes) - 1);
+          if (piece == 0 && r < cnt) about[r].y = exps | (bad_lanes ? 1 << 16 : 0);
+        }
+        arrive(&k_full[st]);
+        arrive(&v_full[st]);
+        continue;
+      }
+      uint4 k[kLoads], vv[kLoads];
+#pragma unroll
+      for (int y = 0; y < kLoads; ++y) {
+        const int r = row_at(y);
+        k[y] = vv[y] = make_uint4(0, 0, 0, 0);
+        if (r < cnt) {
+          const size_t off = static_cast<size_t>(static_cast<uint32_t>(about[r].x)) * D + piece * 16;
+          k[y] = __ldg(reinterpret_cast<const uint4*>(L.c.k + off));
+          vv[y] = __ldg(reinterpret_cast<const uint4*>(L.c.v + off));
+        }
+      }
+      if (tile >= kStages) wait(&qk_done[st], parity, abort, L.err);
+#pragma unroll
+      for (int y = 0; y < kLoads; ++y) {
+        uint32_t w[8];
+        widen(k[y], w);
+        put(k_at, row_at(y), w);
+      }
+      arrive(&k_full[st]);
+      if (tile >= kStages) wait(&pv_done[st], parity, abort, L.err);
+#pragma unroll
+      for (int y = 0; y < kLoads; ++y) {
+        // A row that does not keep a key has weight 0 for it, and 0 * NaN would reach that
+        // row: NaN codes leave the tile and mark the outputs that they reach.
+        const uint32_t m = 0x7f7f7f7fu, one = 0x01010101u;         // a magnitude of 127 carries into the sign's bit
+        const uint32_t any = (((vv[y].x & m) + one) | ((vv[y].y & m) + one)) | (((vv[y].z & m) + one) | ((vv[y].w & m) + one));
+        if (any & 0x80808080u) {
+          const int4 e = about[row_at(y)];
+#pragma unroll 1
+          for (int i = 0; i < 16; ++i) {
+            uint32_t* at = &vv[y].x;
+            const uint32_t word_i = i < 4 ? at[0] : i < 8 ? at[1] : i < 12 ? at[2] : at[3];
+            if ((word_i >> (i % 4 * 8) & 127u) != 127u) continue;
+            const uint32_t clear = ~(0xffu << (i % 4 * 8));
+            if (i < 4) at[0] &= clear;
+            else if (i < 8) at[1] &= clear;
+            else if (i < 12) at[2] &= clear;
+            else at[3] &= clear;
+            const int d = piece * 16 + i;
+            for (uint32_t left = e.z; left; left &= left - 1) atomicOr(&s_nan[row_of_bit(__ffs(left) - 1)][d / 32], 1u << (d % 32));
+            if (R > 32)
+              for (uint32_t left = e.w; left; left &= left - 1) atomicOr(&s_nan[row_of_bit(31 + __ffs(left)) % R][d / 32], 1u << (d % 32));
+          }
+        }
+        uint32_t w[8];
+        widen(vv[y], w);
+        put(v_at, row_at(y), w);
+      }
+      arrive(&v_full[st]);
+    }
+  } else if (warp == kMmaWarp) {
+    // -------------------------------------------------- products
+    if (lane == 0) {
+      const uint32_t kb = smem_u32(smem + C::kK), vb = smem_u32(smem + C::kV), qb = smem_u32(smem + C::kQ), pb = smem_u32(smem + C::kP);
+      bool ok = true;
+      // S of a tile whose K is there; false at the end of the tiles
+      auto scores = [&](int tile) {
+        const int st = tile % kStages;
+        ok = ok && mbar_wait_nap(&k_full[st], (tile / kStages) & 1, abort, L.err);
+        ok = ok && mbar_wait(&listed[tile % kListed], (tile / kListed) & 1, abort, L.err);         // done: orders s_cnt
+        if (!ok || s_cnt[tile & 7] == 0) {
+          mbar_arrive(&s_ready[tile & 1]);
+          return false;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          mma_ss(tmem + (tile & 1) * R, desc_rows(kb + st * C::kTileBytes + x / 4 * C::kChunk + x % 4 * 32, 16),
+                 desc_rows(qb + x / 4 * R * 128 + x % 4 * 32, 16), idesc_f16(R, false, false), x > 0);
+        mma_commit(&qk_done[st]);
+        mma_commit(&s_ready[tile & 1]);
+        return true;
+      };
+      int tile = 0;
+      bool have = scores(0);
+      while (have) {
+        const int st = tile % kStages, cnt = s_cnt[tile & 7] & (kWide - 1);
+        have = scores(tile + 1);                       // needs its K alone: S's other buffer was read before the last P
+        ok = mbar_wait_nap(&p_ready, tile & 1, abort, L.err) && ok;
+        ok = ok && mbar_wait_nap(&v_full[st], (tile / kStages) & 1, abort, L.err);
+        if (ok) {
+          tc_fence_after();
+          for (int x = 0; x < (cnt + 15) / 16; ++x)
+            mma_ss(tmem_o, desc_rows(vb + st * C::kTileBytes + x * 2048, C::kChunk),
+                   desc_rows(pb + x * 2048, C::kChunk), idesc_f16(2 * R, true, true), !(tile == 0 && x == 0));
+        }
+        mma_commit(&pv_done[st]);
+        ++tile;
+      }
+      // every commit has arrived before the block ends
+      if (tile > 0) {
+        mbar_wait(&qk_done[(tile - 1) % kStages], ((tile - 1) / kStages) & 1, abort, L.err);
+        mbar_wait(&pv_done[(tile - 1) % kStages], ((tile - 1) / kStages) & 1, abort, L.err);
+      }
+    }
+  } else {
+    // -------------------------------------------------- weights: one key a thread, a part of the rows
+    const int quad = warp & 3, part = warp >> 2, key = quad * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const float* factor = s_factor + part * RH;
+    float* minus = s_minus + part * RH;
+    uint64_t sum2[RH / 2];                             // row sums, in pairs
+#pragma unroll
+    for (int r = 0; r < RH / 2; ++r) sum2[r] = f2_pack(0.f, 0.f);
+    int tile = 0;
+    for (;; ++tile) {
+      const int buf = tile & 1;
+      const bool ok = __all_sync(~0u, wait(&s_ready[buf], (tile >> 1) & 1, abort, L.err));
+      const int word = ok ? s_cnt[tile & 7] : 0, cnt = word & (kWide - 1);
+      uint32_t s[RH], p[RH], mask = 0;
+      float kf = 1.f, ve = 0.f, over = 0.f;
+      // Weights by the references as they are: p, masked; over, the largest.
+      auto form = [&]() {
+        const uint64_t kf2 = f2_pack(kf, kf), ve2 = f2_pack(ve, ve);
+#pragma unroll
+        for (int r = 0; r < RH; r += 4) {
+          uint64_t f01, f23, m01, m23;
+          lds_f2x2(factor + r, f01, f23);
+          lds_f2x2(minus + r, m01, m23);
+          float d[4];
+          f2_unpack(f2_fma(f2_mul(f2_pack(__uint_as_float(s[r]), __uint_as_float(s[r + 1])), f01), kf2, f2_add(ve2, m01)), d[0], d[1]);
+          f2_unpack(f2_fma(f2_mul(f2_pack(__uint_as_float(s[r + 2]), __uint_as_float(s[r + 3])), f23), kf2, f2_add(ve2, m23)), d[2], d[3]);
+          const uint32_t four = mask << (r / 4);
+          p[r] = __float_as_uint(exp2_fast(d[0])) & spread<0>(four);
+          p[r + 1] = __float_as_uint(exp2_fast(d[1])) & spread<1>(four);
+          p[r + 2] = __float_as_uint(exp2_fast(d[2])) & spread<2>(four);
+          p[r + 3] = __float_as_uint(exp2_fast(d[3])) & spread<3>(four);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) over = fmaxf(over, __uint_as_float(p[r + e]));
+        }
+      };
+      int ex = 0;
+      if (cnt > 0) {
+        tc_fence_after();
+        tmem_ld(tmem + lanes + buf * R + part * RH, s);
+        if (key < cnt) {
+          const int4 e = list[(tile * kTile + key) & (kList - 1)];
+          ex = e.y;
+          mask = static_cast<uint32_t>(part < 2 ? e.z : e.w) << (part & 1) * 4;
+        }
+        kf = ex >> 16 & 1 ? __int_as_float(0x7fffffff) : exp2_int(static_cast<int8_t>(ex));
+        ve = static_cast<float>(static_cast<int8_t>(ex >> 8));
+        tmem_wait_ld();
+        form();
+      }
+      // One vote for "a weight is too large" and "a warp has given up": the four warps of a part go
+      // on together, whatever happens.
+      if (named_barrier_or(1 + part, 128, !ok || over > 32768.f)) {
+        if (named_barrier_or(1 + part, 128, !ok)) break;
+        // Some row's reference moves, by the row's own weights: rows do not touch each other.
+        // Lane r takes row r (the same result in the part's four warps).
+        int top = INT_MIN;
+#pragma unroll
+        for (int r = 0; r < RH; ++r) {
+          const float t = fmaf(__uint_as_float(s[r]) * factor[r], kf, ve);
+          const int u = __float_as_int(t), order = u ^ (u >> 31 & 0x7fffffff);   // floats' order as integers
+          const bool mine = mask >> ((r & 3) * 8 + 7 - r / 4) & 1 && t == t;
+          const int m = __reduce_max_sync(~0u, mine ? order : INT_MIN);
+          if (lane == r) top = m;
+        }
+        if (lane < RH) s_top[quad][part * RH + lane] = top;
+        named_barrier(1 + part, 128);
+        float moved = 0.f, fh = 1.f;                   // the factor's root: it may lie below the normals where sums do not
+        if (lane < RH) {
+          const int rr = part * RH + lane;
+          const int m = max(max(s_top[0][rr], s_top[1][rr]), max(s_top[2][rr], s_top[3][rr]));
+          const float was = -s_minus[rr], highest = m == INT_MIN ? -INFINITY : __int_as_float(m ^ (m >> 31 & 0x7fffffff));
+          moved = highest > was + kTop ? highest - kBelow : was;
+          fh = exp2_fast(0.5f * (was - moved));
+        }
+#pragma unroll
+        for (int r = 0; r < RH; r += 2) {
+          const uint64_t fh2 = f2_pack(__shfl_sync(~0u, fh, r), __shfl_sync(~0u, fh, r + 1));
+          sum2[r / 2] = f2_mul(f2_mul(sum2[r / 2], fh2), fh2);
+        }
+        if (tile > 0) {
+          wait(&pv_done[(tile - 1) % kStages], ((tile - 1) / kStages) & 1, abort, L.err);
+          tc_fence_after();
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {                // both parts of the weights
+            uint32_t o[RH];
+            tmem_ld(tmem_o + lanes + y * R + part * RH, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int r = 0; r < RH; ++r) {
+              const float f = __shfl_sync(~0u, fh, r);
+              if (f != 1.f) o[r] = __float_as_uint(__uint_as_float(o[r]) * (f * f));
+            }
+            tmem_st16(tmem_o + lanes + y * R + part * RH, o);
+          }
+          tmem_wait_st();
+        }
+        named_barrier(1 + part, 128);                  // every warp has read the old references
+        if (quad == 0 && lane < RH) minus[lane] = -moved;
+        named_barrier(1 + part, 128);
+        form();
+      }
+      if (cnt == 0) break;
+      // sums: 2^(s - ref) is the weight times 2^-ve, or where scales lie far apart an exponential of its own
+      float vf = exp2_int(kLift - static_cast<int8_t>(ex >> 8));
+      if (word & kWide) {                              // the same in all warps
+        const float up = static_cast<float>(kLift);
+#pragma unroll
+        for (int r = 0; r < RH; r += 2) {
+          float d[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            d[e] = exp2_fast(fmaf(__uint_as_float(s[r + e]) * factor[r + e], kf, minus[r + e] + up));
+            if (!(mask >> (((r + e) & 3) * 8 + 7 - r / 4) & 1)) d[e] = 0.f;
+          }
+          sum2[r / 2] = f2_add(sum2[r / 2], f2_pack(d[0], d[1]));
+        }
+        vf = 0.f;
+      }
+      if (tile > 0)                                    // the last tile's product has read P
+        wait(&pv_done[(tile - 1) % kStages], ((tile - 1) / kStages) & 1, abort, L.err);
+      const uint64_t vf2 = f2_pack(vf, vf);
+      uint8_t* const row = smem + C::kP + key * 128;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {                    // eight rows: 16 bytes of each part
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * c + 2 * i;
+          // ten bits below the leading one, exact in f16; the rest is exact too, and rounded to eleven
+          const uint32_t h0 = p[r] & 0xffffe000u, h1 = p[r + 1] & 0xffffe000u;
+          const uint64_t p2 = f2_pack(__uint_as_float(p[r]), __uint_as_float(p[r + 1]));
+          if (!(word & kWide)) sum2[r / 2] = f2_fma(p2, vf2, sum2[r / 2]);
+          float l0, l1;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(h0), __uint_as_float(h1)), f2_pack(-1.f, -1.f), p2), l0, l1);
+          hi[i] = half2_bits(__uint_as_float(h0), __uint_as_float(h1));
+          lo[i] = half2_bits(l0, l1);
+        }
+        const int piece = part * 2 + c;                // R = 32: the second parts behind the first in the same row
+        *reinterpret_cast<uint4*>(row + (piece ^ (key & 7)) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(row + (R == 64 ? C::kChunk : 0) + ((R == 64 ? piece : piece + 4) ^ (key & 7)) * 16) =
+            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&p_ready);
+        mbar_arrive(&used[tile % kListed]);
+      }
+    }
+    // ---- the block's partial: every row's sum, and its part of O to the block that writes it
+    tiles = tile;
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+      float l0, l1;
+      f2_unpack(sum2[r / 2], l0, l1);
+      float x = r & 1 ? l1 : l0;
+#pragma unroll
+      for (int y = 16; y > 0; y /= 2) x += __shfl_xor_sync(~0u, x, y);
+      if (lane == 0) s_l[quad][part * RH + r] = x;
+    }
+    if (tiles > 0) {
+      wait(&pv_done[(tiles - 1) % kStages], ((tiles - 1) / kStages) & 1, abort, L.err);
+      tc_fence_after();
+    }
+  }
+  __syncwarp();
+
+  // ---- join: the same exchange as in cache_attn.cuh
+  cluster.sync();                                      // every block runs and is past its tiles
+  const int share = R / cs;                            // rows that a block writes
+  if (warp < kSoftWarps && tiles > 0) {
+    const int quad = warp & 3, part = warp >> 2, d = quad * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    uint32_t hi[RH], lo[RH];
+    tmem_ld(tmem_o + lanes + part * RH, hi);
+    tmem_ld(tmem_o + lanes + R + part * RH, lo);
+    tmem_wait_ld();
+    if (quad < D / 32) {
+#pragma unroll
+      for (int y = 0; y < RH; ++y) {
+        const int r = part * RH + y, to = r / share;
+        float x = __uint_as_float(hi[y]) + __uint_as_float(lo[y]);
+        if (s_nan[r][quad] >> lane & 1) x = __int_as_float(0x7fffffff);
+        *cluster.map_shared_rank(inbox + (rank * share + r - to * share) * D + d, to) = x;
+      }
+    }
+  }
+  for (int i = threadIdx.x; i < R * cs; i += kThreads) {
+    const int r = i % R, to = i / R;
+    *cluster.map_shared_rank(&s_all[rank][r], to) = make_float2(-s_minus[r], (s_l[0][r] + s_l[1][r]) + (s_l[2][r] + s_l[3][r]));
+  }
+  tc_fence_before();
+  cluster.sync();
+  tc_fence_after();
+  if (threadIdx.x < R) {
+    const int r = threadIdx.x;
+    float M = kNoRef, l = 0.f;
+    for (int x = 0; x < cs; ++x) M = fmaxf(M, s_all[x][r].x);
+    for (int x = 0; x < cs; ++x)
+      if (s_all[x][r].y != 0.f) {
+        const float fh = exp2f(0.5f * (s_all[x][r].x - M));
+        l += s_all[x][r].y * fh * fh;
+      }
+    for (int x = 0; x < cs; ++x)
+      s_weight[x][r] = s_all[x][r].y != 0.f ? exp2f(s_all[x][r].x - M) / l * exp2_int(kLift) : 0.f;
+    if (rank == 0 && L.lse && r < live)
+      L.lse[(static_cast<size_t>(b) * L.H + h * G + (r0 + r) % G) * L.n + (r0 + r) / G] =
+          l != 0.f ? (M + (log2f(l) - kLift)) * 0.6931471805599453f : -INFINITY;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < share * (D / 4); i += kThreads) {
+    const int local = i / (D / 4), r = rank * share + local, d = i % (D / 4) * 4;
+    if (r >= live) break;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = 0; x < cs; ++x) {
+      if (s_all[x][r].y == 0.f) continue;              // nothing kept there
+      const float f = s_weight[x][r];
+      const float4 u = *reinterpret_cast<const float4*>(inbox + (x * share + local) * D + d);
+      a.x += u.x * f; a.y += u.y * f; a.z += u.z * f; a.w += u.w * f;
+    }
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(L.O) +
+                              ((static_cast<size_t>(b) * L.H + h * G + (r0 + r) % G) * L.n + (r0 + r) / G) * D + d) =
+        make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+template <int D, int R>
+ClusterFits g_fits;
+
+template <int D, int R>
+cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
+  const ClusterFit* fit;
+  if (cudaError_t e = g_fits<D, R>.get(L.device, reinterpret_cast<const void*>(cache_tree_tc_kernel<D, R>), Cfg<D, R>::kThreads,
+                                       Cfg<D, R>::kSmem, &fit))
+    return e;
+  // Blocks per (sequence, head, block of rows): one wave of the clusters that run at once, as
+  // long as each block scans a round or so.
+  const int blocks = (L.H / L.H_kv * L.n + R - 1) / R;
+  const long long heads = static_cast<long long>(L.B) * blocks * L.H_kv;
+  int cs = 1, i = 0;
+  while (cs < kMaxCluster && cs * 16 <= L.c.max_pages && heads <= fit->n[i + 1]) {
+    cs *= 2;
+    ++i;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(cs * blocks, L.H_kv, L.B);
+  cfg.blockDim = dim3(Cfg<D, R>::kThreads);
+  cfg.dynamicSmemBytes = Cfg<D, R>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cs;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_tree_tc_kernel<D, R>, L);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_tree_tc(const CacheAttnLaunch& L, cudaStream_t st) {
+  const int rows = L.H / L.H_kv * L.n;
+  if (L.d == 128) return rows <= 32 ? launch<128, 32>(L, st) : launch<128, 64>(L, st);
+  return rows <= 32 ? launch<64, 32>(L, st) : launch<64, 64>(L, st);
+}
+
+}  // namespace focus

@@ -280,8 +280,10 @@ constexpr int kCacheRows = 16;   // query rows of a head that cache_attn.cu take
 constexpr int kCacheTableGroups = 1024;
 cudaError_t launch_cache_attn_tc(const CacheAttnLaunch& L, cudaStream_t st);
 cudaError_t launch_cache_attn(const CacheAttnLaunch& L, int dtype, cudaStream_t st);
-// cache_tree.cu: the tokens are the nodes of a tree, not in the cache.
+// cache_tree.cu: the tokens are the nodes of a tree, not in the cache.  cache_tree_tc.cu: the
+// same for bf16 and more than kCacheRows rows, with K up to kCacheTableGroups.
 cudaError_t launch_cache_tree(const CacheAttnLaunch& L, int dtype, cudaStream_t st);
+cudaError_t launch_cache_tree_tc(const CacheAttnLaunch& L, cudaStream_t st);
 
 // rotary.cu: rows turned to their positions.
 struct RotaryLaunch {
