@@ -11,19 +11,21 @@
 //                                 query row times a power of two is one too
 //   O^T [128 dims, 2 R]        += V^T [P1 P2]  weights in two f16 parts, 22 bits, side by side
 //                                 in N with accumulators of their own
-// The gathering warps read codes (and the drafted rows, scaled to f16 by a power of two of
-// their own) into registers, convert and store them as the tensor core reads them: f16 costs
+// The gathering warps copy codes to shared memory a tile ahead, each lane for itself, convert
+// them (and the drafted rows, scaled to f16 by a power of two of their own) and store them as the tensor core reads them: f16 costs
 // twice the shared memory of codes, but half the tensor time of four e4m3 parts and a
 // third of the instructions a weight (cache_attn_tc.cu's form, which keeps codes).
 //
-// A thread of the weight warps owns a key and 16 rows.  Masks are a bit per row, held in an
+// A thread of the weight warps owns a key and half of the rows.  Masks are a bit per row, held in an
 // order in which one shift brings four rows' bits to the tops of four bytes and a byte
 // permute spreads each to a word: a weight is masked by one AND, which also drops a NaN or an
 // infinity that the row does not keep.
 //
 // The reference of a row is common to the block and moves only when a weight would pass
 // 2^kTop: weights are formed with the old one first, and a barrier with a vote tells a part's
-// four warps whether they start over.
+// four warps whether they start over.  With s_j the logit (log2) and e_j the exponent of the
+// key's value row, the exponential is 2^(s_j - ref + kLift), which the row's sum adds as it is,
+// and the weight that multiplies raw codes that times 2^(e_j - kLift).
 //
 // Work split: a cluster of blocks for each sequence, head and block of rows; pages go round
 // over the cluster's blocks, the tree's own keys are the first tile of its last block.
@@ -40,26 +42,26 @@ namespace {
 constexpr int kTile = 128;             // keys of a tile
 constexpr int kMaxCluster = kMaxClusterBlocks;
 constexpr float kBelow = 7.f, kTop = 15.f;   // f16 ends at 2^16: weights start at 2^7 and stay below 2^15
-// Sums are held times 2^kLift: s_max - ref lies within [7 - 120, 15 + 64], so a row's largest
-// term within 2^-96 and 2^96, and a term is lost only below 2^-30 of it.
+// s_max + e - ref lies within [7, 15] for some e of -64 ... 120, so a row's largest term within
+// 2^-96 and 2^96: 2^30 of them do not overflow, and one is lost only below 2^-30 of it.
 constexpr int kLift = 17;
 
 template <int D, int R>
 struct Cfg {
   // Weight warps: four TMEM lane quadrants times kParts parts of the rows; then the scan
   // warps, those that gather, and the one that issues the products.
-  static constexpr int kParts = R / 16, kSoftWarps = 4 * kParts, kScanWarps = R == 64 ? 3 : 5, kGatherWarps = 8,
+  static constexpr int kParts = 2, kSoftWarps = 4 * kParts, kScanWarps = 3, kGatherWarps = 8,
                        kGatherWarp = kSoftWarps + kScanWarps, kMmaWarp = kGatherWarp + kGatherWarps,
                        kThreads = (kMmaWarp + 1) * 32;
-  static constexpr int kStages = 2, kListed = 4;               // tiles gathered, and listed, ahead of the products
+  static constexpr int kListed = 4;                            // tiles listed ahead of the weights
   static constexpr int kAhead = R == 64 ? 8 : 16;              // pages a scan warp fetches group ids of at a time
   static constexpr int kSlots = R == 64 ? 4 : 8, kPages = kSlots / 2, kRound = kPages * kScanWarps;   // slots a lane, pages a warp, a round
   static constexpr int kList = R == 64 ? 1024 : 2048;          // entries of the block's list of kept slots
-  static_assert(kList >= kRound * kPage + kListed * kTile && kStages < kListed, "list too short");
+  static_assert(kList >= kRound * kPage + kListed * kTile, "list too short");
   static constexpr int kChunk = kTile * 128;                   // 64 f16 columns of a tile's rows
   static constexpr int kTileBytes = D / 64 * kChunk, kPBytes = R / 32 * kChunk;
   // byte offsets in dynamic shared memory
-  static constexpr int kK = 0, kV = kK + kStages * kTileBytes, kP = kV + kStages * kTileBytes, kQ = kP + kPBytes,
+  static constexpr int kK = 0, kV = kK + kTileBytes, kRaw = kV + 2 * kTileBytes, kP = kRaw + kTileBytes, kQ = kP + kPBytes,
                        kListAt = kQ + R * D * 2, kIds = kListAt + kList * 16, kTable = kIds + 2 * kScanWarps * kAhead * kPage * 2,
                        kSmem = kTable + kCacheTableGroups * 8 + 1024;   // + alignment
   static constexpr int kInbox = kP;                            // the partials', once the block's tiles are done
@@ -105,30 +107,27 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 template <int D, int R>
 __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(CacheAttnLaunch L) {
   using C = Cfg<D, R>;
-  constexpr int kStages = C::kStages, RH = 16, kList = C::kList, kSlots = C::kSlots, kPages = C::kPages;
+  constexpr int RH = R / 2, kList = C::kList, kSlots = C::kSlots, kPages = C::kPages;
   constexpr int kRound = C::kRound, kLanes = kPage / kSlots, kAhead = C::kAhead, kListed = C::kListed;
   constexpr int kSoftWarps = C::kSoftWarps, kScanWarps = C::kScanWarps, kGatherWarp = C::kGatherWarp,
                 kGatherWarps = C::kGatherWarps, kMmaWarp = C::kMmaWarp, kThreads = C::kThreads;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t k_full[kStages], v_full[kStages], qk_done[kStages], pv_done[kStages], s_ready[2], p_ready;
+  __shared__ uint64_t k_full, v_full[2], qk_done, pv_done[2], s_ready[2], p_ready;
   __shared__ uint64_t listed[kListed], used[kListed];  // a tile's entries are in the list; the weight warps have read them
   __shared__ uint64_t scan_bar;
-  __shared__ uint2 s_found[2][kScanWarps];             // slots that a scan warp lists in a round, and its scales' range
-  // Keys of a tile (by tile modulo 8), kWide where the scales scanned by then lie more than
-  // kScaleSpan apart, kOwn for the tree's own; 0 ends the tiles.
-  __shared__ int s_cnt[8];
-  constexpr int kWide = 256, kOwn = 512;
+  __shared__ int s_found[2][kScanWarps];               // slots that a scan warp lists in a round
+  __shared__ int s_cnt[8];                             // keys of a tile (by tile modulo 8); 0 ends the tiles
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort_word;
-  __shared__ __align__(16) float s_factor[R], s_minus[R];   // the rows' factors; the references, negated
+  __shared__ __align__(16) float s_factor[R], s_minus[R];   // the rows' factors; kLift - the references
   __shared__ int s_top[4][R];                          // per lane quadrant, in integer order
   __shared__ float s_l[4][R];
   __shared__ float s_weight[kMaxCluster][R];           // weight of a block's partial in a row (join)
   __shared__ float2 s_all[kMaxCluster][R];             // the cluster's references and sums
   __shared__ uint32_t s_nan[R][D / 32];                // outputs that a kept NaN value reaches
-  __shared__ unsigned long long s_line[kMaxNodes], s_keepers[kMaxNodes], s_below[kMaxNodes + 1];   // rows that keep a node; rows of a depth below
-  __shared__ int s_node[kMaxNodes], s_depth[R];        // group id of a node, depth of a row
-  __shared__ uint32_t s_range[2];                      // of the drafted values: the largest exponent + 64, 120 - the smallest
+  __shared__ unsigned long long s_line[kMaxNodes];     // a node's line, later what it keeps of it
+  __shared__ unsigned long long s_below[kMaxNodes + 1];   // rows of a depth, later those of a smaller one
+  __shared__ int s_node[kMaxNodes];                    // group id of a node
   volatile int* abort = &s_abort_word;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   int4* list = reinterpret_cast<int4*>(smem + C::kListAt);
@@ -191,10 +190,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   // ---- barriers, tree, masks
   if (threadIdx.x == 0) {
     s_abort_word = 0;
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&k_full[i], kGatherWarps);
+    mbar_init(&k_full, kGatherWarps);
+    mbar_init(&qk_done, 1);
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&v_full[i], kGatherWarps);
-      mbar_init(&qk_done[i], 1);
       mbar_init(&pv_done[i], 1);
     }
     for (int i = 0; i < kListed; ++i) {
@@ -211,8 +210,16 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   if (warp == kGatherWarp) tree_lines(L.parent + static_cast<size_t>(b) * L.n, fresh, s_line, s_node, L.err);
   for (int i = threadIdx.x; i < kCacheTableGroups; i += kThreads) table[i] = 0;
   for (int i = threadIdx.x; i < R * (D / 32); i += kThreads) s_nan[0][i] = 0;
-  if (threadIdx.x < kMaxNodes) s_keepers[threadIdx.x] = 0;
-  if (threadIdx.x < 2) s_range[threadIdx.x] = 0;
+  if (threadIdx.x <= kMaxNodes) s_below[threadIdx.x] = 0;
+  const bool has_own = rank == cs - 1;                 // the block that takes the tree's own keys
+  const size_t own_row = (static_cast<size_t>(b) * L.H_kv + h) * L.n;
+  if (has_own && warp > kGatherWarp && warp < kMmaWarp)        // whose rows are on their way from here on
+    for (int i = threadIdx.x - (kGatherWarp + 1) * 32; i < fresh * D / 64; i += (kGatherWarps - 1) * 32) {
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __nv_bfloat16*>(L.K) + own_row * D + i * 64));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __nv_bfloat16*>(L.V) + own_row * D + i * 64));
+    }
+  int node_gid = 0;
+  if (threadIdx.x < fresh) node_gid = gids[threadIdx.x];
   // queries: f16 by a power of two a row, a warp a row
   if (warp < kSoftWarps) {
     constexpr int kEach = D / 32;                      // elements a lane
@@ -258,48 +265,45 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     fence_proxy_async_smem();
   }
   __syncthreads();
-  if (threadIdx.x < kMaxNodes) s_node[threadIdx.x] = threadIdx.x < fresh ? gids[threadIdx.x] : 0;
-  __syncthreads();
-  const bool has_own = rank == cs - 1;                 // the block that takes the tree's own keys
-  if (has_own && warp >= kGatherWarp && warp < kMmaWarp) {
-    for (int j = warp - kGatherWarp; j < fresh; j += kGatherWarps) {
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(L.V) +
-                                                              ((static_cast<size_t>(b) * L.H_kv + h) * L.n + j) * D);
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        const uint32_t two = src[i * 32 + lane], lo = two << 16 & 0x7fff0000u, hi = two & 0x7fff0000u;
-        if (lo < 0x7f800000u) top = max(top, lo);
-        if (hi < 0x7f800000u) top = max(top, hi);
-      }
-      const int e = min(need_exp(__reduce_max_sync(~0u, top)), kMaxExp);
-      if (lane == 0) {
-        atomicMax(&s_range[0], static_cast<uint32_t>(e - kMinExp));
-        atomicMax(&s_range[1], static_cast<uint32_t>(kMaxExp - e));
-      }
-    }
+  unsigned long long line = 0;
+  if (threadIdx.x < kMaxNodes) {                       // a thread a node
+    line = s_line[threadIdx.x];
+    s_node[threadIdx.x] = node_gid;
   }
-  if (threadIdx.x < R) {                               // a thread a row
-    const int r = threadIdx.x;
-    int depth = INT_MAX;
-    if (r < live) {
-      const int t = (r0 + r) / G, g = s_node[t];
-      const unsigned long long line = s_line[t], bit = row_bit(r);
-      depth = __popcll(line) - 1;
+  __syncthreads();
+  if (threadIdx.x < fresh) {
+    const int depth = __popcll(line) - 1;
+    if (depth >= L.w) {                                // ancestors before the window: of its group only
+      unsigned long long keeps = 0;
       int up = 0;                                      // from the root down: j is `depth - up` steps above
       for (unsigned long long left = line; left; left &= left - 1, ++up) {
         const int j = __ffsll(left) - 1;
-        if (depth - up < L.w || s_node[j] == g) atomicOr(&s_keepers[j], bit);
+        if (depth - up < L.w || s_node[j] == node_gid) keeps |= 1ull << j;
       }
-      if (g >= 0 && g < kCacheTableGroups) atomicOr(&table[g], bit);
+      s_line[threadIdx.x] = keeps;
     }
-    s_depth[r] = depth;
+    // its rows of the block, by group and by depth
+    for (int r = max(static_cast<int>(threadIdx.x) * G - r0, 0); r < min((static_cast<int>(threadIdx.x) + 1) * G - r0, live); ++r) {
+      const uint32_t bit = static_cast<uint32_t>(row_bit(r) >> (r & 32));
+      if (node_gid >= 0 && node_gid < kCacheTableGroups) atomicOr(reinterpret_cast<uint32_t*>(&table[node_gid]) + (r >> 5), bit);
+      atomicOr(reinterpret_cast<uint32_t*>(&s_below[depth]) + (r >> 5), bit);
+    }
   }
   __syncthreads();
-  if (threadIdx.x <= kMaxNodes) {
-    unsigned long long below = 0;
-    for (int r = 0; r < live; ++r) below |= s_depth[r] < static_cast<int>(threadIdx.x) ? row_bit(r) : 0ull;
-    s_below[threadIdx.x] = below;
+  if (warp == 0) {                                     // sums of depths below: lane i has 2 i and 2 i + 1
+    const unsigned long long first = s_below[2 * lane], both = first | s_below[2 * lane + 1];
+    unsigned long long upto = both;
+#pragma unroll
+    for (int y = 1; y < 32; y *= 2) {
+      const unsigned long long u = __shfl_up_sync(~0u, upto, y);
+      if (lane >= y) upto |= u;
+    }
+    unsigned long long below = __shfl_up_sync(~0u, upto, 1);
+    if (lane == 0) below = 0;
+    __syncwarp();
+    s_below[2 * lane] = below;
+    s_below[2 * lane + 1] = below | first;
+    if (lane == 31) s_below[kMaxNodes] = upto;
   }
   tc_fence_before();
   __syncthreads();
@@ -312,15 +316,14 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     int entries = 0, x = 0;                            // listed slots; the warp's next page
     int lane_page = -1, lane_exps = 0;
     uint32_t scan_phase = 0;
-    // Value exponents of the pages begun: the largest + 64 and 120 - the smallest in two
-    // 16-bit halves, of this warp and of all scan warps.
-    uint32_t my_range = has_own ? s_range[0] | s_range[1] << 16 : 0, range = my_range;
-    auto wide = [&]() { return static_cast<int>((range & 0xffffu) + (range >> 16)) - (kMaxExp - kMinExp) > kScaleSpan; };
     if (has_own) {
       entries = kTile;                                 // the first tile is the tree's own
       if (v == 0)
         for (int j = lane; j < fresh; j += 32) {
-          const unsigned long long rows_of = s_keepers[j];
+          unsigned long long rows_of = 0;              // that keep node j
+          for (int t = r0 / G; t * G < r0 + live; ++t)
+            if (s_line[t] >> j & 1)
+              for (int r = max(t * G - r0, 0); r < min((t + 1) * G - r0, live); ++r) rows_of |= row_bit(r);
           list[j] = make_int4(j, 0, static_cast<int>(rows_of), static_cast<int>(rows_of >> 32));   // exponents: by the gathering warp
         }
     }
@@ -328,10 +331,6 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       if (x % kAhead == 0) {                           // a new batch: it becomes current, the next one is fetched
         lane_page = next_page;
         lane_exps = next_scales.bytes();
-        const int ve = static_cast<int8_t>(lane_exps >> 8);
-        const uint32_t high = __reduce_max_sync(~0u, lane_page >= 0 ? static_cast<uint32_t>(ve - kMinExp) : 0u);
-        const uint32_t low = __reduce_max_sync(~0u, lane_page >= 0 ? static_cast<uint32_t>(kMaxExp - ve) : 0u);
-        my_range = __vmaxu2(my_range, high | low << 16);
         fetch(x + kAhead);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
@@ -385,16 +384,14 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
         if (lane >= y) sum += u;
       }
       const int turn = x / kPages & 1;
-      if (lane == 31) s_found[turn][v] = make_uint2(sum, my_range);
+      if (lane == 31) s_found[turn][v] = sum;
       __syncwarp();
       if (lane == 0) mbar_arrive(&scan_bar);
       wait(&scan_bar, scan_phase++ & 1, abort, L.err);
       int at = entries + sum - mine;
 #pragma unroll
       for (int w = 0; w < kScanWarps; ++w) {
-        const uint2 word = s_found[turn][w];
-        const int found = word.x;
-        range = __vmaxu2(range, word.y);
+        const int found = s_found[turn][w];
         if (w < v) at += found;
         entries += found;
       }
@@ -415,7 +412,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       if (!own)
         while (entries < (tile + 1) * kTile && !scanned()) scan_round();
       const int cnt = own ? fresh : max(min(kTile, entries - tile * kTile), 0);
-      if (v == 0 && lane == 0) s_cnt[tile & 7] = (own ? cnt | kOwn : cnt) | (cnt > 0 && wide() ? kWide : 0);
+      if (v == 0 && lane == 0) s_cnt[tile & 7] = cnt;
       __syncwarp();
       if (lane == 0) mbar_arrive(&listed[tile % kListed]);         // with every warp's: the tile's entries are there
       if (__any_sync(~0u, cnt == 0 || *abort)) break;
@@ -423,10 +420,12 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     cp_async_wait_all();
   } else if (warp >= kGatherWarp && warp < kMmaWarp) {
     // -------------------------------------------------- gathers of kept rows, as f16
-    // A lane has 16 codes of a row (kRowLanes lanes a row).
+    // A lane has 16 codes of a row (kRowLanes lanes a row).  Eight lanes store at a time: half rows of an even
+    // and of an odd row, which the swizzle puts on banks of their own.
     constexpr int kRowLanes = D / 16, kRowsAtOnce = 32 / kRowLanes, kLoads = kTile / kGatherWarps / kRowsAtOnce;
-    const int gw = warp - kGatherWarp, sub = lane / kRowLanes, piece = lane % kRowLanes;
-    auto row_at = [&](int y) { return gw * (kTile / kGatherWarps) + y * kRowsAtOnce + sub; };
+    const int gw = warp - kGatherWarp;
+    const int piece = (lane & 3) | (D == 128 ? lane >> 1 & 4 : 0), sub = D == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane >> 2;
+    auto row_at = [&](int y) { return (y * kGatherWarps + gw) * kRowsAtOnce + sub; };
     // 16 f16 numbers, columns piece * 16 ..., of row r of a tile
     auto put = [&](uint8_t* tile_at, int r, const uint32_t (&w)[8]) {
       uint8_t* to = tile_at + piece / 4 * C::kChunk + r * 128;
@@ -447,113 +446,134 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    for (int tile = 0;; ++tile) {
-      const int st = tile % kStages;
-      const uint32_t parity = (tile / kStages + 1) & 1;
-      const bool ok = __all_sync(~0u, wait(&listed[tile % kListed], (tile / kListed) & 1, abort, L.err));
-      const int word = ok ? s_cnt[tile & 7] : 0, cnt = word & (kWide - 1);
-      if (__any_sync(~0u, cnt == 0 || *abort)) {
-        // not before the stage's last phase has been seen: a wait on it would miss two in a row
-        if (tile >= kStages) wait(&qk_done[st], parity, abort, L.err);
-        arrive(&k_full[st]);
-        break;
-      }
-      uint8_t* const k_at = smem + C::kK + st * C::kTileBytes;
-      uint8_t* const v_at = smem + C::kV + st * C::kTileBytes;
-      int4* const about = list + (tile * kTile & (kList - 1));
-      if (word & kOwn) {                               // the tree's rows, each times a power of two
-        if (tile >= kStages) wait(&qk_done[st], parity, abort, L.err);
-        if (tile >= kStages) wait(&pv_done[st], parity, abort, L.err);
-        for (int y = 0; y < kLoads; ++y) {
-          const int r = row_at(y);
-          int exps = 0;
-          bool bad = false;
+    int tile = 0;
+    if (has_own) {                                     // the tree's rows, each times a power of two
+      wait(&listed[0], 0, abort, L.err);
+#pragma unroll 1
+      for (int y = 0; y < kLoads; ++y) {
+        const int r = row_at(y);
+        uint4 u[2][2] = {};
+        if (r < fresh)
+#pragma unroll
           for (int x = 0; x < 2; ++x) {
-            uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-            if (r < cnt) {
-              const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x ? L.V : L.K) +
-                                                                ((static_cast<size_t>(b) * L.H_kv + h) * L.n + r) * D + piece * 16);
-              u[0] = src[0];
-              u[1] = src[1];
-            }
-            float f[16], top = 0.f;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const uint32_t two = (&u[e / 8].x)[e % 8 / 2];
-              f[e] = __uint_as_float(e & 1 ? two & 0xffff0000u : two << 16);
-              if (!(fabsf(f[e]) < INFINITY)) {
-                bad = true;
-                f[e] = 0.f;
-              }
-              top = fmaxf(top, fabsf(f[e]));
-            }
-#pragma unroll
-            for (int z = 1; z < kRowLanes; z *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, z));
-            const int e_row = min(need_exp(__float_as_uint(top)), kMaxExp);
-            const float down = exp2_int(-e_row);
-            exps |= (e_row & 0xff) << (8 * x);
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = half2_bits(f[2 * e] * down, f[2 * e + 1] * down);
-            put(x ? v_at : k_at, r, w);
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x ? L.V : L.K) + (own_row + r) * D + piece * 16);
+            u[x][0] = src[0];
+            u[x][1] = src[1];
           }
-          const uint32_t bad_lanes = __ballot_sync(~0u, bad) >> (sub * kRowLanes) & ((1u << kRowLanes) - 1);
-          if (piece == 0 && r < cnt) about[r].y = exps | (bad_lanes ? 1 << 16 : 0);
+        int exps = 0;
+        bool bad = false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float f[16], top = 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t two = (&u[x][e / 8].x)[e % 8 / 2];
+            f[e] = __uint_as_float(e & 1 ? two & 0xffff0000u : two << 16);
+            if (!(fabsf(f[e]) < INFINITY)) {
+              bad = true;
+              f[e] = 0.f;
+            }
+            top = fmaxf(top, fabsf(f[e]));
+          }
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+          if (D == 128) top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+          const int e_row = min(need_exp(__float_as_uint(top)), kMaxExp);
+          const float down = exp2_int(-e_row);
+          exps |= (e_row & 0xff) << (8 * x);
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = half2_bits(f[2 * e] * down, f[2 * e + 1] * down);
+          put(smem + (x ? C::kV : C::kK), r, w);
         }
-        arrive(&k_full[st]);
-        arrive(&v_full[st]);
-        continue;
+        const uint32_t of_row = D == 128 ? 0x0f0fu << ((sub & 1) * 4 + (sub >> 1) * 16) : 0xfu << sub * 4;   // its lanes
+        if (__ballot_sync(~0u, bad) & of_row) exps |= 1 << 16;
+        if (piece == 0 && r < fresh) list[r].y = exps;
       }
-      uint4 k[kLoads], vv[kLoads];
+      arrive(&k_full);
+      arrive(&v_full[0]);
+      tile = 1;
+    }
+    // Codes on their way wait in shared memory, each piece for the lane that copies it.
+    uint8_t* const mine = smem + C::kRaw + (gw * 2 * kLoads * 32 + lane) * 16;
+    auto issue = [&](int t) {
+      const int cnt = s_cnt[t & 7];
+      const int4* about = list + (t * kTile & (kList - 1));
 #pragma unroll
       for (int y = 0; y < kLoads; ++y) {
         const int r = row_at(y);
-        k[y] = vv[y] = make_uint4(0, 0, 0, 0);
-        if (r < cnt) {
-          const size_t off = static_cast<size_t>(static_cast<uint32_t>(about[r].x)) * D + piece * 16;
-          k[y] = __ldg(reinterpret_cast<const uint4*>(L.c.k + off));
-          vv[y] = __ldg(reinterpret_cast<const uint4*>(L.c.v + off));
-        }
+        const size_t off = r < cnt ? static_cast<size_t>(static_cast<uint32_t>(about[r].x)) * D + piece * 16 : 0;
+        cp_async_16(mine + y * 512, L.c.k + off, r < cnt ? 16 : 0);
+        cp_async_16(mine + (kLoads + y) * 512, L.c.v + off, r < cnt ? 16 : 0);
       }
-      if (tile >= kStages) wait(&qk_done[st], parity, abort, L.err);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    bool issued = false;                               // the tile's rows are on their way
+    for (;; ++tile) {
+      if (!issued) {
+        const bool ok = __all_sync(~0u, wait(&listed[tile % kListed], (tile / kListed) & 1, abort, L.err));
+        if (__any_sync(~0u, !ok || s_cnt[tile & 7] == 0 || *abort)) {
+          // not before the last phase has been seen: a wait on it would miss two in a row
+          if (tile >= 1) wait(&qk_done, (tile - 1) & 1, abort, L.err);
+          arrive(&k_full);
+          break;
+        }
+        issue(tile);
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      uint4 k[kLoads], vv[kLoads];
+#pragma unroll
+      for (int y = 0; y < kLoads; ++y) {
+        k[y] = *reinterpret_cast<const uint4*>(mine + y * 512);
+        vv[y] = *reinterpret_cast<const uint4*>(mine + (kLoads + y) * 512);
+      }
+      if (tile >= 1) wait(&qk_done, (tile - 1) & 1, abort, L.err);
 #pragma unroll
       for (int y = 0; y < kLoads; ++y) {
         uint32_t w[8];
         widen(k[y], w);
-        put(k_at, row_at(y), w);
+        put(smem + C::kK, row_at(y), w);
       }
-      arrive(&k_full[st]);
-      if (tile >= kStages) wait(&pv_done[st], parity, abort, L.err);
+      arrive(&k_full);
+      // A row that does not keep a key has weight 0 for it, and 0 * NaN would reach that row:
+      // NaN codes leave the tile and mark the outputs that they reach.
+      uint32_t any[kLoads];
 #pragma unroll
       for (int y = 0; y < kLoads; ++y) {
-        // A row that does not keep a key has weight 0 for it, and 0 * NaN would reach that
-        // row: NaN codes leave the tile and mark the outputs that they reach.
         const uint32_t m = 0x7f7f7f7fu, one = 0x01010101u;         // a magnitude of 127 carries into the sign's bit
-        const uint32_t any = (((vv[y].x & m) + one) | ((vv[y].y & m) + one)) | (((vv[y].z & m) + one) | ((vv[y].w & m) + one));
-        if (any & 0x80808080u) {
-          const int4 e = about[row_at(y)];
+        any[y] = (((vv[y].x & m) + one) | ((vv[y].y & m) + one)) | (((vv[y].z & m) + one) | ((vv[y].w & m) + one));
+      }
+#pragma unroll
+      for (int y = 0; y < kLoads; ++y)
+        if (any[y] & 0x80808080u) {
+          const int4 e = list[(tile * kTile & (kList - 1)) + row_at(y)];
 #pragma unroll 1
           for (int i = 0; i < 16; ++i) {
-            uint32_t* at = &vv[y].x;
-            const uint32_t word_i = i < 4 ? at[0] : i < 8 ? at[1] : i < 12 ? at[2] : at[3];
-            if ((word_i >> (i % 4 * 8) & 127u) != 127u) continue;
-            const uint32_t clear = ~(0xffu << (i % 4 * 8));
-            if (i < 4) at[0] &= clear;
-            else if (i < 8) at[1] &= clear;
-            else if (i < 12) at[2] &= clear;
-            else at[3] &= clear;
+            const uint32_t word = i < 4 ? vv[y].x : i < 8 ? vv[y].y : i < 12 ? vv[y].z : vv[y].w, at = i % 4 * 8;
+            if ((word >> at & 127u) != 127u) continue;
+            if (i < 4) vv[y].x &= ~(0xffu << at);
+            else if (i < 8) vv[y].y &= ~(0xffu << at);
+            else if (i < 12) vv[y].z &= ~(0xffu << at);
+            else vv[y].w &= ~(0xffu << at);
             const int d = piece * 16 + i;
             for (uint32_t left = e.z; left; left &= left - 1) atomicOr(&s_nan[row_of_bit(__ffs(left) - 1)][d / 32], 1u << (d % 32));
             if (R > 32)
               for (uint32_t left = e.w; left; left &= left - 1) atomicOr(&s_nan[row_of_bit(31 + __ffs(left)) % R][d / 32], 1u << (d % 32));
           }
         }
+      // the next tile's rows, if it is listed by now (this one's have been read)
+      issued = __all_sync(~0u, mbar_test_wait(&listed[(tile + 1) % kListed], ((tile + 1) / kListed) & 1)) && s_cnt[(tile + 1) & 7] > 0;
+      if (issued) issue(tile + 1);
+      if (tile >= 2) wait(&pv_done[tile & 1], (tile / 2 - 1) & 1, abort, L.err);
+#pragma unroll
+      for (int y = 0; y < kLoads; ++y) {
         uint32_t w[8];
         widen(vv[y], w);
-        put(v_at, row_at(y), w);
+        put(smem + C::kV + (tile & 1) * C::kTileBytes, row_at(y), w);
       }
-      arrive(&v_full[st]);
+      arrive(&v_full[tile & 1]);
     }
+    cp_async_wait_all();
   } else if (warp == kMmaWarp) {
     // -------------------------------------------------- products
     if (lane == 0) {
@@ -561,8 +581,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       bool ok = true;
       // S of a tile whose K is there; false at the end of the tiles
       auto scores = [&](int tile) {
-        const int st = tile % kStages;
-        ok = ok && mbar_wait_nap(&k_full[st], (tile / kStages) & 1, abort, L.err);
+        ok = ok && mbar_wait_nap(&k_full, tile & 1, abort, L.err);
         ok = ok && mbar_wait(&listed[tile % kListed], (tile / kListed) & 1, abort, L.err);         // done: orders s_cnt
         if (!ok || s_cnt[tile & 7] == 0) {
           mbar_arrive(&s_ready[tile & 1]);
@@ -571,32 +590,32 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
         tc_fence_after();
 #pragma unroll
         for (int x = 0; x < D / 16; ++x)
-          mma_ss(tmem + (tile & 1) * R, desc_rows(kb + st * C::kTileBytes + x / 4 * C::kChunk + x % 4 * 32, 16),
+          mma_ss(tmem + (tile & 1) * R, desc_rows(kb + x / 4 * C::kChunk + x % 4 * 32, 16),
                  desc_rows(qb + x / 4 * R * 128 + x % 4 * 32, 16), idesc_f16(R, false, false), x > 0);
-        mma_commit(&qk_done[st]);
+        mma_commit(&qk_done);
         mma_commit(&s_ready[tile & 1]);
         return true;
       };
       int tile = 0;
       bool have = scores(0);
       while (have) {
-        const int st = tile % kStages, cnt = s_cnt[tile & 7] & (kWide - 1);
+        const int cnt = s_cnt[tile & 7];
         have = scores(tile + 1);                       // needs its K alone: S's other buffer was read before the last P
         ok = mbar_wait_nap(&p_ready, tile & 1, abort, L.err) && ok;
-        ok = ok && mbar_wait_nap(&v_full[st], (tile / kStages) & 1, abort, L.err);
+        ok = ok && mbar_wait_nap(&v_full[tile & 1], (tile >> 1) & 1, abort, L.err);
         if (ok) {
           tc_fence_after();
           for (int x = 0; x < (cnt + 15) / 16; ++x)
-            mma_ss(tmem_o, desc_rows(vb + st * C::kTileBytes + x * 2048, C::kChunk),
+            mma_ss(tmem_o, desc_rows(vb + (tile & 1) * C::kTileBytes + x * 2048, C::kChunk),
                    desc_rows(pb + x * 2048, C::kChunk), idesc_f16(2 * R, true, true), !(tile == 0 && x == 0));
         }
-        mma_commit(&pv_done[st]);
+        mma_commit(&pv_done[tile & 1]);
         ++tile;
       }
       // every commit has arrived before the block ends
       if (tile > 0) {
-        mbar_wait(&qk_done[(tile - 1) % kStages], ((tile - 1) / kStages) & 1, abort, L.err);
-        mbar_wait(&pv_done[(tile - 1) % kStages], ((tile - 1) / kStages) & 1, abort, L.err);
+        mbar_wait(&qk_done, (tile - 1) & 1, abort, L.err);
+        mbar_wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort, L.err);
       }
     }
   } else {
@@ -611,58 +630,69 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     int tile = 0;
     for (;; ++tile) {
       const int buf = tile & 1;
+      const uint32_t s_at = tmem + lanes + buf * R + part * RH;
       const bool ok = __all_sync(~0u, wait(&s_ready[buf], (tile >> 1) & 1, abort, L.err));
-      const int word = ok ? s_cnt[tile & 7] : 0, cnt = word & (kWide - 1);
-      uint32_t s[RH], p[RH], mask = 0;
-      float kf = 1.f, ve = 0.f, over = 0.f;
-      // Weights by the references as they are: p, masked; over, the largest.
+      const int cnt = ok ? s_cnt[tile & 7] : 0;
+      uint32_t p[RH], mask = 0;
+      float kf = 1.f, vf = 1.f, over = 0.f;
+      // Exponentials by the references as they are: p, masked; over, the largest.
       auto form = [&]() {
-        const uint64_t kf2 = f2_pack(kf, kf), ve2 = f2_pack(ve, ve);
+        const uint64_t kf2 = f2_pack(kf, kf);
+        float over4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < RH; c += 16) tmem_ld(s_at + c, *reinterpret_cast<uint32_t (*)[16]>(p + c));
+        tmem_wait_ld();
 #pragma unroll
         for (int r = 0; r < RH; r += 4) {
-          uint64_t f01, f23, m01, m23;
-          lds_f2x2(factor + r, f01, f23);
-          lds_f2x2(minus + r, m01, m23);
+          const float4 f = *reinterpret_cast<const float4*>(factor + r), m = *reinterpret_cast<const float4*>(minus + r);
           float d[4];
-          f2_unpack(f2_fma(f2_mul(f2_pack(__uint_as_float(s[r]), __uint_as_float(s[r + 1])), f01), kf2, f2_add(ve2, m01)), d[0], d[1]);
-          f2_unpack(f2_fma(f2_mul(f2_pack(__uint_as_float(s[r + 2]), __uint_as_float(s[r + 3])), f23), kf2, f2_add(ve2, m23)), d[2], d[3]);
+          f2_unpack(f2_fma(f2_mul(f2_pack(__uint_as_float(p[r]), __uint_as_float(p[r + 1])), f2_pack(f.x, f.y)), kf2, f2_pack(m.x, m.y)), d[0], d[1]);
+          f2_unpack(f2_fma(f2_mul(f2_pack(__uint_as_float(p[r + 2]), __uint_as_float(p[r + 3])), f2_pack(f.z, f.w)), kf2, f2_pack(m.z, m.w)), d[2], d[3]);
           const uint32_t four = mask << (r / 4);
           p[r] = __float_as_uint(exp2_fast(d[0])) & spread<0>(four);
           p[r + 1] = __float_as_uint(exp2_fast(d[1])) & spread<1>(four);
           p[r + 2] = __float_as_uint(exp2_fast(d[2])) & spread<2>(four);
           p[r + 3] = __float_as_uint(exp2_fast(d[3])) & spread<3>(four);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) over = fmaxf(over, __uint_as_float(p[r + e]));
+          for (int e = 0; e < 4; ++e) over4[e] = fmaxf(over4[e], __uint_as_float(p[r + e]));
         }
+        over = fmaxf(fmaxf(over4[0], over4[1]), fmaxf(over4[2], over4[3]));
       };
       int ex = 0;
       if (cnt > 0) {
         tc_fence_after();
-        tmem_ld(tmem + lanes + buf * R + part * RH, s);
         if (key < cnt) {
           const int4 e = list[(tile * kTile + key) & (kList - 1)];
           ex = e.y;
-          mask = static_cast<uint32_t>(part < 2 ? e.z : e.w) << (part & 1) * 4;
+          // a part's 32 rows are a word; its 16 rows are the word's upper or lower half bytes
+          mask = R == 64 ? static_cast<uint32_t>(part ? e.w : e.z) : static_cast<uint32_t>(e.z) << part * 4;
         }
         kf = ex >> 16 & 1 ? __int_as_float(0x7fffffff) : exp2_int(static_cast<int8_t>(ex));
-        ve = static_cast<float>(static_cast<int8_t>(ex >> 8));
-        tmem_wait_ld();
+        vf = exp2_int(static_cast<int8_t>(ex >> 8) - kLift);
         form();
       }
       // One vote for "a weight is too large" and "a warp has given up": the four warps of a part go
       // on together, whatever happens.
-      if (named_barrier_or(1 + part, 128, !ok || over > 32768.f)) {
+      if (named_barrier_or(1 + part, 128, !ok || over * vf > 32768.f)) {
         if (named_barrier_or(1 + part, 128, !ok)) break;
         // Some row's reference moves, by the row's own weights: rows do not touch each other.
         // Lane r takes row r (the same result in the part's four warps).
         int top = INT_MIN;
+        const float ve = static_cast<float>(static_cast<int8_t>(ex >> 8));
 #pragma unroll
-        for (int r = 0; r < RH; ++r) {
-          const float t = fmaf(__uint_as_float(s[r]) * factor[r], kf, ve);
-          const int u = __float_as_int(t), order = u ^ (u >> 31 & 0x7fffffff);   // floats' order as integers
-          const bool mine = mask >> ((r & 3) * 8 + 7 - r / 4) & 1 && t == t;
-          const int m = __reduce_max_sync(~0u, mine ? order : INT_MIN);
-          if (lane == r) top = m;
+        for (int c = 0; c < RH; c += 16) {
+          uint32_t s[16];
+          tmem_ld(s_at + c, s);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int r = c + i;
+            const float t = fmaf(__uint_as_float(s[i]) * factor[r], kf, ve);
+            const int u = __float_as_int(t), order = u ^ (u >> 31 & 0x7fffffff);   // floats' order as integers
+            const bool mine = mask >> ((r & 3) * 8 + 7 - r / 4) & 1 && t == t;
+            const int m = __reduce_max_sync(~0u, mine ? order : INT_MIN);
+            if (lane == r) top = m;
+          }
         }
         if (lane < RH) s_top[quad][part * RH + lane] = top;
         named_barrier(1 + part, 128);
@@ -670,9 +700,9 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
         if (lane < RH) {
           const int rr = part * RH + lane;
           const int m = max(max(s_top[0][rr], s_top[1][rr]), max(s_top[2][rr], s_top[3][rr]));
-          const float was = -s_minus[rr], highest = m == INT_MIN ? -INFINITY : __int_as_float(m ^ (m >> 31 & 0x7fffffff));
-          moved = highest > was + kTop ? highest - kBelow : was;
-          fh = exp2_fast(0.5f * (was - moved));
+          const float was = s_minus[rr], highest = m == INT_MIN ? -INFINITY : __int_as_float(m ^ (m >> 31 & 0x7fffffff));
+          moved = highest > (kLift - was) + kTop ? kLift - (highest - kBelow) : was;
+          fh = exp2_fast(0.5f * (moved - was));
         }
 #pragma unroll
         for (int r = 0; r < RH; r += 2) {
@@ -680,64 +710,51 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
           sum2[r / 2] = f2_mul(f2_mul(sum2[r / 2], fh2), fh2);
         }
         if (tile > 0) {
-          wait(&pv_done[(tile - 1) % kStages], ((tile - 1) / kStages) & 1, abort, L.err);
+          wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort, L.err);
           tc_fence_after();
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {                // both parts of the weights
-            uint32_t o[RH];
-            tmem_ld(tmem_o + lanes + y * R + part * RH, o);
+          for (int y = 0; y < 2 * RH; y += 16) {       // both parts of the weights
+            const uint32_t o_at = tmem_o + lanes + y / RH * R + part * RH + y % RH;
+            uint32_t o[16];
+            tmem_ld(o_at, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int r = 0; r < RH; ++r) {
-              const float f = __shfl_sync(~0u, fh, r);
+            for (int r = 0; r < 16; ++r) {
+              const float f = __shfl_sync(~0u, fh, y % RH + r);
               if (f != 1.f) o[r] = __float_as_uint(__uint_as_float(o[r]) * (f * f));
             }
-            tmem_st16(tmem_o + lanes + y * R + part * RH, o);
+            tmem_st16(o_at, o);
           }
           tmem_wait_st();
         }
         named_barrier(1 + part, 128);                  // every warp has read the old references
-        if (quad == 0 && lane < RH) minus[lane] = -moved;
+        if (quad == 0 && lane < RH) minus[lane] = moved;
         named_barrier(1 + part, 128);
         form();
       }
       if (cnt == 0) break;
-      // sums: 2^(s - ref) is the weight times 2^-ve, or where scales lie far apart an exponential of its own
-      float vf = exp2_int(kLift - static_cast<int8_t>(ex >> 8));
-      if (word & kWide) {                              // the same in all warps
-        const float up = static_cast<float>(kLift);
-#pragma unroll
-        for (int r = 0; r < RH; r += 2) {
-          float d[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            d[e] = exp2_fast(fmaf(__uint_as_float(s[r + e]) * factor[r + e], kf, minus[r + e] + up));
-            if (!(mask >> (((r + e) & 3) * 8 + 7 - r / 4) & 1)) d[e] = 0.f;
-          }
-          sum2[r / 2] = f2_add(sum2[r / 2], f2_pack(d[0], d[1]));
-        }
-        vf = 0.f;
-      }
       if (tile > 0)                                    // the last tile's product has read P
-        wait(&pv_done[(tile - 1) % kStages], ((tile - 1) / kStages) & 1, abort, L.err);
+        wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort, L.err);
       const uint64_t vf2 = f2_pack(vf, vf);
       uint8_t* const row = smem + C::kP + key * 128;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {                    // eight rows: 16 bytes of each part
+      for (int c = 0; c < RH / 8; ++c) {               // eight rows: 16 bytes of each part
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 8 * c + 2 * i;
-          // ten bits below the leading one, exact in f16; the rest is exact too, and rounded to eleven
-          const uint32_t h0 = p[r] & 0xffffe000u, h1 = p[r + 1] & 0xffffe000u;
           const uint64_t p2 = f2_pack(__uint_as_float(p[r]), __uint_as_float(p[r + 1]));
-          if (!(word & kWide)) sum2[r / 2] = f2_fma(p2, vf2, sum2[r / 2]);
-          float l0, l1;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(h0), __uint_as_float(h1)), f2_pack(-1.f, -1.f), p2), l0, l1);
-          hi[i] = half2_bits(__uint_as_float(h0), __uint_as_float(h1));
+          sum2[r / 2] = f2_add(sum2[r / 2], p2);
+          const uint64_t w2 = f2_mul(p2, vf2);
+          float w0, w1, l0, l1;
+          f2_unpack(w2, w0, w1);
+          // ten bits below the leading one, exact in f16; the rest is exact too, and rounded to eleven
+          const float h0 = __uint_as_float(__float_as_uint(w0) & 0xffffe000u), h1 = __uint_as_float(__float_as_uint(w1) & 0xffffe000u);
+          f2_unpack(f2_fma(f2_pack(h0, h1), f2_pack(-1.f, -1.f), w2), l0, l1);
+          hi[i] = half2_bits(h0, h1);
           lo[i] = half2_bits(l0, l1);
         }
-        const int piece = part * 2 + c;                // R = 32: the second parts behind the first in the same row
+        const int piece = part * (RH / 8) + c;         // R = 32: the second parts behind the first in the same row
         *reinterpret_cast<uint4*>(row + (piece ^ (key & 7)) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(row + (R == 64 ? C::kChunk : 0) + ((R == 64 ? piece : piece + 4) ^ (key & 7)) * 16) =
             make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -762,7 +779,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       if (lane == 0) s_l[quad][part * RH + r] = x;
     }
     if (tiles > 0) {
-      wait(&pv_done[(tiles - 1) % kStages], ((tiles - 1) / kStages) & 1, abort, L.err);
+      wait(&pv_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, abort, L.err);
       tc_fence_after();
     }
   }
@@ -770,21 +787,24 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
 
   // ---- join: the same exchange as in cache_attn.cuh
   cluster.sync();                                      // every block runs and is past its tiles
-  const int share = R / cs;                            // rows that a block writes
+  const int share = R / cs, shift = __ffs(share) - 1;  // rows that a block writes, a power of two
   if (warp < kSoftWarps && tiles > 0) {
     const int quad = warp & 3, part = warp >> 2, d = quad * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    uint32_t hi[RH], lo[RH];
-    tmem_ld(tmem_o + lanes + part * RH, hi);
-    tmem_ld(tmem_o + lanes + R + part * RH, lo);
-    tmem_wait_ld();
-    if (quad < D / 32) {
 #pragma unroll
-      for (int y = 0; y < RH; ++y) {
-        const int r = part * RH + y, to = r / share;
-        float x = __uint_as_float(hi[y]) + __uint_as_float(lo[y]);
-        if (s_nan[r][quad] >> lane & 1) x = __int_as_float(0x7fffffff);
-        *cluster.map_shared_rank(inbox + (rank * share + r - to * share) * D + d, to) = x;
+    for (int c = 0; c < RH; c += 16) {
+      uint32_t hi[16], lo[16];
+      tmem_ld(tmem_o + lanes + part * RH + c, hi);
+      tmem_ld(tmem_o + lanes + R + part * RH + c, lo);
+      tmem_wait_ld();
+      if (quad < D / 32) {
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+          const int r = part * RH + c + y, to = r >> shift;
+          float x = __uint_as_float(hi[y]) + __uint_as_float(lo[y]);
+          if (s_nan[r][quad] >> lane & 1) x = __int_as_float(0x7fffffff);
+          *cluster.map_shared_rank(inbox + (rank * share + (r & (share - 1))) * D + d, to) = x;
+        }
       }
     }
   }
@@ -808,7 +828,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       s_weight[x][r] = s_all[x][r].y != 0.f ? exp2f(s_all[x][r].x - M) / l * exp2_int(kLift) : 0.f;
     if (rank == 0 && L.lse && r < live)
       L.lse[(static_cast<size_t>(b) * L.H + h * G + (r0 + r) % G) * L.n + (r0 + r) / G] =
-          l != 0.f ? (M + (log2f(l) - kLift)) * 0.6931471805599453f : -INFINITY;
+          l != 0.f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < share * (D / 4); i += kThreads) {
