@@ -89,6 +89,15 @@ __device__ __forceinline__ uint32_t spread(uint32_t x) {
   return r;
 }
 
+// A wait's first try is in place and the rest a call: the kernel's roles share the instruction
+// caches, and a launch begins with them cold.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  return mbar_wait(bar, parity, abort, err);
+}
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  return mbar_try_wait_sleep(bar, parity, kWaitSleepNs) || wait_on(bar, parity, abort, err);
+}
+
 // Barrier of `count` threads that returns whether any of them says so.
 __device__ __forceinline__ bool named_barrier_or(int id, int count, bool v) {
   int r;
@@ -192,10 +201,12 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     s_abort_word = 0;
     mbar_init(&k_full, kGatherWarps);
     mbar_init(&qk_done, 1);
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(&v_full[i], kGatherWarps);
       mbar_init(&pv_done[i], 1);
     }
+#pragma unroll 1
     for (int i = 0; i < kListed; ++i) {
       mbar_init(&listed[i], kScanWarps);
       mbar_init(&used[i], kSoftWarps);
@@ -208,42 +219,49 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   }
   if (warp == kMmaWarp) tmem_alloc(&s_tmem, C::kCols);
   if (warp == kGatherWarp) tree_lines(L.parent + static_cast<size_t>(b) * L.n, fresh, s_line, s_node, L.err);
+#pragma unroll 1
   for (int i = threadIdx.x; i < kCacheTableGroups; i += kThreads) table[i] = 0;
+#pragma unroll 1
   for (int i = threadIdx.x; i < R * (D / 32); i += kThreads) s_nan[0][i] = 0;
   if (threadIdx.x <= kMaxNodes) s_below[threadIdx.x] = 0;
   const bool has_own = rank == cs - 1;                 // the block that takes the tree's own keys
   const size_t own_row = (static_cast<size_t>(b) * L.H_kv + h) * L.n;
   if (has_own && warp > kGatherWarp && warp < kMmaWarp)        // whose rows are on their way from here on
+#pragma unroll 1
     for (int i = threadIdx.x - (kGatherWarp + 1) * 32; i < fresh * D / 64; i += (kGatherWarps - 1) * 32) {
       asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __nv_bfloat16*>(L.K) + own_row * D + i * 64));
       asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __nv_bfloat16*>(L.V) + own_row * D + i * 64));
     }
   int node_gid = 0;
   if (threadIdx.x < fresh) node_gid = gids[threadIdx.x];
-  // queries: f16 by a power of two a row, a warp a row
+  // queries: f16 by a power of two a row, a warp a row; they come through the codes' space
   if (warp < kSoftWarps) {
-    constexpr int kEach = D / 32;                      // elements a lane
-    uint32_t u[R / kSoftWarps][kEach / 2];
-#pragma unroll
-    for (int i = 0; i < R / kSoftWarps; ++i) {
-      const int r = warp + i * kSoftWarps, g = (r0 + r) % G, t = (r0 + r) / G;
-#pragma unroll
-      for (int e = 0; e < kEach / 2; ++e) u[i][e] = 0;
-      if (r < live) {
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(L.Q) +
-                                                                ((static_cast<size_t>(b) * L.H + h * G + g) * L.n + t) * D);
-#pragma unroll
-        for (int e = 0; e < kEach / 2; ++e) u[i][e] = src[lane * (kEach / 2) + e];
-      }
+    constexpr int kEach = D / 32, kCopies = D / 8;     // elements a lane; 16-byte pieces of a row
+    uint8_t* const raw = smem + C::kRaw + warp * (R / kSoftWarps) * D * 2;
+#pragma unroll 1
+    for (int i = lane; i < R / kSoftWarps * kCopies; i += 32) {
+      const int r = warp + i / kCopies * kSoftWarps, g = (r0 + r) % G, t = (r0 + r) / G;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(L.Q);
+      if (r < live) src += ((static_cast<size_t>(b) * L.H + h * G + g) * L.n + t) * D + i % kCopies * 8;
+      cp_async_16(raw + i * 16, src, r < live ? 16 : 0);
     }
-#pragma unroll
+    cp_async_wait_all();
+    __syncwarp();
+#pragma unroll 1
     for (int i = 0; i < R / kSoftWarps; ++i) {
       const int r = warp + i * kSoftWarps;
+      float q[kEach];
+#pragma unroll
+      for (int e = 0; e < kEach; e += 2) {
+        const uint32_t two = *reinterpret_cast<const uint32_t*>(raw + i * D * 2 + (lane * kEach + e) * 2);
+        q[e] = __uint_as_float(two << 16);
+        q[e + 1] = __uint_as_float(two & 0xffff0000u);
+      }
       uint32_t top = 0;
       bool finite = true;
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
-        const uint32_t a = (e & 1 ? u[i][e / 2] & 0x7fff0000u : u[i][e / 2] << 16 & 0x7fff0000u);
+        const uint32_t a = __float_as_uint(q[e]) & 0x7fffffffu;
         if (a < 0x7f800000u) top = max(top, a);
         else finite = false;
       }
@@ -251,11 +269,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       finite = __all_sync(~0u, finite);
       const int eq = min(max(static_cast<int>(top >> 23) - 127 - 13, kMinQueryExp), 115);   // |q| 2^-eq < 2^14
       const float down = exp2_int(-eq);
-      const int d = lane * kEach;                      // a row's 16-byte piece d / 8 of its chunk
+      const int d = lane * kEach;                      // in the row's 16-byte piece d / 8 of its chunk
       uint8_t* to = smem + C::kQ + d / 64 * R * 128 + r * 128 + ((d % 64 / 8) ^ (r & 7)) * 16 + d % 8 * 2;
 #pragma unroll
-      for (int e = 0; e < kEach / 2; ++e)
-        reinterpret_cast<uint32_t*>(to)[e] = half2_bits(__uint_as_float(u[i][e] << 16) * down, __uint_as_float(u[i][e] & 0xffff0000u) * down);
+      for (int e = 0; e < kEach; e += 2) *reinterpret_cast<uint32_t*>(to + e * 2) = half2_bits(q[e] * down, q[e + 1] * down);
       if (lane == 0) {
         // rows with an infinite or NaN element become NaN through their factor
         s_factor[r] = finite ? exp2_int(eq) * L.scale_log2 : __int_as_float(0x7fffffff);
@@ -276,6 +293,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     if (depth >= L.w) {                                // ancestors before the window: of its group only
       unsigned long long keeps = 0;
       int up = 0;                                      // from the root down: j is `depth - up` steps above
+#pragma unroll 1
       for (unsigned long long left = line; left; left &= left - 1, ++up) {
         const int j = __ffsll(left) - 1;
         if (depth - up < L.w || s_node[j] == node_gid) keeps |= 1ull << j;
@@ -283,6 +301,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       s_line[threadIdx.x] = keeps;
     }
     // its rows of the block, by group and by depth
+#pragma unroll 1
     for (int r = max(static_cast<int>(threadIdx.x) * G - r0, 0); r < min((static_cast<int>(threadIdx.x) + 1) * G - r0, live); ++r) {
       const uint32_t bit = static_cast<uint32_t>(row_bit(r) >> (r & 32));
       if (node_gid >= 0 && node_gid < kCacheTableGroups) atomicOr(reinterpret_cast<uint32_t*>(&table[node_gid]) + (r >> 5), bit);
@@ -319,10 +338,13 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     if (has_own) {
       entries = kTile;                                 // the first tile is the tree's own
       if (v == 0)
+#pragma unroll 1
         for (int j = lane; j < fresh; j += 32) {
           unsigned long long rows_of = 0;              // that keep node j
+#pragma unroll 1
           for (int t = r0 / G; t * G < r0 + live; ++t)
             if (s_line[t] >> j & 1)
+#pragma unroll 1
               for (int r = max(t * G - r0, 0); r < min((t + 1) * G - r0, live); ++r) rows_of |= row_bit(r);
           list[j] = make_int4(j, 0, static_cast<int>(rows_of), static_cast<int>(rows_of >> 32));   // exponents: by the gathering warp
         }
@@ -387,7 +409,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       if (lane == 31) s_found[turn][v] = sum;
       __syncwarp();
       if (lane == 0) mbar_arrive(&scan_bar);
-      wait(&scan_bar, scan_phase++ & 1, abort, L.err);
+      await(&scan_bar, scan_phase++ & 1, abort, L.err);
       int at = entries + sum - mine;
 #pragma unroll
       for (int w = 0; w < kScanWarps; ++w) {
@@ -406,10 +428,12 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     };
     // the round's first page lies behind the end (the same in all scan warps)
     auto scanned = [&]() { return rank + x / kPages * kRound * cs >= pages; };
+#pragma unroll 1
     for (int tile = 0;; ++tile) {
-      if (tile >= kListed) wait(&used[tile % kListed], (tile / kListed + 1) & 1, abort, L.err);
+      if (tile >= kListed) await(&used[tile % kListed], (tile / kListed + 1) & 1, abort, L.err);
       const bool own = has_own && tile == 0;
       if (!own)
+#pragma unroll 1
         while (entries < (tile + 1) * kTile && !scanned()) scan_round();
       const int cnt = own ? fresh : max(min(kTile, entries - tile * kTile), 0);
       if (v == 0 && lane == 0) s_cnt[tile & 7] = cnt;
@@ -448,7 +472,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     };
     int tile = 0;
     if (has_own) {                                     // the tree's rows, each times a power of two
-      wait(&listed[0], 0, abort, L.err);
+      await(&listed[0], 0, abort, L.err);
 #pragma unroll 1
       for (int y = 0; y < kLoads; ++y) {
         const int r = row_at(y);
@@ -462,12 +486,12 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
           }
         int exps = 0;
         bool bad = false;
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < 2; ++x) {
           float f[16], top = 0.f;
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const uint32_t two = (&u[x][e / 8].x)[e % 8 / 2];
+            const uint32_t k_two = (&u[0][e / 8].x)[e % 8 / 2], v_two = (&u[1][e / 8].x)[e % 8 / 2], two = x ? v_two : k_two;
             f[e] = __uint_as_float(e & 1 ? two & 0xffff0000u : two << 16);
             if (!(fabsf(f[e]) < INFINITY)) {
               bad = true;
@@ -511,10 +535,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     bool issued = false;                               // the tile's rows are on their way
     for (;; ++tile) {
       if (!issued) {
-        const bool ok = __all_sync(~0u, wait(&listed[tile % kListed], (tile / kListed) & 1, abort, L.err));
+        const bool ok = __all_sync(~0u, await(&listed[tile % kListed], (tile / kListed) & 1, abort, L.err));
         if (__any_sync(~0u, !ok || s_cnt[tile & 7] == 0 || *abort)) {
           // not before the last phase has been seen: a wait on it would miss two in a row
-          if (tile >= 1) wait(&qk_done, (tile - 1) & 1, abort, L.err);
+          if (tile >= 1) await(&qk_done, (tile - 1) & 1, abort, L.err);
           arrive(&k_full);
           break;
         }
@@ -527,7 +551,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
         k[y] = *reinterpret_cast<const uint4*>(mine + y * 512);
         vv[y] = *reinterpret_cast<const uint4*>(mine + (kLoads + y) * 512);
       }
-      if (tile >= 1) wait(&qk_done, (tile - 1) & 1, abort, L.err);
+      if (tile >= 1) await(&qk_done, (tile - 1) & 1, abort, L.err);
 #pragma unroll
       for (int y = 0; y < kLoads; ++y) {
         uint32_t w[8];
@@ -537,34 +561,31 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       arrive(&k_full);
       // A row that does not keep a key has weight 0 for it, and 0 * NaN would reach that row:
       // NaN codes leave the tile and mark the outputs that they reach.
-      uint32_t any[kLoads];
+      uint32_t any = 0;
 #pragma unroll
       for (int y = 0; y < kLoads; ++y) {
         const uint32_t m = 0x7f7f7f7fu, one = 0x01010101u;         // a magnitude of 127 carries into the sign's bit
-        any[y] = (((vv[y].x & m) + one) | ((vv[y].y & m) + one)) | (((vv[y].z & m) + one) | ((vv[y].w & m) + one));
+        any |= (((vv[y].x & m) + one) | ((vv[y].y & m) + one)) | (((vv[y].z & m) + one) | ((vv[y].w & m) + one));
       }
-#pragma unroll
-      for (int y = 0; y < kLoads; ++y)
-        if (any[y] & 0x80808080u) {
-          const int4 e = list[(tile * kTile & (kList - 1)) + row_at(y)];
+      if (any & 0x80808080u) {
 #pragma unroll 1
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t word = i < 4 ? vv[y].x : i < 8 ? vv[y].y : i < 12 ? vv[y].z : vv[y].w, at = i % 4 * 8;
-            if ((word >> at & 127u) != 127u) continue;
-            if (i < 4) vv[y].x &= ~(0xffu << at);
-            else if (i < 8) vv[y].y &= ~(0xffu << at);
-            else if (i < 12) vv[y].z &= ~(0xffu << at);
-            else vv[y].w &= ~(0xffu << at);
-            const int d = piece * 16 + i;
-            for (uint32_t left = e.z; left; left &= left - 1) atomicOr(&s_nan[row_of_bit(__ffs(left) - 1)][d / 32], 1u << (d % 32));
-            if (R > 32)
-              for (uint32_t left = e.w; left; left &= left - 1) atomicOr(&s_nan[row_of_bit(31 + __ffs(left)) % R][d / 32], 1u << (d % 32));
-          }
+        for (int i = 0; i < kLoads * 16; ++i) {
+          uint8_t* at = mine + (kLoads + i / 16) * 512 + i % 16;
+          if ((*at & 127) != 127) continue;
+          *at = 0;
+          const int4 e = list[(tile * kTile & (kList - 1)) + row_at(i / 16)];
+          const int d = piece * 16 + i % 16;
+#pragma unroll 1
+          for (uint64_t left = static_cast<uint32_t>(e.z) | static_cast<uint64_t>(static_cast<uint32_t>(e.w)) << 32; left; left &= left - 1)
+            atomicOr(&s_nan[row_of_bit(__ffsll(left) - 1) % R][d / 32], 1u << (d % 32));
         }
+#pragma unroll
+        for (int y = 0; y < kLoads; ++y) vv[y] = *reinterpret_cast<const uint4*>(mine + (kLoads + y) * 512);
+      }
       // the next tile's rows, if it is listed by now (this one's have been read)
       issued = __all_sync(~0u, mbar_test_wait(&listed[(tile + 1) % kListed], ((tile + 1) / kListed) & 1)) && s_cnt[(tile + 1) & 7] > 0;
       if (issued) issue(tile + 1);
-      if (tile >= 2) wait(&pv_done[tile & 1], (tile / 2 - 1) & 1, abort, L.err);
+      if (tile >= 2) await(&pv_done[tile & 1], (tile / 2 - 1) & 1, abort, L.err);
 #pragma unroll
       for (int y = 0; y < kLoads; ++y) {
         uint32_t w[8];
@@ -581,8 +602,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       bool ok = true;
       // S of a tile whose K is there; false at the end of the tiles
       auto scores = [&](int tile) {
-        ok = ok && mbar_wait_nap(&k_full, tile & 1, abort, L.err);
-        ok = ok && mbar_wait(&listed[tile % kListed], (tile / kListed) & 1, abort, L.err);         // done: orders s_cnt
+        ok = ok && await(&k_full, tile & 1, abort, L.err);
+        ok = ok && await(&listed[tile % kListed], (tile / kListed) & 1, abort, L.err);         // done: orders s_cnt
         if (!ok || s_cnt[tile & 7] == 0) {
           mbar_arrive(&s_ready[tile & 1]);
           return false;
@@ -598,13 +619,15 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       };
       int tile = 0;
       bool have = scores(0);
+#pragma unroll 1
       while (have) {
         const int cnt = s_cnt[tile & 7];
         have = scores(tile + 1);                       // needs its K alone: S's other buffer was read before the last P
-        ok = mbar_wait_nap(&p_ready, tile & 1, abort, L.err) && ok;
-        ok = ok && mbar_wait_nap(&v_full[tile & 1], (tile >> 1) & 1, abort, L.err);
+        ok = await(&p_ready, tile & 1, abort, L.err) && ok;
+        ok = ok && await(&v_full[tile & 1], (tile >> 1) & 1, abort, L.err);
         if (ok) {
           tc_fence_after();
+#pragma unroll 1
           for (int x = 0; x < (cnt + 15) / 16; ++x)
             mma_ss(tmem_o, desc_rows(vb + (tile & 1) * C::kTileBytes + x * 2048, C::kChunk),
                    desc_rows(pb + x * 2048, C::kChunk), idesc_f16(2 * R, true, true), !(tile == 0 && x == 0));
@@ -614,8 +637,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       }
       // every commit has arrived before the block ends
       if (tile > 0) {
-        mbar_wait(&qk_done, (tile - 1) & 1, abort, L.err);
-        mbar_wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort, L.err);
+        await(&qk_done, (tile - 1) & 1, abort, L.err);
+        await(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort, L.err);
       }
     }
   } else {
@@ -631,7 +654,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     for (;; ++tile) {
       const int buf = tile & 1;
       const uint32_t s_at = tmem + lanes + buf * R + part * RH;
-      const bool ok = __all_sync(~0u, wait(&s_ready[buf], (tile >> 1) & 1, abort, L.err));
+      const bool ok = __all_sync(~0u, await(&s_ready[buf], (tile >> 1) & 1, abort, L.err));
       const int cnt = ok ? s_cnt[tile & 7] : 0;
       uint32_t p[RH], mask = 0;
       float kf = 1.f, vf = 1.f, over = 0.f;
@@ -669,23 +692,26 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
         }
         kf = ex >> 16 & 1 ? __int_as_float(0x7fffffff) : exp2_int(static_cast<int8_t>(ex));
         vf = exp2_int(static_cast<int8_t>(ex >> 8) - kLift);
-        form();
       }
-      // One vote for "a weight is too large" and "a warp has given up": the four warps of a part go
-      // on together, whatever happens.
-      if (named_barrier_or(1 + part, 128, !ok || over * vf > 32768.f)) {
-        if (named_barrier_or(1 + part, 128, !ok)) break;
+      bool dead = false;
+      for (bool again = false;; again = true) {
+        if (cnt > 0) form();
+        // One vote for "a weight is too large" and "a warp has given up": the four warps of a part go
+        // on together, whatever happens.
+        if (again || !named_barrier_or(1 + part, 128, !ok || over * vf > 32768.f)) break;
+        dead = named_barrier_or(1 + part, 128, !ok);
+        if (dead) break;
         // Some row's reference moves, by the row's own weights: rows do not touch each other.
         // Lane r takes row r (the same result in the part's four warps).
         int top = INT_MIN;
         const float ve = static_cast<float>(static_cast<int8_t>(ex >> 8));
-#pragma unroll
-        for (int c = 0; c < RH; c += 16) {
-          uint32_t s[16];
+#pragma unroll 1
+        for (int c = 0; c < RH; c += 8) {
+          uint32_t s[8];
           tmem_ld(s_at + c, s);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 8; ++i) {
             const int r = c + i;
             const float t = fmaf(__uint_as_float(s[i]) * factor[r], kf, ve);
             const int u = __float_as_int(t), order = u ^ (u >> 31 & 0x7fffffff);   // floats' order as integers
@@ -710,31 +736,30 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
           sum2[r / 2] = f2_mul(f2_mul(sum2[r / 2], fh2), fh2);
         }
         if (tile > 0) {
-          wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort, L.err);
+          await(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort, L.err);
           tc_fence_after();
-#pragma unroll
-          for (int y = 0; y < 2 * RH; y += 16) {       // both parts of the weights
+#pragma unroll 1
+          for (int y = 0; y < 2 * RH; y += 8) {        // both parts of the weights
             const uint32_t o_at = tmem_o + lanes + y / RH * R + part * RH + y % RH;
-            uint32_t o[16];
+            uint32_t o[8];
             tmem_ld(o_at, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
+            for (int r = 0; r < 8; ++r) {
               const float f = __shfl_sync(~0u, fh, y % RH + r);
               if (f != 1.f) o[r] = __float_as_uint(__uint_as_float(o[r]) * (f * f));
             }
-            tmem_st16(o_at, o);
+            tmem_st8(o_at, o);
           }
           tmem_wait_st();
         }
         named_barrier(1 + part, 128);                  // every warp has read the old references
         if (quad == 0 && lane < RH) minus[lane] = moved;
         named_barrier(1 + part, 128);
-        form();
       }
-      if (cnt == 0) break;
+      if (dead || cnt == 0) break;
       if (tile > 0)                                    // the last tile's product has read P
-        wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort, L.err);
+        await(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort, L.err);
       const uint64_t vf2 = f2_pack(vf, vf);
       uint8_t* const row = smem + C::kP + key * 128;
 #pragma unroll
@@ -769,17 +794,23 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     }
     // ---- the block's partial: every row's sum, and its part of O to the block that writes it
     tiles = tile;
+    float l[RH];
 #pragma unroll
-    for (int r = 0; r < RH; ++r) {
-      float l0, l1;
-      f2_unpack(sum2[r / 2], l0, l1);
-      float x = r & 1 ? l1 : l0;
+    for (int r = 0; r < RH; r += 2) f2_unpack(sum2[r / 2], l[r], l[r + 1]);
+    // halves change lanes until one row is left
 #pragma unroll
-      for (int y = 16; y > 0; y /= 2) x += __shfl_xor_sync(~0u, x, y);
-      if (lane == 0) s_l[quad][part * RH + r] = x;
+    for (int step = 0; step < 5; ++step) {
+      const int x = 16 >> step, w = RH / 2 >> step;
+      if (w == 0) l[0] += __shfl_xor_sync(~0u, l[0], x);
+#pragma unroll
+      for (int r = 0; r < w; ++r) {
+        const float give = lane & x ? l[r] : l[r + w], keep = lane & x ? l[r + w] : l[r];
+        l[r] = keep + __shfl_xor_sync(~0u, give, x);
+      }
     }
+    if (RH == 32 || !(lane & 1)) s_l[quad][part * RH + (RH == 32 ? lane : lane >> 1)] = l[0];
     if (tiles > 0) {
-      wait(&pv_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, abort, L.err);
+      await(&pv_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, abort, L.err);
       tc_fence_after();
     }
   }
@@ -791,15 +822,15 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   if (warp < kSoftWarps && tiles > 0) {
     const int quad = warp & 3, part = warp >> 2, d = quad * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-#pragma unroll
-    for (int c = 0; c < RH; c += 16) {
-      uint32_t hi[16], lo[16];
+#pragma unroll 1
+    for (int c = 0; c < RH; c += 8) {
+      uint32_t hi[8], lo[8];
       tmem_ld(tmem_o + lanes + part * RH + c, hi);
       tmem_ld(tmem_o + lanes + R + part * RH + c, lo);
       tmem_wait_ld();
       if (quad < D / 32) {
 #pragma unroll
-        for (int y = 0; y < 16; ++y) {
+        for (int y = 0; y < 8; ++y) {
           const int r = part * RH + c + y, to = r >> shift;
           float x = __uint_as_float(hi[y]) + __uint_as_float(lo[y]);
           if (s_nan[r][quad] >> lane & 1) x = __int_as_float(0x7fffffff);
@@ -808,6 +839,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       }
     }
   }
+#pragma unroll 1
   for (int i = threadIdx.x; i < R * cs; i += kThreads) {
     const int r = i % R, to = i / R;
     *cluster.map_shared_rank(&s_all[rank][r], to) = make_float2(-s_minus[r], (s_l[0][r] + s_l[1][r]) + (s_l[2][r] + s_l[3][r]));
@@ -818,12 +850,15 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   if (threadIdx.x < R) {
     const int r = threadIdx.x;
     float M = kNoRef, l = 0.f;
+#pragma unroll 1
     for (int x = 0; x < cs; ++x) M = fmaxf(M, s_all[x][r].x);
+#pragma unroll 1
     for (int x = 0; x < cs; ++x)
       if (s_all[x][r].y != 0.f) {
         const float fh = exp2f(0.5f * (s_all[x][r].x - M));
         l += s_all[x][r].y * fh * fh;
       }
+#pragma unroll 1
     for (int x = 0; x < cs; ++x)
       s_weight[x][r] = s_all[x][r].y != 0.f ? exp2f(s_all[x][r].x - M) / l * exp2_int(kLift) : 0.f;
     if (rank == 0 && L.lse && r < live)
@@ -831,6 +866,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
           l != 0.f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
   __syncthreads();
+#pragma unroll 1
   for (int i = threadIdx.x; i < share * (D / 4); i += kThreads) {
     const int local = i / (D / 4), r = rank * share + local, d = i % (D / 4) * 4;
     if (r >= live) break;
