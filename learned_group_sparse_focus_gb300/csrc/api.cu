@@ -1259,6 +1259,8 @@ focus_status_t focus_cache_append_rotary(const focus_params_t* p, const focus_ro
     L.rot.scale = rot->scale;
   }
   L.rows = rows;
+  L.device = device_index();
+  if (L.device < 0) return FOCUS_ERR_CUDA;
   return cuda_status(launch_cache_append_rotary(L, p->dtype, static_cast<cudaStream_t>(stream)));
 }
 

@@ -306,6 +306,7 @@ struct CacheAppendRotaryLaunch {
   CacheAppendLaunch a;
   RotaryLaunch rot;        // dim 0: nothing turns; Hk 0 (the keys go by pages)
   const int32_t* rows;     // [B, n] source row of each token, or null
+  int device;
   int touched;             // pages a head may touch (set by the launch)
 };
 cudaError_t launch_cache_append_rotary(CacheAppendRotaryLaunch L, int dtype, cudaStream_t st);

@@ -42,7 +42,8 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryLaunch L) {
 
 // --------------------------------------------------------------- append ---
 
-// A turned pair in 64 bits: element hi (0, 1) of (a, b) at a phase in 2^-64 turns.
+// A turned pair in 64 bits: element hi (0, 1) of (a, b) at a phase in 2^-64 turns.  A call, and a
+// loop around it: it is needed for few elements, and its code would crowd out the rest.
 __device__ __noinline__ double turned_exactly(float a, float b, unsigned long long phase, float scale, bool hi) {
   double s, c;
   sincospi(static_cast<double>(static_cast<long long>(phase)) * 0x1p-63, &s, &c);
@@ -58,15 +59,20 @@ __device__ __forceinline__ uint32_t code_of(double y) {
   return float2_to_e4m3x2(f, 0.f) & 0xffu;
 }
 
+// A page's rows in shared memory: a thread's duos, row step after row step, in 16-byte
+// pieces that lie a thread apart.  K's are turned in place (fp32), V's stay as they are.
 template <typename T, int D>
 struct PageRows {
   static constexpr int kDuos = D / 16, kRowsAtOnce = kHalf / kDuos, kSteps = kPage / kRowsAtOnce;
+  static constexpr int kRaw = sizeof(T);                 // 16-byte pieces of a duo as it comes: 2 or 4
+  static constexpr int kStep = kHalf * 16;               // bytes of one piece of every thread
+  static constexpr int kBytes = kSteps * (4 + kRaw) * kStep;
 };
 
 // One page of one head: as cache_append_kernel, with a thread on duos.
 template <typename T, int D>
 __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, int b, int h, int j, int n0, int m,
-                                            unsigned long long* s_turn, uint32_t (*s_max)[2], int* s_more) {
+                                            unsigned long long* s_turn, uint32_t (*s_max)[2], int* s_more, uint8_t* smem) {
   using C = PageRows<T, D>;
   const CacheAppendLaunch& A = L.a;
   const RotaryLaunch& R = L.rot;
@@ -74,8 +80,7 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
   const int lo = max(n0, j * kPage), hi = min(n0 + m, (j + 1) * kPage);
   const int r0 = lo - j * kPage, rows = hi - lo, t0 = lo - n0;
   const int k = ht % C::kDuos, row0 = ht / C::kDuos;
-  const int dim = half ? 0 : R.dim;
-  const Duo duo(k, dim, R.interleaved);
+  const Duo duo(k, half ? 0 : R.dim, R.interleaved);
   const int next = A.c.next[b];
   // the source row of a token
   auto source = [&](int t) {
@@ -86,17 +91,15 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
     return r < 0 ? 0 : A.n - 1;
   };
   const T* src = static_cast<const T*>(half ? A.V : A.K) + (static_cast<size_t>(b) * A.H_kv + h) * A.n * D;
-  float y[C::kSteps][16];
+  uint8_t* const mine = smem + (half ? C::kSteps * 4 * C::kStep : 0) + ht * 16;
+  const int apart = (half ? C::kRaw : 4) * C::kStep;     // from a row step to the next
+  const int steps = row0 < rows ? (rows - row0 + C::kRowsAtOnce - 1) / C::kRowsAtOnce : 0;
+#pragma unroll 1
+  for (int i = 0; i < steps; ++i) {
+    const T* row = src + static_cast<size_t>(source(t0 + row0 + i * C::kRowsAtOnce)) * D;
 #pragma unroll
-  for (int i = 0; i < C::kSteps; ++i) {
-    const int r = row0 + i * C::kRowsAtOnce;
-    if (r >= rows) continue;
-    const T* row = src + static_cast<size_t>(source(t0 + r)) * D;
-    Piece<T> p[2];
-    p[0].load(row + duo.at[0]);
-    p[1].load(row + duo.at[1]);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) y[i][e] = p[e / 8].at(e % 8);
+    for (int e = 0; e < C::kRaw; ++e)
+      cp_async_16(mine + i * apart + e * C::kStep, row + duo.at[e / (C::kRaw / 2)] + e % (C::kRaw / 2) * (16 / static_cast<int>(sizeof(T))), 16);
   }
   const int page = cache_page(A.c, b, j, A.err);
   const size_t plane = static_cast<size_t>(max(page, 0)) * A.H_kv + h;
@@ -104,42 +107,66 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
   const int e_old = r0 > 0 && page >= 0 ? scale_exp(*scale) : kMinExp;
   if (threadIdx.x < R.dim / 2) s_turn[threadIdx.x] = turn_of(R.inv_freq[threadIdx.x]);
   if (threadIdx.x == 0) *s_more = 0;
+  cp_async_wait_all();
   __syncthreads();
-  if (duo.turns) {
+  // A duo of a row step as floats; y: K's turned ones.
+  auto read = [&](int i, bool turned, float (&y)[16]) {
+    const uint8_t* at = mine + i * apart;
+    if (sizeof(T) == 4 || turned) {
 #pragma unroll
-    for (int i = 0; i < C::kSteps; ++i) {
-      const int r = row0 + i * C::kRowsAtOnce;
-      if (r >= rows) continue;
+      for (int e = 0; e < 4; ++e) {
+        const float4 f = *reinterpret_cast<const float4*>(at + (sizeof(T) == 4 || turned ? e : 0) * C::kStep);
+        y[4 * e] = f.x; y[4 * e + 1] = f.y; y[4 * e + 2] = f.z; y[4 * e + 3] = f.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint4 u = *reinterpret_cast<const uint4*>(at + e * C::kStep);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          y[8 * e + 2 * x] = __uint_as_float((&u.x)[x] << 16);
+          y[8 * e + 2 * x + 1] = __uint_as_float((&u.x)[x] & 0xffff0000u);
+        }
+      }
+    }
+  };
+  // how far an element may be from exact arithmetic, by its pair's size
+  auto unsure = [&](const float (&y)[16], int e) {
+    if (!duo.turns) return 0.f;
+    const float other = R.interleaved ? y[e ^ 1] : y[e ^ 8];
+    return (fabsf(y[e]) + fabsf(other)) * kUnsure;
+  };
+  // Turned rows, their largest finite magnitude, and the most that it may be in exact arithmetic.
+  uint32_t top[2] = {0, 0};
+#pragma unroll 1
+  for (int i = 0; i < steps; ++i) {
+    float y[16];
+    read(i, false, y);
+    if (duo.turns) {
       float c[8], s[8];
-      const unsigned long long x = static_cast<unsigned long long>(next) + (t0 + r);
+      const unsigned long long x = static_cast<unsigned long long>(next) + (t0 + row0 + i * C::kRowsAtOnce);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         cos_sin(x * s_turn[k * 8 + e], c[e], s[e]);
         c[e] *= R.scale;
         s[e] *= R.scale;
       }
-      if (R.interleaved) turn_pairs<true>(y[i], c, s);
-      else turn_pairs<false>(y[i], c, s);
+      if (R.interleaved) turn_pairs<true>(y, c, s);
+      else turn_pairs<false>(y, c, s);
+    }
+    if (!half)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<float4*>(mine + i * apart + e * C::kStep) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float a = fabsf(y[e]);
+      if (!(a < INFINITY)) continue;
+      const float u = unsure(y, e);
+      top[0] = max(top[0], __float_as_uint(fmaxf(a - u, 0.f)));
+      top[1] = max(top[1], __float_as_uint(a + u < INFINITY ? a + u : a));
     }
   }
-  // Largest finite magnitude, and the most that it may be in exact arithmetic.
-  uint32_t top[2] = {0, 0};
-  auto unsure = [&](int i, int e) {                      // of element e: its pair's size
-    if (!duo.turns) return 0.f;
-    const float other = R.interleaved ? y[i][e ^ 1] : y[i][e ^ 8];
-    return (fabsf(y[i][e]) + fabsf(other)) * kUnsure;
-  };
-#pragma unroll
-  for (int i = 0; i < C::kSteps; ++i)
-    if (row0 + i * C::kRowsAtOnce < rows)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float a = fabsf(y[i][e]);
-        if (!(a < INFINITY)) continue;
-        const float u = unsure(i, e);
-        top[0] = max(top[0], __float_as_uint(fmaxf(a - u, 0.f)));
-        top[1] = max(top[1], __float_as_uint(a + u < INFINITY ? a + u : a));
-      }
 #pragma unroll
   for (int x = 0; x < 2; ++x) top[x] = __reduce_max_sync(~0u, top[x]);
   if ((threadIdx.x & 31) == 0) {
@@ -153,67 +180,65 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
     top[1] = max(top[1], s_max[half * (kHalf / 32) + i][1]);
   }
   auto exactly = [&](int i, int e) {                     // element e of row step i in 64 bits
-    const int r = row0 + i * C::kRowsAtOnce;
-    const T* row = src + static_cast<size_t>(source(t0 + r)) * D;
+    const int t = t0 + row0 + i * C::kRowsAtOnce;
+    const T* row = src + static_cast<size_t>(source(t)) * D;
     const int pair = R.interleaved ? e / 2 : e % 8;
-    const int first = R.interleaved ? duo.at[0] + 2 * pair : duo.at[0] + pair, apart = R.interleaved ? 1 : R.dim / 2;
-    const float a = static_cast<float>(row[first]), c = static_cast<float>(row[first + apart]);
-    const unsigned long long x = static_cast<unsigned long long>(next) + (t0 + r);
-    return turned_exactly(a, c, x * s_turn[k * 8 + pair], R.scale,
+    const int first = R.interleaved ? duo.at[0] + 2 * pair : duo.at[0] + pair, other = R.interleaved ? 1 : R.dim / 2;
+    const float a = static_cast<float>(row[first]), c = static_cast<float>(row[first + other]);
+    return turned_exactly(a, c, (static_cast<unsigned long long>(next) + t) * s_turn[k * 8 + pair], R.scale,
                           R.interleaved ? e & 1 : e >= 8);
   };
   int e_new = need_exp(top[0]);
   if (!half && need_exp(top[1]) != e_new) {              // the same in the whole half
     const double edge = static_cast<double>(exp2_int(e_new)) * 448.0;
+    if (duo.turns)
 #pragma unroll 1
-    for (int i = 0; i < C::kSteps; ++i)
-#pragma unroll 1
-      for (int e = 0; e < 16; ++e) {
-        if (row0 + i * C::kRowsAtOnce >= rows || !duo.turns) continue;
-        const double v = fabs(exactly(i, e));
+      for (int x = 0; x < steps * 16; ++x) {
+        const double v = fabs(exactly(x / 16, x % 16));
         if (v > edge && v < INFINITY && v <= static_cast<double>(__uint_as_float(top[1]))) atomicOr(s_more, 1);
       }
-    asm volatile("bar.sync 1, %0;" ::"n"(kHalf) : "memory");
+    named_barrier(1, kHalf);
     e_new += *s_more;
   }
-  // K_out takes the rows before they are scaled; rows that K_out shares with K have been read
-  // by the thread that writes them, unless a later look in 64 bits needs them: that comes first.
   uint8_t* dst = (half ? A.c.v : A.c.k) + plane * kPage * D;
   const int e = max(e_new, e_old);
   if (page >= 0) {
     if (ht == 0) *scale = exp2_int(e);
     if (e > e_old) {                                     // the page's older rows, at the new scale
       uint4* old = reinterpret_cast<uint4*>(dst);
+#pragma unroll 1
       for (int at = ht; at < r0 * D / 16; at += kHalf) old[at] = rescale16(old[at], e_old - e);
     }
   }
+  // Rows that K_out shares with K are read in 64 bits, where that is needed, before they are written.
   const float f = exp2_int(-e);
-#pragma unroll
-  for (int i = 0; i < C::kSteps; ++i) {
+#pragma unroll 1
+  for (int i = 0; i < steps; ++i) {
     const int r = row0 + i * C::kRowsAtOnce;
-    if (r >= rows) continue;
+    float y[16];
+    read(i, !half, y);
     uint32_t w[4], differ = 0;
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
       uint32_t code;
       if (duo.turns) {
-        const float u0 = unsure(i, 2 * x), u1 = unsure(i, 2 * x + 1), y0 = y[i][2 * x], y1 = y[i][2 * x + 1];
-        code = float2_to_e4m3x2((y0 - u0) * f, (y1 - u1) * f);
-        differ |= (code ^ float2_to_e4m3x2((y0 + u0) * f, (y1 + u1) * f)) ? 1u << x : 0u;
+        const float u0 = unsure(y, 2 * x), u1 = unsure(y, 2 * x + 1);
+        code = float2_to_e4m3x2((y[2 * x] - u0) * f, (y[2 * x + 1] - u1) * f);
+        differ |= code != float2_to_e4m3x2((y[2 * x] + u0) * f, (y[2 * x + 1] + u1) * f) ? 1u << x : 0u;
       } else {
-        code = float2_to_e4m3x2(y[i][2 * x] * f, y[i][2 * x + 1] * f);
+        code = float2_to_e4m3x2(y[2 * x] * f, y[2 * x + 1] * f);
       }
       if (x & 1) w[x / 2] |= code << 16;
       else w[x / 2] = code;
     }
-    if (differ) {
+#pragma unroll 1
+    for (; differ; differ &= differ - 1) {
+      const int x = __ffs(differ) - 1;
       const double down = exp2_int(-e);
+      const uint32_t code = code_of(exactly(i, 2 * x) * down) | code_of(exactly(i, 2 * x + 1) * down) << 8;
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
-        if (differ >> x & 1) {
-          const uint32_t code = code_of(exactly(i, 2 * x) * down) | code_of(exactly(i, 2 * x + 1) * down) << 8;
-          w[x / 2] = x & 1 ? (w[x / 2] & 0xffffu) | code << 16 : (w[x / 2] & 0xffff0000u) | code;
-        }
+      for (int z = 0; z < 4; ++z)
+        if (z == x / 2) w[z] = x & 1 ? (w[z] & 0xffffu) | code << 16 : (w[z] & 0xffff0000u) | code;
     }
     if (page >= 0) {
       uint8_t* to = dst + static_cast<size_t>(r0 + r) * D;
@@ -222,8 +247,8 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
     }
     if (!half && R.K_out) {
       T* out = static_cast<T*>(R.K_out) + ((static_cast<size_t>(b) * A.H_kv + h) * A.n + t0 + r) * D;
-      store8(out + duo.at[0], y[i]);
-      store8(out + duo.at[1], y[i] + 8);
+      store8(out + duo.at[0], y);
+      store8(out + duo.at[1], y + 8);
     }
   }
   if (page >= 0 && ht < rows) {
@@ -244,10 +269,11 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
 
 // Grid x: first the blocks of pages, one per touched page and head, then those of query rows.
 template <typename T, int D>
-__global__ void __launch_bounds__(kRotThreads) cache_append_rotary_kernel(CacheAppendRotaryLaunch L) {
+__global__ void __launch_bounds__(kRotThreads, 3) cache_append_rotary_kernel(CacheAppendRotaryLaunch L) {
   __shared__ unsigned long long s_turn[D / 2];
   __shared__ uint32_t s_max[kRotThreads / 32][2];
   __shared__ int s_more;
+  extern __shared__ __align__(16) uint8_t smem[];
   const CacheAppendLaunch& A = L.a;
   const int b = blockIdx.z;
   const int m = cache_new(A.n_new, A.n, b, A.err);
@@ -259,7 +285,7 @@ __global__ void __launch_bounds__(kRotThreads) cache_append_rotary_kernel(CacheA
     h = blockIdx.x / L.touched;
     n0 = A.c.len[b * A.H_kv + h];
     const int j = n0 / kPage + blockIdx.x % L.touched;
-    if (fits && max(n0, j * kPage) < min(n0 + m, (j + 1) * kPage)) append_page<T, D>(L, b, h, j, n0, m, s_turn, s_max, &s_more);
+    if (fits && max(n0, j * kPage) < min(n0 + m, (j + 1) * kPage)) append_page<T, D>(L, b, h, j, n0, m, s_turn, s_max, &s_more, smem);
   } else if (fits) {
     const int x = blockIdx.x - of_pages, chunks = (A.n + L.rot.tokens - 1) / L.rot.tokens;
     const int t0 = x % chunks * L.rot.tokens;
@@ -279,6 +305,22 @@ void split_rows(RotaryLaunch* L, int d) {
   const long long blocks = static_cast<long long>(L->B) * ((L->n + L->tokens - 1) / L->tokens);
   const int least = slots / L->tokens;
   while (L->heads > least && blocks * ((all + L->heads - 1) / L->heads) < kFillBlocks) L->heads = (L->heads + 1) / 2;
+}
+
+// Devices on which the kernel's shared memory is set up.
+template <typename T, int D>
+std::atomic<bool> g_ready[kMaxDevices];
+
+template <typename T, int D>
+cudaError_t launch_append(const CacheAppendRotaryLaunch& L, dim3 grid, cudaStream_t st) {
+  constexpr int kSmem = PageRows<T, D>::kBytes;
+  const void* kernel = reinterpret_cast<const void*>(cache_append_rotary_kernel<T, D>);
+  if (!g_ready<T, D>[L.device].load(std::memory_order_acquire)) {
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return e;
+    g_ready<T, D>[L.device].store(true, std::memory_order_release);
+  }
+  cache_append_rotary_kernel<T, D><<<grid, kRotThreads, kSmem, st>>>(L);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -305,14 +347,8 @@ cudaError_t launch_cache_append_rotary(CacheAppendRotaryLaunch L, int dtype, cud
               ((L.rot.Hq + L.rot.heads - 1) / L.rot.heads);
   }
   const dim3 grid(static_cast<unsigned>(blocks), 1, L.a.B);
-  if (dtype == FOCUS_BF16) {
-    if (L.a.d == 128) cache_append_rotary_kernel<__nv_bfloat16, 128><<<grid, kRotThreads, 0, st>>>(L);
-    else cache_append_rotary_kernel<__nv_bfloat16, 64><<<grid, kRotThreads, 0, st>>>(L);
-  } else {
-    if (L.a.d == 128) cache_append_rotary_kernel<float, 128><<<grid, kRotThreads, 0, st>>>(L);
-    else cache_append_rotary_kernel<float, 64><<<grid, kRotThreads, 0, st>>>(L);
-  }
-  return cudaGetLastError();
+  if (dtype == FOCUS_BF16) return L.a.d == 128 ? launch_append<__nv_bfloat16, 128>(L, grid, st) : launch_append<__nv_bfloat16, 64>(L, grid, st);
+  return L.a.d == 128 ? launch_append<float, 128>(L, grid, st) : launch_append<float, 64>(L, grid, st);
 }
 
 }  // namespace focus
