@@ -42,13 +42,34 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryLaunch L) {
 
 // --------------------------------------------------------------- append ---
 
-// A turned pair in 64 bits: element hi (0, 1) of (a, b) at a phase in 2^-64 turns.  A call, and a
-// loop around it: it is needed for few elements, and its code would crowd out the rest.
+// A turned pair in 64 bits: element hi (0, 1) of (a, b) at a phase in 2^-64 turns.  Taylor
+// polynomials of degree 15 and 16 on an eighth of a turn, as in cos_sin (the next terms are below
+// 2^-54 and 2^-58).  A call: it is needed for few elements, and its code would crowd out the rest.
 __device__ __noinline__ double turned_exactly(float a, float b, unsigned long long phase, float scale, bool hi) {
-  double s, c;
-  sincospi(static_cast<double>(static_cast<long long>(phase)) * 0x1p-63, &s, &c);
-  const double x = a, y = b;
-  return (hi ? x * s + y * c : x * c - y * s) * scale;
+  const uint32_t quarter = static_cast<uint32_t>((phase + (1ull << 61)) >> 62);
+  const long long rest = static_cast<long long>(phase - (static_cast<unsigned long long>(quarter) << 62));
+  const double x = static_cast<double>(rest) * (6.283185307179586477 * 0x1p-64), z = x * x;
+  double s = -1. / 1307674368000., c = 1. / 20922789888000.;     // -1 / 15!, 1 / 16!
+  s = fma(s, z, 1. / 6227020800.);
+  c = fma(c, z, -1. / 87178291200.);
+  s = fma(s, z, -1. / 39916800.);
+  c = fma(c, z, 1. / 479001600.);
+  s = fma(s, z, 1. / 362880.);
+  c = fma(c, z, -1. / 3628800.);
+  s = fma(s, z, -1. / 5040.);
+  c = fma(c, z, 1. / 40320.);
+  s = fma(s, z, 1. / 120.);
+  c = fma(c, z, -1. / 720.);
+  s = fma(s, z, -1. / 6.);
+  c = fma(c, z, 1. / 24.);
+  c = fma(c, z, -0.5);
+  s = fma(x * z, s, x);
+  c = fma(c, z, 1.);
+  double cq = quarter & 1 ? s : c, sq = quarter & 1 ? c : s;
+  if (quarter == 1 || quarter == 2) cq = -cq;
+  if (quarter >= 2) sq = -sq;
+  const double u = a, v = b;
+  return (hi ? u * sq + v * cq : u * cq - v * sq) * scale;
 }
 
 // e4m3 code of a double, rounded once: to a float by truncation with the lost bits in its
