@@ -5,7 +5,7 @@
 // heads, so a block takes tokens and walks over heads.
 //
 // Appended keys go from the turned fp32 value to e4m3 in one rounding.  What is stored is
-// what exact arithmetic would store: the fp32 value is within 2^-20 of its pair's size, so
+// what exact arithmetic would store: the fp32 value is within kUnsure of its pair's size, so
 // both ends of that range are rounded, and where they give different codes (about one
 // element in 10^5) or different page exponents the value is formed again in 64 bits.
 // A cache then holds the same codes however its tokens came in, one by one, in a
@@ -16,11 +16,13 @@ namespace focus {
 namespace {
 
 constexpr int kHalf = kRotThreads / 2;      // of a page's block the first half moves K, the second V
-constexpr float kUnsure = 0x1p-20f;         // of |a| + |b|, for the fp32 value of a turned pair (a, b)
+// Of |y| + |z|, for the fp32 value of a turned pair (y, z): what sine and cosine are off by (2^-22.7: the
+// angle's roundings and the polynomial's), two roundings of 2^-25, and sqrt(2) for the sizes of the pair before.
+constexpr float kUnsure = 0x1.8p-22f;
 
 // ------------------------------------------------------------- rotation ---
 
-template <typename T, int D>
+template <typename T, int D, bool kInterleaved>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryLaunch L) {
   __shared__ unsigned long long s_turn[D / 2];
   __shared__ unsigned long long s_line[kMaxNodes];
@@ -37,7 +39,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryLaunch L) {
     }
     __syncthreads();
   }
-  rotate_rows<T, D>(L, b, t0, blockIdx.y * L.heads, m, L.base ? L.base[b] : 0, L.parent ? s_up : nullptr, s_turn);
+  rotate_rows<T, D, kInterleaved, 128>(L, b, t0, blockIdx.y * L.heads, m, L.base ? L.base[b] : 0, L.parent ? s_up : nullptr, s_turn);
 }
 
 // --------------------------------------------------------------- append ---
@@ -91,9 +93,9 @@ struct PageRows {
 };
 
 // One page of one head: as cache_append_kernel, with a thread on duos.
-template <typename T, int D>
+template <typename T, int D, bool kInterleaved>
 __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, int b, int h, int j, int n0, int m,
-                                            unsigned long long* s_turn, uint32_t (*s_max)[2], int* s_more, uint8_t* smem) {
+                                            unsigned long long* s_turn, uint2* s_max, int* s_more, uint8_t* smem) {
   using C = PageRows<T, D>;
   const CacheAppendLaunch& A = L.a;
   const RotaryLaunch& R = L.rot;
@@ -101,7 +103,7 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
   const int lo = max(n0, j * kPage), hi = min(n0 + m, (j + 1) * kPage);
   const int r0 = lo - j * kPage, rows = hi - lo, t0 = lo - n0;
   const int k = ht % C::kDuos, row0 = ht / C::kDuos;
-  const Duo duo(k, half ? 0 : R.dim, R.interleaved);
+  const Duo duo(k, half ? 0 : R.dim, kInterleaved);
   const int next = A.c.next[b];
   // the source row of a token
   auto source = [&](int t) {
@@ -126,23 +128,25 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
   const size_t plane = static_cast<size_t>(max(page, 0)) * A.H_kv + h;
   float* scale = (half ? A.c.v_scale : A.c.k_scale) + plane;
   const int e_old = r0 > 0 && page >= 0 ? scale_exp(*scale) : kMinExp;
-  if (threadIdx.x < R.dim / 2) s_turn[threadIdx.x] = turn_of(R.inv_freq[threadIdx.x]);
+  fill_turns<C::kDuos>(R, s_turn);
   if (threadIdx.x == 0) *s_more = 0;
   cp_async_wait_all();
   __syncthreads();
-  // A duo of a row step as floats; y: K's turned ones.
-  auto read = [&](int i, bool turned, float (&y)[16]) {
-    const uint8_t* at = mine + i * apart;
-    if (sizeof(T) == 4 || turned) {
+  // A duo of a row step as floats, as it came and as it was turned.
+  auto floats = [&](int i, float (&y)[16]) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 f = *reinterpret_cast<const float4*>(at + (sizeof(T) == 4 || turned ? e : 0) * C::kStep);
-        y[4 * e] = f.x; y[4 * e + 1] = f.y; y[4 * e + 2] = f.z; y[4 * e + 3] = f.w;
-      }
+    for (int e = 0; e < 4; ++e) {
+      const float4 f = *reinterpret_cast<const float4*>(mine + i * apart + e * C::kStep);
+      y[4 * e] = f.x; y[4 * e + 1] = f.y; y[4 * e + 2] = f.z; y[4 * e + 3] = f.w;
+    }
+  };
+  auto read = [&](int i, float (&y)[16]) {
+    if constexpr (sizeof(T) == 4) {
+      floats(i, y);
     } else {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint4 u = *reinterpret_cast<const uint4*>(at + e * C::kStep);
+        const uint4 u = *reinterpret_cast<const uint4*>(mine + i * apart + e * C::kStep);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           y[8 * e + 2 * x] = __uint_as_float((&u.x)[x] << 16);
@@ -151,72 +155,68 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
       }
     }
   };
-  // how far an element may be from exact arithmetic, by its pair's size
-  auto unsure = [&](const float (&y)[16], int e) {
-    if (!duo.turns) return 0.f;
-    const float other = R.interleaved ? y[e ^ 1] : y[e ^ 8];
-    return (fabsf(y[e]) + fabsf(other)) * kUnsure;
-  };
-  // Turned rows, their largest finite magnitude, and the most that it may be in exact arithmetic.
-  uint32_t top[2] = {0, 0};
+  // Turned rows, and the largest finite magnitude.
+  float top = 0.f;
 #pragma unroll 1
   for (int i = 0; i < steps; ++i) {
     float y[16];
-    read(i, false, y);
-    if (duo.turns) {
-      float c[8], s[8];
-      const unsigned long long x = static_cast<unsigned long long>(next) + (t0 + row0 + i * C::kRowsAtOnce);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        cos_sin(x * s_turn[k * 8 + e], c[e], s[e]);
-        c[e] *= R.scale;
-        s[e] *= R.scale;
+    read(i, y);
+    if (!half) {
+      if (duo.turns) {
+        uint64_t c[4], s[4];
+        duo_cos_sin<C::kDuos>(static_cast<uint32_t>(next) + (t0 + row0 + i * C::kRowsAtOnce), s_turn + k, R.scale, R.scale, c, s);
+        turn_pairs<kInterleaved>(y, c, s);
       }
-      if (R.interleaved) turn_pairs<true>(y, c, s);
-      else turn_pairs<false>(y, c, s);
-    }
-    if (!half)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         *reinterpret_cast<float4*>(mine + i * apart + e * C::kStep) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float a = fabsf(y[e]);
-      if (!(a < INFINITY)) continue;
-      const float u = unsure(y, e);
-      top[0] = max(top[0], __float_as_uint(fmaxf(a - u, 0.f)));
-      top[1] = max(top[1], __float_as_uint(a + u < INFINITY ? a + u : a));
     }
-  }
+    float a = 0.f, b = 0.f;                              // (fmaxf leaves NaN out)
 #pragma unroll
-  for (int x = 0; x < 2; ++x) top[x] = __reduce_max_sync(~0u, top[x]);
-  if ((threadIdx.x & 31) == 0) {
-    s_max[threadIdx.x / 32][0] = top[0];
-    s_max[threadIdx.x / 32][1] = top[1];
+    for (int e = 0; e < 16; e += 2) {
+      a = fmaxf(a, fabsf(y[e]));
+      b = fmaxf(b, fabsf(y[e + 1]));
+    }
+    a = fmaxf(a, b);
+    if (a == INFINITY) {
+      a = 0.f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) a = fmaxf(a, fabsf(y[e]) < INFINITY ? fabsf(y[e]) : 0.f);
+    }
+    top = fmaxf(top, a);
+  }
+  {
+    const uint32_t fixed = __reduce_max_sync(~0u, duo.turns ? 0u : __float_as_uint(top));
+    const uint32_t turned = __reduce_max_sync(~0u, duo.turns ? __float_as_uint(top) : 0u);
+    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x / 32] = make_uint2(fixed, turned);
   }
   __syncthreads();
+  uint32_t fixed = 0, turned = 0;                        // largest of the elements as they came, of the turned ones
 #pragma unroll
   for (int i = 0; i < kHalf / 32; ++i) {
-    top[0] = max(top[0], s_max[half * (kHalf / 32) + i][0]);
-    top[1] = max(top[1], s_max[half * (kHalf / 32) + i][1]);
+    fixed = max(fixed, s_max[half * (kHalf / 32) + i].x);
+    turned = max(turned, s_max[half * (kHalf / 32) + i].y);
   }
   auto exactly = [&](int i, int e) {                     // element e of row step i in 64 bits
     const int t = t0 + row0 + i * C::kRowsAtOnce;
     const T* row = src + static_cast<size_t>(source(t)) * D;
-    const int pair = R.interleaved ? e / 2 : e % 8;
-    const int first = R.interleaved ? duo.at[0] + 2 * pair : duo.at[0] + pair, other = R.interleaved ? 1 : R.dim / 2;
+    const int pair = kInterleaved ? e / 2 : e % 8;
+    const int first = kInterleaved ? duo.at[0] + 2 * pair : duo.at[0] + pair, other = kInterleaved ? 1 : R.dim / 2;
     const float a = static_cast<float>(row[first]), c = static_cast<float>(row[first + other]);
-    return turned_exactly(a, c, (static_cast<unsigned long long>(next) + t) * s_turn[k * 8 + pair], R.scale,
-                          R.interleaved ? e & 1 : e >= 8);
+    return turned_exactly(a, c, (static_cast<unsigned long long>(next) + t) * s_turn[pair * C::kDuos + k], R.scale,
+                          kInterleaved ? e & 1 : e >= 8);
   };
-  int e_new = need_exp(top[0]);
-  if (!half && need_exp(top[1]) != e_new) {              // the same in the whole half
-    const double edge = static_cast<double>(exp2_int(e_new)) * 448.0;
+  // In exact arithmetic the largest turned one is within 2 kUnsure of `turned`.
+  const float most = __uint_as_float(turned) * (1.f + 2.f * kUnsure);
+  int e_new = max(need_exp(fixed), need_exp(__float_as_uint(__uint_as_float(turned) * (1.f - 2.f * kUnsure))));
+  if (need_exp(__float_as_uint(most)) > e_new) {         // the same in the whole half; not in V's, where nothing turns
+    const float edge = exp2_int(e_new) * 448.f;          // (infinite past fp32's range: then nothing is past it)
     if (duo.turns)
 #pragma unroll 1
       for (int x = 0; x < steps * 16; ++x) {
-        const double v = fabs(exactly(x / 16, x % 16));
-        if (v > edge && v < INFINITY && v <= static_cast<double>(__uint_as_float(top[1]))) atomicOr(s_more, 1);
+        const float y = *reinterpret_cast<const float*>(mine + x / 16 * apart + x % 16 / 4 * C::kStep + x % 4 * 4);
+        if (!(fabsf(y) >= edge * (1.f - 4.f * kUnsure) && fabsf(y) < INFINITY)) continue;
+        if (fabs(exactly(x / 16, x % 16)) > edge) atomicOr(s_more, 1);
       }
     named_barrier(1, kHalf);
     e_new += *s_more;
@@ -237,29 +237,51 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
   for (int i = 0; i < steps; ++i) {
     const int r = row0 + i * C::kRowsAtOnce;
     float y[16];
-    read(i, !half, y);
-    uint32_t w[4], differ = 0;
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      uint32_t code;
-      if (duo.turns) {
-        const float u0 = unsure(y, 2 * x), u1 = unsure(y, 2 * x + 1);
-        code = float2_to_e4m3x2((y[2 * x] - u0) * f, (y[2 * x + 1] - u1) * f);
-        differ |= code != float2_to_e4m3x2((y[2 * x] + u0) * f, (y[2 * x + 1] + u1) * f) ? 1u << x : 0u;
-      } else {
-        code = float2_to_e4m3x2(y[2 * x] * f, y[2 * x + 1] * f);
-      }
-      if (x & 1) w[x / 2] |= code << 16;
-      else w[x / 2] = code;
-    }
-#pragma unroll 1
-    for (; differ; differ &= differ - 1) {
-      const int x = __ffs(differ) - 1;
-      const double down = exp2_int(-e);
-      const uint32_t code = code_of(exactly(i, 2 * x) * down) | code_of(exactly(i, 2 * x + 1) * down) << 8;
+    uint32_t w[4];
+    if (half) {
+      read(i, y);
 #pragma unroll
       for (int z = 0; z < 4; ++z)
-        if (z == x / 2) w[z] = x & 1 ? (w[z] & 0xffffu) | code << 16 : (w[z] & 0xffff0000u) | code;
+        w[z] = static_cast<uint32_t>(float2_to_e4m3x2(y[4 * z] * f, y[4 * z + 1] * f)) |
+               static_cast<uint32_t>(float2_to_e4m3x2(y[4 * z + 2] * f, y[4 * z + 3] * f)) << 16;
+    } else {
+      floats(i, y);
+      // both ends of what an element may be, by its pair's size; where they differ, in 64 bits
+      float u[16];
+      const float unsure = kUnsure * f;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int a = kInterleaved ? 2 * x : x, b = kInterleaved ? 2 * x + 1 : x + 8;
+        u[a] = u[b] = duo.turns ? (fabsf(y[a]) + fabsf(y[b])) * unsure : 0.f;
+      }
+      const uint64_t f2 = f2_pack(f, f), minus = f2_pack(-1.f, -1.f);
+      uint32_t differ[4];                                // by byte
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        uint32_t low = 0, high = 0;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int a = 4 * z + 2 * x;
+          const uint64_t y2 = f2_pack(y[a], y[a + 1]), u2 = f2_pack(u[a], u[a + 1]);
+          float v0, v1;
+          f2_unpack(f2_fma(y2, f2, f2_mul(u2, minus)), v0, v1);
+          low |= static_cast<uint32_t>(float2_to_e4m3x2(v0, v1)) << 16 * x;
+          f2_unpack(f2_fma(y2, f2, u2), v0, v1);
+          high |= static_cast<uint32_t>(float2_to_e4m3x2(v0, v1)) << 16 * x;
+        }
+        w[z] = low;
+        differ[z] = low ^ high;
+      }
+      if (differ[0] | differ[1] | differ[2] | differ[3])
+#pragma unroll 1
+        for (int x = 0; x < 16; ++x) {
+          const uint32_t word = x < 4 ? differ[0] : x < 8 ? differ[1] : x < 12 ? differ[2] : differ[3];
+          if (!(word >> x % 4 * 8 & 255u)) continue;
+          const uint32_t code = code_of(exactly(i, x) * exp2_int(-e)) << x % 4 * 8, rest = ~(255u << x % 4 * 8);
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            if (z == x / 4) w[z] = (w[z] & rest) | code;
+        }
     }
     if (page >= 0) {
       uint8_t* to = dst + static_cast<size_t>(r0 + r) * D;
@@ -288,11 +310,12 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
   }
 }
 
-// Grid x: first the blocks of pages, one per touched page and head, then those of query rows.
-template <typename T, int D>
+// Grid x: blocks of pages, one per touched page and head, and those of query rows, spread evenly
+// among each other: the former are bound by instructions, the latter by HBM.
+template <typename T, int D, bool kInterleaved>
 __global__ void __launch_bounds__(kRotThreads, 3) cache_append_rotary_kernel(CacheAppendRotaryLaunch L) {
   __shared__ unsigned long long s_turn[D / 2];
-  __shared__ uint32_t s_max[kRotThreads / 32][2];
+  __shared__ uint2 s_max[kRotThreads / 32];
   __shared__ int s_more;
   extern __shared__ __align__(16) uint8_t smem[];
   const CacheAppendLaunch& A = L.a;
@@ -300,19 +323,21 @@ __global__ void __launch_bounds__(kRotThreads, 3) cache_append_rotary_kernel(Cac
   const int m = cache_new(A.n_new, A.n, b, A.err);
   const bool fits = sequence_fits(A, b, m);
   if (!fits && threadIdx.x == 0) atomicOr(A.err, kErrBadCache);
-  const int of_pages = L.touched * A.H_kv;
+  const unsigned long long of_pages = static_cast<unsigned long long>(L.touched) * A.H_kv;
+  const uint32_t before = static_cast<uint32_t>(blockIdx.x * of_pages / gridDim.x);      // blocks of pages before this one
+  const bool is_page = static_cast<uint32_t>((blockIdx.x + 1ull) * of_pages / gridDim.x) > before;
   int h = 0, n0 = 0;
-  if (static_cast<int>(blockIdx.x) < of_pages) {
-    h = blockIdx.x / L.touched;
+  if (is_page) {
+    h = before / L.touched;
     n0 = A.c.len[b * A.H_kv + h];
-    const int j = n0 / kPage + blockIdx.x % L.touched;
-    if (fits && max(n0, j * kPage) < min(n0 + m, (j + 1) * kPage)) append_page<T, D>(L, b, h, j, n0, m, s_turn, s_max, &s_more, smem);
+    const int j = n0 / kPage + before % L.touched;
+    if (fits && max(n0, j * kPage) < min(n0 + m, (j + 1) * kPage)) append_page<T, D, kInterleaved>(L, b, h, j, n0, m, s_turn, s_max, &s_more, smem);
   } else if (fits) {
-    const int x = blockIdx.x - of_pages, chunks = (A.n + L.rot.tokens - 1) / L.rot.tokens;
+    const int x = blockIdx.x - before, chunks = (A.n + L.rot.tokens - 1) / L.rot.tokens;
     const int t0 = x % chunks * L.rot.tokens;
-    if (t0 < m) rotate_rows<T, D>(L.rot, b, t0, x / chunks * L.rot.heads, m, A.c.next[b], nullptr, s_turn);
+    if (t0 < m) rotate_rows<T, D, kInterleaved, 64>(L.rot, b, t0, x / chunks * L.rot.heads, m, A.c.next[b], nullptr, s_turn);
   }
-  append_counts(A, b, h, n0, fits ? m : 0, static_cast<int>(blockIdx.x) < of_pages && blockIdx.x % L.touched == 0,
+  append_counts(A, b, h, n0, fits ? m : 0, is_page && before % L.touched == 0,
                 gridDim.x * gridDim.y * gridDim.z);
 }
 
@@ -329,18 +354,31 @@ void split_rows(RotaryLaunch* L, int d) {
 }
 
 // Devices on which the kernel's shared memory is set up.
-template <typename T, int D>
+template <typename T, int D, bool kInterleaved>
 std::atomic<bool> g_ready[kMaxDevices];
+
+template <typename T, int D, bool kInterleaved>
+cudaError_t launch_append(const CacheAppendRotaryLaunch& L, dim3 grid, cudaStream_t st) {
+  constexpr int kSmem = PageRows<T, D>::kBytes;
+  const auto kernel = cache_append_rotary_kernel<T, D, kInterleaved>;
+  std::atomic<bool>& ready = g_ready<T, D, kInterleaved>[L.device];
+  if (!ready.load(std::memory_order_acquire)) {
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return e;
+    ready.store(true, std::memory_order_release);
+  }
+  kernel<<<grid, kRotThreads, kSmem, st>>>(L);
+  return cudaGetLastError();
+}
 
 template <typename T, int D>
 cudaError_t launch_append(const CacheAppendRotaryLaunch& L, dim3 grid, cudaStream_t st) {
-  constexpr int kSmem = PageRows<T, D>::kBytes;
-  const void* kernel = reinterpret_cast<const void*>(cache_append_rotary_kernel<T, D>);
-  if (!g_ready<T, D>[L.device].load(std::memory_order_acquire)) {
-    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return e;
-    g_ready<T, D>[L.device].store(true, std::memory_order_release);
-  }
-  cache_append_rotary_kernel<T, D><<<grid, kRotThreads, kSmem, st>>>(L);
+  return L.rot.interleaved ? launch_append<T, D, true>(L, grid, st) : launch_append<T, D, false>(L, grid, st);
+}
+
+template <typename T, int D>
+cudaError_t launch_rows(const RotaryLaunch& L, dim3 grid, cudaStream_t st) {
+  if (L.interleaved) rotary_kernel<T, D, true><<<grid, kRotThreads, 0, st>>>(L);
+  else rotary_kernel<T, D, false><<<grid, kRotThreads, 0, st>>>(L);
   return cudaGetLastError();
 }
 
@@ -349,14 +387,8 @@ cudaError_t launch_append(const CacheAppendRotaryLaunch& L, dim3 grid, cudaStrea
 cudaError_t launch_rotary(RotaryLaunch L, int d, int dtype, cudaStream_t st) {
   split_rows(&L, d);
   const dim3 grid((L.n + L.tokens - 1) / L.tokens, (L.Hq + L.Hk + L.heads - 1) / L.heads, L.B);
-  if (dtype == FOCUS_BF16) {
-    if (d == 128) rotary_kernel<__nv_bfloat16, 128><<<grid, kRotThreads, 0, st>>>(L);
-    else rotary_kernel<__nv_bfloat16, 64><<<grid, kRotThreads, 0, st>>>(L);
-  } else {
-    if (d == 128) rotary_kernel<float, 128><<<grid, kRotThreads, 0, st>>>(L);
-    else rotary_kernel<float, 64><<<grid, kRotThreads, 0, st>>>(L);
-  }
-  return cudaGetLastError();
+  if (dtype == FOCUS_BF16) return d == 128 ? launch_rows<__nv_bfloat16, 128>(L, grid, st) : launch_rows<__nv_bfloat16, 64>(L, grid, st);
+  return d == 128 ? launch_rows<float, 128>(L, grid, st) : launch_rows<float, 64>(L, grid, st);
 }
 
 cudaError_t launch_cache_append_rotary(CacheAppendRotaryLaunch L, int dtype, cudaStream_t st) {

@@ -36,14 +36,15 @@ __device__ __forceinline__ unsigned long long turn_of(float inv_freq) {
   return u >> 31 ? 0ull - t : t;
 }
 
-// Cosine and sine of a phase in 2^-64 turns: Taylor polynomials of degree 10 and 9 on an
-// eighth of a turn (the next terms are below 2^-32 and 2^-29), evaluated in fp32.
-__device__ __forceinline__ void cos_sin(unsigned long long phase, float& c, float& s) {
-  const uint32_t quarter = static_cast<uint32_t>((phase + (1ull << 61)) >> 62);
-  const long long rest = static_cast<long long>(phase - (static_cast<unsigned long long>(quarter) << 62));   // at most an eighth
-  const float x = static_cast<float>(static_cast<int>(rest >> 30)) * (3.14159265358979f * 0x1p-33f);   // bits 61 ... 30: |rest| <= 2^61
-  const float z = x * x;
-  const float a = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 2.7557319e-6f, -1.9841270e-4f), 8.3333333e-3f), -0.16666667f), x);
+// Cosine and sine at position x of a frequency's t: the phase's upper 32 bits (2^-33 turns), a
+// quarter's remainder in radians, Taylor polynomials of degree 10 and 9 on an eighth of a turn (the
+// next terms are below 2^-32 and 2^-29), all in fp32.
+__device__ __forceinline__ void cos_sin(uint32_t x, unsigned long long t, float& c, float& s) {
+  const uint32_t phase = x * static_cast<uint32_t>(t >> 32) + __umulhi(x, static_cast<uint32_t>(t));
+  const uint32_t quarter = phase + (1u << 29) >> 30;
+  const float r = static_cast<float>(static_cast<int>(phase - (quarter << 30))) * (6.28318530717959f * 0x1p-32f);
+  const float z = r * r;
+  const float a = fmaf(r * z, fmaf(z, fmaf(z, fmaf(z, 2.7557319e-6f, -1.9841270e-4f), 8.3333333e-3f), -0.16666667f), r);
   const float b = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -2.7557319e-7f, 2.4801587e-5f), -1.3888889e-3f), 4.1666667e-2f), -0.5f), 1.f);
   c = quarter & 1 ? a : b;
   s = quarter & 1 ? b : a;
@@ -63,17 +64,42 @@ struct Duo {
   }
 };
 
-// Pair e of a duo's 16 elements y: places of its two elements.
-__device__ __forceinline__ constexpr int pair_lo(int e, bool interleaved) { return interleaved ? 2 * e : e; }
-__device__ __forceinline__ constexpr int pair_hi(int e, bool interleaved) { return interleaved ? 2 * e + 1 : 8 + e; }
-
+// A duo's eight pairs: places e and 8 + e, or neighbours.  Two pairs a step, packed.
 template <bool kInterleaved>
-__device__ __forceinline__ void turn_pairs(float (&y)[16], const float (&c)[8], const float (&s)[8]) {
+__device__ __forceinline__ void turn_pairs(float (&y)[16], const uint64_t (&c)[4], const uint64_t (&s)[4]) {
+  const uint64_t minus = f2_pack(-1.f, -1.f);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float a = y[pair_lo(e, kInterleaved)], b = y[pair_hi(e, kInterleaved)];
-    y[pair_lo(e, kInterleaved)] = fmaf(-b, s[e], a * c[e]);
-    y[pair_hi(e, kInterleaved)] = fmaf(b, c[e], a * s[e]);
+  for (int e = 0; e < 4; ++e) {
+    float& a0 = y[kInterleaved ? 4 * e : 2 * e];
+    float& a1 = y[kInterleaved ? 4 * e + 2 : 2 * e + 1];
+    float& b0 = y[kInterleaved ? 4 * e + 1 : 8 + 2 * e];
+    float& b1 = y[kInterleaved ? 4 * e + 3 : 9 + 2 * e];
+    const uint64_t a = f2_pack(a0, a1), b = f2_pack(b0, b1);
+    const uint64_t x = f2_fma(f2_mul(b, minus), s[e], f2_mul(a, c[e])), z = f2_fma(b, c[e], f2_mul(a, s[e]));
+    f2_unpack(x, a0, a1);
+    f2_unpack(z, b0, b1);
+  }
+}
+
+// The frequencies' t in shared memory: that of duo k's pair e at e * kDuos + k, on a bank of its
+// own among the lanes that read it together.
+template <int kDuos>
+__device__ __forceinline__ void fill_turns(const RotaryLaunch& L, unsigned long long* turn) {
+  const int i = threadIdx.x;
+  if (i < L.dim / 2) turn[i % 8 * kDuos + i / 8] = turn_of(L.inv_freq[i]);
+}
+
+// Cosines and sines of duo k's frequencies at position x, times scale and sine_scale (turn: those of k).
+template <int kDuos>
+__device__ __forceinline__ void duo_cos_sin(uint32_t x, const unsigned long long* turn, float scale, float sine_scale,
+                                            uint64_t (&c)[4], uint64_t (&s)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float c0, c1, s0, s1;
+    cos_sin(x, turn[2 * e * kDuos], c0, s0);
+    cos_sin(x, turn[(2 * e + 1) * kDuos], c1, s1);
+    c[e] = f2_mul(f2_pack(c0, c1), f2_pack(scale, scale));
+    s[e] = f2_mul(f2_pack(s0, s1), f2_pack(sine_scale, sine_scale));
   }
 }
 
@@ -87,61 +113,63 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* y) {
 }
 
 // Rows of a block's tokens and heads: `tokens` tokens (a power of two) of `heads` heads.
-// Head g < L.H is a query head, the others are key heads.
-template <typename T, int D>
+// Head g < L.Hq is a query head, the others are key heads.
+// kBytes: of rows that a thread has in flight.
+template <typename T, int D, bool kInterleaved, int kBytes>
 __device__ __forceinline__ void rotate_rows(const RotaryLaunch& L, int b, int t0, int head0, int valid,
                                             long long first, const int* depth, unsigned long long* s_turn) {
-  constexpr int kDuos = D / 16, kSlots = kRotThreads / kDuos, kAtOnce = sizeof(T) == 2 ? 4 : 2;
-  if (threadIdx.x < L.dim / 2) s_turn[threadIdx.x] = turn_of(L.inv_freq[threadIdx.x]);
+  constexpr int kDuos = D / 16, kSlots = kRotThreads / kDuos, kAtOnce = kBytes / (16 * sizeof(T));
+  fill_turns<kDuos>(L, s_turn);
   __syncthreads();
   const int k = threadIdx.x % kDuos, slot = threadIdx.x / kDuos;
   const int t = t0 + slot % L.tokens, across = kSlots / L.tokens;
   if (t >= valid) return;
-  const Duo duo(k, L.dim, L.interleaved);
-  float c[8], s[8];
+  const Duo duo(k, L.dim, kInterleaved);
+  uint64_t c[4], s[4];
   if (duo.turns) {
-    const long long x = first + (depth ? depth[t] : t);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      cos_sin(static_cast<unsigned long long>(x) * s_turn[k * 8 + e], c[e], s[e]);
-      c[e] *= L.scale;
-      s[e] *= L.transpose ? -L.scale : L.scale;
-    }
+    const long long x = first + (depth ? depth[t] : t);              // |x| < 2^32: an int and a token's number
+    duo_cos_sin<kDuos>(static_cast<uint32_t>(x < 0 ? -x : x), s_turn + k, L.scale, (x < 0) != (L.transpose != 0) ? -L.scale : L.scale, c, s);
   }
-  const int end = min(head0 + L.heads, L.Hq + L.Hk);
-  for (int g0 = head0 + slot / L.tokens; g0 < end; g0 += across * kAtOnce) {
-    Piece<T> p[kAtOnce][2];
-    const T* from[kAtOnce];
-    T* to[kAtOnce];
+  const size_t head = static_cast<size_t>(L.n) * D;                  // elements of one
+  // Heads [from, end) of one of the two tensors, rows in steps of `across` heads.
+  auto walk = [&](const void* in, void* out, int heads, int from, int end) {
+    const size_t at = (static_cast<size_t>(b) * heads + from) * head + static_cast<size_t>(t) * D;
+    const T* src = static_cast<const T*>(in) + at;
+    T* dst = static_cast<T*>(out) + at;
+    if (!duo.turns && src == dst) return;
+    for (int g = from; g < end; g += across * kAtOnce) {
+      Piece<T> p[kAtOnce][2];
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int g = g0 + i * across;
-      if (g >= end) break;
-      const bool q = g < L.Hq;
-      const size_t row = ((static_cast<size_t>(b) * (q ? L.Hq : L.Hk) + (q ? g : g - L.Hq)) * L.n + t) * D;
-      from[i] = static_cast<const T*>(q ? L.Q : L.K) + row;
-      to[i] = static_cast<T*>(q ? L.Q_out : L.K_out) + row;
-      p[i][0].load(from[i] + duo.at[0]);
-      p[i][1].load(from[i] + duo.at[1]);
-    }
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      if (g0 + i * across >= end) break;
-      if (!duo.turns) {                                  // as they are, to the last bit
-        if (from[i] != to[i]) {
-          p[i][0].store(to[i] + duo.at[0]);
-          p[i][1].store(to[i] + duo.at[1]);
+      for (int i = 0; i < kAtOnce; ++i)
+        if (g + i * across < end) {
+          p[i][0].load(src + i * across * head + duo.at[0]);
+          p[i][1].load(src + i * across * head + duo.at[1]);
         }
-        continue;
-      }
-      float y[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) y[e] = p[i][e / 8].at(e % 8);
-      if (L.interleaved) turn_pairs<true>(y, c, s);
-      else turn_pairs<false>(y, c, s);
-      store8(to[i] + duo.at[0], y);
-      store8(to[i] + duo.at[1], y + 8);
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (g + i * across >= end) break;
+        T* to = dst + i * across * head;
+        if (duo.turns) {
+          float y[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] = p[i][e / 8].at(e % 8);
+          turn_pairs<kInterleaved>(y, c, s);
+          store8(to + duo.at[0], y);
+          store8(to + duo.at[1], y + 8);
+        } else {                                         // as they are, to the last bit
+          p[i][0].store(to + duo.at[0]);
+          p[i][1].store(to + duo.at[1]);
+        }
+      }
+      src += across * kAtOnce * head;
+      dst += across * kAtOnce * head;
     }
+  };
+  const int mine = head0 + slot / L.tokens, end = min(head0 + L.heads, L.Hq + L.Hk);
+  if (L.Hq) walk(L.Q, L.Q_out, L.Hq, mine, min(end, L.Hq));
+  if (L.Hk) {
+    const int past = mine < L.Hq ? mine + (L.Hq - mine + across - 1) / across * across : mine;   // the first that is a key head
+    walk(L.K, L.K_out, L.Hk, past - L.Hq, end - L.Hq);
   }
 }
 
