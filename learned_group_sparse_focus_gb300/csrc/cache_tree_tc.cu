@@ -64,8 +64,8 @@ struct Cfg {
   static constexpr int kK = 0, kV = kK + kTileBytes, kRaw = kV + 2 * kTileBytes, kP = kRaw + kTileBytes, kQ = kP + kPBytes,
                        kListAt = kQ + R * D * 2, kIds = kListAt + kList * 16, kTable = kIds + 2 * kScanWarps * kAhead * kPage * 2,
                        kSmem = kTable + kCacheTableGroups * 8 + 1024;   // + alignment
-  static constexpr int kInbox = kP;                            // the partials', once the block's tiles are done
-  static_assert(R * D * 4 <= kPBytes && R % kMaxCluster == 0, "inbox does not fit");
+  static constexpr int kInbox = kP;                            // the partials', over P and Q, once the block's tiles are done
+  static_assert((R + kMaxCluster - 1) * D * 4 <= kListAt - kInbox, "inbox does not fit");
   static constexpr int kCols = 4 * R;                          // TMEM: S twice, O in two parts
 };
 
@@ -818,7 +818,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
 
   // ---- join: the same exchange as in cache_attn.cuh
   cluster.sync();                                      // every block runs and is past its tiles
-  const int share = R / cs, shift = __ffs(share) - 1;  // rows that a block writes, a power of two
+  const int share = (R + cs - 1) / cs;                 // rows that a block writes
+  const uint32_t inverse = 65536u / share + 1;         // r / share = r * inverse / 2^16 for r < 64
   if (warp < kSoftWarps && tiles > 0) {
     const int quad = warp & 3, part = warp >> 2, d = quad * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
@@ -831,10 +832,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       if (quad < D / 32) {
 #pragma unroll
         for (int y = 0; y < 8; ++y) {
-          const int r = part * RH + c + y, to = r >> shift;
+          const int r = part * RH + c + y, to = r * inverse >> 16;
           float x = __uint_as_float(hi[y]) + __uint_as_float(lo[y]);
           if (s_nan[r][quad] >> lane & 1) x = __int_as_float(0x7fffffff);
-          *cluster.map_shared_rank(inbox + (rank * share + (r & (share - 1))) * D + d, to) = x;
+          *cluster.map_shared_rank(inbox + (rank * share + r - to * share) * D + d, to) = x;
         }
       }
     }
@@ -890,23 +891,60 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   }
 }
 
+// Clusters of 1 ... 16 blocks that a device runs at once, asked for at a kernel's first launch there
+// (with a block an SM: 152, 76, 46, 36, 28, 23, 15, 15, 15, 13, 8, 8, 7, 7, 7, 7).
+struct ClusterSizes {
+  std::mutex mu;
+  std::atomic<bool> ready{false};
+  int n[kMaxCluster + 1];
+};
+
+cudaError_t cluster_sizes(ClusterSizes* at, const void* kernel, int threads, int smem) {
+  if (at->ready.load(std::memory_order_acquire)) return cudaSuccess;
+  std::lock_guard<std::mutex> lock(at->mu);
+  if (at->ready.load(std::memory_order_relaxed)) return cudaSuccess;
+  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) return e;
+  for (int cs = 1; cs <= kMaxCluster; ++cs) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(cs);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cs;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaError_t e = cudaOccupancyMaxActiveClusters(&at->n[cs], kernel, &cfg)) return e;
+  }
+  at->ready.store(true, std::memory_order_release);
+  return cudaSuccess;
+}
+
 template <int D, int R>
-ClusterFits g_fits;
+ClusterSizes g_sizes[kMaxDevices];
 
 template <int D, int R>
 cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
-  const ClusterFit* fit;
-  if (cudaError_t e = g_fits<D, R>.get(L.device, reinterpret_cast<const void*>(cache_tree_tc_kernel<D, R>), Cfg<D, R>::kThreads,
-                                       Cfg<D, R>::kSmem, &fit))
+  ClusterSizes& sizes = g_sizes<D, R>[L.device];
+  if (cudaError_t e = cluster_sizes(&sizes, reinterpret_cast<const void*>(cache_tree_tc_kernel<D, R>), Cfg<D, R>::kThreads, Cfg<D, R>::kSmem))
     return e;
-  // Blocks per (sequence, head, block of rows): one wave of the clusters that run at once, as
-  // long as each block scans a round or so.
+  // Blocks per (sequence, head, block of rows): the fewest of those that take the least time, with a block's
+  // fixed part worth kFixedPages pages, and clusters that follow each other as the SMs come free.
+  constexpr int kFixedPages = 20;
   const int blocks = (L.H / L.H_kv * L.n + R - 1) / R;
-  const long long heads = static_cast<long long>(L.B) * blocks * L.H_kv;
-  int cs = 1, i = 0;
-  while (cs < kMaxCluster && cs * 16 <= L.c.max_pages && heads <= fit->n[i + 1]) {
-    cs *= 2;
-    ++i;
+  const double heads = static_cast<double>(L.B) * blocks * L.H_kv;
+  int cs = 1;
+  double least = 0;
+  for (int c = 1; c <= kMaxCluster && (c == 1 || 4 * c <= L.c.max_pages); ++c) {
+    if (sizes.n[c] < 1) continue;
+    const double waves = heads <= sizes.n[c] ? 1. : heads / sizes.n[c] + 0.5;
+    const double time = waves * (kFixedPages + (L.c.max_pages + c - 1) / c);
+    if (c == 1 || time < least) {
+      least = time;
+      cs = c;
+    }
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(cs * blocks, L.H_kv, L.B);
