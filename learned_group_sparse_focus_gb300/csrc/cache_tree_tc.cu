@@ -7,14 +7,15 @@
 // slot is read once a block of rows (2 d bytes), and costs 6 d flops a row as computed
 // (4 d for S and P V, 2 d more for the weights' second half).
 //
-//   S^T [128 keys, R rows]      = K Q^T        kind::f16: a code is an f16 number, a bf16
-//                                 query row times a power of two is one too
-//   O^T [128 dims, 2 R]        += V^T [P1 P2]  weights in two f16 parts, 22 bits, side by side
-//                                 in N with accumulators of their own
-// The gathering warps copy codes to shared memory a tile ahead, each lane for itself, convert
-// them (and the drafted rows, scaled to f16 by a power of two of their own) and store them as the tensor core reads them: f16 costs
-// twice the shared memory of codes, but half the tensor time of four e4m3 parts and a
-// third of the instructions a weight (cache_attn_tc.cu's form, which keeps codes).
+//   S^T [128 keys, 2 R]         = K Q^T        kind::f8f6f4 on the codes as they are; Q as
+//                                 2^e (q1 + q2 / 16) in e4m3, side by side in N (see cache_attn_tc.cu)
+//   O^T [128 dims, 2 R]        += V^T [P1 P2]  kind::f16: codes as f16 numbers, weights in two f16
+//                                 parts, 22 bits, side by side in N
+// Keys are copied straight to where the tensor core reads them.  Values are copied to shared memory a tile
+// ahead, each piece for the lane that copied it, which converts it: four e4m3 parts of the weights would
+// need no conversion, but twice the tensor time and three times the instructions a weight
+// (cache_attn_tc.cu's form, made for few rows).  The drafted rows, in the tree's own tile, become two e4m3
+// parts (keys, a product each) or f16 (values), times a power of two a row.
 //
 // A thread of the weight warps owns a key and half of the rows.  Masks are a bit per row, held in an
 // order in which one shift brings four rows' bits to the tops of four bytes and a byte
@@ -59,20 +60,43 @@ struct Cfg {
   static constexpr int kList = R == 64 ? 1024 : 2048;          // entries of the block's list of kept slots
   static_assert(kList >= kRound * kPage + kListed * kTile, "list too short");
   static constexpr int kChunk = kTile * 128;                   // 64 f16 columns of a tile's rows
-  static constexpr int kTileBytes = D / 64 * kChunk, kPBytes = R / 32 * kChunk;
+  static constexpr int kTileBytes = D / 64 * kChunk, kPBytes = R / 32 * kChunk;   // of a value tile; of the weights
+  static constexpr int kKeySlots = 3, kKeyBytes = kTile * 128;   // of codes, rows 128 bytes apart for either d
   // byte offsets in dynamic shared memory
-  static constexpr int kK = 0, kV = kK + kTileBytes, kRaw = kV + 2 * kTileBytes, kP = kRaw + kTileBytes, kQ = kP + kPBytes,
-                       kListAt = kQ + R * D * 2, kIds = kListAt + kList * 16, kTable = kIds + 2 * kScanWarps * kAhead * kPage * 2,
+  static constexpr int kK = 0, kV = kK + kKeySlots * kKeyBytes, kP = kV + 2 * kTileBytes, kQ = kP + kPBytes,
+                       kRaw = kQ + 2 * R * 128, kListAt = kRaw + kTile * D, kIds = kListAt + kList * 16, kTable = kIds + 2 * kScanWarps * kAhead * kPage * 2,
                        kSmem = kTable + kCacheTableGroups * 8 + 1024;   // + alignment
   static constexpr int kInbox = kP;                            // the partials', over P and Q, once the block's tiles are done
-  static_assert((R + kMaxCluster - 1) * D * 4 <= kListAt - kInbox, "inbox does not fit");
-  static constexpr int kCols = 4 * R;                          // TMEM: S twice, O in two parts
+  static_assert((R + kMaxCluster - 1) * D * 4 <= kRaw - kInbox && R / kSoftWarps * kSoftWarps * D * 2 <= kTile * D, "inbox does not fit");
+  static constexpr int kCols = 8 * R;                          // TMEM: S twice and O, in two parts each (6 R used)
 };
 
 // kind::f16, A and B f16, fp32 accumulate; M = 128.
 constexpr uint32_t idesc_f16(int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+// kind::f8f6f4, A and B e4m3, K-major, fp32 accumulate; M = 128: the descriptor has the same zeros.
+constexpr uint32_t idesc_f8(int N) { return idesc_f16(N, false, false); }
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
+      ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// Arrives on `bar` (counted in its arrivals) when this thread's cp.async so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// tmem_wait_ld for two loads of eight, which are not used before it.
+__device__ __forceinline__ void tmem_wait_for(uint32_t (&a)[8], uint32_t (&b)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                 "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
+               :: "memory");
 }
 
 // Row masks: row 4 q + i of 32 is bit 8 i + 7 - q of its word.
@@ -121,7 +145,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   constexpr int kSoftWarps = C::kSoftWarps, kScanWarps = C::kScanWarps, kGatherWarp = C::kGatherWarp,
                 kGatherWarps = C::kGatherWarps, kMmaWarp = C::kMmaWarp, kThreads = C::kThreads;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t k_full, v_full[2], qk_done, pv_done[2], s_ready[2], p_ready;
+  __shared__ uint64_t k_full[C::kKeySlots], qk_done[C::kKeySlots], v_full[2], pv_done[2], s_ready[2], p_ready;
   __shared__ uint64_t listed[kListed], used[kListed];  // a tile's entries are in the list; the weight warps have read them
   __shared__ uint64_t scan_bar;
   __shared__ int s_found[2][kScanWarps];               // slots that a scan warp lists in a round
@@ -199,8 +223,11 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   // ---- barriers, tree, masks
   if (threadIdx.x == 0) {
     s_abort_word = 0;
-    mbar_init(&k_full, kGatherWarps);
-    mbar_init(&qk_done, 1);
+#pragma unroll 1
+    for (int i = 0; i < C::kKeySlots; ++i) {
+      mbar_init(&k_full[i], kGatherWarps * 32);
+      mbar_init(&qk_done[i], 1);
+    }
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(&v_full[i], kGatherWarps);
@@ -267,12 +294,23 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       }
       top = __reduce_max_sync(~0u, top);
       finite = __all_sync(~0u, finite);
-      const int eq = min(max(static_cast<int>(top >> 23) - 127 - 13, kMinQueryExp), 115);   // |q| 2^-eq < 2^14
+      const int eq = need_exp(top, kMinQueryExp), d = lane * kEach;
       const float down = exp2_int(-eq);
-      const int d = lane * kEach;                      // in the row's 16-byte piece d / 8 of its chunk
-      uint8_t* to = smem + C::kQ + d / 64 * R * 128 + r * 128 + ((d % 64 / 8) ^ (r & 7)) * 16 + d % 8 * 2;
+      uint32_t part[2] = {0, 0};
 #pragma unroll
-      for (int e = 0; e < kEach; e += 2) *reinterpret_cast<uint32_t*>(to + e * 2) = half2_bits(q[e] * down, q[e + 1] * down);
+      for (int e = 0; e < kEach; e += 2) {
+        const float a = q[e] * down, c = q[e + 1] * down;
+        const uint32_t first = float2_to_e4m3x2(a, c);
+        const float2 f = e4m3x2_to_float2(static_cast<uint16_t>(first));
+        part[0] |= first << 8 * e;
+        part[1] |= static_cast<uint32_t>(float2_to_e4m3x2((a - f.x) * 16.f, (c - f.y) * 16.f)) << 8 * e;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint8_t* to = smem + C::kQ + (x * R + r) * 128 + ((d / 16) ^ (r & 7)) * 16 + d % 16;
+        if (kEach == 4) *reinterpret_cast<uint32_t*>(to) = part[x];
+        else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(part[x]);
+      }
       if (lane == 0) {
         // rows with an infinite or NaN element become NaN through their factor
         s_factor[r] = finite ? exp2_int(eq) * L.scale_log2 : __int_as_float(0x7fffffff);
@@ -327,8 +365,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem, tmem_o = tmem + 2 * R;
+  const uint32_t tmem = s_tmem, tmem_o = tmem + 4 * R;
 
+  // A tile's slot among the keys' (by kKeySlots); the tree's own tile, the first, takes slots 0 and 1.
+  auto key_slot = [&](int tile) { return static_cast<uint32_t>(tile) + (has_own && tile > 0 ? 1 : 0); };
   int tiles = 0;                                       // weight warps: tiles of the block
   if (scans) {
     // -------------------------------------------------- scan
@@ -505,31 +545,54 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
           const int e_row = min(need_exp(__float_as_uint(top)), kMaxExp);
           const float down = exp2_int(-e_row);
           exps |= (e_row & 0xff) << (8 * x);
-          uint32_t w[8];
+          if (x) {
+            uint32_t w[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = half2_bits(f[2 * e] * down, f[2 * e + 1] * down);
-          put(smem + (x ? C::kV : C::kK), r, w);
+            for (int e = 0; e < 8; ++e) w[e] = half2_bits(f[2 * e] * down, f[2 * e + 1] * down);
+            put(smem + C::kV, r, w);
+          } else {
+            // four bits, and the rest: what is below 2^-11 of the row's largest is held to 2^-19 of that
+            uint32_t one[4] = {0, 0, 0, 0}, two[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const uint32_t first = float2_to_e4m3x2(f[e] * down, f[e + 1] * down);
+              const float2 g = e4m3x2_to_float2(static_cast<uint16_t>(first));
+              one[e / 4] |= first << e % 4 * 8;
+              two[e / 4] |= static_cast<uint32_t>(float2_to_e4m3x2(f[e] * down - g.x, f[e + 1] * down - g.y)) << e % 4 * 8;
+            }
+            uint8_t* to = smem + C::kK + r * 128 + (piece ^ (r & 7)) * 16;
+            *reinterpret_cast<uint4*>(to) = make_uint4(one[0], one[1], one[2], one[3]);
+            *reinterpret_cast<uint4*>(to + C::kKeyBytes) = make_uint4(two[0], two[1], two[2], two[3]);
+          }
         }
         const uint32_t of_row = D == 128 ? 0x0f0fu << ((sub & 1) * 4 + (sub >> 1) * 16) : 0xfu << sub * 4;   // its lanes
         if (__ballot_sync(~0u, bad) & of_row) exps |= 1 << 16;
         if (piece == 0 && r < fresh) list[r].y = exps;
       }
-      arrive(&k_full);
+      fence_proxy_async_smem();
+      mbar_arrive(&k_full[0]);
+      mbar_arrive(&k_full[1]);
       arrive(&v_full[0]);
       tile = 1;
     }
-    // Codes on their way wait in shared memory, each piece for the lane that copies it.
-    uint8_t* const mine = smem + C::kRaw + (gw * 2 * kLoads * 32 + lane) * 16;
+    // Values on their way wait in shared memory, each piece for the lane that copies it.
+    uint8_t* const mine = smem + C::kRaw + (gw * kLoads * 32 + lane) * 16;
     auto issue = [&](int t) {
       const int cnt = s_cnt[t & 7];
+      const uint32_t u = key_slot(t), slot = u % C::kKeySlots;
       const int4* about = list + (t * kTile & (kList - 1));
+      uint8_t* const keys = smem + C::kK + slot * C::kKeyBytes;
+      if (u >= C::kKeySlots) await(&qk_done[slot], (u / C::kKeySlots + 1) & 1, abort, L.err);
+      size_t off[kLoads];
 #pragma unroll
       for (int y = 0; y < kLoads; ++y) {
         const int r = row_at(y);
-        const size_t off = r < cnt ? static_cast<size_t>(static_cast<uint32_t>(about[r].x)) * D + piece * 16 : 0;
-        cp_async_16(mine + y * 512, L.c.k + off, r < cnt ? 16 : 0);
-        cp_async_16(mine + (kLoads + y) * 512, L.c.v + off, r < cnt ? 16 : 0);
+        off[y] = r < cnt ? static_cast<size_t>(static_cast<uint32_t>(about[r].x)) * D + piece * 16 : 0;
+        cp_async_16(keys + r * 128 + (piece ^ (r & 7)) * 16, L.c.k + off[y], r < cnt ? 16 : 0);
       }
+      cp_async_arrive(&k_full[slot]);
+#pragma unroll
+      for (int y = 0; y < kLoads; ++y) cp_async_16(mine + y * 512, L.c.v + off[y], row_at(y) < cnt ? 16 : 0);
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     bool issued = false;                               // the tile's rows are on their way
@@ -537,28 +600,18 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       if (!issued) {
         const bool ok = __all_sync(~0u, await(&listed[tile % kListed], (tile / kListed) & 1, abort, L.err));
         if (__any_sync(~0u, !ok || s_cnt[tile & 7] == 0 || *abort)) {
-          // not before the last phase has been seen: a wait on it would miss two in a row
-          if (tile >= 1) await(&qk_done, (tile - 1) & 1, abort, L.err);
-          arrive(&k_full);
+          // not before the slot's last phase has been seen: a wait on it would miss two in a row
+          const uint32_t u = key_slot(tile), slot = u % C::kKeySlots;
+          if (u >= C::kKeySlots) await(&qk_done[slot], (u / C::kKeySlots + 1) & 1, abort, L.err);
+          mbar_arrive(&k_full[slot]);
           break;
         }
         issue(tile);
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
-      uint4 k[kLoads], vv[kLoads];
+      uint4 vv[kLoads];
 #pragma unroll
-      for (int y = 0; y < kLoads; ++y) {
-        k[y] = *reinterpret_cast<const uint4*>(mine + y * 512);
-        vv[y] = *reinterpret_cast<const uint4*>(mine + (kLoads + y) * 512);
-      }
-      if (tile >= 1) await(&qk_done, (tile - 1) & 1, abort, L.err);
-#pragma unroll
-      for (int y = 0; y < kLoads; ++y) {
-        uint32_t w[8];
-        widen(k[y], w);
-        put(smem + C::kK, row_at(y), w);
-      }
-      arrive(&k_full);
+      for (int y = 0; y < kLoads; ++y) vv[y] = *reinterpret_cast<const uint4*>(mine + y * 512);
       // A row that does not keep a key has weight 0 for it, and 0 * NaN would reach that row:
       // NaN codes leave the tile and mark the outputs that they reach.
       uint32_t any = 0;
@@ -570,7 +623,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       if (any & 0x80808080u) {
 #pragma unroll 1
         for (int i = 0; i < kLoads * 16; ++i) {
-          uint8_t* at = mine + (kLoads + i / 16) * 512 + i % 16;
+          uint8_t* at = mine + i / 16 * 512 + i % 16;
           if ((*at & 127) != 127) continue;
           *at = 0;
           const int4 e = list[(tile * kTile & (kList - 1)) + row_at(i / 16)];
@@ -580,7 +633,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
             atomicOr(&s_nan[row_of_bit(__ffsll(left) - 1) % R][d / 32], 1u << (d % 32));
         }
 #pragma unroll
-        for (int y = 0; y < kLoads; ++y) vv[y] = *reinterpret_cast<const uint4*>(mine + (kLoads + y) * 512);
+        for (int y = 0; y < kLoads; ++y) vv[y] = *reinterpret_cast<const uint4*>(mine + y * 512);
       }
       // the next tile's rows, if it is listed by now (this one's have been read)
       issued = __all_sync(~0u, mbar_test_wait(&listed[(tile + 1) % kListed], ((tile + 1) / kListed) & 1)) && s_cnt[(tile + 1) & 7] > 0;
@@ -602,18 +655,25 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       bool ok = true;
       // S of a tile whose K is there; false at the end of the tiles
       auto scores = [&](int tile) {
-        ok = ok && await(&k_full, tile & 1, abort, L.err);
+        const uint32_t u = key_slot(tile), slot = u % C::kKeySlots;
+        const bool own = has_own && tile == 0;
+        ok = ok && await(&k_full[slot], (u / C::kKeySlots) & 1, abort, L.err);
+        if (own) ok = ok && await(&k_full[1], 0, abort, L.err);
         ok = ok && await(&listed[tile % kListed], (tile / kListed) & 1, abort, L.err);         // done: orders s_cnt
         if (!ok || s_cnt[tile & 7] == 0) {
           mbar_arrive(&s_ready[tile & 1]);
           return false;
         }
+        fence_proxy_async_smem();                      // the copies, like all writes of threads, to the tensor core
         tc_fence_after();
+#pragma unroll 1
+        for (int y = 0; y <= (own ? 1 : 0); ++y) {     // both parts of the drafted keys
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x)
-          mma_ss(tmem + (tile & 1) * R, desc_rows(kb + x / 4 * C::kChunk + x % 4 * 32, 16),
-                 desc_rows(qb + x / 4 * R * 128 + x % 4 * 32, 16), idesc_f16(R, false, false), x > 0);
-        mma_commit(&qk_done);
+          for (int x = 0; x < D / 32; ++x)
+            mma_f8(tmem + (tile & 1) * 2 * R, desc_rows(kb + (slot + y) * C::kKeyBytes + x * 32, 16), desc_rows(qb + x * 32, 16),
+                   idesc_f8(2 * R), x + y > 0);
+          mma_commit(&qk_done[slot + y]);
+        }
         mma_commit(&s_ready[tile & 1]);
         return true;
       };
@@ -637,7 +697,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       }
       // every commit has arrived before the block ends
       if (tile > 0) {
-        await(&qk_done, (tile - 1) & 1, abort, L.err);
+        const uint32_t u = key_slot(tile - 1);
+        await(&qk_done[u % C::kKeySlots], (u / C::kKeySlots) & 1, abort, L.err);
         await(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort, L.err);
       }
     }
@@ -653,7 +714,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     int tile = 0;
     for (;; ++tile) {
       const int buf = tile & 1;
-      const uint32_t s_at = tmem + lanes + buf * R + part * RH;
+      const uint32_t s_at = tmem + lanes + buf * 2 * R + part * RH;
       const bool ok = __all_sync(~0u, await(&s_ready[buf], (tile >> 1) & 1, abort, L.err));
       const int cnt = ok ? s_cnt[tile & 7] : 0;
       uint32_t p[RH], mask = 0;
@@ -662,15 +723,29 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       auto form = [&]() {
         const uint64_t kf2 = f2_pack(kf, kf);
         float over4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < RH; c += 16) tmem_ld(s_at + c, *reinterpret_cast<uint32_t (*)[16]>(p + c));
-        tmem_wait_ld();
+        const uint64_t sixteenth = f2_pack(0.0625f, 0.0625f);
+        uint32_t hi[2][8], lo[2][8];                   // eight rows, and the next eight on their way
+        tmem_ld(s_at, hi[0]);
+        tmem_ld(s_at + R, lo[0]);
 #pragma unroll
         for (int r = 0; r < RH; r += 4) {
+          if (r % 8 == 0) {
+            tmem_wait_for(hi[r / 8 & 1], lo[r / 8 & 1]);
+            if (r + 8 < RH) {
+              tmem_ld(s_at + r + 8, hi[(r / 8 + 1) & 1]);
+              tmem_ld(s_at + R + r + 8, lo[(r / 8 + 1) & 1]);
+            }
+          }
+          const uint32_t* h = hi[r / 8 & 1] + r % 8;
+          const uint32_t* l = lo[r / 8 & 1] + r % 8;
+          auto both = [&](int e) {                       // S of rows r + e, r + e + 1
+            return f2_fma(f2_pack(__uint_as_float(l[e]), __uint_as_float(l[e + 1])), sixteenth,
+                          f2_pack(__uint_as_float(h[e]), __uint_as_float(h[e + 1])));
+          };
           const float4 f = *reinterpret_cast<const float4*>(factor + r), m = *reinterpret_cast<const float4*>(minus + r);
           float d[4];
-          f2_unpack(f2_fma(f2_mul(f2_pack(__uint_as_float(p[r]), __uint_as_float(p[r + 1])), f2_pack(f.x, f.y)), kf2, f2_pack(m.x, m.y)), d[0], d[1]);
-          f2_unpack(f2_fma(f2_mul(f2_pack(__uint_as_float(p[r + 2]), __uint_as_float(p[r + 3])), f2_pack(f.z, f.w)), kf2, f2_pack(m.z, m.w)), d[2], d[3]);
+          f2_unpack(f2_fma(f2_mul(both(0), f2_pack(f.x, f.y)), kf2, f2_pack(m.x, m.y)), d[0], d[1]);
+          f2_unpack(f2_fma(f2_mul(both(2), f2_pack(f.z, f.w)), kf2, f2_pack(m.z, m.w)), d[2], d[3]);
           const uint32_t four = mask << (r / 4);
           p[r] = __float_as_uint(exp2_fast(d[0])) & spread<0>(four);
           p[r + 1] = __float_as_uint(exp2_fast(d[1])) & spread<1>(four);
@@ -707,13 +782,14 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
         const float ve = static_cast<float>(static_cast<int8_t>(ex >> 8));
 #pragma unroll 1
         for (int c = 0; c < RH; c += 8) {
-          uint32_t s[8];
+          uint32_t s[8], low[8];
           tmem_ld(s_at + c, s);
+          tmem_ld(s_at + R + c, low);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int r = c + i;
-            const float t = fmaf(__uint_as_float(s[i]) * factor[r], kf, ve);
+            const float t = fmaf(fmaf(__uint_as_float(low[i]), 0.0625f, __uint_as_float(s[i])) * factor[r], kf, ve);
             const int u = __float_as_int(t), order = u ^ (u >> 31 & 0x7fffffff);   // floats' order as integers
             const bool mine = mask >> ((r & 3) * 8 + 7 - r / 4) & 1 && t == t;
             const int m = __reduce_max_sync(~0u, mine ? order : INT_MIN);
