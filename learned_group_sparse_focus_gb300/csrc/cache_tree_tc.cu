@@ -67,7 +67,7 @@ struct Cfg {
                        kRaw = kQ + 2 * R * 128, kListAt = kRaw + kTile * D, kIds = kListAt + kList * 16, kTable = kIds + 2 * kScanWarps * kAhead * kPage * 2,
                        kSmem = kTable + kCacheTableGroups * 8 + 1024;   // + alignment
   static constexpr int kInbox = kP;                            // the partials', over P and Q, once the block's tiles are done
-  static_assert((R + kMaxCluster - 1) * D * 4 <= kRaw - kInbox && R / kSoftWarps * kSoftWarps * D * 2 <= kTile * D, "inbox does not fit");
+  static_assert((R + kMaxCluster - 1) * D * 4 <= kRaw - kInbox && R % (kSoftWarps + kGatherWarps) == 0 && R * D * 2 <= kTile * D, "inbox does not fit");
   static constexpr int kCols = 8 * R;                          // TMEM: S twice and O, in two parts each (6 R used)
 };
 
@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   __shared__ uint32_t s_nan[R][D / 32];                // outputs that a kept NaN value reaches
   __shared__ unsigned long long s_line[kMaxNodes];     // a node's line, later what it keeps of it
   __shared__ unsigned long long s_below[kMaxNodes + 1];   // rows of a depth, later those of a smaller one
+  __shared__ unsigned long long s_rows[kMaxNodes];     // a node's own rows of the block
   __shared__ int s_node[kMaxNodes];                    // group id of a node
   volatile int* abort = &s_abort_word;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc(&s_tmem, C::kCols);
-  if (warp == kGatherWarp) tree_lines(L.parent + static_cast<size_t>(b) * L.n, fresh, s_line, s_node, L.err);
+  if (warp == kGatherWarp - 1) tree_lines(L.parent + static_cast<size_t>(b) * L.n, fresh, s_line, s_node, L.err);
 #pragma unroll 1
   for (int i = threadIdx.x; i < kCacheTableGroups; i += kThreads) table[i] = 0;
 #pragma unroll 1
@@ -259,21 +260,24 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   if (threadIdx.x <= kMaxNodes) s_below[threadIdx.x] = 0;
   const bool has_own = rank == cs - 1;                 // the block that takes the tree's own keys
   const size_t own_row = (static_cast<size_t>(b) * L.H_kv + h) * L.n;
-  if (has_own && warp > kGatherWarp && warp < kMmaWarp)        // whose rows are on their way from here on
+  if (has_own && warp >= kGatherWarp && warp < kMmaWarp)       // whose rows are on their way from here on
 #pragma unroll 1
-    for (int i = threadIdx.x - (kGatherWarp + 1) * 32; i < fresh * D / 64; i += (kGatherWarps - 1) * 32) {
+    for (int i = threadIdx.x - kGatherWarp * 32; i < fresh * D / 64; i += kGatherWarps * 32) {
       asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __nv_bfloat16*>(L.K) + own_row * D + i * 64));
       asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __nv_bfloat16*>(L.V) + own_row * D + i * 64));
     }
   int node_gid = 0;
   if (threadIdx.x < fresh) node_gid = gids[threadIdx.x];
-  // queries: f16 by a power of two a row, a warp a row; they come through the codes' space
-  if (warp < kSoftWarps) {
+  // queries: two e4m3 parts, a warp a row, by the warps that have nothing to do yet; they come through the
+  // values' space
+  constexpr int kQueryWarps = kSoftWarps + kGatherWarps;
+  if (warp < kSoftWarps || (warp >= kGatherWarp && warp < kMmaWarp)) {
     constexpr int kEach = D / 32, kCopies = D / 8;     // elements a lane; 16-byte pieces of a row
-    uint8_t* const raw = smem + C::kRaw + warp * (R / kSoftWarps) * D * 2;
+    const int w = warp < kSoftWarps ? warp : warp - kScanWarps;
+    uint8_t* const raw = smem + C::kRaw + w * (R / kQueryWarps) * D * 2;
 #pragma unroll 1
-    for (int i = lane; i < R / kSoftWarps * kCopies; i += 32) {
-      const int r = warp + i / kCopies * kSoftWarps, g = (r0 + r) % G, t = (r0 + r) / G;
+    for (int i = lane; i < R / kQueryWarps * kCopies; i += 32) {
+      const int r = w + i / kCopies * kQueryWarps, g = (r0 + r) % G, t = (r0 + r) / G;
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(L.Q);
       if (r < live) src += ((static_cast<size_t>(b) * L.H + h * G + g) * L.n + t) * D + i % kCopies * 8;
       cp_async_16(raw + i * 16, src, r < live ? 16 : 0);
@@ -281,8 +285,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     cp_async_wait_all();
     __syncwarp();
 #pragma unroll 1
-    for (int i = 0; i < R / kSoftWarps; ++i) {
-      const int r = warp + i * kSoftWarps;
+    for (int i = 0; i < R / kQueryWarps; ++i) {
+      const int r = w + i * kQueryWarps;
       float q[kEach];
 #pragma unroll
       for (int e = 0; e < kEach; e += 2) {
@@ -345,12 +349,15 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       s_line[threadIdx.x] = keeps;
     }
     // its rows of the block, by group and by depth
+    unsigned long long own_rows = 0;
 #pragma unroll 1
     for (int r = max(static_cast<int>(threadIdx.x) * G - r0, 0); r < min((static_cast<int>(threadIdx.x) + 1) * G - r0, live); ++r) {
       const uint32_t bit = static_cast<uint32_t>(row_bit(r) >> (r & 32));
+      own_rows |= row_bit(r);
       if (node_gid >= 0 && node_gid < kCacheTableGroups) atomicOr(reinterpret_cast<uint32_t*>(&table[node_gid]) + (r >> 5), bit);
       atomicOr(reinterpret_cast<uint32_t*>(&s_below[depth]) + (r >> 5), bit);
     }
+    s_rows[threadIdx.x] = own_rows;
   }
   __syncthreads();
   if (warp == 0) {                                     // sums of depths below: lane i has 2 i and 2 i + 1
@@ -387,11 +394,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
 #pragma unroll 1
         for (int j = lane; j < fresh; j += 32) {
           unsigned long long rows_of = 0;              // that keep node j
-#pragma unroll 1
-          for (int t = r0 / G; t * G < r0 + live; ++t)
-            if (s_line[t] >> j & 1)
-#pragma unroll 1
-              for (int r = max(t * G - r0, 0); r < min((t + 1) * G - r0, live); ++r) rows_of |= row_bit(r);
+#pragma unroll 4
+          for (int t = r0 / G; t <= (r0 + live - 1) / G; ++t) rows_of |= s_line[t] >> j & 1 ? s_rows[t] : 0ull;
           list[j] = make_int4(j, 0, static_cast<int>(rows_of), static_cast<int>(rows_of >> 32));   // exponents: by the gathering warp
         }
     }
@@ -522,6 +526,13 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
 #pragma unroll 1
       for (int y = 0; y < kLoads; ++y) {
         const int r = row_at(y);
+        if ((y * kGatherWarps + gw) * kRowsAtOnce >= fresh) {          // none of the warp's: zeros
+          const uint32_t none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+          put(smem + C::kV, r, none);
+          uint8_t* to = smem + C::kK + r * 128 + (piece ^ (r & 7)) * 16;
+          *reinterpret_cast<uint4*>(to) = *reinterpret_cast<uint4*>(to + C::kKeyBytes) = make_uint4(0, 0, 0, 0);
+          continue;
+        }
         uint4 u[2][2] = {};
         if (r < fresh)
 #pragma unroll
