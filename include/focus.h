@@ -578,8 +578,8 @@ FOCUS_API focus_status_t focus_rotary(const focus_params_t* p, const focus_rotar
  *   rot may be NULL (nothing turns; Q and Q_out NULL); Q with Q_out, and K_out, may be
  *   NULL; Q_out may be Q and K_out K, no other overlap;
  *   rows [B, n] int32 or NULL: token t is row rows[b][t] of K, V and gid (a tree's
- *   accepted path; each row at most once; needs Q and K_out NULL); rows behind
- *   n_new[b] are not read, a row outside [0, n) is flagged as FOCUS_ERR_BAD_TREE (clamped).
+ *   accepted path; needs Q and K_out NULL); rows behind n_new[b] are not read, a row
+ *   outside [0, n) is flagged as FOCUS_ERR_BAD_TREE (clamped).
  * The rest as focus_cache_append; Q_out and K_out rows of a sequence that does not fit,
  * and those behind n_new[b], stay as they were.  ws: of focus_cache_workspace_bytes. */
 FOCUS_API focus_status_t focus_cache_append_rotary(const focus_params_t* p, const focus_rotary_t* rot,
@@ -617,9 +617,11 @@ FOCUS_API size_t focus_tree_workspace_bytes(const focus_params_t* p);
  *   gid [B, A, n], parent [B, n] int32; n_new [B] int32 or NULL: nodes of a sequence; rows
  *   behind them of O and lse_opt stay as they were;
  *   lse_opt [B, H, n] fp32 or NULL.
- * O overlaps no input.  Precision, logits and NaN codes as focus_cache_attention_fwd; a
+ * O overlaps no input.  A sequence whose next + n_new would pass 2^31 - 1 is flagged as
+ * FOCUS_ERR_BAD_CACHE, as are bad counts and pages (clamped, left out).  Precision, logits and NaN codes as focus_cache_attention_fwd; a
  * drafted key or value row with an infinite or NaN element gives NaN to the nodes that keep
- * it and to no others; drafted values below 2^-73 count as 0.  To gather mass for an
+ * it and to no others; drafted keys' elements below 2^-11 of their row's largest are held to
+ * 2^-19 of that, drafted values below 2^-73 count as 0.  To gather mass for an
  * eviction, attend the accepted tokens with focus_cache_attention_fwd once they are
  * appended.  ws: of focus_tree_workspace_bytes. */
 FOCUS_API focus_status_t focus_cache_attention_tree_fwd(const focus_params_t* p, const void* Q,

@@ -28,6 +28,15 @@ __device__ __forceinline__ int cache_page(const focus_cache_t& c, int b, int j, 
   return -1;
 }
 
+// Position behind the last cached token of sequence b, with m more positions from there on
+// inside 32 bits (a bad one raises the flag).
+__device__ __forceinline__ int cache_next(const focus_cache_t& c, int m, int b, int* err) {
+  const int next = c.next[b], last = 0x7fffffff - m;
+  if (next >= 0 && next <= last) return next;
+  atomicOr(err, kErrBadCache);
+  return next < 0 ? 0 : last;
+}
+
 // New tokens of sequence b: n_new[b] inside [0, n] (n without the array).
 __device__ __forceinline__ int cache_new(const int32_t* n_new, int n, int b, int* err) {
   if (!n_new) return n;

@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
       n = cache_len(L.c, L.H_kv, b, h, L.err);
       fresh = cache_new(L.n_new, L.n, b, L.err);
       // position of token 0; of a node at depth 0, which lies behind every cached slot
-      pos0 = L.c.next[b] - (kTree ? 0 : fresh);
+      pos0 = kTree ? cache_next(L.c, fresh, b, L.err) : L.c.next[b] - fresh;
       rows = G * fresh;
       const int pages = (n + kPage - 1) / kPage;
       near_from = n - static_cast<int>(min(static_cast<long long>(n), static_cast<long long>(L.w) + (kTree ? 0 : fresh)));

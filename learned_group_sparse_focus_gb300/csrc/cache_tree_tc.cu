@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   if (r0 >= rows) return;                              // the same in the whole cluster
   const int live = min(R, rows - r0);
   const int n = cache_len(L.c, L.H_kv, b, h, L.err);
-  const int next = L.c.next[b];                        // position of a node at depth 0
+  const int next = cache_next(L.c, fresh, b, L.err);   // position of a node at depth 0
   const int pages = (n + kPage - 1) / kPage;
   const int near_from = n - min(n, L.w);               // slots are in ascending position, before `next`
   const int32_t* gids = L.gid + (static_cast<size_t>(b) * L.A + (L.A == 1 ? 0 : h)) * L.n;
