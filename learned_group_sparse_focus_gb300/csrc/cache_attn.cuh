@@ -217,12 +217,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) cache_attn_kernel(C
       __syncthreads();
       unsigned long long line = 0, keeps = 0;
       if (threadIdx.x < kMaxNodes) {
-        line = s_line[threadIdx.x];
-        const int g = s_node_gid[threadIdx.x];
-        int up = 0;                                    // from the root down: j is `depth - up` steps above
-        for (unsigned long long left = line; left; left &= left - 1, ++up) {
-          const int j = __ffsll(left) - 1;
-          if (__popcll(line) - 1 - up < L.w || s_node_gid[j] == g) keeps |= 1ull << j;
+        keeps = line = s_line[threadIdx.x];
+        const int g = s_node_gid[threadIdx.x], depth = __popcll(line) - 1;
+        if (depth >= L.w) {                            // ancestors before the window: of its group only
+          keeps = 0;
+          int up = 0;                                  // from the root down: j is `depth - up` steps above
+          for (unsigned long long left = line; left; left &= left - 1, ++up) {
+            const int j = __ffsll(left) - 1;
+            if (depth - up < L.w || s_node_gid[j] == g) keeps |= 1ull << j;
+          }
         }
       }
       __syncthreads();
@@ -840,7 +843,10 @@ cudaError_t launch(const CacheAttnLaunch& L, cudaStream_t st) {
     return e;
   const long long heads = static_cast<long long>(L.B) * L.H_kv;
   int cs = 1, i = 0;
-  while (cs < kMaxCluster && cs * kWarps < L.c.max_pages) {
+  // What a warp can take alone: a page, or where a window may lie a quarter of one (a tree keeps more of
+  // such pages than a token does).
+  const int units = L.c.max_pages + (kTree ? 3 * min(L.c.max_pages, L.w / kPage + 1) : 0);
+  while (cs < kMaxCluster && cs * kWarps < units) {
     const int runs = fit->n[i + 1];
     const long long worth = static_cast<long long>(2 * cs * kWarps) * (L.accumulate ? 4 : 8);   // pages, for one wave
     const bool pays = heads * worth <= static_cast<long long>(L.c.max_pages) * runs;
