@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   __shared__ unsigned long long s_line[kMaxNodes];     // a node's line, later what it keeps of it
   __shared__ unsigned long long s_below[kMaxNodes + 1];   // rows of a depth, later those of a smaller one
   __shared__ unsigned long long s_rows[kMaxNodes];     // a node's own rows of the block
-  __shared__ int s_node[kMaxNodes];                    // group id of a node
+  __shared__ int s_node[kMaxNodes], s_order[kMaxNodes];   // group id of a node; nodes by group id
   volatile int* abort = &s_abort_word;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   int4* list = reinterpret_cast<int4*>(smem + C::kListAt);
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc(&s_tmem, C::kCols);
-  if (warp == kGatherWarp - 1) tree_lines(L.parent + static_cast<size_t>(b) * L.n, fresh, s_line, s_node, L.err);
+  if (warp == kGatherWarp - 1) tree_lines(L.parent + static_cast<size_t>(b) * L.n, fresh, s_line, s_order, L.err);
 #pragma unroll 1
   for (int i = threadIdx.x; i < kCacheTableGroups; i += kThreads) table[i] = 0;
 #pragma unroll 1
@@ -267,19 +267,27 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __nv_bfloat16*>(L.V) + own_row * D + i * 64));
     }
   int node_gid = 0;
-  if (threadIdx.x < fresh) node_gid = gids[threadIdx.x];
+  if (threadIdx.x < kMaxNodes) {
+    if (threadIdx.x < fresh) node_gid = gids[threadIdx.x];
+    s_node[threadIdx.x] = node_gid;
+  }
+  // Rows are nodes (times query heads) in order, or, where they are more than a block's, by group id: a block then keeps
+  // few groups' slots (64 nodes in 64 groups of very different sizes: 0.9 of the slots over four blocks of 16
+  // nodes, against 2.3).
+  const bool sorted = rows > R;
+  auto node_of = [&](int i) { return sorted ? s_order[i] : i; };
   // queries: two e4m3 parts, a warp a row, by the warps that have nothing to do yet; they come through the
   // values' space
   constexpr int kQueryWarps = kSoftWarps + kGatherWarps;
-  if (warp < kSoftWarps || (warp >= kGatherWarp && warp < kMmaWarp)) {
+  auto queries = [&]() {
     constexpr int kEach = D / 32, kCopies = D / 8;     // elements a lane; 16-byte pieces of a row
     const int w = warp < kSoftWarps ? warp : warp - kScanWarps;
     uint8_t* const raw = smem + C::kRaw + w * (R / kQueryWarps) * D * 2;
 #pragma unroll 1
     for (int i = lane; i < R / kQueryWarps * kCopies; i += 32) {
-      const int r = w + i / kCopies * kQueryWarps, g = (r0 + r) % G, t = (r0 + r) / G;
+      const int r = w + i / kCopies * kQueryWarps, g = (r0 + r) % G;
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(L.Q);
-      if (r < live) src += ((static_cast<size_t>(b) * L.H + h * G + g) * L.n + t) * D + i % kCopies * 8;
+      if (r < live) src += ((static_cast<size_t>(b) * L.H + h * G + g) * L.n + node_of((r0 + r) / G)) * D + i % kCopies * 8;
       cp_async_16(raw + i * 16, src, r < live ? 16 : 0);
     }
     cp_async_wait_all();
@@ -328,52 +336,66 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       }
     }
     fence_proxy_async_smem();
-  }
-  __syncthreads();
-  unsigned long long line = 0;
-  if (threadIdx.x < kMaxNodes) {                       // a thread a node
-    line = s_line[threadIdx.x];
-    s_node[threadIdx.x] = node_gid;
-  }
-  __syncthreads();
-  if (threadIdx.x < fresh) {
-    const int depth = __popcll(line) - 1;
-    if (depth >= L.w) {                                // ancestors before the window: of its group only
-      unsigned long long keeps = 0;
-      int up = 0;                                      // from the root down: j is `depth - up` steps above
+  };
 #pragma unroll 1
-      for (unsigned long long left = line; left; left &= left - 1, ++up) {
-        const int j = __ffsll(left) - 1;
-        if (depth - up < L.w || s_node[j] == node_gid) keeps |= 1ull << j;
+  for (int phase = 0; phase < 2; ++phase) {
+    if (phase == (sorted ? 1 : 0) && (warp < kSoftWarps || (warp >= kGatherWarp && warp < kMmaWarp))) queries();
+    if (phase == 1) break;
+    __syncthreads();
+    unsigned long long line = 0;
+    int place = threadIdx.x;                           // of the thread's node among the rows
+    if (threadIdx.x < fresh) {                         // a thread a node
+      line = s_line[threadIdx.x];
+      if (sorted) {
+        place = 0;
+#pragma unroll 4
+        for (int j = 0; j < fresh; ++j) {
+          const int g = s_node[j];
+          place += g < node_gid || (g == node_gid && j < static_cast<int>(threadIdx.x));
+        }
+        s_order[place] = threadIdx.x;
       }
-      s_line[threadIdx.x] = keeps;
     }
-    // its rows of the block, by group and by depth
-    unsigned long long own_rows = 0;
+    __syncthreads();
+    if (threadIdx.x < fresh) {
+      const int depth = __popcll(line) - 1;
+      if (depth >= L.w) {                              // ancestors before the window: of its group only
+        unsigned long long keeps = 0;
+        int up = 0;                                    // from the root down: j is `depth - up` steps above
 #pragma unroll 1
-    for (int r = max(static_cast<int>(threadIdx.x) * G - r0, 0); r < min((static_cast<int>(threadIdx.x) + 1) * G - r0, live); ++r) {
-      const uint32_t bit = static_cast<uint32_t>(row_bit(r) >> (r & 32));
-      own_rows |= row_bit(r);
-      if (node_gid >= 0 && node_gid < kCacheTableGroups) atomicOr(reinterpret_cast<uint32_t*>(&table[node_gid]) + (r >> 5), bit);
-      atomicOr(reinterpret_cast<uint32_t*>(&s_below[depth]) + (r >> 5), bit);
+        for (unsigned long long left = line; left; left &= left - 1, ++up) {
+          const int j = __ffsll(left) - 1;
+          if (depth - up < L.w || s_node[j] == node_gid) keeps |= 1ull << j;
+        }
+        s_line[threadIdx.x] = keeps;
+      }
+      // its rows of the block, by group and by depth
+      unsigned long long own_rows = 0;
+#pragma unroll 1
+      for (int r = max(place * G - r0, 0); r < min((place + 1) * G - r0, live); ++r) {
+        const uint32_t bit = static_cast<uint32_t>(row_bit(r) >> (r & 32));
+        own_rows |= row_bit(r);
+        if (node_gid >= 0 && node_gid < kCacheTableGroups) atomicOr(reinterpret_cast<uint32_t*>(&table[node_gid]) + (r >> 5), bit);
+        atomicOr(reinterpret_cast<uint32_t*>(&s_below[depth]) + (r >> 5), bit);
+      }
+      s_rows[threadIdx.x] = own_rows;
     }
-    s_rows[threadIdx.x] = own_rows;
-  }
-  __syncthreads();
-  if (warp == 0) {                                     // sums of depths below: lane i has 2 i and 2 i + 1
-    const unsigned long long first = s_below[2 * lane], both = first | s_below[2 * lane + 1];
-    unsigned long long upto = both;
+    __syncthreads();
+    if (warp == 0) {                                   // sums of depths below: lane i has 2 i and 2 i + 1
+      const unsigned long long first = s_below[2 * lane], both = first | s_below[2 * lane + 1];
+      unsigned long long upto = both;
 #pragma unroll
-    for (int y = 1; y < 32; y *= 2) {
-      const unsigned long long u = __shfl_up_sync(~0u, upto, y);
-      if (lane >= y) upto |= u;
+      for (int y = 1; y < 32; y *= 2) {
+        const unsigned long long u = __shfl_up_sync(~0u, upto, y);
+        if (lane >= y) upto |= u;
+      }
+      unsigned long long below = __shfl_up_sync(~0u, upto, 1);
+      if (lane == 0) below = 0;
+      __syncwarp();
+      s_below[2 * lane] = below;
+      s_below[2 * lane + 1] = below | first;
+      if (lane == 31) s_below[kMaxNodes] = upto;
     }
-    unsigned long long below = __shfl_up_sync(~0u, upto, 1);
-    if (lane == 0) below = 0;
-    __syncwarp();
-    s_below[2 * lane] = below;
-    s_below[2 * lane + 1] = below | first;
-    if (lane == 31) s_below[kMaxNodes] = upto;
   }
   tc_fence_before();
   __syncthreads();
@@ -395,7 +417,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
         for (int j = lane; j < fresh; j += 32) {
           unsigned long long rows_of = 0;              // that keep node j
 #pragma unroll 4
-          for (int t = r0 / G; t <= (r0 + live - 1) / G; ++t) rows_of |= s_line[t] >> j & 1 ? s_rows[t] : 0ull;
+          for (int i = r0 / G; i <= (r0 + live - 1) / G; ++i) {
+            const int t = node_of(i);
+            rows_of |= s_line[t] >> j & 1 ? s_rows[t] : 0ull;
+          }
           list[j] = make_int4(j, 0, static_cast<int>(rows_of), static_cast<int>(rows_of >> 32));   // exponents: by the gathering warp
         }
     }
@@ -956,7 +981,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     for (int x = 0; x < cs; ++x)
       s_weight[x][r] = s_all[x][r].y != 0.f ? exp2f(s_all[x][r].x - M) / l * exp2_int(kLift) : 0.f;
     if (rank == 0 && L.lse && r < live)
-      L.lse[(static_cast<size_t>(b) * L.H + h * G + (r0 + r) % G) * L.n + (r0 + r) / G] =
+      L.lse[(static_cast<size_t>(b) * L.H + h * G + (r0 + r) % G) * L.n + node_of((r0 + r) / G)] =
           l != 0.f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
   __syncthreads();
@@ -973,7 +998,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       a.x += u.x * f; a.y += u.y * f; a.z += u.z * f; a.w += u.w * f;
     }
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(L.O) +
-                              ((static_cast<size_t>(b) * L.H + h * G + (r0 + r) % G) * L.n + (r0 + r) / G) * D + d) =
+                              ((static_cast<size_t>(b) * L.H + h * G + (r0 + r) % G) * L.n + node_of((r0 + r) / G)) * D + d) =
         make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
   }
   tc_fence_before();
