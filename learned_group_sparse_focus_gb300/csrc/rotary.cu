@@ -15,10 +15,10 @@
 namespace focus {
 namespace {
 
-constexpr int kHalf = kRotThreads / 2;      // of a page's block the first half moves K, the second V
-// Of |y| + |z|, for the fp32 value of a turned pair (y, z): what sine and cosine are off by (2^-22.7: the
-// angle's roundings and the polynomial's), two roundings of 2^-25, and sqrt(2) for the sizes of the pair before.
-constexpr float kUnsure = 0x1.8p-22f;
+// Of |y| + |z|, for the fp32 value of a turned pair (y, z), in units of 2^-24: (cosine, sine) of an angle are off
+// by 2.1 (all phases, against 64 bits), of a sum of two angles by twice that and 1.5 for its roundings; scale and
+// the turn itself round by 1 each.  Together 7.7.
+constexpr float kUnsure = 0x1p-21f;
 
 // ------------------------------------------------------------- rotation ---
 
@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryLaunch L) {
     }
     __syncthreads();
   }
-  rotate_rows<T, D, kInterleaved, 128>(L, b, t0, blockIdx.y * L.heads, m, L.base ? L.base[b] : 0, L.parent ? s_up : nullptr, s_turn);
+  rotate_rows<T, D, kInterleaved>(L, b, t0, blockIdx.y * L.heads, m, L.base ? L.base[b] : 0, L.parent ? s_up : nullptr, s_turn);
 }
 
 // --------------------------------------------------------------- append ---
@@ -86,24 +86,99 @@ __device__ __forceinline__ uint32_t code_of(double y) {
 // pieces that lie a thread apart.  K's are turned in place (fp32), V's stay as they are.
 template <typename T, int D>
 struct PageRows {
-  static constexpr int kDuos = D / 16, kRowsAtOnce = kHalf / kDuos, kSteps = kPage / kRowsAtOnce;
+  static constexpr int kDuos = D / 16, kRowsAtOnce = kRotThreads / kDuos, kSteps = kPage / kRowsAtOnce;
   static constexpr int kRaw = sizeof(T);                 // 16-byte pieces of a duo as it comes: 2 or 4
-  static constexpr int kStep = kHalf * 16;               // bytes of one piece of every thread
-  static constexpr int kBytes = kSteps * (4 + kRaw) * kStep;
+  static constexpr int kStep = kRotThreads * 16;         // bytes of one piece of every thread
+  // Query rows wait there as well, each piece for the thread that copied it: 128 bytes of a thread on their way.
+  static constexpr int kQueue = 8 / kRaw;                // rows
+  static constexpr int kBytes = (kSteps * (4 + kRaw) > 8 ? kSteps * (4 + kRaw) : 8) * kStep;
 };
 
-// One page of one head: as cache_append_kernel, with a thread on duos.
+// Eight floats of a piece of a row as it came: a thread's 16-byte pieces, kStep apart.
+template <int kStep>
+__device__ __forceinline__ void read8(const uint8_t* at, float* y, float) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float4 f = *reinterpret_cast<const float4*>(at + e * kStep);
+    y[4 * e] = f.x; y[4 * e + 1] = f.y; y[4 * e + 2] = f.z; y[4 * e + 3] = f.w;
+  }
+}
+template <int kStep>
+__device__ __forceinline__ void read8(const uint8_t* at, float* y, __nv_bfloat16) {
+  const uint4 u = *reinterpret_cast<const uint4*>(at);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    y[2 * x] = __uint_as_float((&u.x)[x] << 16);
+    y[2 * x + 1] = __uint_as_float((&u.x)[x] & 0xffff0000u);
+  }
+}
+
+// Query rows of `tokens` tokens from t0 on and `heads` heads from head0 on.  Rows are fetched through shared
+// memory: in registers, what is on its way would cost the blocks of pages their fourth block an SM.
+template <typename T, int D, bool kInterleaved>
+__device__ __forceinline__ void rotate_queries(const RotaryLaunch& L, int b, int t0, int head0, int valid, int next,
+                                               unsigned long long* s_turn, uint8_t* smem) {
+  using C = PageRows<T, D>;
+  constexpr int kSlots = kRotThreads / C::kDuos, kEach = 16 / static_cast<int>(sizeof(T));
+  const int k = threadIdx.x % C::kDuos, slot = threadIdx.x / C::kDuos;
+  const int t = t0 + slot % L.tokens, across = kSlots / L.tokens;
+  const Duo duo(k, L.dim, kInterleaved);
+  const int g = head0 + slot / L.tokens, end = min(head0 + L.heads, L.Hq);
+  const int rows = t < valid && g < end ? (end - g + across - 1) / across : 0;
+  const size_t head = static_cast<size_t>(L.n) * D, at = (static_cast<size_t>(b) * L.Hq + g) * head + static_cast<size_t>(t) * D;
+  const T* src = static_cast<const T*>(L.Q) + at;
+  T* dst = static_cast<T*>(L.Q_out) + at;
+  uint8_t* const mine = smem + threadIdx.x * 16;
+  auto fetch = [&](int i) {
+    if (i < rows) {
+      const T* row = src + i * across * head;
+      uint8_t* to = mine + i % C::kQueue * C::kRaw * C::kStep;
+#pragma unroll
+      for (int e = 0; e < C::kRaw; ++e)
+        cp_async_16(to + e * C::kStep, row + duo.at[e / (C::kRaw / 2)] + e % (C::kRaw / 2) * kEach, 16);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < C::kQueue; ++i) fetch(i);
+  fill_turns<C::kDuos>(L, s_turn);
+  __syncthreads();
+  uint64_t c[4], s[4];
+  if (duo.turns && rows > 0) duo_cos_sin<C::kDuos>(static_cast<uint32_t>(next) + t, s_turn + k, L.scale, L.scale, c, s);
+#pragma unroll 1
+  for (int i = 0; i < rows; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(C::kQueue - 1) : "memory");
+    const uint8_t* from = mine + i % C::kQueue * C::kRaw * C::kStep;
+    T* to = dst + i * across * head;
+    if (duo.turns) {
+      float y[16];
+      read8<C::kStep>(from, y, T{});
+      read8<C::kStep>(from + C::kRaw / 2 * C::kStep, y + 8, T{});
+      turn_pairs<kInterleaved>(y, c, s);
+      store8(to + duo.at[0], y);
+      store8(to + duo.at[1], y + 8);
+    } else if (L.Q != L.Q_out) {                         // as they are, to the last bit
+#pragma unroll
+      for (int e = 0; e < C::kRaw; ++e)
+        *reinterpret_cast<uint4*>(to + duo.at[0] + e * kEach) = *reinterpret_cast<const uint4*>(from + e * C::kStep);
+    }
+    fetch(i + C::kQueue);
+  }
+  cp_async_wait_all();
+}
+
+// One page of one head: as cache_append_kernel, with a thread on duos of K and of V.
 template <typename T, int D, bool kInterleaved>
 __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, int b, int h, int j, int n0, int m,
-                                            unsigned long long* s_turn, uint2* s_max, int* s_more, uint8_t* smem) {
+                                            unsigned long long* s_turn, float4* s_step, uint32_t (*s_max)[3], int* s_more,
+                                            uint8_t* smem) {
   using C = PageRows<T, D>;
   const CacheAppendLaunch& A = L.a;
   const RotaryLaunch& R = L.rot;
-  const int half = threadIdx.x / kHalf, ht = threadIdx.x % kHalf;
   const int lo = max(n0, j * kPage), hi = min(n0 + m, (j + 1) * kPage);
   const int r0 = lo - j * kPage, rows = hi - lo, t0 = lo - n0;
-  const int k = ht % C::kDuos, row0 = ht / C::kDuos;
-  const Duo duo(k, half ? 0 : R.dim, kInterleaved);
+  const int k = threadIdx.x % C::kDuos, row0 = threadIdx.x / C::kDuos;
+  const Duo duo(k, R.dim, kInterleaved);
   const int next = A.c.next[b];
   // the source row of a token
   auto source = [&](int t) {
@@ -113,64 +188,51 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
     atomicOr(A.err, kErrBadTree);
     return r < 0 ? 0 : A.n - 1;
   };
-  const T* src = static_cast<const T*>(half ? A.V : A.K) + (static_cast<size_t>(b) * A.H_kv + h) * A.n * D;
-  uint8_t* const mine = smem + (half ? C::kSteps * 4 * C::kStep : 0) + ht * 16;
-  const int apart = (half ? C::kRaw : 4) * C::kStep;     // from a row step to the next
+  const size_t head = (static_cast<size_t>(b) * A.H_kv + h) * A.n * D;
+  const T* const src = static_cast<const T*>(A.K) + head;
+  uint8_t* const mine = smem + threadIdx.x * 16;
+  uint8_t* const mine_v = mine + C::kSteps * 4 * C::kStep;
   const int steps = row0 < rows ? (rows - row0 + C::kRowsAtOnce - 1) / C::kRowsAtOnce : 0;
-#pragma unroll 1
-  for (int i = 0; i < steps; ++i) {
+  constexpr int kEach = 16 / static_cast<int>(sizeof(T));
+#pragma unroll
+  for (int i = 0; i < C::kSteps; ++i) {
+    if (i >= steps) break;
     const T* row = src + static_cast<size_t>(source(t0 + row0 + i * C::kRowsAtOnce)) * D;
 #pragma unroll
     for (int e = 0; e < C::kRaw; ++e)
-      cp_async_16(mine + i * apart + e * C::kStep, row + duo.at[e / (C::kRaw / 2)] + e % (C::kRaw / 2) * (16 / static_cast<int>(sizeof(T))), 16);
+      cp_async_16(mine + (i * 4 + e) * C::kStep, row + duo.at[e / (C::kRaw / 2)] + e % (C::kRaw / 2) * kEach, 16);
   }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < C::kSteps; ++i) {
+    if (i >= steps) break;
+    const T* row = static_cast<const T*>(A.V) + head + static_cast<size_t>(source(t0 + row0 + i * C::kRowsAtOnce)) * D + k * 16;
+#pragma unroll
+    for (int e = 0; e < C::kRaw; ++e) cp_async_16(mine_v + (i * C::kRaw + e) * C::kStep, row + e * kEach, 16);
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
   const int page = cache_page(A.c, b, j, A.err);
   const size_t plane = static_cast<size_t>(max(page, 0)) * A.H_kv + h;
-  float* scale = (half ? A.c.v_scale : A.c.k_scale) + plane;
-  const int e_old = r0 > 0 && page >= 0 ? scale_exp(*scale) : kMinExp;
+  const bool shared = r0 > 0 && page >= 0;               // the page has older rows
+  const int old_k = shared ? scale_exp(A.c.k_scale[plane]) : kMinExp, old_v = shared ? scale_exp(A.c.v_scale[plane]) : kMinExp;
   fill_turns<C::kDuos>(R, s_turn);
-  if (threadIdx.x == 0) *s_more = 0;
-  cp_async_wait_all();
-  __syncthreads();
-  // A duo of a row step as floats, as it came and as it was turned.
-  auto floats = [&](int i, float (&y)[16]) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float4 f = *reinterpret_cast<const float4*>(mine + i * apart + e * C::kStep);
-      y[4 * e] = f.x; y[4 * e + 1] = f.y; y[4 * e + 2] = f.z; y[4 * e + 3] = f.w;
-    }
-  };
-  auto read = [&](int i, float (&y)[16]) {
-    if constexpr (sizeof(T) == 4) {
-      floats(i, y);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint4 u = *reinterpret_cast<const uint4*>(mine + i * apart + e * C::kStep);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          y[8 * e + 2 * x] = __uint_as_float((&u.x)[x] << 16);
-          y[8 * e + 2 * x + 1] = __uint_as_float((&u.x)[x] & 0xffff0000u);
-        }
-      }
-    }
-  };
-  // Turned rows, and the largest finite magnitude.
-  float top = 0.f;
+  if (rows > C::kRowsAtOnce)                             // cosines and sines of the row steps
 #pragma unroll 1
-  for (int i = 0; i < steps; ++i) {
-    float y[16];
-    read(i, y);
-    if (!half) {
-      if (duo.turns) {
-        uint64_t c[4], s[4];
-        duo_cos_sin<C::kDuos>(static_cast<uint32_t>(next) + (t0 + row0 + i * C::kRowsAtOnce), s_turn + k, R.scale, R.scale, c, s);
-        turn_pairs<kInterleaved>(y, c, s);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<float4*>(mine + i * apart + e * C::kStep) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+    for (int x = threadIdx.x; x < (C::kSteps - 1) * D / 2; x += kRotThreads) {
+      const int f = x % (D / 2), i = x / (D / 2);
+      if (f >= R.dim / 2) continue;
+      float* at = reinterpret_cast<float*>(s_step + (i * 4 + f % 8 / 4) * C::kDuos + f / 8) + f % 4;
+      cos_sin((i + 1) * C::kRowsAtOnce, turn_of(R.inv_freq[f]), *at, at[2 * C::kDuos * 4]);
     }
+  if (threadIdx.x == 0) *s_more = 0;
+  __syncthreads();
+  uint64_t c0[4], s0[4];                                 // of the thread's first row
+  if (duo.turns && steps > 0) duo_cos_sin<C::kDuos>(static_cast<uint32_t>(next) + (t0 + row0), s_turn + k, R.scale, R.scale, c0, s0);
+  auto read = [&](const uint8_t* at, float (&y)[16]) {   // a duo as it came
+    read8<C::kStep>(at, y, T{});
+    read8<C::kStep>(at + C::kRaw / 2 * C::kStep, y + 8, T{});
+  };
+  auto finite_top = [&](const float (&y)[16]) {          // largest finite magnitude
     float a = 0.f, b = 0.f;                              // (fmaxf leaves NaN out)
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
@@ -183,20 +245,70 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
 #pragma unroll
       for (int e = 0; e < 16; ++e) a = fmaxf(a, fabsf(y[e]) < INFINITY ? fabsf(y[e]) : 0.f);
     }
-    top = fmaxf(top, a);
+    return a;
+  };
+  // Turned rows of K, and the largest magnitudes of K and of V.
+  float top_k = 0.f, top_v = 0.f;
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll 1
+  for (int i = 0; i < steps; ++i) {
+    float y[16];
+    uint8_t* const at = mine + i * 4 * C::kStep;
+    read(at, y);
+    if (duo.turns) {
+      uint64_t c[4], s[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c[e] = c0[e];
+        s[e] = s0[e];
+      }
+      if (i > 0) {                                       // the sum of two angles
+        const uint64_t minus = f2_pack(-1.f, -1.f);
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const float4 u = s_step[((i - 1) * 4 + e / 2) * C::kDuos + k], v = s_step[((i - 1) * 4 + 2 + e / 2) * C::kDuos + k];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint64_t cd = x ? f2_pack(u.z, u.w) : f2_pack(u.x, u.y), sd = x ? f2_pack(v.z, v.w) : f2_pack(v.x, v.y);
+            c[e + x] = f2_fma(f2_mul(s0[e + x], minus), sd, f2_mul(c0[e + x], cd));
+            s[e + x] = f2_fma(s0[e + x], cd, f2_mul(c0[e + x], sd));
+          }
+        }
+      }
+      turn_pairs<kInterleaved>(y, c, s);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *reinterpret_cast<float4*>(at + e * C::kStep) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+    top_k = fmaxf(top_k, finite_top(y));
+  }
+  cp_async_wait_all();
+#pragma unroll 1
+  for (int i = 0; i < steps; ++i) {
+    float y[16];
+    read(mine_v + i * C::kRaw * C::kStep, y);
+    top_v = fmaxf(top_v, finite_top(y));
   }
   {
-    const uint32_t fixed = __reduce_max_sync(~0u, duo.turns ? 0u : __float_as_uint(top));
-    const uint32_t turned = __reduce_max_sync(~0u, duo.turns ? __float_as_uint(top) : 0u);
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x / 32] = make_uint2(fixed, turned);
+    const uint32_t bits = __float_as_uint(top_k);
+    const uint32_t fixed = __reduce_max_sync(~0u, duo.turns ? 0u : bits), turned = __reduce_max_sync(~0u, duo.turns ? bits : 0u);
+    const uint32_t value = __reduce_max_sync(~0u, __float_as_uint(top_v));
+    if ((threadIdx.x & 31) == 0) {
+      uint32_t* const to = s_max[threadIdx.x / 32];
+      to[0] = fixed; to[1] = turned; to[2] = value;
+    }
   }
   __syncthreads();
-  uint32_t fixed = 0, turned = 0;                        // largest of the elements as they came, of the turned ones
+  uint32_t fixed = 0, turned = 0, value = 0;             // largest of K as it came, of what was turned, of V
 #pragma unroll
-  for (int i = 0; i < kHalf / 32; ++i) {
-    fixed = max(fixed, s_max[half * (kHalf / 32) + i].x);
-    turned = max(turned, s_max[half * (kHalf / 32) + i].y);
+  for (int i = 0; i < kRotThreads / 32; ++i) {
+    fixed = max(fixed, s_max[i][0]);
+    turned = max(turned, s_max[i][1]);
+    value = max(value, s_max[i][2]);
   }
+  // In exact arithmetic the largest turned one is within 2 kUnsure of `turned`.
+  const float most = __uint_as_float(turned) * (1.f + 2.f * kUnsure);
+  int e_new = max(need_exp(fixed), need_exp(__float_as_uint(__uint_as_float(turned) * (1.f - 2.f * kUnsure))));
   auto exactly = [&](int i, int e) {                     // element e of row step i in 64 bits
     const int t = t0 + row0 + i * C::kRowsAtOnce;
     const T* row = src + static_cast<size_t>(source(t)) * D;
@@ -206,116 +318,123 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
     return turned_exactly(a, c, (static_cast<unsigned long long>(next) + t) * s_turn[pair * C::kDuos + k], R.scale,
                           kInterleaved ? e & 1 : e >= 8);
   };
-  // In exact arithmetic the largest turned one is within 2 kUnsure of `turned`.
-  const float most = __uint_as_float(turned) * (1.f + 2.f * kUnsure);
-  int e_new = max(need_exp(fixed), need_exp(__float_as_uint(__uint_as_float(turned) * (1.f - 2.f * kUnsure))));
-  if (need_exp(__float_as_uint(most)) > e_new) {         // the same in the whole half; not in V's, where nothing turns
+  if (need_exp(__float_as_uint(most)) > e_new) {         // the same in the whole block
     const float edge = exp2_int(e_new) * 448.f;          // (infinite past fp32's range: then nothing is past it)
     if (duo.turns)
 #pragma unroll 1
       for (int x = 0; x < steps * 16; ++x) {
-        const float y = *reinterpret_cast<const float*>(mine + x / 16 * apart + x % 16 / 4 * C::kStep + x % 4 * 4);
+        const float y = *reinterpret_cast<const float*>(mine + x / 4 * C::kStep + x % 4 * 4);
         if (!(fabsf(y) >= edge * (1.f - 4.f * kUnsure) && fabsf(y) < INFINITY)) continue;
         if (fabs(exactly(x / 16, x % 16)) > edge) atomicOr(s_more, 1);
       }
-    named_barrier(1, kHalf);
+    __syncthreads();
     e_new += *s_more;
   }
-  uint8_t* dst = (half ? A.c.v : A.c.k) + plane * kPage * D;
-  const int e = max(e_new, e_old);
+  const int e_k = max(e_new, old_k), e_v = max(need_exp(value), old_v);
+  uint8_t* const to_k = A.c.k + plane * kPage * D;
+  uint8_t* const to_v = A.c.v + plane * kPage * D;
   if (page >= 0) {
-    if (ht == 0) *scale = exp2_int(e);
-    if (e > e_old) {                                     // the page's older rows, at the new scale
-      uint4* old = reinterpret_cast<uint4*>(dst);
+    if (threadIdx.x == 0) {
+      A.c.k_scale[plane] = exp2_int(e_k);
+      A.c.v_scale[plane] = exp2_int(e_v);
+    }
 #pragma unroll 1
-      for (int at = ht; at < r0 * D / 16; at += kHalf) old[at] = rescale16(old[at], e_old - e);
+    for (int x = 0; x < 2; ++x) {                        // the page's older rows, at the new scales
+      const int d = x ? old_v - e_v : old_k - e_k;
+      if (d == 0) continue;
+      uint4* old = reinterpret_cast<uint4*>(x ? to_v : to_k);
+#pragma unroll 1
+      for (int at = threadIdx.x; at < r0 * D / 16; at += kRotThreads) old[at] = rescale16(old[at], d);
     }
   }
   // Rows that K_out shares with K are read in 64 bits, where that is needed, before they are written.
-  const float f = exp2_int(-e);
+  const float f = exp2_int(-e_k), f_v = exp2_int(-e_v);
 #pragma unroll 1
   for (int i = 0; i < steps; ++i) {
-    const int r = row0 + i * C::kRowsAtOnce;
+    const size_t r = row0 + i * C::kRowsAtOnce;
     float y[16];
     uint32_t w[4];
-    if (half) {
-      read(i, y);
+    read8<C::kStep>(mine + i * 4 * C::kStep, y, 0.f);
+    read8<C::kStep>(mine + (i * 4 + 2) * C::kStep, y + 8, 0.f);
+    // both ends of what an element may be, by its pair's size; where they differ, in 64 bits
+    float u[16];
+    const float unsure = kUnsure * f;
 #pragma unroll
-      for (int z = 0; z < 4; ++z)
-        w[z] = static_cast<uint32_t>(float2_to_e4m3x2(y[4 * z] * f, y[4 * z + 1] * f)) |
-               static_cast<uint32_t>(float2_to_e4m3x2(y[4 * z + 2] * f, y[4 * z + 3] * f)) << 16;
-    } else {
-      floats(i, y);
-      // both ends of what an element may be, by its pair's size; where they differ, in 64 bits
-      float u[16];
-      const float unsure = kUnsure * f;
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const int a = kInterleaved ? 2 * x : x, b = kInterleaved ? 2 * x + 1 : x + 8;
-        u[a] = u[b] = duo.turns ? (fabsf(y[a]) + fabsf(y[b])) * unsure : 0.f;
-      }
-      const uint64_t f2 = f2_pack(f, f), minus = f2_pack(-1.f, -1.f);
-      uint32_t differ[4];                                // by byte
-#pragma unroll
-      for (int z = 0; z < 4; ++z) {
-        uint32_t low = 0, high = 0;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int a = 4 * z + 2 * x;
-          const uint64_t y2 = f2_pack(y[a], y[a + 1]), u2 = f2_pack(u[a], u[a + 1]);
-          float v0, v1;
-          f2_unpack(f2_fma(y2, f2, f2_mul(u2, minus)), v0, v1);
-          low |= static_cast<uint32_t>(float2_to_e4m3x2(v0, v1)) << 16 * x;
-          f2_unpack(f2_fma(y2, f2, u2), v0, v1);
-          high |= static_cast<uint32_t>(float2_to_e4m3x2(v0, v1)) << 16 * x;
-        }
-        w[z] = low;
-        differ[z] = low ^ high;
-      }
-      if (differ[0] | differ[1] | differ[2] | differ[3])
-#pragma unroll 1
-        for (int x = 0; x < 16; ++x) {
-          const uint32_t word = x < 4 ? differ[0] : x < 8 ? differ[1] : x < 12 ? differ[2] : differ[3];
-          if (!(word >> x % 4 * 8 & 255u)) continue;
-          const uint32_t code = code_of(exactly(i, x) * exp2_int(-e)) << x % 4 * 8, rest = ~(255u << x % 4 * 8);
-#pragma unroll
-          for (int z = 0; z < 4; ++z)
-            if (z == x / 4) w[z] = (w[z] & rest) | code;
-        }
+    for (int x = 0; x < 8; ++x) {
+      const int a = kInterleaved ? 2 * x : x, b = kInterleaved ? 2 * x + 1 : x + 8;
+      u[a] = u[b] = duo.turns ? (fabsf(y[a]) + fabsf(y[b])) * unsure : 0.f;
     }
+    const uint64_t f2 = f2_pack(f, f), minus = f2_pack(-1.f, -1.f);
+    uint32_t differ[4];                                  // by byte
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      uint32_t low = 0, high = 0;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int a = 4 * z + 2 * x;
+        const uint64_t y2 = f2_pack(y[a], y[a + 1]), u2 = f2_pack(u[a], u[a + 1]);
+        float v0, v1;
+        f2_unpack(f2_fma(y2, f2, f2_mul(u2, minus)), v0, v1);
+        low |= static_cast<uint32_t>(float2_to_e4m3x2(v0, v1)) << 16 * x;
+        f2_unpack(f2_fma(y2, f2, u2), v0, v1);
+        high |= static_cast<uint32_t>(float2_to_e4m3x2(v0, v1)) << 16 * x;
+      }
+      w[z] = low;
+      differ[z] = low ^ high;
+    }
+    if (differ[0] | differ[1] | differ[2] | differ[3])
+#pragma unroll 1
+      for (int x = 0; x < 16; ++x) {
+        const uint32_t word = x < 4 ? differ[0] : x < 8 ? differ[1] : x < 12 ? differ[2] : differ[3];
+        if (!(word >> x % 4 * 8 & 255u)) continue;
+        const uint32_t code = code_of(exactly(i, x) * exp2_int(-e_k)) << x % 4 * 8, rest = ~(255u << x % 4 * 8);
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          if (z == x / 4) w[z] = (w[z] & rest) | code;
+      }
     if (page >= 0) {
-      uint8_t* to = dst + static_cast<size_t>(r0 + r) * D;
+      uint8_t* to = to_k + (r0 + r) * D;
       *reinterpret_cast<uint2*>(to + duo.at[0]) = make_uint2(w[0], w[1]);
       *reinterpret_cast<uint2*>(to + duo.at[1]) = make_uint2(w[2], w[3]);
     }
-    if (!half && R.K_out) {
-      T* out = static_cast<T*>(R.K_out) + ((static_cast<size_t>(b) * A.H_kv + h) * A.n + t0 + r) * D;
+    if (R.K_out) {
+      T* out = static_cast<T*>(R.K_out) + head + (t0 + r) * D;
       store8(out + duo.at[0], y);
       store8(out + duo.at[1], y + 8);
     }
   }
-  if (page >= 0 && ht < rows) {
-    const size_t at = plane * kPage + r0 + ht;
-    if (half == 0) {
-      int g = A.gid[(static_cast<size_t>(b) * A.A + (A.A == 1 ? 0 : h)) * A.n + source(t0 + ht)];
-      if (g < 0 || g >= A.K_groups) {
-        atomicOr(A.err, kErrBadGroup);
-        g = g < 0 ? 0 : A.K_groups - 1;
-      }
-      A.c.pos[at] = next + t0 + ht;
-      A.c.gid[at] = static_cast<int16_t>(g);
-    } else if (A.c.mass) {
-      A.c.mass[at] = 0.f;
+  if (page < 0) return;
+#pragma unroll 1
+  for (int i = 0; i < steps; ++i) {
+    float y[16];
+    uint32_t w[4];
+    read(mine_v + i * C::kRaw * C::kStep, y);
+#pragma unroll
+    for (int z = 0; z < 4; ++z)
+      w[z] = static_cast<uint32_t>(float2_to_e4m3x2(y[4 * z] * f_v, y[4 * z + 1] * f_v)) |
+             static_cast<uint32_t>(float2_to_e4m3x2(y[4 * z + 2] * f_v, y[4 * z + 3] * f_v)) << 16;
+    *reinterpret_cast<uint4*>(to_v + static_cast<size_t>(r0 + row0 + i * C::kRowsAtOnce) * D + k * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (threadIdx.x < rows) {
+    const size_t at = plane * kPage + r0 + threadIdx.x;
+    int g = A.gid[(static_cast<size_t>(b) * A.A + (A.A == 1 ? 0 : h)) * A.n + source(t0 + threadIdx.x)];
+    if (g < 0 || g >= A.K_groups) {
+      atomicOr(A.err, kErrBadGroup);
+      g = g < 0 ? 0 : A.K_groups - 1;
     }
+    A.c.pos[at] = next + t0 + threadIdx.x;
+    A.c.gid[at] = static_cast<int16_t>(g);
+    if (A.c.mass) A.c.mass[at] = 0.f;
   }
 }
 
 // Grid x: blocks of pages, one per touched page and head, and those of query rows, spread evenly
 // among each other: the former are bound by instructions, the latter by HBM.
 template <typename T, int D, bool kInterleaved>
-__global__ void __launch_bounds__(kRotThreads, 3) cache_append_rotary_kernel(CacheAppendRotaryLaunch L) {
+__global__ void __launch_bounds__(kRotThreads, 4) cache_append_rotary_kernel(CacheAppendRotaryLaunch L) {
   __shared__ unsigned long long s_turn[D / 2];
-  __shared__ uint2 s_max[kRotThreads / 32];
+  __shared__ float4 s_step[PageRows<T, D>::kSteps * D / 4];
+  __shared__ uint32_t s_max[kRotThreads / 32][3];
   __shared__ int s_more;
   extern __shared__ __align__(16) uint8_t smem[];
   const CacheAppendLaunch& A = L.a;
@@ -331,11 +450,11 @@ __global__ void __launch_bounds__(kRotThreads, 3) cache_append_rotary_kernel(Cac
     h = before / L.touched;
     n0 = A.c.len[b * A.H_kv + h];
     const int j = n0 / kPage + before % L.touched;
-    if (fits && max(n0, j * kPage) < min(n0 + m, (j + 1) * kPage)) append_page<T, D, kInterleaved>(L, b, h, j, n0, m, s_turn, s_max, &s_more, smem);
+    if (fits && max(n0, j * kPage) < min(n0 + m, (j + 1) * kPage)) append_page<T, D, kInterleaved>(L, b, h, j, n0, m, s_turn, s_step, s_max, &s_more, smem);
   } else if (fits) {
     const int x = blockIdx.x - before, chunks = (A.n + L.rot.tokens - 1) / L.rot.tokens;
     const int t0 = x % chunks * L.rot.tokens;
-    if (t0 < m) rotate_rows<T, D, kInterleaved, 64>(L.rot, b, t0, x / chunks * L.rot.heads, m, A.c.next[b], nullptr, s_turn);
+    if (t0 < m) rotate_queries<T, D, kInterleaved>(L.rot, b, t0, x / chunks * L.rot.heads, m, A.c.next[b], s_turn, smem);
   }
   append_counts(A, b, h, n0, fits ? m : 0, is_page && before % L.touched == 0,
                 gridDim.x * gridDim.y * gridDim.z);

@@ -114,11 +114,11 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* y) {
 
 // Rows of a block's tokens and heads: `tokens` tokens (a power of two) of `heads` heads.
 // Head g < L.Hq is a query head, the others are key heads.
-// kBytes: of rows that a thread has in flight.
-template <typename T, int D, bool kInterleaved, int kBytes>
+// A thread has 128 bytes of rows in flight.
+template <typename T, int D, bool kInterleaved>
 __device__ __forceinline__ void rotate_rows(const RotaryLaunch& L, int b, int t0, int head0, int valid,
                                             long long first, const int* depth, unsigned long long* s_turn) {
-  constexpr int kDuos = D / 16, kSlots = kRotThreads / kDuos, kAtOnce = kBytes / (16 * sizeof(T));
+  constexpr int kDuos = D / 16, kSlots = kRotThreads / kDuos, kAtOnce = 128 / (16 * sizeof(T));
   fill_turns<kDuos>(L, s_turn);
   __syncthreads();
   const int k = threadIdx.x % kDuos, slot = threadIdx.x / kDuos;
