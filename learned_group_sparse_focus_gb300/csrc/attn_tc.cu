@@ -110,13 +110,6 @@ static_assert(AttnCfg<128>::kSmem <= 227 * 1024, "attention shared memory above 
 static_assert(AttnCfg<128>::kO + 128 <= AttnCfg<128>::kTmemCols, "S buffers and O exceed TMEM");
 static_assert(kBN / 2 % 16 == 0, "the half-row max walks 16 columns per step");
 
-// max(a, b, c) in one instruction
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 __device__ __forceinline__ float ex2f(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

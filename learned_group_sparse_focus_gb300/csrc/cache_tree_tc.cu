@@ -132,12 +132,6 @@ __device__ __forceinline__ bool named_barrier_or(int id, int count, bool v) {
   return r != 0;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -793,8 +787,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
           p[r + 1] = __float_as_uint(exp2_fast(d[1])) & spread<1>(four);
           p[r + 2] = __float_as_uint(exp2_fast(d[2])) & spread<2>(four);
           p[r + 3] = __float_as_uint(exp2_fast(d[3])) & spread<3>(four);
-          over4[r / 4 & 1] = max3(over4[r / 4 & 1], __uint_as_float(p[r]), __uint_as_float(p[r + 1]));
-          over4[2 + (r / 4 & 1)] = max3(over4[2 + (r / 4 & 1)], __uint_as_float(p[r + 2]), __uint_as_float(p[r + 3]));
+          over4[r / 4 & 1] = fmax3(over4[r / 4 & 1], __uint_as_float(p[r]), __uint_as_float(p[r + 1]));
+          over4[2 + (r / 4 & 1)] = fmax3(over4[2 + (r / 4 & 1)], __uint_as_float(p[r + 2]), __uint_as_float(p[r + 3]));
         }
         over = fmaxf(fmaxf(over4[0], over4[1]), fmaxf(over4[2], over4[3]));
       };

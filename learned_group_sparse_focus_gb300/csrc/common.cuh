@@ -370,6 +370,13 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// Largest of three; NaN is left out.
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Packed fp32 pairs (one 64-bit register pair, two lanes of work per instruction).
 __device__ __forceinline__ uint64_t f2_pack(float a, float b) {
   uint64_t r;

@@ -308,6 +308,7 @@ struct CacheAppendRotaryLaunch {
   const int32_t* rows;     // [B, n] source row of each token, or null
   int device;
   int touched;             // pages a head may touch (set by the launch)
+  unsigned long long page_share;   // of the grid's blocks, in 2^-32 (set by the launch)
 };
 cudaError_t launch_cache_append_rotary(CacheAppendRotaryLaunch L, int dtype, cudaStream_t st);
 

@@ -87,6 +87,7 @@ __device__ __forceinline__ uint32_t code_of(double y) {
 template <typename T, int D>
 struct PageRows {
   static constexpr int kDuos = D / 16, kRowsAtOnce = kRotThreads / kDuos, kSteps = kPage / kRowsAtOnce;
+  static constexpr int kWarpRows = 32 / kDuos;           // neighbouring rows of a warp in a row step
   static constexpr int kRaw = sizeof(T);                 // 16-byte pieces of a duo as it comes: 2 or 4
   static constexpr int kStep = kRotThreads * 16;         // bytes of one piece of every thread
   // Query rows wait there as well, each piece for the thread that copied it: 128 bytes of a thread on their way.
@@ -117,7 +118,7 @@ __device__ __forceinline__ void read8(const uint8_t* at, float* y, __nv_bfloat16
 // memory: in registers, what is on its way would cost the blocks of pages their fourth block an SM.
 template <typename T, int D, bool kInterleaved>
 __device__ __forceinline__ void rotate_queries(const RotaryLaunch& L, int b, int t0, int head0, int valid, int next,
-                                               unsigned long long* s_turn, uint8_t* smem) {
+                                               float freq, unsigned long long* s_turn, uint8_t* smem) {
   using C = PageRows<T, D>;
   constexpr int kSlots = kRotThreads / C::kDuos, kEach = 16 / static_cast<int>(sizeof(T));
   const int k = threadIdx.x % C::kDuos, slot = threadIdx.x / C::kDuos;
@@ -141,7 +142,7 @@ __device__ __forceinline__ void rotate_queries(const RotaryLaunch& L, int b, int
   };
 #pragma unroll
   for (int i = 0; i < C::kQueue; ++i) fetch(i);
-  fill_turns<C::kDuos>(L, s_turn);
+  if (threadIdx.x < L.dim / 2) s_turn[threadIdx.x % 8 * C::kDuos + threadIdx.x / 8] = turn_of(freq);
   __syncthreads();
   uint64_t c[4], s[4];
   if (duo.turns && rows > 0) duo_cos_sin<C::kDuos>(static_cast<uint32_t>(next) + t, s_turn + k, L.scale, L.scale, c, s);
@@ -169,17 +170,17 @@ __device__ __forceinline__ void rotate_queries(const RotaryLaunch& L, int b, int
 
 // One page of one head: as cache_append_kernel, with a thread on duos of K and of V.
 template <typename T, int D, bool kInterleaved>
-__device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, int b, int h, int j, int n0, int m,
-                                            unsigned long long* s_turn, float4* s_step, uint32_t (*s_max)[3], int* s_more,
-                                            uint8_t* smem) {
+__device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, int b, int h, int j, int n0, int m, int next,
+                                            float freq, unsigned long long* s_turn, float4* s_step, uint32_t* s_max,
+                                            int* s_more, uint8_t* smem) {
   using C = PageRows<T, D>;
   const CacheAppendLaunch& A = L.a;
   const RotaryLaunch& R = L.rot;
   const int lo = max(n0, j * kPage), hi = min(n0 + m, (j + 1) * kPage);
   const int r0 = lo - j * kPage, rows = hi - lo, t0 = lo - n0;
+  const int entry = A.c.table[static_cast<size_t>(b) * A.c.max_pages + j];     // unchecked
   const int k = threadIdx.x % C::kDuos, row0 = threadIdx.x / C::kDuos;
   const Duo duo(k, R.dim, kInterleaved);
-  const int next = A.c.next[b];
   // the source row of a token
   auto source = [&](int t) {
     if (!L.rows) return t;
@@ -211,33 +212,66 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
     for (int e = 0; e < C::kRaw; ++e) cp_async_16(mine_v + (i * C::kRaw + e) * C::kStep, row + e * kEach, 16);
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
-  const int page = cache_page(A.c, b, j, A.err);
-  const size_t plane = static_cast<size_t>(max(page, 0)) * A.H_kv + h;
-  const bool shared = r0 > 0 && page >= 0;               // the page has older rows
-  const int old_k = shared ? scale_exp(A.c.k_scale[plane]) : kMinExp, old_v = shared ? scale_exp(A.c.v_scale[plane]) : kMinExp;
-  fill_turns<C::kDuos>(R, s_turn);
-  if (rows > C::kRowsAtOnce)                             // cosines and sines of the row steps
-#pragma unroll 1
-    for (int x = threadIdx.x; x < (C::kSteps - 1) * D / 2; x += kRotThreads) {
-      const int f = x % (D / 2), i = x / (D / 2);
-      if (f >= R.dim / 2) continue;
-      float* at = reinterpret_cast<float*>(s_step + (i * 4 + f % 8 / 4) * C::kDuos + f / 8) + f % 4;
-      cos_sin((i + 1) * C::kRowsAtOnce, turn_of(R.inv_freq[f]), *at, at[2 * C::kDuos * 4]);
+  int gid = 0;
+  if (threadIdx.x < rows) gid = A.gid[(static_cast<size_t>(b) * A.A + (A.A == 1 ? 0 : h)) * A.n + source(t0 + threadIdx.x)];
+  // A row's angles are those of its warp's first row and those of what it lies behind that one: fewer
+  // polynomials by far.  The latter, for every place in a warp and row step, are the block's.
+  {
+    constexpr int kFreqs = D / 2, kPlaces = C::kSteps * C::kWarpRows;
+    static_assert(kRotThreads % kFreqs == 0, "a thread has one frequency");
+    const int f = threadIdx.x % kFreqs;
+    if (f < R.dim / 2) {
+      const unsigned long long turn = turn_of(freq);
+      if (static_cast<int>(threadIdx.x) < kFreqs) s_turn[f % 8 * C::kDuos + f / 8] = turn;
+#pragma unroll
+      for (int x = threadIdx.x / kFreqs; x < kPlaces; x += kRotThreads / kFreqs) {
+        float* at = reinterpret_cast<float*>(s_step + (x * 4 + f % 8 / 4) * C::kDuos + f / 8) + f % 4;
+        cos_sin(x / C::kWarpRows * C::kRowsAtOnce + x % C::kWarpRows, turn, *at, at[2 * C::kDuos * 4]);
+      }
     }
-  if (threadIdx.x == 0) *s_more = 0;
+  }
+  if (threadIdx.x == 0) *s_more = s_max[0] = s_max[1] = s_max[2] = 0;
   __syncthreads();
-  uint64_t c0[4], s0[4];                                 // of the thread's first row
-  if (duo.turns && steps > 0) duo_cos_sin<C::kDuos>(static_cast<uint32_t>(next) + (t0 + row0), s_turn + k, R.scale, R.scale, c0, s0);
+  int page = entry;
+  if (entry < 0 || entry >= A.c.n_pages) {
+    atomicOr(A.err, kErrBadCache);
+    page = -1;
+  }
+  const size_t plane = static_cast<size_t>(max(page, 0)) * A.H_kv + h;
+  float scale_k = 0.f, scale_v = 0.f;
+  if (r0 > 0 && page >= 0) {                             // the page has older rows
+    scale_k = A.c.k_scale[plane];
+    scale_v = A.c.v_scale[plane];
+  }
+  uint64_t c0[4], s0[4];                                 // of the warp's first row, times scale
+  {
+    constexpr int kEval = 8 / C::kWarpRows;              // frequencies of a duo a lane, for all that share the duo
+    const int place = threadIdx.x % 32 / C::kDuos;
+    float c[kEval], s[kEval];
+#pragma unroll
+    for (int e = 0; e < kEval; ++e) {
+      c[e] = s[e] = 0.f;
+      if (duo.turns) cos_sin(static_cast<uint32_t>(next) + (t0 + row0 - place), s_turn[(place * kEval + e) * C::kDuos + k], c[e], s[e]);
+      c[e] *= R.scale;
+      s[e] *= R.scale;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const int lane0 = e / kEval * C::kDuos + k, lane1 = (e + 1) / kEval * C::kDuos + k;
+      c0[e / 2] = f2_pack(__shfl_sync(~0u, c[e % kEval], lane0), __shfl_sync(~0u, c[(e + 1) % kEval], lane1));
+      s0[e / 2] = f2_pack(__shfl_sync(~0u, s[e % kEval], lane0), __shfl_sync(~0u, s[(e + 1) % kEval], lane1));
+    }
+  }
   auto read = [&](const uint8_t* at, float (&y)[16]) {   // a duo as it came
     read8<C::kStep>(at, y, T{});
     read8<C::kStep>(at + C::kRaw / 2 * C::kStep, y + 8, T{});
   };
   auto finite_top = [&](const float (&y)[16]) {          // largest finite magnitude
-    float a = 0.f, b = 0.f;                              // (fmaxf leaves NaN out)
+    float a = 0.f, b = 0.f;                              // (the maximum leaves NaN out)
 #pragma unroll
-    for (int e = 0; e < 16; e += 2) {
-      a = fmaxf(a, fabsf(y[e]));
-      b = fmaxf(b, fabsf(y[e + 1]));
+    for (int e = 0; e < 16; e += 4) {
+      a = fmax3(a, fabsf(y[e]), fabsf(y[e + 1]));
+      b = fmax3(b, fabsf(y[e + 2]), fabsf(y[e + 3]));
     }
     a = fmaxf(a, b);
     if (a == INFINITY) {
@@ -256,23 +290,17 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
     uint8_t* const at = mine + i * 4 * C::kStep;
     read(at, y);
     if (duo.turns) {
-      uint64_t c[4], s[4];
+      uint64_t c[4], s[4];                               // of the sum of two angles
+      const uint64_t minus = f2_pack(-1.f, -1.f);
+      const float4* step = s_step + (i * C::kWarpRows + threadIdx.x % 32 / C::kDuos) * 4 * C::kDuos + k;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        c[e] = c0[e];
-        s[e] = s0[e];
-      }
-      if (i > 0) {                                       // the sum of two angles
-        const uint64_t minus = f2_pack(-1.f, -1.f);
+      for (int e = 0; e < 4; e += 2) {
+        const float4 u = step[e / 2 * C::kDuos], v = step[(2 + e / 2) * C::kDuos];
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const float4 u = s_step[((i - 1) * 4 + e / 2) * C::kDuos + k], v = s_step[((i - 1) * 4 + 2 + e / 2) * C::kDuos + k];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint64_t cd = x ? f2_pack(u.z, u.w) : f2_pack(u.x, u.y), sd = x ? f2_pack(v.z, v.w) : f2_pack(v.x, v.y);
-            c[e + x] = f2_fma(f2_mul(s0[e + x], minus), sd, f2_mul(c0[e + x], cd));
-            s[e + x] = f2_fma(s0[e + x], cd, f2_mul(c0[e + x], sd));
-          }
+        for (int x = 0; x < 2; ++x) {
+          const uint64_t cd = x ? f2_pack(u.z, u.w) : f2_pack(u.x, u.y), sd = x ? f2_pack(v.z, v.w) : f2_pack(v.x, v.y);
+          c[e + x] = f2_fma(f2_mul(s0[e + x], minus), sd, f2_mul(c0[e + x], cd));
+          s[e + x] = f2_fma(s0[e + x], cd, f2_mul(c0[e + x], sd));
         }
       }
       turn_pairs<kInterleaved>(y, c, s);
@@ -294,18 +322,13 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
     const uint32_t fixed = __reduce_max_sync(~0u, duo.turns ? 0u : bits), turned = __reduce_max_sync(~0u, duo.turns ? bits : 0u);
     const uint32_t value = __reduce_max_sync(~0u, __float_as_uint(top_v));
     if ((threadIdx.x & 31) == 0) {
-      uint32_t* const to = s_max[threadIdx.x / 32];
-      to[0] = fixed; to[1] = turned; to[2] = value;
+      atomicMax(&s_max[0], fixed);
+      atomicMax(&s_max[1], turned);
+      atomicMax(&s_max[2], value);
     }
   }
   __syncthreads();
-  uint32_t fixed = 0, turned = 0, value = 0;             // largest of K as it came, of what was turned, of V
-#pragma unroll
-  for (int i = 0; i < kRotThreads / 32; ++i) {
-    fixed = max(fixed, s_max[i][0]);
-    turned = max(turned, s_max[i][1]);
-    value = max(value, s_max[i][2]);
-  }
+  const uint32_t fixed = s_max[0], turned = s_max[1], value = s_max[2];     // of K as it came, of what was turned, of V
   // In exact arithmetic the largest turned one is within 2 kUnsure of `turned`.
   const float most = __uint_as_float(turned) * (1.f + 2.f * kUnsure);
   int e_new = max(need_exp(fixed), need_exp(__float_as_uint(__uint_as_float(turned) * (1.f - 2.f * kUnsure))));
@@ -330,6 +353,7 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
     __syncthreads();
     e_new += *s_more;
   }
+  const int old_k = scale_exp(scale_k), old_v = scale_exp(scale_v);         // kMinExp without older rows
   const int e_k = max(e_new, old_k), e_v = max(need_exp(value), old_v);
   uint8_t* const to_k = A.c.k + plane * kPage * D;
   uint8_t* const to_v = A.c.v + plane * kPage * D;
@@ -417,13 +441,12 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
   }
   if (threadIdx.x < rows) {
     const size_t at = plane * kPage + r0 + threadIdx.x;
-    int g = A.gid[(static_cast<size_t>(b) * A.A + (A.A == 1 ? 0 : h)) * A.n + source(t0 + threadIdx.x)];
-    if (g < 0 || g >= A.K_groups) {
+    if (gid < 0 || gid >= A.K_groups) {
       atomicOr(A.err, kErrBadGroup);
-      g = g < 0 ? 0 : A.K_groups - 1;
+      gid = gid < 0 ? 0 : A.K_groups - 1;
     }
     A.c.pos[at] = next + t0 + threadIdx.x;
-    A.c.gid[at] = static_cast<int16_t>(g);
+    A.c.gid[at] = static_cast<int16_t>(gid);
     if (A.c.mass) A.c.mass[at] = 0.f;
   }
 }
@@ -433,30 +456,32 @@ __device__ __forceinline__ void append_page(const CacheAppendRotaryLaunch& L, in
 template <typename T, int D, bool kInterleaved>
 __global__ void __launch_bounds__(kRotThreads, 4) cache_append_rotary_kernel(CacheAppendRotaryLaunch L) {
   __shared__ unsigned long long s_turn[D / 2];
-  __shared__ float4 s_step[PageRows<T, D>::kSteps * D / 4];
-  __shared__ uint32_t s_max[kRotThreads / 32][3];
+  __shared__ float4 s_step[PageRows<T, D>::kSteps * PageRows<T, D>::kWarpRows * D / 4];
+  __shared__ uint32_t s_max[3];
   __shared__ int s_more;
   extern __shared__ __align__(16) uint8_t smem[];
   const CacheAppendLaunch& A = L.a;
   const int b = blockIdx.z;
+  const uint32_t before = static_cast<uint32_t>(blockIdx.x * L.page_share >> 32);          // blocks of pages before this one
+  const bool is_page = static_cast<uint32_t>((blockIdx.x + 1ull) * L.page_share >> 32) > before;
+  const int h = is_page ? before / L.touched : 0, nth = before - h * L.touched;            // its page is the nth touched
+  // on their way together: the chain of loads is what a block of few tokens takes
+  const float freq = threadIdx.x % (D / 2) < L.rot.dim / 2 ? L.rot.inv_freq[threadIdx.x % (D / 2)] : 0.f;
+  const int n0 = A.c.len[b * A.H_kv + h], next = A.c.next[b];
   const int m = cache_new(A.n_new, A.n, b, A.err);
   const bool fits = sequence_fits(A, b, m);
   if (!fits && threadIdx.x == 0) atomicOr(A.err, kErrBadCache);
-  const unsigned long long of_pages = static_cast<unsigned long long>(L.touched) * A.H_kv;
-  const uint32_t before = static_cast<uint32_t>(blockIdx.x * of_pages / gridDim.x);      // blocks of pages before this one
-  const bool is_page = static_cast<uint32_t>((blockIdx.x + 1ull) * of_pages / gridDim.x) > before;
-  int h = 0, n0 = 0;
-  if (is_page) {
-    h = before / L.touched;
-    n0 = A.c.len[b * A.H_kv + h];
-    const int j = n0 / kPage + before % L.touched;
-    if (fits && max(n0, j * kPage) < min(n0 + m, (j + 1) * kPage)) append_page<T, D, kInterleaved>(L, b, h, j, n0, m, s_turn, s_step, s_max, &s_more, smem);
-  } else if (fits) {
+  if (!fits) {
+  } else if (is_page) {
+    const int j = n0 / kPage + nth;
+    if (max(n0, j * kPage) < min(n0 + m, (j + 1) * kPage))
+      append_page<T, D, kInterleaved>(L, b, h, j, n0, m, next, freq, s_turn, s_step, s_max, &s_more, smem);
+  } else {
     const int x = blockIdx.x - before, chunks = (A.n + L.rot.tokens - 1) / L.rot.tokens;
     const int t0 = x % chunks * L.rot.tokens;
-    if (t0 < m) rotate_queries<T, D, kInterleaved>(L.rot, b, t0, x / chunks * L.rot.heads, m, A.c.next[b], s_turn, smem);
+    if (t0 < m) rotate_queries<T, D, kInterleaved>(L.rot, b, t0, x / chunks * L.rot.heads, m, next, freq, s_turn, smem);
   }
-  append_counts(A, b, h, n0, fits ? m : 0, is_page && before % L.touched == 0,
+  append_counts(A, b, h, n0, fits ? m : 0, is_page && nth == 0,
                 gridDim.x * gridDim.y * gridDim.z);
 }
 
@@ -518,6 +543,8 @@ cudaError_t launch_cache_append_rotary(CacheAppendRotaryLaunch L, int dtype, cud
     blocks += static_cast<unsigned long long>((L.a.n + L.rot.tokens - 1) / L.rot.tokens) *
               ((L.rot.Hq + L.rot.heads - 1) / L.rot.heads);
   }
+  // Its first x blocks hold floor(x page_share / 2^32) of pages: none ... all of them, one more at most at each.
+  L.page_share = (static_cast<unsigned long long>(L.touched) * L.a.H_kv << 32) / blocks + 1;
   const dim3 grid(static_cast<unsigned>(blocks), 1, L.a.B);
   if (dtype == FOCUS_BF16) return L.a.d == 128 ? launch_append<__nv_bfloat16, 128>(L, grid, st) : launch_append<__nv_bfloat16, 64>(L, grid, st);
   return L.a.d == 128 ? launch_append<float, 128>(L, grid, st) : launch_append<float, 64>(L, grid, st);
