@@ -61,6 +61,7 @@ struct Cfg {
   static constexpr int kAhead = R == 64 ? 8 : 16;              // pages a scan warp fetches group ids of at a time
   static constexpr int kSlots = R == 64 ? 4 : 8, kPages = kSlots / 2, kRound = kPages * kScanWarps;   // slots a lane, pages a warp, a round
   static constexpr int kList = R == 64 ? 1024 : 2048;          // entries of the block's list of kept slots
+  static_assert(kScanWarps * 32 >= kMaxNodes && R % 2 == 0, "a scan thread a node, half a warp a row");
   static_assert(kList >= kRound * kPage + kListed * kTile, "list too short");
   static constexpr int kChunk = kTile * 128;                   // 64 f16 columns of a tile's rows
   static constexpr int kTileBytes = D / 64 * kChunk, kPBytes = R / 32 * kChunk;   // of a value tile; of the weights
@@ -249,7 +250,6 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc(&s_tmem, C::kCols);
-  if (warp == kGatherWarp - 1) tree_lines(L.parent + static_cast<size_t>(b) * L.n, fresh, s_line, s_order, L.err);
 #pragma unroll 1
   for (int i = threadIdx.x; i < kCacheTableGroups; i += kThreads) table[i] = 0;
 #pragma unroll 1
@@ -263,11 +263,16 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __nv_bfloat16*>(L.K) + own_row * D + i * 64));
       asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __nv_bfloat16*>(L.V) + own_row * D + i * 64));
     }
+  const int node = threadIdx.x - kSoftWarps * 32;      // scan warps: a thread a node
   int node_gid = 0;
-  if (threadIdx.x < kMaxNodes) {
-    if (threadIdx.x < fresh) node_gid = gids[threadIdx.x];
-    s_node[threadIdx.x] = node_gid;
+  if (scans && node < kMaxNodes) {
+    if (node < fresh) node_gid = gids[node];
+    s_node[node] = node_gid;
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem, tmem_o = tmem + 4 * R;
   // Rows are nodes (times query heads) in order, or, where they are more than a block's, by group id: a block then keeps
   // few groups' slots (64 nodes in 64 groups of very different sizes: 0.9 of the slots over four blocks of 16
   // nodes, against 2.3).
@@ -351,27 +356,28 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     }
     fence_proxy_async_smem();
   };
-#pragma unroll 1
-  for (int phase = 0; phase < 2; ++phase) {
-    if (phase == (sorted ? 1 : 0) && (warp < kSoftWarps || (warp >= kGatherWarp && warp < kMmaWarp))) queries();
-    if (phase == 1) break;
-    __syncthreads();
-    unsigned long long line = 0;
-    int place = threadIdx.x;                           // of the thread's node among the rows
-    if (threadIdx.x < fresh) {                         // a thread a node
-      line = s_line[threadIdx.x];
-      if (sorted) {
-        place = 0;
+  // The scan warps form the masks while the others lay out the queries.
+  constexpr int kScanBar = 3, kQueryBar = 4, kOrderBar = 5;            // (the parts' votes have 1 and 2)
+  if (scans) {
+    if (v == kScanWarps - 1) tree_lines(L.parent + static_cast<size_t>(b) * L.n, fresh, s_line, s_order, L.err);
+    int place = node;                                  // of the thread's node among the rows
+    if (sorted && node < fresh) {
+      place = 0;
 #pragma unroll 4
-        for (int j = 0; j < fresh; ++j) {
-          const int g = s_node[j];
-          place += g < node_gid || (g == node_gid && j < static_cast<int>(threadIdx.x));
-        }
-        s_order[place] = threadIdx.x;
+      for (int j = 0; j < fresh; ++j) {
+        const int g = s_node[j];
+        place += g < node_gid || (g == node_gid && j < node);
       }
     }
-    __syncthreads();
-    if (threadIdx.x < fresh) {
+    __syncwarp();
+    named_barrier(kScanBar, kScanWarps * 32);
+    if (sorted) {
+      if (node < fresh) s_order[place] = node;
+      __syncwarp();
+      named_barrier_arrive(kOrderBar, (kQueryWarps + kScanWarps) * 32);
+    }
+    if (node < fresh) {
+      const unsigned long long line = s_line[node];
       const int depth = __popcll(line) - 1;
       if (depth >= L.w) {                              // ancestors before the window: of its group only
         unsigned long long keeps = 0;
@@ -381,7 +387,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
           const int j = __ffsll(left) - 1;
           if (depth - up < L.w || s_node[j] == node_gid) keeps |= 1ull << j;
         }
-        s_line[threadIdx.x] = keeps;
+        s_line[node] = keeps;
       }
       // its rows of the block, by group and by depth
       unsigned long long own_rows = 0;
@@ -392,10 +398,11 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
         if (node_gid >= 0 && node_gid < kCacheTableGroups) atomicOr(reinterpret_cast<uint32_t*>(&table[node_gid]) + (r >> 5), bit);
         atomicOr(reinterpret_cast<uint32_t*>(&s_below[depth]) + (r >> 5), bit);
       }
-      s_rows[threadIdx.x] = own_rows;
+      s_rows[node] = own_rows;
     }
-    __syncthreads();
-    if (warp == 0) {                                   // sums of depths below: lane i has 2 i and 2 i + 1
+    __syncwarp();
+    named_barrier(kScanBar, kScanWarps * 32);
+    if (v == 0) {                                      // sums of depths below: lane i has 2 i and 2 i + 1
       const unsigned long long first = s_below[2 * lane], both = first | s_below[2 * lane + 1];
       unsigned long long upto = both;
 #pragma unroll
@@ -409,12 +416,17 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       s_below[2 * lane] = below;
       s_below[2 * lane + 1] = below | first;
       if (lane == 31) s_below[kMaxNodes] = upto;
+      __syncwarp();
     }
+    named_barrier(kScanBar, kScanWarps * 32);
+  } else {
+    if (warp != kMmaWarp) {
+      if (sorted) named_barrier(kOrderBar, (kQueryWarps + kScanWarps) * 32);
+      queries();
+    }
+    __syncwarp();
+    named_barrier(kQueryBar, (kQueryWarps + 1) * 32);  // (the space that they came through is the tiles' from here on)
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = s_tmem, tmem_o = tmem + 4 * R;
 
   // A tile's slot among the keys' (by kKeySlots); the tree's own tile, the first, takes slots 0 and 1.
   auto key_slot = [&](int tile) { return static_cast<uint32_t>(tile) + (has_own && tile > 0 ? 1 : 0); };
@@ -980,21 +992,20 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   tc_fence_before();
   cluster.sync();
   tc_fence_after();
-  if (threadIdx.x < R) {
-    const int r = threadIdx.x;
-    float M = kNoRef, l = 0.f;
+  // half a warp a row, a lane a block (the same order of sums in every block)
 #pragma unroll 1
-    for (int x = 0; x < cs; ++x) M = fmaxf(M, s_all[x][r].x);
-#pragma unroll 1
-    for (int x = 0; x < cs; ++x)
-      if (s_all[x][r].y != 0.f) {
-        const float fh = exp2f(0.5f * (s_all[x][r].x - M));
-        l += s_all[x][r].y * fh * fh;
-      }
-#pragma unroll 1
-    for (int x = 0; x < cs; ++x)
-      s_weight[x][r] = s_all[x][r].y != 0.f ? exp2f(s_all[x][r].x - M) / l * exp2_int(kLift) : 0.f;
-    if (rank == 0 && L.lse && r < live)
+  for (int r = threadIdx.x / kMaxCluster; r < R; r += kThreads / kMaxCluster) {
+    const int x = lane % kMaxCluster;
+    const float2 a = x < cs ? s_all[x][r] : make_float2(kNoRef, 0.f);
+    float M = a.x;
+#pragma unroll
+    for (int y = kMaxCluster / 2; y > 0; y /= 2) M = fmaxf(M, __shfl_xor_sync(~0u, M, y));
+    const float fh = exp2f(0.5f * (a.x - M));
+    float l = a.y != 0.f ? a.y * fh * fh : 0.f;
+#pragma unroll
+    for (int y = kMaxCluster / 2; y > 0; y /= 2) l += __shfl_xor_sync(~0u, l, y);
+    if (x < cs) s_weight[x][r] = a.y != 0.f ? exp2f(a.x - M) / l * exp2_int(kLift) : 0.f;
+    if (rank == 0 && x == 0 && L.lse && r < live)
       L.lse[(static_cast<size_t>(b) * L.H + h * G + (r0 + r) % G) * L.n + node_of((r0 + r) / G)] =
           l != 0.f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
