@@ -1279,6 +1279,12 @@ focus_status_t focus_cache_attention_tree_fwd(const focus_params_t* p, const voi
   CacheAttnLaunch L{Q, gid, n_new, *cache, O, lse_opt, 0,
                     p->B, p->H, p->H_kv, p->n, p->d, p->A, p->w > 1 ? p->w : 1,
                     p->scale * 1.4426950408889634f, at<int>(ws, 0), dev, K, V, parent};
+  // As in the attention of new tokens, more than 16 rows go to the tensor cores (the mma.sync kernel forms them 16 at a
+  // time) and up to 16 do not: mma.sync / tcgen05 in us, 20 rows (4 heads, 5 nodes) over one sequence of 64 slots 25/17, of
+  // 32K 41/25, over 16 of up to 32K 200/148; 64 rows (1 x 64) 52/25, 165/52, 696/318; 16 rows (4 x 4) 17/17, 24/23,
+  // 113/140, (1 x 16) 19/17, 46/35, 187/232; 8 rows 15/17, 31/31, 105/193.  Of 342 cases of 1 to 32 sequences,
+  // d = 64 and 128, more than 16 rows are slower there in two (24 rows, 16 sequences, d = 64: 152/162, 113/117).
+  // Where mma.sync loses with 16 rows of as many nodes, it is by a few us on few sequences, and it wins 45 on many.
   if (p->dtype == FOCUS_BF16 && p->H / p->H_kv * p->n > kCacheRows && p->K <= kCacheTableGroups)
     return cuda_status(launch_cache_tree_tc(L, static_cast<cudaStream_t>(stream)));
   return cuda_status(launch_cache_tree(L, p->dtype, static_cast<cudaStream_t>(stream)));

@@ -1,5 +1,8 @@
 // Attention of a tree of drafted tokens over the paged 8-bit cache and over the tree itself
-// (contract: focus.h), on cache_attn.cu's kernel.
+// (contract: focus.h), on cache_attn.cu's kernel: drafted keys are two tiles a warp more, masked by their lines.
+//
+// Bound by latencies like a step of new tokens: 8 trees of 16 nodes, 12 heads of 64 over 1K tokens 17 us (17.4 on
+// the tcgen05 kernel), 3 of 7 nodes, fp32, 11 us.  fp32 tensors and more than 16 rows take a pass per 16 rows.
 #include "cache_attn.cuh"
 
 namespace focus {

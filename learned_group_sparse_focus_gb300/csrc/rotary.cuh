@@ -5,7 +5,7 @@
 // is kept as a fraction of a turn in 64-bit fixed point: x * t modulo 2^64, with
 // t = f / (2 pi) times 2^64, wraps by itself and is off by at most 2^-33 turns for any
 // 32-bit x.  The turn is taken to the nearest quarter, so sine and cosine see at most
-// an eighth of a turn, held to 2^-24 of itself, and are off by less than 2^-23.
+// an eighth of a turn, held to 2^-24 of itself.
 //
 // A thread turns a "duo" of two 8-element pieces of a row: elements k * 8 + e and
 // r / 2 + k * 8 + e, or, for neighbouring pairs, the 16 from k * 16 on; both use the
@@ -36,7 +36,8 @@ __device__ __forceinline__ unsigned long long turn_of(float inv_freq) {
   return u >> 31 ? 0ull - t : t;
 }
 
-// Cosine and sine at position x of a frequency's t: the phase's upper 32 bits (2^-33 turns), a
+// Cosine and sine at position x of a frequency's t, as a vector off by at most 2.13 x 2^-24 (all phases of an
+// eighth of a turn tried against 64 bits): the phase's upper 32 bits (2^-33 turns), a
 // quarter's remainder in radians, Taylor polynomials of degree 10 and 9 on an eighth of a turn (the
 // next terms are below 2^-32 and 2^-29), all in fp32.
 __device__ __forceinline__ void cos_sin(uint32_t x, unsigned long long t, float& c, float& s) {
