@@ -400,13 +400,15 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
       // its rows of the block, by group and by depth
       unsigned long long own_rows = 0;
 #pragma unroll 1
-      for (int r = max(place * G - r0, 0); r < min((place + 1) * G - r0, live); ++r) {
-        const uint32_t bit = static_cast<uint32_t>(row_bit(r) >> (r & 32));
-        own_rows |= row_bit(r);
-        if (node_gid >= 0 && node_gid < kCacheTableGroups) atomicOr(reinterpret_cast<uint32_t*>(&table[node_gid]) + (r >> 5), bit);
-        atomicOr(reinterpret_cast<uint32_t*>(&s_below[depth]) + (r >> 5), bit);
-      }
+      for (int r = max(place * G - r0, 0); r < min((place + 1) * G - r0, live); ++r) own_rows |= row_bit(r);
       s_rows[node] = own_rows;
+#pragma unroll
+      for (int x = 0; x < R / 32; ++x) {
+        const uint32_t bits = static_cast<uint32_t>(own_rows >> (32 * x));
+        if (bits == 0) continue;
+        if (node_gid >= 0 && node_gid < kCacheTableGroups) atomicOr(reinterpret_cast<uint32_t*>(&table[node_gid]) + x, bits);
+        atomicOr(reinterpret_cast<uint32_t*>(&s_below[depth]) + x, bits);
+      }
     }
     __syncwarp();
     named_barrier(kScanBar, kScanWarps * 32);
@@ -976,35 +978,40 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     const int quad = warp & 3, part = warp >> 2, d = quad * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
 #pragma unroll 1
-    for (int c = 0; c < RH; c += 8) {
-      uint32_t hi[8], lo[8];
-      tmem_ld(tmem_o + lanes + part * RH + c, hi);
-      tmem_ld(tmem_o + lanes + R + part * RH + c, lo);
-      tmem_wait_ld();
+    for (int c = 0; c < RH; c += 16) {
+      uint32_t hi[2][8], lo[2][8];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        tmem_ld(tmem_o + lanes + part * RH + c + 8 * x, hi[x]);
+        tmem_ld(tmem_o + lanes + R + part * RH + c + 8 * x, lo[x]);
+      }
+      tmem_wait_for(hi[0], lo[0]);
+      tmem_wait_for(hi[1], lo[1]);
       if (quad < D / 32) {
 #pragma unroll
-        for (int y = 0; y < 8; ++y) {
+        for (int y = 0; y < 16; ++y) {
           const int r = part * RH + c + y, to = r * inverse >> 16;
-          float x = __uint_as_float(hi[y]) + __uint_as_float(lo[y]);
+          float x = __uint_as_float(hi[y / 8][y % 8]) + __uint_as_float(lo[y / 8][y % 8]);
           if (s_nan[r][quad] >> lane & 1) x = __int_as_float(0x7fffffff);
           *cluster.map_shared_rank(inbox + (rank * share + r - to * share) * D + d, to) = x;
         }
       }
     }
   }
-#pragma unroll 1
-  for (int i = threadIdx.x; i < R * cs; i += kThreads) {
-    const int r = i % R, to = i / R;
-    *cluster.map_shared_rank(&s_all[rank][r], to) = make_float2(-s_minus[r], (s_l[0][r] + s_l[1][r]) + (s_l[2][r] + s_l[3][r]));
+  if (threadIdx.x >= kSoftWarps * 32 && threadIdx.x < kSoftWarps * 32 + R) {           // (by warps that send no rows)
+    const int r = threadIdx.x - kSoftWarps * 32;
+    *cluster.map_shared_rank(&s_all[rank][r], r * inverse >> 16) =
+        make_float2(-s_minus[r], (s_l[0][r] + s_l[1][r]) + (s_l[2][r] + s_l[3][r]));
   }
   tc_fence_before();
   cluster.sync();
   tc_fence_after();
-  // half a warp a row, a lane a block (the same order of sums in every block)
+  // the block's rows: half a warp a row, a lane a block
+  const int mine_to = min((rank + 1) * share, R);
 #pragma unroll 1
-  for (int r = threadIdx.x / kMaxCluster; r < R; r += kThreads / kMaxCluster) {
-    const int x = lane % kMaxCluster;
-    const float2 a = x < cs ? s_all[x][r] : make_float2(kNoRef, 0.f);
+  for (int r0w = rank * share + threadIdx.x / 32 * 2; r0w < mine_to; r0w += kThreads / kMaxCluster) {
+    const int r = r0w + lane / kMaxCluster, x = lane % kMaxCluster;
+    const float2 a = x < cs && r < mine_to ? s_all[x][r] : make_float2(kNoRef, 0.f);
     float M = a.x;
 #pragma unroll
     for (int y = kMaxCluster / 2; y > 0; y /= 2) M = fmaxf(M, __shfl_xor_sync(~0u, M, y));
@@ -1012,8 +1019,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     float l = a.y != 0.f ? a.y * fh * fh : 0.f;
 #pragma unroll
     for (int y = kMaxCluster / 2; y > 0; y /= 2) l += __shfl_xor_sync(~0u, l, y);
-    if (x < cs) s_weight[x][r] = a.y != 0.f ? exp2f(a.x - M) / l * exp2_int(kLift) : 0.f;
-    if (rank == 0 && x == 0 && L.lse && r < live)
+    if (x < cs && r < mine_to) s_weight[x][r] = a.y != 0.f ? fh * (fh * exp2_int(kLift)) / l : 0.f;
+    if (x == 0 && L.lse && r < min(mine_to, live))
       L.lse[(static_cast<size_t>(b) * L.H + h * G + (r0 + r) % G) * L.n + node_of((r0 + r) / G)] =
           l != 0.f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
@@ -1025,9 +1032,9 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int x = 0; x < cs; ++x) {
-      if (s_all[x][r].y == 0.f) continue;              // nothing kept there
       const float f = s_weight[x][r];
-      const float4 u = *reinterpret_cast<const float4*>(inbox + (x * share + local) * D + d);
+      float4 u = *reinterpret_cast<const float4*>(inbox + (x * share + local) * D + d);
+      if (s_all[x][r].y == 0.f) u = make_float4(0.f, 0.f, 0.f, 0.f);       // nothing kept there, nothing written if it had no tile
       a.x += u.x * f; a.y += u.y * f; a.z += u.z * f; a.w += u.w * f;
     }
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(L.O) +
