@@ -1,8 +1,8 @@
 // Attention of a tree of drafted tokens over the paged 8-bit cache and over the tree itself
 // (contract: focus.h), on cache_attn.cu's kernel: drafted keys are two tiles a warp more, masked by their lines.
 //
-// Bound by latencies like a step of new tokens: 8 trees of 16 nodes, 12 heads of 64 over 1K tokens 17 us (17.4 on
-// the tcgen05 kernel), 3 of 7 nodes, fp32, 11 us.  fp32 tensors and more than 16 rows take a pass per 16 rows.
+// Bound by latencies like a step of new tokens: 3 trees of 7 nodes, 6 / 3 fp32 heads, 11 us, 4 heads x 4 nodes over one
+// sequence of 16K 23 us.  More than 16 rows (fp32) take a pass per 16: 64 rows over 32K tokens of fp32 heads 99 to 119 us.
 #include "cache_attn.cuh"
 
 namespace focus {

@@ -1,6 +1,6 @@
 // Attention of a tree of drafted tokens over the paged 8-bit cache and over the tree itself
-// on the tcgen05 tensor cores: bf16 tensors, more than 16 query rows a head (contract:
-// focus.h; cache_tree.cu launches the mma.sync kernel for every other case).
+// on the tcgen05 tensor cores: bf16 tensors, more than 16 query rows a head or many nodes (contract:
+// focus.h; the rule: api.cu; cache_tree.cu launches the mma.sync kernel for every other case).
 //
 // A tree's nodes fall into many groups, so most slots are kept by some node, and few by any
 // one: products over gathered tiles of 128 keys and 32 or 64 query rows, masked.  A kept
@@ -32,9 +32,9 @@
 // Work split: a cluster of blocks for each sequence, head and block of rows; pages go round
 // over the cluster's blocks, the tree's own keys are the first tile of its last block.
 //
-// Measured: 16 nodes over one sequence of 32K tokens of 32 / 8 heads 35 us, over 19 of 16K 160 us (360 MB: 2.3 TB/s),
-// trees of up to 64 nodes over 16 sequences of up to 32K 366 us (690 MB).  A tile of 128 keys and 64 rows takes
-// 3,200 clocks, a block's fixed part 28,000 (set-up 10,000 to 14,000, the first tile 5,000, the join 8,000).
+// Measured: 16 nodes over one sequence of 32K tokens of 32 / 8 heads 33 us, over 19 of 16K 158 us (360 MB: 2.3 TB/s),
+// trees of up to 64 nodes over 16 sequences of up to 32K 356 us (690 MB).  A tile of 128 keys and 64 rows takes
+// 3,200 clocks, a block's fixed part 22,000 to 28,000 (scores of the first tile after 11,000 to 17,000, the join 7,000).
 // No single role sets the pace: without forming weights a batch takes 84% of its time, without the values' conversion
 // 96%, with an eighth of the second products 97%, with rows fetched three tiles ahead 103%; warps issue
 // 54% of the time, and what is left is the chain of waits between the roles.  32 rows a block in place of 64 where a head
