@@ -27,13 +27,14 @@
 // and moves only when a weight would pass 2^kTop: weights are formed with the old one first, and a barrier with a
 // vote tells a part's four warps whether they start over.  With s_j the logit (log2) and e_j the exponent of the
 // key's value row, the exponential is 2^(s_j - ref + kLift), which the row's sum adds as it is,
-// and the weight that multiplies raw codes that times 2^(e_j - kLift).
+// and the weight that multiplies raw codes that times 2^(e_j - kLift).  Where logits lie past 2^20 the constants of the
+// exponent would be lost in ref, so it is kept in two parts there (1% for the test that it takes).
 //
 // Work split: a cluster of blocks for each sequence, head and block of rows; pages go round
 // over the cluster's blocks, the tree's own keys are the first tile of its last block.
 //
-// Measured: 16 nodes over one sequence of 32K tokens of 32 / 8 heads 33 us, over 19 of 16K 158 us (360 MB: 2.3 TB/s),
-// trees of up to 64 nodes over 16 sequences of up to 32K 356 us (690 MB).  A tile of 128 keys and 64 rows takes
+// Measured: 16 nodes over one sequence of 32K tokens of 32 / 8 heads 33 us, over 19 of 16K 162 us (360 MB: 2.2 TB/s),
+// trees of up to 64 nodes over 16 sequences of up to 32K 362 us (690 MB).  A tile of 128 keys and 64 rows takes
 // 3,200 clocks, a block's fixed part 22,000 to 28,000 (scores of the first tile after 11,000 to 17,000, the join 7,000).
 // No single role sets the pace: without forming weights a batch takes 84% of its time, without the values' conversion
 // 96%, with an eighth of the second products 97%, with rows fetched three tiles ahead 103%; warps issue
@@ -164,11 +165,12 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   __shared__ int s_cnt[8];                             // keys of a tile (by tile modulo 8); 0 ends the tiles
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort_word;
-  __shared__ __align__(16) float s_factor[R], s_minus[R];   // the rows' factors; kLift - the references
-  __shared__ int s_top[4][R];                          // per lane quadrant, in integer order
+  __shared__ __align__(16) float s_factor[R], s_minus[R], s_low[R];   // the rows' factors; kLift - the references, in two parts
+  __shared__ int s_far;                                // some row's second part is not 0
+  __shared__ int2 s_top[4][R];                         // per lane quadrant, in integer order: s, and t past it
   __shared__ float s_l[4][R];
-  __shared__ float s_weight[kMaxCluster][R];           // weight of a block's partial in a row (join)
-  __shared__ float2 s_all[kMaxCluster][R];             // the cluster's references and sums
+  __shared__ float s_weight[R + kMaxCluster];          // join, by block and by row of this block: the partial's weight,
+  __shared__ float4 s_all[R + kMaxCluster];            // its reference and sum
   __shared__ uint32_t s_nan[R][D / 32];                // outputs that a kept NaN value reaches
   __shared__ unsigned long long s_line[kMaxNodes];     // a node's line, later what it keeps of it
   __shared__ unsigned long long s_below[kMaxNodes + 1];   // rows of a depth, later those of a smaller one
@@ -236,6 +238,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   // ---- barriers, tree, masks
   if (threadIdx.x == 0) {
     s_abort_word = 0;
+    s_far = 0;
 #pragma unroll 1
     for (int i = 0; i < C::kKeySlots; ++i) {
       mbar_init(&k_full[i], kGatherWarps * 32);
@@ -312,8 +315,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
 #pragma unroll 1
     for (int i = 0; i < R / kQueryWarps; ++i) {
       const int r = w + i * kQueryWarps;
-      float q[kEach], dot = 0.f;
-      uint32_t v_top = 0;                              // largest finite element of the own value
+      float q[kEach], dot = 0.f, size = 0.f;           // q k of the own key; the sum of |q|
+      uint32_t k_top = 0, v_top = 0;                   // largest elements: of the own key, finite ones of the value
 #pragma unroll
       for (int e = 0; e < kEach; e += 2) {
         const int at = i * D * 2 + (lane * kEach + e) * 2;
@@ -322,11 +325,17 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
         q[e] = __uint_as_float(two << 16);
         q[e + 1] = __uint_as_float(two & 0xffff0000u);
         dot = fmaf(q[e], __uint_as_float(k_two << 16), fmaf(q[e + 1], __uint_as_float(k_two & 0xffff0000u), dot));
+        size += fabsf(q[e]) + fabsf(q[e + 1]);
+        k_top = max(k_top, max(k_two << 16 & 0x7fff0000u, k_two & 0x7fff0000u));
         const uint32_t v0 = v_two << 16 & 0x7fff0000u, v1 = v_two & 0x7fff0000u;
         v_top = max(v_top, max(v0 < 0x7f800000u ? v0 : 0u, v1 < 0x7f800000u ? v1 : 0u));
       }
 #pragma unroll
-      for (int x = 16; x > 0; x /= 2) dot += __shfl_xor_sync(~0u, dot, x);
+      for (int x = 16; x > 0; x /= 2) {
+        dot += __shfl_xor_sync(~0u, dot, x);
+        size += __shfl_xor_sync(~0u, size, x);
+      }
+      k_top = __reduce_max_sync(~0u, k_top);
       v_top = __reduce_max_sync(~0u, v_top);
       uint32_t top = 0;
       bool finite = true;
@@ -359,7 +368,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
         // rows with an infinite or NaN element become NaN through their factor
         s_factor[r] = finite ? exp2_int(eq) * L.scale_log2 : __int_as_float(0x7fffffff);
         const float t = dot * L.scale_log2 + min(need_exp(v_top), kMaxExp);
-        s_minus[r] = r < live && fabsf(t) < 1e29f ? kLift - (t - kStart) : -kNoRef;
+        // only where the tensor core's sum is sure to be near this one: its parts are off by 2^-18 of sum |q| max |k|
+        const bool sure = size * __uint_as_float(k_top) * L.scale_log2 < 4096.f;
+        s_minus[r] = r < live && sure ? kLift - (t - kStart) : -kNoRef;
+        s_low[r] = 0.f;
       }
     }
     fence_proxy_async_smem();
@@ -802,35 +814,44 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
         const uint64_t kf2 = f2_pack(kf, kf);
         float over4[4] = {0.f, 0.f, 0.f, 0.f};
         const uint64_t sixteenth = f2_pack(0.0625f, 0.0625f);
+        const bool far = *static_cast<volatile int*>(&s_far) != 0;
         uint32_t hi[2][8], lo[2][8];                   // eight rows, and the next eight on their way
         tmem_ld(s_at, hi[0]);
         tmem_ld(s_at + R, lo[0]);
 #pragma unroll
-        for (int r = 0; r < RH; r += 4) {
-          if (r % 8 == 0) {
-            tmem_wait_for(hi[r / 8 & 1], lo[r / 8 & 1]);
-            if (r + 8 < RH) {
-              tmem_ld(s_at + r + 8, hi[(r / 8 + 1) & 1]);
-              tmem_ld(s_at + R + r + 8, lo[(r / 8 + 1) & 1]);
-            }
+        for (int r = 0; r < RH; r += 8) {
+          const uint32_t* h = hi[r / 8 & 1];
+          const uint32_t* l = lo[r / 8 & 1];
+          tmem_wait_for(hi[r / 8 & 1], lo[r / 8 & 1]);
+          if (r + 8 < RH) {
+            tmem_ld(s_at + r + 8, hi[(r / 8 + 1) & 1]);
+            tmem_ld(s_at + R + r + 8, lo[(r / 8 + 1) & 1]);
           }
-          const uint32_t* h = hi[r / 8 & 1] + r % 8;
-          const uint32_t* l = lo[r / 8 & 1] + r % 8;
           auto both = [&](int e) {                       // S of rows r + e, r + e + 1
             return f2_fma(f2_pack(__uint_as_float(l[e]), __uint_as_float(l[e + 1])), sixteenth,
                           f2_pack(__uint_as_float(h[e]), __uint_as_float(h[e + 1])));
           };
-          const float4 f = *reinterpret_cast<const float4*>(factor + r), m = *reinterpret_cast<const float4*>(minus + r);
-          float d[4];
-          f2_unpack(f2_fma(f2_mul(both(0), f2_pack(f.x, f.y)), kf2, f2_pack(m.x, m.y)), d[0], d[1]);
-          f2_unpack(f2_fma(f2_mul(both(2), f2_pack(f.z, f.w)), kf2, f2_pack(m.z, m.w)), d[2], d[3]);
-          const uint32_t four = mask << (r / 4);
-          p[r] = __float_as_uint(exp2_fast(d[0])) & spread<0>(four);
-          p[r + 1] = __float_as_uint(exp2_fast(d[1])) & spread<1>(four);
-          p[r + 2] = __float_as_uint(exp2_fast(d[2])) & spread<2>(four);
-          p[r + 3] = __float_as_uint(exp2_fast(d[3])) & spread<3>(four);
-          over4[r / 4 & 1] = fmax3(over4[r / 4 & 1], __uint_as_float(p[r]), __uint_as_float(p[r + 1]));
-          over4[2 + (r / 4 & 1)] = fmax3(over4[2 + (r / 4 & 1)], __uint_as_float(p[r + 2]), __uint_as_float(p[r + 3]));
+          float d[8];
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(factor + r + e), m = *reinterpret_cast<const float4*>(minus + r + e);
+            f2_unpack(f2_fma(f2_mul(both(e), f2_pack(f.x, f.y)), kf2, f2_pack(m.x, m.y)), d[e], d[e + 1]);
+            f2_unpack(f2_fma(f2_mul(both(e + 2), f2_pack(f.z, f.w)), kf2, f2_pack(m.z, m.w)), d[e + 2], d[e + 3]);
+          }
+          if (far) {                                   // the references' second parts
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] += s_low[part * RH + r + e];
+          }
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            const uint32_t four = mask << ((r + e) / 4);
+            p[r + e] = __float_as_uint(exp2_fast(d[e])) & spread<0>(four);
+            p[r + e + 1] = __float_as_uint(exp2_fast(d[e + 1])) & spread<1>(four);
+            p[r + e + 2] = __float_as_uint(exp2_fast(d[e + 2])) & spread<2>(four);
+            p[r + e + 3] = __float_as_uint(exp2_fast(d[e + 3])) & spread<3>(four);
+            over4[e / 4] = fmax3(over4[e / 4], __uint_as_float(p[r + e]), __uint_as_float(p[r + e + 1]));
+            over4[2 + e / 4] = fmax3(over4[2 + e / 4], __uint_as_float(p[r + e + 2]), __uint_as_float(p[r + e + 3]));
+          }
         }
         over = fmaxf(fmaxf(over4[0], over4[1]), fmaxf(over4[2], over4[3]));
       };
@@ -856,8 +877,13 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
         if (dead) break;
         // Some row's reference moves, by the row's own weights: rows do not touch each other.
         // Lane r takes row r (the same result in the part's four warps).
-        int top = INT_MIN;
+        int2 top = make_int2(INT_MIN, INT_MIN);        // largest s; largest t - that
         const float ve = static_cast<float>(static_cast<int8_t>(ex >> 8));
+        auto order = [](float x) {                     // floats' order as integers, and back
+          const int u = __float_as_int(x);
+          return u ^ (u >> 31 & 0x7fffffff);
+        };
+        auto number = [](int m) { return m == INT_MIN ? -INFINITY : __int_as_float(m ^ (m >> 31 & 0x7fffffff)); };
 #pragma unroll 1
         for (int c = 0; c < RH; c += 8) {
           uint32_t s[8], low[8];
@@ -867,22 +893,39 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int r = c + i;
-            const float t = fmaf(fmaf(__uint_as_float(low[i]), 0.0625f, __uint_as_float(s[i])) * factor[r], kf, ve);
-            const int u = __float_as_int(t), order = u ^ (u >> 31 & 0x7fffffff);   // floats' order as integers
-            const bool mine = mask >> ((r & 3) * 8 + 7 - r / 4) & 1 && t == t;
-            const int m = __reduce_max_sync(~0u, mine ? order : INT_MIN);
-            if (lane == r) top = m;
+            const float logit = fmaf(__uint_as_float(low[i]), 0.0625f, __uint_as_float(s[i])) * factor[r] * kf;
+            const bool mine = mask >> ((r & 3) * 8 + 7 - r / 4) & 1 && logit == logit;
+            const int m = __reduce_max_sync(~0u, mine ? order(logit) : INT_MIN);
+            const int past = __reduce_max_sync(~0u, mine ? order(logit - number(m) + ve) : INT_MIN);
+            if (lane == r) top = make_int2(m, past);
           }
         }
         if (lane < RH) s_top[quad][part * RH + lane] = top;
         named_barrier(1 + part, 128);
-        float moved = 0.f, fh = 1.f;                   // the factor's root: it may lie below the normals where sums do not
+        float moved = 0.f, moved_low = 0.f, fh = 1.f;  // the factor's root: it may lie below the normals where sums do not
         if (lane < RH) {
           const int rr = part * RH + lane;
-          const int m = max(max(s_top[0][rr], s_top[1][rr]), max(s_top[2][rr], s_top[3][rr]));
-          const float was = s_minus[rr], highest = m == INT_MIN ? -INFINITY : __int_as_float(m ^ (m >> 31 & 0x7fffffff));
-          moved = highest > (kLift - was) + kTop ? kLift - (highest - kBelow) : was;
-          fh = exp2_fast(0.5f * (moved - was));
+          const float was = s_minus[rr], was_low = s_low[rr];
+          float highest = -INFINITY, past = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) highest = fmaxf(highest, number(s_top[x][rr].x));
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (s_top[x][rr].x != INT_MIN) past = fmaxf(past, number(s_top[x][rr].x) - highest + number(s_top[x][rr].y));
+          moved = was;
+          moved_low = was_low;
+          if (highest + was + (past + was_low) - kLift > kTop) {
+            moved_low = kLift - (past - kBelow);
+            moved = -highest;
+            // far from 0 the second part would be lost in the first
+            if (fabsf(highest) < 0x1p20f) {
+              moved += moved_low;
+              moved_low = 0.f;
+            } else {
+              s_far = 1;
+            }
+          }
+          fh = exp2_fast(0.5f * (moved - was + (moved_low - was_low)));
         }
 #pragma unroll
         for (int r = 0; r < RH; r += 2) {
@@ -908,7 +951,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
           tmem_wait_st();
         }
         named_barrier(1 + part, 128);                  // every warp has read the old references
-        if (quad == 0 && lane < RH) minus[lane] = moved;
+        if (quad == 0 && lane < RH) {
+          minus[lane] = moved;
+          s_low[part * RH + lane] = moved_low;
+        }
         named_barrier(1 + part, 128);
       }
       if (dead || cnt == 0) break;
@@ -1000,29 +1046,33 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
   }
   if (threadIdx.x >= kSoftWarps * 32 && threadIdx.x < kSoftWarps * 32 + R) {           // (by warps that send no rows)
     const int r = threadIdx.x - kSoftWarps * 32;
-    *cluster.map_shared_rank(&s_all[rank][r], r * inverse >> 16) =
-        make_float2(-s_minus[r], (s_l[0][r] + s_l[1][r]) + (s_l[2][r] + s_l[3][r]));
+    const int to = r * inverse >> 16;
+    *cluster.map_shared_rank(&s_all[rank * share + r - to * share], to) =
+        make_float4(-s_minus[r], -s_low[r], (s_l[0][r] + s_l[1][r]) + (s_l[2][r] + s_l[3][r]), 0.f);
   }
   tc_fence_before();
   cluster.sync();
   tc_fence_after();
   // the block's rows: half a warp a row, a lane a block
-  const int mine_to = min((rank + 1) * share, R);
 #pragma unroll 1
-  for (int r0w = rank * share + threadIdx.x / 32 * 2; r0w < mine_to; r0w += kThreads / kMaxCluster) {
-    const int r = r0w + lane / kMaxCluster, x = lane % kMaxCluster;
-    const float2 a = x < cs && r < mine_to ? s_all[x][r] : make_float2(kNoRef, 0.f);
-    float M = a.x;
+  for (int local = warp * 2 + lane / kMaxCluster; __any_sync(~0u, local < share); local += kThreads / kMaxCluster) {
+    const int x = lane % kMaxCluster, r = rank * share + local, at = x * share + local;
+    const bool there = x < cs && local < share && r < R;
+    const float4 a = there ? s_all[at] : make_float4(kNoRef, 0.f, 0.f, 0.f);
+    float M = a.x + a.y;                               // the largest reference, and its parts
 #pragma unroll
     for (int y = kMaxCluster / 2; y > 0; y /= 2) M = fmaxf(M, __shfl_xor_sync(~0u, M, y));
-    const float fh = exp2f(0.5f * (a.x - M));
-    float l = a.y != 0.f ? a.y * fh * fh : 0.f;
+    const uint32_t top = __ballot_sync(~0u, a.x + a.y == M) >> (lane & kMaxCluster) & ((1u << kMaxCluster) - 1);
+    const int from = (lane & kMaxCluster) + max(__ffs(top) - 1, 0);
+    const float hi = __shfl_sync(~0u, a.x, from), lo = __shfl_sync(~0u, a.y, from);
+    const float fh = exp2f(0.5f * (a.x - hi + (a.y - lo)));
+    float l = a.z != 0.f ? a.z * fh * fh : 0.f;
 #pragma unroll
     for (int y = kMaxCluster / 2; y > 0; y /= 2) l += __shfl_xor_sync(~0u, l, y);
-    if (x < cs && r < mine_to) s_weight[x][r] = a.y != 0.f ? fh * (fh * exp2_int(kLift)) / l : 0.f;
-    if (x == 0 && L.lse && r < min(mine_to, live))
+    if (there) s_weight[at] = a.z != 0.f ? fh * (fh * exp2_int(kLift)) / l : 0.f;
+    if (x == 0 && L.lse && there && r < live)
       L.lse[(static_cast<size_t>(b) * L.H + h * G + (r0 + r) % G) * L.n + node_of((r0 + r) / G)] =
-          l != 0.f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          l != 0.f ? (hi + (lo + log2f(l))) * 0.6931471805599453f : -INFINITY;
   }
   __syncthreads();
 #pragma unroll 1
@@ -1032,9 +1082,9 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, 1) cache_tree_tc_kernel(C
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int x = 0; x < cs; ++x) {
-      const float f = s_weight[x][r];
+      const float f = s_weight[x * share + local];
       float4 u = *reinterpret_cast<const float4*>(inbox + (x * share + local) * D + d);
-      if (s_all[x][r].y == 0.f) u = make_float4(0.f, 0.f, 0.f, 0.f);       // nothing kept there, nothing written if it had no tile
+      if (s_all[x * share + local].z == 0.f) u = make_float4(0.f, 0.f, 0.f, 0.f);       // nothing kept there, nothing written if it had no tile
       a.x += u.x * f; a.y += u.y * f; a.z += u.z * f; a.w += u.w * f;
     }
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(L.O) +

@@ -240,3 +240,25 @@ def test_gid_outside_the_groups_matches_nothing_cached(fz):
         Q, Kd, Vd, gid, parent = _draft(rng, 1, G, 1, T, 128, 3, 1, "bf16")
         gid[0, 0, 1], gid[0, 0, 2] = 5000, -3
         _check(fz, c, Q, Kd, Vd, gid, parent, 3, 2, "bf16")
+
+
+@pytest.mark.parametrize("size", [0, 6, 12, 18, 40])
+def test_weights_of_huge_logits_still_sum_to_one(fz, size):
+    """Values are all one, so outputs are, however large the logits and their rounding: off by bf16's half
+    step, and 2^-12 for the weights' and the sum's roundings."""
+    import torch
+    rng = np.random.default_rng(21)
+    G, T, d = 4, 12, 128
+    for shape in ("star", "chain"):
+        for lens in ([0], [100]):
+            c = _make(22, 1, 1, d, lens, 2, 1)
+            Q, Kd, Vd, gid, parent = _draft(rng, 1, G, 1, T, d, 2, 1, "bf16", shape)
+            Q, Kd = Q * 2.0 ** (size + 4), Kd * 2.0 ** size
+            p, cache = _params(fz, 1, G, 1, T, d, 2, 1, 9, "bf16"), _cache(fz, c)
+            cache.v.copy_(torch.ones_like(cache.v, dtype=torch.float32).to(torch.float8_e4m3fn).view(torch.uint8))
+            cache.v_scale.fill_(1.0)
+            q, k = _dev(Q, torch.bfloat16), _dev(Kd, torch.bfloat16)
+            O, lse, ws = torch.zeros_like(q), torch.zeros(1, G, T, device="cuda"), fz.alloc_workspace_tree(p)
+            fz.focus_cache_attention_tree_fwd(p, q, k, torch.ones_like(k), _dev(gid), _dev(parent), cache, O, lse, ws)
+            assert fz.focus_check_errors(ws) == 0 and torch.isfinite(lse).all()
+            assert ((O.float() - 1).abs() <= 2.0 ** -8 + 2.0 ** -12).all()
