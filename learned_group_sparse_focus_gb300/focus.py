@@ -486,13 +486,13 @@ def _cache_call(fn: str, p: Params, cache: Cache, ws, stream, *args):
 def _device_call(fn: str, p: Params, dev, owner: str, ws, stream, *args):
     """Runs a call on device dev, that of `owner` (args: the C arguments between p
     and ws)."""
-    if dev.type != "cuda":
-        raise ValueError(f"{owner} must be on a CUDA device, not {dev}")
-    if ws.device != dev or (stream is not None and stream.device != dev):
+    if ws.device != dev or not ws.is_cuda or (stream is not None and stream.device != dev):
+        if dev.type != "cuda":
+            raise ValueError(f"{owner} must be on a CUDA device, not {dev}")
         raise ValueError(f"workspace and stream must be on {owner}'s device {dev}")
-    call = getattr(_lib, fn)
-    raw = _raw_stream(dev.index) if stream is None else stream.cuda_stream
-    if dev.index == torch.cuda.current_device():
+    call, index = getattr(_lib, fn), dev.index
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == torch._C._cuda_getDevice():              # (torch.cuda.current_device costs twice that; CUDA is up)
         st = call(p, *args, _ptr(ws), ws.numel(), raw)
     else:
         with torch.cuda.device(dev):
