@@ -618,12 +618,13 @@ FOCUS_API size_t focus_tree_workspace_bytes(const focus_params_t* p);
  *   behind them of O and lse_opt stay as they were;
  *   lse_opt [B, H, n] fp32 or NULL.
  * O overlaps no input.  A sequence whose next + n_new would pass 2^31 - 1 is flagged as
- * FOCUS_ERR_BAD_CACHE, as are bad counts and pages (clamped, left out).  Precision, logits and NaN codes as focus_cache_attention_fwd; a
- * drafted key or value row with an infinite or NaN element gives NaN to the nodes that keep
- * it and to no others; drafted keys' elements below 2^-11 of their row's largest are held to
- * 2^-19 of that, drafted values below 2^-73 count as 0.  To gather mass for an
- * eviction, attend the accepted tokens with focus_cache_attention_fwd once they are
- * appended.  ws: of focus_tree_workspace_bytes. */
+ * FOCUS_ERR_BAD_CACHE, as are bad counts and pages (clamped, left out).  Precision, logits
+ * and NaN codes as focus_cache_attention_fwd; a drafted key or value row with an infinite or
+ * NaN element gives NaN to the nodes that keep it and to no others; drafted keys' elements
+ * below 2^-11 of their row's largest are held to 2^-19 of that, drafted values below 2^-73
+ * count as 0.  A group id outside [0, K) equals no cached slot's.  To gather
+ * mass for an eviction, attend the accepted tokens with focus_cache_attention_fwd once they
+ * are appended.  ws: of focus_tree_workspace_bytes. */
 FOCUS_API focus_status_t focus_cache_attention_tree_fwd(const focus_params_t* p, const void* Q,
                                                         const void* K, const void* V, const int32_t* gid,
                                                         const int32_t* parent, const int32_t* n_new,

@@ -10,7 +10,7 @@
 // Measured: the gradient of 2 x 8K tokens of 32 + 32 heads 85 us (6.3 TB/s: 93% of a plain copy's rate); trees of
 // 64 nodes, 8 x 72 fp32 heads 8.0 us.  The append of a prompt of 32K tokens of 32 / 8 heads with queries and turned
 // keys 130 us (6.2 TB/s), without queries 71 us (2.8 TB/s: a page's block takes 12,000 clocks, of which half are
-// the loads' latencies and the tables, and blocks of four an SM hide a part); one token of 16 sequences 8 us.
+// the loads' latencies and the tables; four blocks an SM hide a part); one token of 16 sequences 8 us.
 //
 // Appended keys go from the turned fp32 value to e4m3 in one rounding.  What is stored is
 // what exact arithmetic would store: the fp32 value is within kUnsure of its pair's size, so
